@@ -365,6 +365,89 @@ gq_status lut_gemv(const uint32_t* Q, const float* C, int64_t d_out, int64_t d_i
                    const void* x, gq_dtype x_dt, int32_t batch, float* y, void* stream);
 
 /*
+ * MXFP4: rows of microscaled 4-bit floating point (the OCP Microscaling format of e2m1
+ * elements with e8m0 scales), the quantised format that the matrix cores multiply
+ * directly; these entry points stand beside the lookup-table format above.
+ *
+ * Layout.  A row of d values is cut into blocks of 32 and padded to whole groups of 128
+ * values (4 blocks).  Q holds the codes, mxfp4_row_bytes(d) = 64 ceil(d / 128) bytes a row,
+ * element 2 i in the low and 2 i + 1 in the high nibble of byte i; a code is a sign bit over
+ * the index of one of the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.  S holds one byte s a
+ * block, mxfp4_row_scales(d) = 4 ceil(d / 128) bytes a row: the block's scale 2^(s - 127),
+ * s = 255 meaning NaN.  Codes past d are 0, scale bytes past the last block 127.  Where d
+ * is a multiple of 128 this is the plain row-major layout of codes and scales.  The two
+ * size functions return 0 for d < 1 or d > 2^20.
+ *
+ * Every Q is 16-byte and every S 4-byte aligned.  d_in, d_out and d are at most 2^20
+ * (GQ_ENOTIMPL beyond).  n = 0 and rows = 0 are valid and do nothing.
+ */
+int64_t mxfp4_row_bytes(int64_t d);
+int64_t mxfp4_row_scales(int64_t d);
+
+/*
+ * x [rows][d] (x_dt) -> Q, S.  Per block, s = floor(log2 max|x|) - 2 + 127, at least 0 (a
+ * block of zeros has s = 0); each value over 2^(s - 127) is rounded to the nearest magnitude, ties to
+ * the even index, 6 above it (the block's maximum lies in [4, 8) scale units).  A sign is
+ * kept, also of a value that rounds to zero.  A block with a NaN or an infinity has s = 255
+ * and codes 0.  x element-aligned.
+ * Weights (once per layer, rows = d_out, d = d_in; several experts' weights are one call
+ * with rows = experts * d_out) and activations (per call, rows = tokens) are packed alike.
+ */
+gq_status mxfp4_quantize(const void* x, gq_dtype x_dt, int64_t rows, int64_t d, uint8_t* Q,
+                         uint8_t* S, void* stream);
+
+/*
+ * Q, S -> y [rows][d] (y_dt), the values they stand for: exact in either type (below the
+ * normal range too), but for codes over its largest value, which give infinity (s >= 253;
+ * mxfp4_quantize writes at most 252 but for NaN).  y element-aligned.
+ */
+gq_status mxfp4_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t d, void* y,
+                           gq_dtype y_dt, void* stream);
+
+/*
+ * Products with an MXFP4 weight W [d_out][d_in]:
+ *   mxfp4_gemm     y [n][d_out] = x W^T, x [n][d_in] (x_dt) as given;
+ *   mxfp4_gemm_mx  y [n][d_out] = x W^T, x [n][d_in] in MXFP4 too (XQ, XS);
+ *   mxfp4_gemm_dx  dx [n][d_in] = g W, g [n][d_out] (g_dt): the gradient of either product's
+ *                  input from that of its output (W itself is frozen).
+ * experts = 1 with offsets = NULL is one weight for all rows.  Otherwise Q and S hold
+ * `experts` weights one after another, offsets (device int64 [experts + 1]) is
+ * nondecreasing within [0, n], and rows offsets[e] .. offsets[e + 1] - 1 are multiplied by
+ * weight e (none where the two are equal).  Rows before offsets[0] and from
+ * offsets[experts] on are neither read nor written.  The library cannot refuse bad offsets
+ * (they are on the device): each is clamped to [0, n] and an expert whose end lies before its
+ * start has no rows, so nothing is read or written out of range; rows that two experts
+ * claim, or that bad offsets leave over, hold unspecified values.
+ *
+ * Precision.  A weight's value is exact in bfloat16, products with bfloat16 x are exact and
+ * sums are float32.  float32 x is split into three bfloat16 planes whose sum is x, so its
+ * products are exact too.  mxfp4_gemm_mx: the matrix cores' scaled product, exact products
+ * and float32 sums.  y is rounded once to y_dt.  A NaN or infinity stays within its row of
+ * x (and, from a NaN block, its row of W).  The order of the sums depends on the sizes
+ * alone, so equal calls give equal bits.
+ *
+ * Alignment: x and g 16-byte aligned where they are bfloat16 and their rows are a multiple
+ * of 8 elements, else element-aligned; y and dx element-aligned.  ws as for every entry
+ * point, of at least the matching size (which can be 0).  y and dx must not overlap the
+ * inputs or ws.  1 <= experts <= 4096 (GQ_ENOTIMPL beyond), n < 2^31.
+ */
+size_t mxfp4_gemm_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts,
+                                 gq_dtype x_dt);
+gq_status mxfp4_gemm(const void* x, gq_dtype x_dt, int64_t n, int64_t d_in, const uint8_t* Q,
+                     const uint8_t* S, int64_t d_out, int32_t experts, const int64_t* offsets,
+                     void* y, gq_dtype y_dt, void* ws, size_t ws_bytes, void* stream);
+size_t mxfp4_gemm_mx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts);
+gq_status mxfp4_gemm_mx(const uint8_t* XQ, const uint8_t* XS, int64_t n, int64_t d_in,
+                        const uint8_t* Q, const uint8_t* S, int64_t d_out, int32_t experts,
+                        const int64_t* offsets, void* y, gq_dtype y_dt, void* ws,
+                        size_t ws_bytes, void* stream);
+size_t mxfp4_gemm_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts,
+                                    gq_dtype g_dt);
+gq_status mxfp4_gemm_dx(const void* g, gq_dtype g_dt, int64_t n, int64_t d_out, const uint8_t* Q,
+                        const uint8_t* S, int64_t d_in, int32_t experts, const int64_t* offsets,
+                        void* dx, gq_dtype dx_dt, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * GANQ-style alternation.  The GANQ summary page ("Approach") solves each row by
  * alternating a closed-form least-squares codebook update with an assignment of
  * the indices by Cholesky / back-substitution.  Here: F'_g = L L^T (float64
@@ -428,8 +511,8 @@ typedef enum {
     GQ_STAGE_LNQ_SMALL,         /* sums and counters */
     GQ_STAGE_FISHER_PACK,       /* feature-major bf16 operands of the Fisher contraction */
     GQ_STAGE_LNQ_DELTA,         /* Gram and residual updates from the changed coordinates */
-    GQ_STAGE_LUT_PACK,          /* code packing for the lookup-table product */
-    GQ_STAGE_LUT_GEMV,          /* the lookup-table product */
+    GQ_STAGE_LUT_PACK,          /* code packing: lookup-table codes, and MXFP4 both ways */
+    GQ_STAGE_LUT_GEMV,          /* products with packed weights: lookup-table and MXFP4 */
     GQ_STAGE_FISHER_H2D,        /* host-to-device copies of the streamed Fisher (copy stream) */
     GQ_STAGE_GANQ_CHOL,         /* Cholesky factor of F' for the back-substitution assignment */
     GQ_STAGE_GANQ_PASS,         /* the back-substitution assignment */

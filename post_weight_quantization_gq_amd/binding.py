@@ -9,6 +9,7 @@ host-sanitized libgq_asan.so, see build.py).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -35,6 +36,9 @@ EXPORTS = (
     "grid_quantize", "lut_packed_row_words", "lut_pack_codes",
     "lut_gemv", "gq_fisher_stream_workspace_size", "gq_fisher_accumulate_host",
     "ganq_workspace_size", "ganq_quantize", "ganq_factor_damped",
+    "mxfp4_row_bytes", "mxfp4_row_scales", "mxfp4_quantize", "mxfp4_dequantize",
+    "mxfp4_gemm_workspace_size", "mxfp4_gemm", "mxfp4_gemm_mx_workspace_size", "mxfp4_gemm_mx",
+    "mxfp4_gemm_dx_workspace_size", "mxfp4_gemm_dx",
     "gq_timing_enable", "gq_timing_read", "gq_stage_name",
 )
 STAGE_COUNT = 18
@@ -95,6 +99,19 @@ _SIGS = {
                                      ctypes.POINTER(lnq_options), _vp, _vp, _vp, _vp, _vp, _vp,
                                      _sz, _vp]),
     "ganq_factor_damped": (ctypes.c_int, [_vp, _i32, _i64, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "mxfp4_row_bytes": (_i64, [_i64]),
+    "mxfp4_row_scales": (_i64, [_i64]),
+    "mxfp4_quantize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _vp, _vp, _vp]),
+    "mxfp4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i32, _vp]),
+    "mxfp4_gemm_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "mxfp4_gemm": (ctypes.c_int, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _i32,
+                                  _vp, _sz, _vp]),
+    "mxfp4_gemm_mx_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "mxfp4_gemm_mx": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _i32,
+                                     _vp, _sz, _vp]),
+    "mxfp4_gemm_dx_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "mxfp4_gemm_dx": (ctypes.c_int, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _i32,
+                                     _vp, _sz, _vp]),
     "gq_timing_enable": (None, [ctypes.c_int]),
     "gq_timing_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gq_stage_name": (ctypes.c_char_p, [ctypes.c_int]),
@@ -554,6 +571,179 @@ def lut_gemv(Q, C, x, bits: int, d_in: int | None = None, y=None, stream=None) -
     _check(lib.lut_gemv(_ptr(Q), _ptr(C), d_out, d_in, bits, _ptr(xx), _dt(xx), batch, _ptr(y),
                         _stream(stream)))
     return y if x.dim() == 2 else y[0]
+
+
+def mxfp4_row_bytes(d: int) -> int:
+    return int(library().mxfp4_row_bytes(d))
+
+
+def mxfp4_row_scales(d: int) -> int:
+    return int(library().mxfp4_row_scales(d))
+
+
+@contextlib.contextmanager
+def _on(t, stream):
+    """The stream pointer of a call on t's device: that device is current, and what the call
+    allocates belongs to the stream it runs on (its memory is reused in that stream's order)."""
+    with torch.cuda.device(t.device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        else:
+            if stream.device != t.device:
+                raise GQError(GQ_EINVAL, f"stream of {stream.device} for tensors on {t.device}")
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _mx_packed(Q, S, d, lead, names=("Q", "S")):
+    """Shapes of packed rows of d values, the leading dimensions being `lead`."""
+    rb, rs = mxfp4_row_bytes(d), mxfp4_row_scales(d)
+    if rb == 0:
+        raise GQError(GQ_ESHAPE if d < 1 else GQ_ENOTIMPL, f"rows of {d} values: 1 to 2^20")
+    _shape(Q, (*lead, rb), names[0])
+    _shape(S, (*lead, rs), names[1])
+    for t, name in ((Q, names[0]), (S, names[1])):
+        if t is not None:
+            _dev(t, name, torch.uint8)
+
+
+def mxfp4_quantize(x, Q=None, S=None, stream=None):
+    """x [..][d] float32 or bfloat16 -> (Q [..][64 ceil(d / 128)], S [..][4 ceil(d / 128)])
+    uint8: 4-bit codes and a scale byte for each block of 32 along the last dimension."""
+    lib = library()
+    if x.dim() < 1:
+        raise GQError(GQ_ESHAPE, "x needs a last dimension to quantise along")
+    lead, d = tuple(x.shape[:-1]), x.shape[-1]
+    _mx_packed(Q, S, d, lead)
+    dt = _dt(_dev(x, "x"))
+    _same_device(x, Q, S)
+    with _on(x, stream) as st:
+        if Q is None:
+            Q = torch.empty((*lead, mxfp4_row_bytes(d)), dtype=torch.uint8, device=x.device)
+        if S is None:
+            S = torch.empty((*lead, mxfp4_row_scales(d)), dtype=torch.uint8, device=x.device)
+        _check(lib.mxfp4_quantize(_ptr(x), dt, x.numel() // d, d, _ptr(Q), _ptr(S), st))
+    return Q, S
+
+
+def mxfp4_dequantize(Q, S, d: int, dtype=torch.bfloat16, y=None, stream=None) -> torch.Tensor:
+    """The values [..][d] that packed rows stand for, in float32 or bfloat16."""
+    lib = library()
+    lead = tuple(Q.shape[:-1])
+    _mx_packed(Q, S, d, lead)
+    _shape(y, (*lead, d), "y")
+    if y is not None:
+        _dev(y, "y", dtype)
+    _same_device(Q, S, y)
+    with _on(Q, stream) as st:
+        if y is None:
+            y = torch.empty((*lead, d), dtype=dtype, device=Q.device)
+        _check(lib.mxfp4_dequantize(_ptr(Q), _ptr(S), y.numel() // d, d, _ptr(y), _dt(y), st))
+    return y
+
+
+def mxfp4_gemm_workspace_size(n, d_in, d_out, experts=1, dtype=GQ_BF16) -> int:
+    return int(library().mxfp4_gemm_workspace_size(n, d_in, d_out, experts, dtype))
+
+
+def mxfp4_gemm_mx_workspace_size(n, d_in, d_out, experts=1) -> int:
+    return int(library().mxfp4_gemm_mx_workspace_size(n, d_in, d_out, experts))
+
+
+def mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts=1, dtype=GQ_BF16) -> int:
+    return int(library().mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts, dtype))
+
+
+def _mx_weight(Q, S, d_in, offsets):
+    """(experts, d_out) of a packed weight, one ([d_out][..]) or, with offsets, several
+    ([experts][d_out][..])."""
+    if Q.dim() != (2 if offsets is None else 3):
+        raise GQError(GQ_ESHAPE, "Q must be [d_out][row bytes], or [experts][d_out][row bytes] "
+                                 "with offsets")
+    _mx_packed(Q, S, d_in, tuple(Q.shape[:-1]))
+    if offsets is None:
+        return 1, Q.shape[0]
+    if offsets.dtype != torch.int64:
+        raise GQError(GQ_EDTYPE, f"offsets must be int64, got {offsets.dtype}")
+    _shape(offsets, (Q.shape[0] + 1,), "offsets")
+    _dev(offsets, "offsets")
+    return Q.shape[0], Q.shape[1]
+
+
+def _mx_run(name, x, x_args, size_dt, n, d_in, d_out, width, Q, S, experts, offsets, y, out_dtype,
+            ws, stream):
+    """The part that the three products share: output, workspace and the call itself.  Only
+    with an output of its own does a grouped product need y's rows past the last expert: they
+    are zeroed."""
+    lib = library()
+    if y is not None and out_dtype is not None and y.dtype != out_dtype:
+        raise GQError(GQ_EDTYPE, f"y is {y.dtype}, out_dtype {out_dtype}")
+    _shape(y, (n, width), "y")
+    if y is not None:
+        _dev(y, "y")
+    _same_device(x, Q, S, offsets, y, ws if isinstance(ws, torch.Tensor) else None)
+    with _on(x, stream) as st:
+        if y is None:
+            new = torch.empty if offsets is None else torch.zeros
+            y = new((n, width), dtype=out_dtype, device=x.device)
+        if ws is None:
+            ws = _ws(int(getattr(lib, name + "_workspace_size")(n, d_in, d_out, experts, *size_dt)),
+                     x.device)
+        wp, wn = _ws_arg(ws)
+        _check(getattr(lib, name)(*x_args, _ptr(Q), _ptr(S),
+                                  d_in if name == "mxfp4_gemm_dx" else d_out, experts,
+                                  _ptr(offsets), _ptr(y), _dt(y), wp, wn, st))
+    return y
+
+
+def mxfp4_gemm(x, Q, S, offsets=None, y=None, out_dtype=None, ws=None, stream=None) -> torch.Tensor:
+    """y [n][d_out] = x W^T for x [n][d_in] (float32 or bfloat16) and the packed weight (Q, S)
+    of mxfp4_quantize.  With offsets (int64 [experts + 1] on the device) rows offsets[e] ..
+    offsets[e + 1] - 1 of x are multiplied by weight e of Q [experts][d_out][row bytes], and
+    the rows past offsets[experts] of a given y keep their values (of a new one: zeros).
+    out_dtype: float32 or bfloat16, x's unless given."""
+    if x.dim() != 2:
+        raise GQError(GQ_ESHAPE, "x must be [n][d_in]")
+    n, d_in = x.shape
+    experts, d_out = _mx_weight(Q, S, d_in, offsets)
+    dt = _dt(_dev(x, "x"))
+    if y is None and out_dtype is None:
+        out_dtype = x.dtype
+    return _mx_run("mxfp4_gemm", x, (_ptr(x), dt, n, d_in), (dt,), n, d_in, d_out, d_out, Q, S,
+                   experts, offsets, y, out_dtype, ws, stream)
+
+
+def mxfp4_gemm_mx(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,
+                  stream=None) -> torch.Tensor:
+    """mxfp4_gemm with the activations packed by mxfp4_quantize as well: XQ [n][row bytes],
+    XS [n][row scales].  out_dtype: bfloat16 unless given."""
+    if XQ.dim() != 2:
+        raise GQError(GQ_ESHAPE, "XQ must be [n][row bytes]")
+    n = XQ.shape[0]
+    experts, d_out = _mx_weight(Q, S, d_in, offsets)
+    _mx_packed(XQ, XS, d_in, (n,), ("XQ", "XS"))
+    _same_device(XQ, XS)
+    if y is None and out_dtype is None:
+        out_dtype = torch.bfloat16
+    return _mx_run("mxfp4_gemm_mx", XQ, (_ptr(XQ), _ptr(XS), n, d_in), (), n, d_in, d_out, d_out,
+                   Q, S, experts, offsets, y, out_dtype, ws, stream)
+
+
+def mxfp4_gemm_dx(g, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,
+                  stream=None) -> torch.Tensor:
+    """dx [n][d_in] = g W for the output's gradient g [n][d_out] (float32 or bfloat16): the
+    gradient of mxfp4_gemm's x (and, straight through the rounding, of the values that
+    mxfp4_gemm_mx's were packed from).  Grouped by offsets like mxfp4_gemm."""
+    if g.dim() != 2:
+        raise GQError(GQ_ESHAPE, "g must be [n][d_out]")
+    n = g.shape[0]
+    experts, d_out = _mx_weight(Q, S, d_in, offsets)
+    _shape(g, (n, d_out), "g")
+    dt = _dt(_dev(g, "g"))
+    if y is None and out_dtype is None:
+        out_dtype = g.dtype
+    return _mx_run("mxfp4_gemm_dx", g, (_ptr(g), dt, n, d_out), (dt,), n, d_in, d_out, d_in, Q, S,
+                   experts, offsets, y, out_dtype, ws, stream)
 
 
 STAGES = ("group_scale", "fisher_mfma", "fisher_finalize", "fisher_plain", "lnq_prepare",

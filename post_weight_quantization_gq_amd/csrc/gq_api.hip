@@ -792,6 +792,127 @@ gq_status lut_gemv(const uint32_t* Q, const float* C, int64_t d_out, int64_t d_i
     return GQ_OK;
 }
 
+int64_t mxfp4_row_bytes(int64_t d) {
+    return d < 1 || d > gq::MX_MAX_D ? 0 : gq::mx_row_bytes(d);
+}
+
+int64_t mxfp4_row_scales(int64_t d) {
+    return d < 1 || d > gq::MX_MAX_D ? 0 : gq::mx_row_scales(d);
+}
+
+static bool mx_el_al(const void* p, gq_dtype t) { return ((uintptr_t)p & (t == GQ_BF16 ? 1u : 3u)) == 0; }
+
+static gq_status mx_rows_check(const void* x, gq_dtype dt, int64_t rows, int64_t d,
+                               const uint8_t* Q, const uint8_t* S) {
+    if (!dtype_ok(dt)) return fail(GQ_EDTYPE, "unsupported dtype %d", (int)dt);
+    if (rows < 0 || d < 1) return fail(GQ_ESHAPE, "rows=%lld d=%lld", (long long)rows, (long long)d);
+    if (d > gq::MX_MAX_D) return fail(GQ_ENOTIMPL, "d=%lld above 2^20", (long long)d);
+    if (rows > ((int64_t)1 << 40) / d)
+        return fail(GQ_ENOTIMPL, "rows=%lld of d=%lld: more than 2^40 values", (long long)rows, (long long)d);
+    if (rows == 0) return GQ_OK;
+    if (!x || !Q || !S) return fail(GQ_EINVAL, "null values, Q or S");
+    if (!al16(Q) || ((uintptr_t)S & 3u) || !mx_el_al(x, dt))
+        return fail(GQ_EINVAL, "Q must be 16-byte, S 4-byte aligned and the values element-aligned");
+    return GQ_OK;
+}
+
+gq_status mxfp4_quantize(const void* x, gq_dtype x_dt, int64_t rows, int64_t d, uint8_t* Q,
+                         uint8_t* S, void* stream) {
+    gq_status rc = mx_rows_check(x, x_dt, rows, d, Q, S);
+    if (rc != GQ_OK || rows == 0) return rc;
+    hipError_t e = gq::mx_quantize_run(x, x_dt == GQ_BF16, rows, d, Q, S, (hipStream_t)stream);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, "mxfp4_quantize");
+}
+
+gq_status mxfp4_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t d, void* y,
+                           gq_dtype y_dt, void* stream) {
+    gq_status rc = mx_rows_check(y, y_dt, rows, d, Q, S);
+    if (rc != GQ_OK || rows == 0) return rc;
+    hipError_t e = gq::mx_dequantize_run(Q, S, rows, d, y, y_dt == GQ_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, "mxfp4_dequantize");
+}
+
+static bool mx_sizes_ok(int64_t n, int64_t d_in, int64_t d_out, int32_t experts) {
+    return n >= 0 && n < ((int64_t)1 << 31) && d_in >= 1 && d_out >= 1 && d_in <= gq::MX_MAX_D &&
+           d_out <= gq::MX_MAX_D && experts >= 1 && experts <= gq::MX_MAX_EXPERTS;
+}
+
+static size_t mx_workspace(gq::MxOp op, gq_dtype a_dt, int64_t n, int64_t d_in, int64_t d_out,
+                           int32_t experts) {
+    if (!mx_sizes_ok(n, d_in, d_out, experts) || !dtype_ok(a_dt) || n == 0) return 0;
+    return gq::mx_gemm_workspace(op, a_dt == GQ_BF16, n, d_in, d_out, experts);
+}
+
+size_t mxfp4_gemm_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts,
+                                 gq_dtype x_dt) {
+    return mx_workspace(gq::MX_GEMM, x_dt, n, d_in, d_out, experts);
+}
+
+size_t mxfp4_gemm_mx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts) {
+    return mx_workspace(gq::MX_GEMM_MX, GQ_BF16, n, d_in, d_out, experts);
+}
+
+size_t mxfp4_gemm_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts,
+                                    gq_dtype g_dt) {
+    return mx_workspace(gq::MX_GEMM_DX, g_dt, n, d_in, d_out, experts);
+}
+
+static gq_status mx_product(gq::MxOp op, const void* a, const uint8_t* as, gq_dtype a_dt, int64_t n,
+                            int64_t d_in, const uint8_t* Q, const uint8_t* S, int64_t d_out,
+                            int32_t experts, const int64_t* offsets, void* y, gq_dtype y_dt,
+                            void* ws, size_t ws_bytes, void* stream, const char* name) {
+    if (!dtype_ok(a_dt) || !dtype_ok(y_dt)) return fail(GQ_EDTYPE, "unsupported dtype");
+    if (n < 0 || d_in < 1 || d_out < 1)
+        return fail(GQ_ESHAPE, "n=%lld d_in=%lld d_out=%lld", (long long)n, (long long)d_in,
+                    (long long)d_out);
+    if (experts < 1) return fail(GQ_EINVAL, "experts must be >= 1 (got %d)", experts);
+    if (!mx_sizes_ok(n, d_in, d_out, experts))
+        return fail(GQ_ENOTIMPL, "n=%lld d_in=%lld d_out=%lld experts=%d: at most 2^31 - 1, 2^20, "
+                    "2^20 and 4096", (long long)n, (long long)d_in, (long long)d_out, experts);
+    if (experts > 1 && !offsets) return fail(GQ_EINVAL, "several experts need offsets");
+    if ((uintptr_t)offsets & 7u) return fail(GQ_EINVAL, "offsets must be 8-byte aligned");
+    if (n == 0) return GQ_OK;
+    if (!a || !Q || !S || !y || (op == gq::MX_GEMM_MX && !as))
+        return fail(GQ_EINVAL, "null activations, Q, S or output");
+    if (!al16(Q) || ((uintptr_t)S & 3u) || ((uintptr_t)as & 3u))
+        return fail(GQ_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
+    const int64_t k = op == gq::MX_GEMM_DX ? d_out : d_in;
+    const bool vec = op == gq::MX_GEMM_MX || (a_dt == GQ_BF16 && k % 8 == 0);
+    if ((vec && !al16(a)) || !mx_el_al(a, a_dt) || !mx_el_al(y, y_dt) || ((uintptr_t)ws & 255u))
+        return fail(GQ_EINVAL, "activations must be 16-byte aligned (element-aligned in float32 or "
+                    "with rows of no multiple of 8), the output element- and ws 256-byte aligned");
+    hipStream_t st = (hipStream_t)stream;
+    const bool ab = a_dt == GQ_BF16;
+    Scratch s;
+    gq_status rc = s.acquire(ws, ws_bytes, gq::mx_gemm_workspace(op, ab, n, d_in, d_out, experts), st);
+    if (rc != GQ_OK) return rc;
+    const gq::MxCall c{op, a, as, ab, n, d_in, d_out, Q, S, experts, offsets, y, y_dt == GQ_BF16};
+    hipError_t e = gq::mx_gemm_run(c, s.ptr, st);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, name);
+}
+
+gq_status mxfp4_gemm(const void* x, gq_dtype x_dt, int64_t n, int64_t d_in, const uint8_t* Q,
+                     const uint8_t* S, int64_t d_out, int32_t experts, const int64_t* offsets,
+                     void* y, gq_dtype y_dt, void* ws, size_t ws_bytes, void* stream) {
+    return mx_product(gq::MX_GEMM, x, nullptr, x_dt, n, d_in, Q, S, d_out, experts, offsets, y, y_dt,
+                      ws, ws_bytes, stream, "mxfp4_gemm");
+}
+
+gq_status mxfp4_gemm_mx(const uint8_t* XQ, const uint8_t* XS, int64_t n, int64_t d_in,
+                        const uint8_t* Q, const uint8_t* S, int64_t d_out, int32_t experts,
+                        const int64_t* offsets, void* y, gq_dtype y_dt, void* ws,
+                        size_t ws_bytes, void* stream) {
+    return mx_product(gq::MX_GEMM_MX, XQ, XS, GQ_BF16, n, d_in, Q, S, d_out, experts, offsets, y,
+                      y_dt, ws, ws_bytes, stream, "mxfp4_gemm_mx");
+}
+
+gq_status mxfp4_gemm_dx(const void* g, gq_dtype g_dt, int64_t n, int64_t d_out, const uint8_t* Q,
+                        const uint8_t* S, int64_t d_in, int32_t experts, const int64_t* offsets,
+                        void* dx, gq_dtype dx_dt, void* ws, size_t ws_bytes, void* stream) {
+    return mx_product(gq::MX_GEMM_DX, g, nullptr, g_dt, n, d_in, Q, S, d_out, experts, offsets, dx,
+                      dx_dt, ws, ws_bytes, stream, "mxfp4_gemm_dx");
+}
+
 size_t ganq_workspace_size(int64_t d_out, int64_t d_in, int32_t groups, int32_t bits,
                            gq_dtype w_dt) {
     const size_t base = gq_lnq_workspace_size(d_out, d_in, groups, bits, w_dt);

@@ -1,0 +1,158 @@
+// MXFP4 rows on gfx950: quantisation and reading back.
+//
+// A block of 32 values x_i has the scale 2^e, e = clamp(floor(log2 max|x_i|) - 2, -127, 125),
+// so its maximum lies in [4, 8) units of the scale; code_i is x_i 2^-e rounded to the nearest
+// of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the even index, 6 above it) with the sign of x_i.
+// Both directions are one pass over the data, bound by HBM: a row of d values moves
+// d (2 or 4) + 68 ceil(d / 128) bytes each way.
+//
+// A lane takes 8 consecutive values (a 16-byte load of bfloat16), so a block is 4 lanes and
+// its maximum two exchanges between neighbours; the codes are a 4-byte store a lane.
+#include "gq_common.h"
+#include "gq_internal.h"
+#include "gq_mx.h"
+
+namespace gq {
+
+// 8 consecutive values of a row of d, from element i of it (p: the row's start); VEC: the
+// row's 8-value pieces are whole and 16-byte aligned, else values past d read as 0.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void mx_load8(const void* p, int64_t row0, int64_t i, int64_t d,
+                                         float (&v)[8]) {
+    if constexpr (VEC) {
+        if (i < d) {
+            if constexpr (BF16) {
+                const u32x4 w = *(const u32x4*)((const uint16_t*)p + row0 + i);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[2 * k] = __uint_as_float(w[k] << 16);
+                    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                }
+            } else {
+                const f32x4 a = *(const f32x4*)((const float*)p + row0 + i);
+                const f32x4 b = *(const f32x4*)((const float*)p + row0 + i + 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) { v[k] = a[k]; v[4 + k] = b[k]; }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = i + k < d ? load_elem<BF16>(p, row0 + i + k) : 0.f;
+    }
+}
+
+// Lane t of the grid takes the 8-value piece t of the padded rows (16 pieces a group of 128).
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ x, int64_t pieces,
+                                                    int64_t d, int ppr, uint32_t* __restrict__ Q,
+                                                    uint8_t* __restrict__ S) {
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= pieces) return;             // pieces is a multiple of 16: blocks stay whole
+    const int64_t r = t / ppr;
+    const int64_t i = (t - r * ppr) * 8;
+    float v[8];
+    mx_load8<BF16, VEC>(x, r * d, i, d, v);
+    // the maximum by magnitude as its bits: they order like the values, NaN above infinity
+    uint32_t top = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t b = __float_as_uint(v[k]) & 0x7fffffffu;
+        top = top > b ? top : b;
+    }
+    uint32_t o = (uint32_t)__shfl_xor((int)top, 1, 64);
+    top = top > o ? top : o;
+    o = (uint32_t)__shfl_xor((int)top, 2, 64);
+    top = top > o ? top : o;
+    // exponent field of the maximum minus 2 is the scale byte; below 2 (maximum under
+    // 2^-125, subnormals and zero) it is 0
+    const uint32_t ef = top >> 23;
+    const bool bad = ef == 255u;
+    const uint32_t s = bad ? 255u : (ef > 2u ? ef - 2u : 0u);
+    const float scale = mx_scale(s);
+    uint32_t q = 0u;
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], scale, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], scale, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], scale, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], scale, 3);
+    Q[t] = bad ? 0u : q;
+    if ((t & 3) == 0) S[t >> 2] = (uint8_t)(i < d ? s : 127u);
+}
+
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(256) void k_mx_dequantize(const uint32_t* __restrict__ Q,
+                                                      const uint8_t* __restrict__ S,
+                                                      int64_t pieces, int64_t d, int ppr,
+                                                      void* __restrict__ y) {
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= pieces) return;
+    const int64_t r = t / ppr;
+    const int64_t i = (t - r * ppr) * 8;
+    if (i >= d) return;
+    const uint32_t q = Q[t];
+    const float scale = mx_scale(S[t >> 2]);
+    const int64_t at = r * d + i;
+    if constexpr (BF16) {
+        const u32x4 w{mx_bf16<0>(q, scale), mx_bf16<1>(q, scale), mx_bf16<2>(q, scale),
+                      mx_bf16<3>(q, scale)};
+        uint16_t* o = (uint16_t*)y + at;
+        if constexpr (VEC) {
+            *(u32x4*)o = w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k < d) o[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+        }
+    } else {
+        const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 0);
+        const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 1);
+        const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 2);
+        const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 3);
+        const float v[8] = {a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
+        float* o = (float*)y + at;
+        if constexpr (VEC) {
+            *(f32x4*)o = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4*)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k < d) o[k] = v[k];
+        }
+    }
+}
+
+hipError_t mx_quantize_run(const void* x, bool x_bf16, int64_t rows, int64_t d, uint8_t* Q,
+                           uint8_t* S, hipStream_t st) {
+    StageTimer tm(ST_LUT_PACK, st);
+    const int ppr = (int)(16 * mx_groups(d));
+    const int64_t pieces = rows * ppr;
+    const bool vec = d % 8 == 0 && ((uintptr_t)x & 15u) == 0;
+    const dim3 grid((unsigned)((pieces + 255) / 256)), block(256);
+    uint32_t* q = (uint32_t*)Q;
+    if (x_bf16 && vec) hipLaunchKernelGGL((k_mx_quantize<true, true>), grid, block, 0, st, x, pieces, d, ppr, q, S);
+    else if (x_bf16) hipLaunchKernelGGL((k_mx_quantize<true, false>), grid, block, 0, st, x, pieces, d, ppr, q, S);
+    else if (vec) hipLaunchKernelGGL((k_mx_quantize<false, true>), grid, block, 0, st, x, pieces, d, ppr, q, S);
+    else hipLaunchKernelGGL((k_mx_quantize<false, false>), grid, block, 0, st, x, pieces, d, ppr, q, S);
+    GQ_LAUNCH_CHECK();
+    return hipSuccess;
+}
+
+hipError_t mx_dequantize_run(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t d, void* y,
+                             bool y_bf16, hipStream_t st) {
+    StageTimer tm(ST_LUT_PACK, st);
+    const int ppr = (int)(16 * mx_groups(d));
+    const int64_t pieces = rows * ppr;
+    const bool vec = d % 8 == 0 && ((uintptr_t)y & 15u) == 0;
+    const dim3 grid((unsigned)((pieces + 255) / 256)), block(256);
+    const uint32_t* q = (const uint32_t*)Q;
+    if (y_bf16 && vec) hipLaunchKernelGGL((k_mx_dequantize<true, true>), grid, block, 0, st, q, S, pieces, d, ppr, y);
+    else if (y_bf16) hipLaunchKernelGGL((k_mx_dequantize<true, false>), grid, block, 0, st, q, S, pieces, d, ppr, y);
+    else if (vec) hipLaunchKernelGGL((k_mx_dequantize<false, true>), grid, block, 0, st, q, S, pieces, d, ppr, y);
+    else hipLaunchKernelGGL((k_mx_dequantize<false, false>), grid, block, 0, st, q, S, pieces, d, ppr, y);
+    GQ_LAUNCH_CHECK();
+    return hipSuccess;
+}
+
+}  // namespace gq

@@ -420,8 +420,8 @@ gq_status mxfp4_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, int
  * claim, or that bad offsets leave over, hold unspecified values.
  *
  * Precision.  A weight's value is exact in bfloat16, products with bfloat16 x are exact and
- * sums are float32.  float32 x is split into three bfloat16 planes whose sum is x, so its
- * products are exact too.  mxfp4_gemm_mx: the matrix cores' scaled product, exact products
+ * sums are float32.  float32 x is split into three bfloat16 planes whose sum is x (for |x|
+ * below 2^-110 x to within 2^-133, the smallest bfloat16), so its products are exact too.  mxfp4_gemm_mx: the matrix cores' scaled product, exact products
  * and float32 sums.  y is rounded once to y_dt.  A NaN or infinity stays within its row of
  * x (and, from a NaN block, its row of W).  The order of the sums depends on the sizes
  * alone, so equal calls give equal bits.

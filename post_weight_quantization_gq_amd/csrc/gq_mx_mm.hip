@@ -3,61 +3,607 @@
 #include "gq_internal.h"
 #include "gq_mx.h"
 
+#include <type_traits>
+
 namespace gq {
+
+typedef __attribute__((address_space(3))) void* mx_lds_t;
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------------------------
+// Staged activations.  Float32 rows, and bfloat16 rows of no multiple of 8, are first written
+// as rows of bfloat16 pieces of 64 values, P pieces (planes) for each 64 values of the row,
+// zero past its end: value i of plane p is element (i / 64 * P + p) * 64 + i % 64.  The
+// three planes of a float32 are its bits cut after 8, 16 and 24 significant ones (each
+// difference is exact), so their sum is the value; a NaN or infinity is in the first alone.
+// ---------------------------------------------------------------------------
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_mx_stage(const void* __restrict__ x, int64_t n, int64_t k,
+                                                 int64_t pieces, uint16_t* __restrict__ out) {
+    constexpr int P = BF16 ? 1 : 3;
+    const int64_t total = n * pieces * 64;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
+        const int64_t piece = t >> 6, r = piece / pieces;
+        const int64_t i = (piece - r * pieces) * 64 + (t & 63);
+        uint16_t* o = out + piece * P * 64 + (t & 63);
+        if constexpr (BF16) {
+            o[0] = i < k ? ((const uint16_t*)x)[r * k + i] : (uint16_t)0;
+        } else {
+            const float v = i < k ? ((const float*)x)[r * k + i] : 0.f;
+            const uint32_t b = __float_as_uint(v);
+            uint32_t h = b & 0xffff0000u;
+            float rest = 0.f;
+            if ((b & 0x7f800000u) != 0x7f800000u) rest = v - __uint_as_float(h);
+            else if (b & 0x007fffffu) h |= 0x00400000u;            // a NaN stays one
+            const uint32_t m = __float_as_uint(rest) & 0xffff0000u;
+            const float low = rest - __uint_as_float(m);
+            o[0] = (uint16_t)(h >> 16);
+            o[64] = (uint16_t)(m >> 16);
+            o[128] = (uint16_t)(__float_as_uint(low) >> 16);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The tiled product.
+// ---------------------------------------------------------------------------
+struct MxTile {
+    const uint8_t* A;             // rows of the activations (bfloat16, or codes)
+    int64_t a_row;                // bytes from one row to the next
+    int64_t a_bytes;              // bytes of a row that the product reads (zeros follow)
+    const uint8_t* AS;            // scales of the codes
+    const uint8_t *Q, *S;
+    int64_t qb, sb;               // bytes of a weight row's codes and scales
+    const int64_t* offsets;
+    int experts;
+    int64_t n, m, d_out;          // rows, output columns, rows of one weight
+    int stages;                   // stages of the whole contraction
+    int unit;                     // a split's range is a multiple of this many stages
+    void* y;
+    int y_bf16, y_vec;            // y_vec: runs of 4 (MODE 2: 8) outputs may be stored whole
+    float* part;                  // partial sums [split][n][m], or null
+};
+
+template <int N>
+__device__ __forceinline__ void mx_wait_vmcnt() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+}
+
+__device__ __forceinline__ void mx_dma(__amdgpu_buffer_rsrc_t r, u32x4* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mx_lds_t)dst, 16, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const uint8_t* p, int64_t bytes) {
+    const uint32_t nb = bytes < 0 ? 0u : (bytes > 0xffffffffll ? 0xffffffffu : (uint32_t)bytes);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)nb, 0x00020000);
+}
 
 // Rows of expert e, clamped to [0, n].
 __device__ __forceinline__ void mx_expert_rows(const int64_t* offsets, int e, int64_t n, int64_t& lo,
                                                int64_t& hi) {
-    lo = 0;
-    hi = n;
-    if (!offsets) return;
     lo = offsets[e];
     hi = offsets[e + 1];
     lo = lo < 0 ? 0 : (lo > n ? n : lo);
     hi = hi < 0 ? 0 : (hi > n ? n : hi);
 }
 
-// One output a thread: the definition as it stands.
-template <int OP>
-__global__ __launch_bounds__(256) void k_mx_plain(MxCall c) {
-    const int64_t m = OP == MX_GEMM_DX ? c.d_in : c.d_out, k = OP == MX_GEMM_DX ? c.d_out : c.d_in;
-    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int e = blockIdx.z;
-    int64_t lo, hi;
-    mx_expert_rows(c.offsets, e, c.n, lo, hi);
-    const int64_t t = lo + blockIdx.y;
-    if (j >= m || t >= hi) return;
-    const int64_t qb = mx_row_bytes(c.d_in), sb = mx_row_scales(c.d_in);
-    const uint8_t* Q = c.Q + (int64_t)e * c.d_out * qb;
-    const uint8_t* S = c.S + (int64_t)e * c.d_out * sb;
-    auto get = [](const uint8_t* q, const uint8_t* s, int64_t row, int64_t i, int64_t qb, int64_t sb) {
-        const uint32_t b = q[row * qb + (i >> 1)], sc = s[row * sb + (i >> 5)];
-        const float v = mx_value((i & 1) ? b >> 4 : b & 15u);
-        return sc == 255u ? __uint_as_float(0x7fc00000u) : ldexpf(v, (int)sc - 127);
+struct MxPlace {
+    int e;
+    int64_t t0, rows;             // first row of the tile, rows of it
+    int col;                      // column tile
+    bool ok;
+};
+
+// Block hw -> its tile.  XCD x (= hw % 8) takes a contiguous eighth of the tiles, which run
+// row-tile fastest within groups of 8 row tiles, so the blocks that one L2 serves at a time
+// share both operands.  With several experts the row tiles are counted from the offsets,
+// by each wave for itself.
+__device__ __forceinline__ MxPlace mx_place(const MxTile& p, int bm, int ncol) {
+    const int lane = threadIdx.x & 63;
+    auto tiles = [&](int e) -> int {
+        if (e >= p.experts) return 0;
+        int64_t lo, hi;
+        mx_expert_rows(p.offsets, e, p.n, lo, hi);
+        return hi > lo ? (int)((hi - lo + bm - 1) / bm) : 0;
     };
-    float acc = 0.f;
-    for (int64_t i = 0; i < k; ++i) {
-        float a;
-        if (OP == MX_GEMM_MX) a = get((const uint8_t*)c.a, c.as, t, i, qb, sb);
-        else a = c.a_bf16 ? load_elem<true>(c.a, t * k + i) : load_elem<false>(c.a, t * k + i);
-        acc = fmaf(a, OP == MX_GEMM_DX ? get(Q, S, i, j, qb, sb) : get(Q, S, j, i, qb, sb), acc);
+    MxPlace r;
+    r.ok = false;
+    int64_t nrow;
+    if (p.offsets) {
+        int c = 0;
+        for (int b = 0; b < p.experts; b += 64) c += tiles(b + lane);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) c += __shfl_xor(c, o, 64);
+        nrow = __builtin_amdgcn_readfirstlane(c);
+    } else {
+        nrow = (p.n + bm - 1) / bm;
     }
-    if (c.y_bf16) ((uint16_t*)c.y)[t * m + j] = (uint16_t)f32_to_bf16_bits(acc);
-    else ((float*)c.y)[t * m + j] = acc;
+    const int64_t total = nrow * ncol, eighth = (total + 7) / 8;
+    const int64_t in = blockIdx.x >> 3, lin = (int64_t)(blockIdx.x & 7) * eighth + in;
+    if (in >= eighth || lin >= total) return r;
+    constexpr int H = 8;
+    const int64_t g = lin / (H * ncol), rest = lin - g * (H * ncol);
+    const int64_t left = nrow - g * H;
+    const int64_t h = left < H ? left : H;
+    int64_t row = g * H + rest % h;
+    r.col = (int)(rest / h);
+    if (p.offsets) {
+        int first = 0;
+        for (int b = 0; b < p.experts; b += 64) {
+            const int c = tiles(b + lane);
+            int s = c;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(s, o, 64);
+                if (lane >= o) s += v;
+            }
+            const unsigned long long hit = __ballot(first + s > (int)row);
+            if (hit) {
+                const int l = __ffsll((unsigned long long)hit) - 1;
+                r.e = __builtin_amdgcn_readfirstlane(b + l);
+                const int before = __builtin_amdgcn_readfirstlane(first + __shfl(s - c, l, 64));
+                int64_t lo, hi;
+                mx_expert_rows(p.offsets, r.e, p.n, lo, hi);
+                r.t0 = lo + (row - before) * bm;
+                r.rows = hi - r.t0 < bm ? hi - r.t0 : bm;
+                r.ok = row >= before && r.rows > 0;     // (offsets out of order could count wrongly)
+                return r;
+            }
+            first += __builtin_amdgcn_readfirstlane(__shfl(s, 63, 64));
+        }
+        return r;
+    }
+    r.e = 0;
+    r.t0 = row * bm;
+    r.rows = p.n - r.t0 < bm ? p.n - r.t0 : bm;
+    r.ok = true;
+    return r;
 }
 
-size_t mx_gemm_workspace(MxOp, bool, int64_t, int64_t, int64_t, int) { return 0; }
-
-hipError_t mx_gemm_run(const MxCall& c, void*, hipStream_t st) {
-    StageTimer tm(ST_LUT_GEMV, st);
-    const int64_t m = c.op == MX_GEMM_DX ? c.d_in : c.d_out;
-    const dim3 grid((unsigned)((m + 255) / 256), (unsigned)c.n, (unsigned)c.experts);
-    switch (c.op) {
-        case MX_GEMM: hipLaunchKernelGGL(k_mx_plain<MX_GEMM>, grid, dim3(256), 0, st, c); break;
-        case MX_GEMM_MX: hipLaunchKernelGGL(k_mx_plain<MX_GEMM_MX>, grid, dim3(256), 0, st, c); break;
-        default: hipLaunchKernelGGL(k_mx_plain<MX_GEMM_DX>, grid, dim3(256), 0, st, c); break;
+// N consecutive outputs from column j of a row of m (at: their index)
+template <int N>
+__device__ __forceinline__ void mx_store(const MxTile& p, float* part, int64_t at, int64_t j,
+                                         const float (&v)[N]) {
+    const bool whole = j + N <= p.m;
+    if (part || !p.y_bf16) {
+        float* o = (part ? part : (float*)p.y) + at;
+        if (whole && p.y_vec) {
+#pragma unroll
+            for (int k = 0; k < N; k += 4) *(f32x4*)(o + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (j + k < p.m) o[k] = v[k];
+        }
+    } else {
+        uint16_t* o = (uint16_t*)p.y + at;
+        if (whole && p.y_vec) {
+            if constexpr (N == 4)
+                *(u32x2*)o = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            else
+                *(u32x4*)o = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (j + k < p.m) o[k] = (uint16_t)f32_to_bf16_bits(v[k]);
+        }
     }
+}
+
+// Geometry of a stage in 16-byte LDS slots.
+template <int MODE, int BM, int BN>
+struct MxGeo {
+    static constexpr int RING = (MODE != MX_GEMM_MX && BM == 256) ? 3 : 4;
+    static constexpr int XSPR = MODE == MX_GEMM_MX ? 4 : 8;        // slots a row of activations
+    static constexpr int WROWS = MODE == MX_GEMM_DX ? 64 : BN;
+    static constexpr int WSPR = MODE == MX_GEMM ? 2 : (MODE == MX_GEMM_MX ? 4 : BN / 32);
+    static constexpr int X = BM * XSPR, W = WROWS * WSPR;
+    static constexpr int SRING = MODE == MX_GEMM_DX ? 64 : 0;      // scales that travel in the ring
+    static constexpr int STAGE = X + W + SRING;
+    // stages that one 16-byte piece of a row's scales serves, and its three buffers
+    static constexpr int SPAN = MODE == MX_GEMM ? 8 : 4;
+    static constexpr int SROWS = MODE == MX_GEMM_DX ? 0 : (MODE == MX_GEMM ? BN : BN + BM);
+    static constexpr size_t BYTES = (size_t)(RING * STAGE + 3 * SROWS) * 16;
+};
+
+template <int MODE, int P, int BM, int BN, int WM>
+__global__ __launch_bounds__(256) void k_mx_tile(MxTile p) {
+    typedef MxGeo<MODE, BM, BN> G;
+    constexpr int WN = 4 / WM, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+    constexpr int R = G::RING, SPAN = G::SPAN;
+    static_assert(MODE != MX_GEMM_DX || TN == 128, "a wave of the gradient takes 128 columns");
+    extern __shared__ u32x4 mx_lds[];
+    u32x4* const sc_lds = mx_lds + R * G::STAGE;
+
+    const MxPlace at = mx_place(p, BM, (int)((p.m + BN - 1) / BN));
+    if (!at.ok) return;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int64_t j0 = (int64_t)at.col * BN;
+
+    // this split's stages
+    int s_lo = 0, s_hi = p.stages;
+    if (gridDim.y > 1) {
+        const int units = (p.stages + p.unit - 1) / p.unit;
+        const int per = (units + (int)gridDim.y - 1) / (int)gridDim.y;
+        s_lo = (int)blockIdx.y * per * p.unit;
+        s_hi = s_lo + per * p.unit;
+        s_lo = s_lo < p.stages ? s_lo : p.stages;
+        s_hi = s_hi < p.stages ? s_hi : p.stages;
+    }
+
+    // ---- sources
+    const __amdgpu_buffer_rsrc_t xr = mx_rsrc(p.A + at.t0 * p.a_row, at.rows * p.a_row);
+    const uint8_t* const Qe = p.Q + (int64_t)at.e * p.d_out * p.qb;
+    const uint8_t* const Se = p.S + (int64_t)at.e * p.d_out * p.sb;
+    const int64_t wrows = p.m - j0 < BN ? p.m - j0 : BN;
+    const __amdgpu_buffer_rsrc_t wr = mx_rsrc(Qe + j0 * p.qb, wrows * p.qb);
+    const __amdgpu_buffer_rsrc_t sr = mx_rsrc(Se + j0 * p.sb, wrows * p.sb);
+    const __amdgpu_buffer_rsrc_t xsr =
+        MODE == MX_GEMM_MX ? mx_rsrc(p.AS + at.t0 * p.sb, at.rows * p.sb) : sr;
+
+    constexpr int XPW = G::X / 4, WPW = G::W / 4;          // slots a wave copies
+    constexpr int XI = (XPW + 63) / 64, WI = (WPW + 63) / 64;
+    constexpr int LOADS = XI + WI + (MODE == MX_GEMM_MX ? 2 : 1);
+    uint32_t xv[XI], xc[XI], wv[WI];
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+        const int slot = wave * XPW + i * 64 + lane, row = slot / G::XSPR, c = slot % G::XSPR;
+        const int chunk = MODE == MX_GEMM_MX ? c ^ ((row >> 2) & 3) : c ^ ((row >> 1) & 7);
+        xc[i] = 16u * chunk;
+        xv[i] = (uint32_t)(row * p.a_row) + 16u * chunk;
+    }
+#pragma unroll
+    for (int i = 0; i < WI; ++i) {
+        const int slot = wave * WPW + i * 64 + lane;
+        int row = slot / G::WSPR, c = slot % G::WSPR;
+        if constexpr (MODE == MX_GEMM) c ^= (row >> 3) & 1;
+        if constexpr (MODE == MX_GEMM_MX) c ^= (row >> 2) & 3;
+        if constexpr (MODE == MX_GEMM_DX && BN == 256) {
+            row ^= (row >> 5) & 1;
+            c ^= 4 * ((row >> 4) & 1);
+        }
+        if constexpr (MODE == MX_GEMM_DX && BN == 128) row ^= (row >> 4) & 3;
+        wv[i] = (uint32_t)(row * p.qb) + 16u * c;
+    }
+
+    auto issue = [&](int s) {
+        u32x4* base = mx_lds + (s % R) * G::STAGE;
+        const uint32_t xo = (uint32_t)s * (16u * G::XSPR);
+        const bool tail = (int64_t)xo + 16 * G::XSPR > p.a_bytes;
+#pragma unroll
+        for (int i = 0; i < XI; ++i) {
+            uint32_t v = xv[i];
+            if (tail && (int64_t)xo + xc[i] >= p.a_bytes) v = 0xC0000000u;     // reads as zeros
+            if (XPW % 64 == 0 || lane < XPW % 64) mx_dma(xr, base + wave * XPW + i * 64, v, xo);
+        }
+        u32x4* wb = base + G::X;
+        if constexpr (MODE == MX_GEMM_DX) {
+            const int ks = s / P;
+            const int64_t o0 = (int64_t)ks * 64, left = p.d_out - o0 < 64 ? p.d_out - o0 : 64;
+            const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + o0 * p.qb + j0 / 2, left * p.qb - j0 / 2);
+            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + o0 * p.sb + j0 / 32, left * p.sb - j0 / 32);
+#pragma unroll
+            for (int i = 0; i < WI; ++i) mx_dma(q, wb + wave * WPW + i * 64, wv[i], 0);
+            if (lane < 16) mx_dma(z, wb + G::W + wave * 16, (uint32_t)((wave * 16 + lane) * p.sb), 0);
+        } else {
+            const int ks = s / P;
+            const uint32_t wo = (uint32_t)ks * (16u * G::WSPR);
+#pragma unroll
+            for (int i = 0; i < WI; ++i) mx_dma(wr, wb + wave * WPW + i * 64, wv[i], wo);
+            // a share of the next span's scales
+            const int span = ks / SPAN + 1, part = ks % SPAN;
+            u32x4* sb = sc_lds + (span % 3) * G::SROWS;
+            constexpr int WR = BN / SPAN / 4;
+            const int row = part * (BN / SPAN) + wave * WR;
+            if (lane < WR) mx_dma(sr, sb + row, (uint32_t)((row + lane) * p.sb) + 16u * span, 0);
+            if constexpr (MODE == MX_GEMM_MX) {
+                constexpr int XR = BM / SPAN / 4;
+                const int xrow = part * (BM / SPAN) + wave * XR;
+                if (lane < XR) mx_dma(xsr, sb + BN + xrow, (uint32_t)((xrow + lane) * p.sb) + 16u * span, 0);
+            }
+        }
+    };
+
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int q = 0; q < FM; ++q) acc[f][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if constexpr (MODE != MX_GEMM_DX) {
+        // the first span's scales whole
+        const int span = s_lo / P / SPAN;
+        u32x4* sb = sc_lds + (span % 3) * G::SROWS;
+        constexpr int WR = BN / 4;
+        if (lane < WR) mx_dma(sr, sb + wave * WR, (uint32_t)((wave * WR + lane) * p.sb) + 16u * span, 0);
+        if constexpr (MODE == MX_GEMM_MX) {
+            constexpr int XR = BM / 4;
+            if (lane < XR) mx_dma(xsr, sb + BN + wave * XR, (uint32_t)((wave * XR + lane) * p.sb) + 16u * span, 0);
+        }
+    }
+    for (int s = s_lo; s < s_lo + R - 1 && s < s_hi; ++s) issue(s);
+
+    const uint8_t* const lds = (const uint8_t*)mx_lds;
+    for (int s = s_lo; s < s_hi; ++s) {
+        // all but the loads of the R - 2 stages after this one have landed
+        if (s + R - 2 < s_hi) mx_wait_vmcnt<LOADS * (R - 2)>();
+        else mx_wait_vmcnt<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + R - 1 < s_hi) issue(s + R - 1);
+
+        const int xb = (s % R) * G::STAGE * 16, wb = xb + G::X * 16;
+        const int ks = s / P;
+        if constexpr (MODE == MX_GEMM) {
+            u32x2 wq[FN];
+            float ws[FN];
+            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 2 * (ks % SPAN) + (g >> 1);
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                const int row = wn * TN + 16 * f + r;
+                wq[f] = *(const u32x2*)(lds + wb + row * 32 + 16 * ((g >> 1) ^ ((r >> 3) & 1)) + 8 * (g & 1));
+                ws[f] = mx_scale(lds[sb + row * 16]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                u32x4 x[FM];
+#pragma unroll
+                for (int q = 0; q < FM; ++q)
+                    x[q] = *(const u32x4*)(lds + xb + (wm * TM + 16 * q + r) * 128 + 16 * ((2 * g + j) ^ ((r >> 1) & 7)));
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    const uint32_t w = wq[f][j];
+                    const u32x4 a{mx_bf16<0>(w, ws[f]), mx_bf16<1>(w, ws[f]), mx_bf16<2>(w, ws[f]),
+                                  mx_bf16<3>(w, ws[f])};
+#pragma unroll
+                    for (int q = 0; q < FM; ++q)
+                        acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(x[q]),
+                                                                           acc[f][q], 0, 0, 0);
+                }
+            }
+        } else if constexpr (MODE == MX_GEMM_MX) {
+            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 4 * (ks % SPAN) + g;
+            u32x4 x[FM];
+            int xs[FM];
+#pragma unroll
+            for (int q = 0; q < FM; ++q) {
+                const int row = wm * TM + 16 * q + r;
+                x[q] = *(const u32x4*)(lds + xb + row * 64 + 16 * (g ^ ((r >> 2) & 3)));
+                xs[q] = lds[sb + (BN + row) * 16];
+            }
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                const int row = wn * TN + 16 * f + r;
+                const u32x4 w = *(const u32x4*)(lds + wb + row * 64 + 16 * (g ^ ((r >> 2) & 3)));
+                const int ws = lds[sb + row * 16];
+                const i32x8 a{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+#pragma unroll
+                for (int q = 0; q < FM; ++q) {
+                    const i32x8 b{(int)x[q][0], (int)x[q][1], (int)x[q][2], (int)x[q][3], 0, 0, 0, 0};
+                    acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[f][q], 4, 4, 0, ws, 0, xs[q]);
+                }
+            }
+        } else {
+            const int sb = wb + G::W * 16 + wn * 4 + (r >> 2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                u32x4 x[FM];
+#pragma unroll
+                for (int q = 0; q < FM; ++q)
+                    x[q] = *(const u32x4*)(lds + xb + (wm * TM + 16 * q + r) * 128 + 16 * ((2 * g + j) ^ ((r >> 1) & 7)));
+                uint32_t w[8];
+                float ws[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int o = 16 * g + 8 * j + i;
+                    if constexpr (BN == 256)
+                        w[i] = *(const uint32_t*)(lds + wb + (o ^ (g >> 1)) * 128 + 16 * ((wn * 4 + (r >> 2)) ^ (4 * (g & 1))) + 4 * (r & 3));
+                    else
+                        w[i] = *(const uint32_t*)(lds + wb + (o ^ g) * 64 + 4 * r);
+                    ws[i] = mx_scale(lds[sb + o * 16]);
+                }
+                // byte b of the words: columns 8 r + 2 b and 8 r + 2 b + 1 of the wave's 128
+                auto two = [&](auto byte) {
+                    constexpr int b = decltype(byte)::value;
+                    u32x4 lo, hi;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t u = mx_bf16<b>(w[2 * i], ws[2 * i]), v = mx_bf16<b>(w[2 * i + 1], ws[2 * i + 1]);
+                        lo[i] = __builtin_amdgcn_perm(v, u, 0x05040100u);
+                        hi[i] = __builtin_amdgcn_perm(v, u, 0x07060302u);
+                    }
+#pragma unroll
+                    for (int q = 0; q < FM; ++q) {
+                        acc[2 * b][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(lo), as_bf16x8(x[q]), acc[2 * b][q], 0, 0, 0);
+                        acc[2 * b + 1][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(hi), as_bf16x8(x[q]), acc[2 * b + 1][q], 0, 0, 0);
+                    }
+                };
+                two(std::integral_constant<int, 0>{});
+                two(std::integral_constant<int, 1>{});
+                two(std::integral_constant<int, 2>{});
+                two(std::integral_constant<int, 3>{});
+            }
+        }
+    }
+    mx_wait_vmcnt<0>();          // no load into this block's LDS may land after it ends
+
+    // ---- store: lane (r, g) holds row 16 q + r and columns 4 g + v of each 16 (MODE 2: 8 (4 g + v) + f)
+    float* part = p.part ? p.part + (int64_t)blockIdx.y * p.n * p.m : nullptr;
+#pragma unroll
+    for (int q = 0; q < FM; ++q) {
+        const int row = wm * TM + 16 * q + r;
+        if (row >= at.rows) continue;
+        const int64_t base = (at.t0 + row) * p.m;
+        if constexpr (MODE == MX_GEMM_DX) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int64_t j = j0 + wn * TN + 8 * (4 * g + v);
+                float o[8];
+#pragma unroll
+                for (int f = 0; f < 8; ++f) o[f] = acc[f][q][v];
+                if (j < p.m) mx_store<8>(p, part, base + j, j, o);
+            }
+        } else {
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                const int64_t j = j0 + wn * TN + 16 * f + 4 * g;
+                const float o[4] = {acc[f][q][0], acc[f][q][1], acc[f][q][2], acc[f][q][3]};
+                if (j < p.m) mx_store<4>(p, part, base + j, j, o);
+            }
+        }
+    }
+}
+
+// y = the sum of a split contraction's parts, in their order; rows that belong to an expert
+// (all of them without offsets).
+__global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part, int split, int64_t n,
+                                                int64_t m, const int64_t* __restrict__ offsets,
+                                                int experts, void* __restrict__ y, int y_bf16) {
+    int64_t lo = 0, hi = n;
+    if (offsets) {
+        int64_t a, b;
+        mx_expert_rows(offsets, 0, n, lo, a);
+        mx_expert_rows(offsets, experts - 1, n, b, hi);
+    }
+    const int64_t first = lo * m, end = hi * m, all = n * m;
+    for (int64_t t = first + (int64_t)blockIdx.x * 256 + threadIdx.x; t < end; t += (int64_t)gridDim.x * 256) {
+        float s = part[t];
+        for (int k = 1; k < split; ++k) s += part[k * all + t];
+        if (y_bf16) ((uint16_t*)y)[t] = (uint16_t)f32_to_bf16_bits(s);
+        else ((float*)y)[t] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+static size_t mx_al256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// What a call does, from its sizes and types alone.
+struct MxPlan {
+    bool staged;                  // activations are copied into planes first
+    int planes;
+    int bm, bn, split;
+    int stages, unit;
+    size_t stage_bytes, part_bytes;
+};
+
+static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts) {
+    MxPlan P;
+    const int64_t k = op == MX_GEMM_DX ? d_out : d_in, m = op == MX_GEMM_DX ? d_in : d_out;
+    P.planes = a_bf16 ? 1 : 3;
+    P.staged = op != MX_GEMM_MX && (!a_bf16 || k % 8 != 0);
+    const int64_t k64 = op == MX_GEMM_DX ? (k + 63) / 64 : 2 * mx_groups(k);
+    P.stages = (int)(op == MX_GEMM_MX ? mx_groups(k) : k64 * P.planes);
+    P.unit = op == MX_GEMM ? 8 * P.planes : (op == MX_GEMM_MX ? 4 : P.planes);
+    P.stage_bytes = P.staged ? mx_al256((size_t)n * k64 * 64 * P.planes * 2) : 0;
+    const int64_t per = (n + experts - 1) / experts;
+    P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 ? 64 : 32));
+    P.bn = P.bm == 256 ? 256 : 128;
+    if (op == MX_GEMM_DX && P.bm == 32) P.bm = 64;
+    P.split = 1;
+    const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;
+    const int64_t tiles = rows * ((m + P.bn - 1) / P.bn);
+    const int units = (P.stages + P.unit - 1) / P.unit;
+    if (tiles < 256) {
+        int64_t s = 512 / tiles;
+        s = s < units ? s : units;
+        P.split = (int)(s < 1 ? 1 : (s > 16 ? 16 : s));
+    }
+    P.part_bytes = P.split > 1 ? mx_al256((size_t)P.split * n * m * 4) : 0;
+    return P;
+}
+
+size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts) {
+    const MxPlan P = mx_plan(op, a_bf16, n, d_in, d_out, experts);
+    return P.stage_bytes + P.part_bytes;
+}
+
+template <int MODE, int P, int BM, int BN, int WM>
+static hipError_t mx_launch(const MxTile& t, int split, hipStream_t st) {
+    const void* k = (const void*)k_mx_tile<MODE, P, BM, BN, WM>;
+    const size_t lds = MxGeo<MODE, BM, BN>::BYTES;
+    hipError_t e = ensure_dynamic_lds(k, lds);
+    if (e != hipSuccess) return e;
+    const int64_t rows = (t.n + BM - 1) / BM + (t.offsets ? t.experts : 0);
+    const int64_t tiles = rows * ((t.m + BN - 1) / BN);
+    const int64_t grid = (tiles + 7) / 8 * 8;
+    if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_mx_tile<MODE, P, BM, BN, WM>), dim3((unsigned)grid, (unsigned)split), dim3(256), lds, st, t);
     GQ_LAUNCH_CHECK();
+    return hipSuccess;
+}
+
+template <int MODE, int P>
+static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t st) {
+    if constexpr (MODE == MX_GEMM_DX) {
+        switch (pl.bm) {
+            case 256: return mx_launch<MODE, P, 256, 256, 2>(t, pl.split, st);
+            case 128: return mx_launch<MODE, P, 128, 128, 4>(t, pl.split, st);
+            default: return mx_launch<MODE, P, 64, 128, 4>(t, pl.split, st);
+        }
+    } else {
+        switch (pl.bm) {
+            case 256: return mx_launch<MODE, P, 256, 256, 2>(t, pl.split, st);
+            case 128: return mx_launch<MODE, P, 128, 128, 2>(t, pl.split, st);
+            case 64: return mx_launch<MODE, P, 64, 128, 1>(t, pl.split, st);
+            default: return mx_launch<MODE, P, 32, 128, 1>(t, pl.split, st);
+        }
+    }
+}
+
+hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
+    StageTimer tm(ST_LUT_GEMV, st);
+    const MxPlan pl = mx_plan(c.op, c.a_bf16, c.n, c.d_in, c.d_out, c.experts);
+    const int64_t k = c.op == MX_GEMM_DX ? c.d_out : c.d_in, m = c.op == MX_GEMM_DX ? c.d_in : c.d_out;
+    MxTile t{};
+    t.A = (const uint8_t*)c.a;
+    t.AS = c.as;
+    t.a_row = t.a_bytes = c.op == MX_GEMM_MX ? mx_row_bytes(k) : 2 * k;
+    if (pl.staged) {
+        const int64_t pieces = pl.stages / pl.planes;
+        t.A = (const uint8_t*)ws;
+        t.a_row = t.a_bytes = pieces * pl.planes * 128;
+        const int64_t blocks = (c.n * pieces * 64 + 255) / 256;
+        const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
+        if (c.a_bf16) hipLaunchKernelGGL(k_mx_stage<true>, grid, dim3(256), 0, st, c.a, c.n, k, pieces, (uint16_t*)ws);
+        else hipLaunchKernelGGL(k_mx_stage<false>, grid, dim3(256), 0, st, c.a, c.n, k, pieces, (uint16_t*)ws);
+        GQ_LAUNCH_CHECK();
+    }
+    t.Q = c.Q;
+    t.S = c.S;
+    t.qb = mx_row_bytes(c.d_in);
+    t.sb = mx_row_scales(c.d_in);
+    t.offsets = c.offsets;
+    t.experts = c.experts;
+    t.n = c.n;
+    t.m = m;
+    t.d_out = c.d_out;
+    t.stages = pl.stages;
+    t.unit = pl.unit;
+    t.y = c.y;
+    t.y_bf16 = c.y_bf16;
+    const int run = c.op == MX_GEMM_DX ? 8 : 4;
+    t.part = pl.split > 1 ? (float*)((char*)ws + pl.stage_bytes) : nullptr;
+    // a run's vector stores: whole runs in every row, and an aligned base (float32 runs go by 4)
+    t.y_vec = m % run == 0 && (t.part || ((uintptr_t)c.y & (c.y_bf16 ? 2u * run - 1u : 15u)) == 0);
+    hipError_t e;
+    switch (c.op) {
+        case MX_GEMM: e = pl.planes == 1 ? mx_launch_size<MX_GEMM, 1>(t, pl, st) : mx_launch_size<MX_GEMM, 3>(t, pl, st); break;
+        case MX_GEMM_MX: e = mx_launch_size<MX_GEMM_MX, 1>(t, pl, st); break;
+        default: e = pl.planes == 1 ? mx_launch_size<MX_GEMM_DX, 1>(t, pl, st) : mx_launch_size<MX_GEMM_DX, 3>(t, pl, st); break;
+    }
+    if (e != hipSuccess) return e;
+    if (t.part) {
+        const int64_t blocks = (c.n * m + 255) / 256;
+        hipLaunchKernelGGL(k_mx_join, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, t.part, pl.split,
+                           c.n, m, c.offsets, c.experts, c.y, (int)c.y_bf16);
+        GQ_LAUNCH_CHECK();
+    }
     return hipSuccess;
 }
 

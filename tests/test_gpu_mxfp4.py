@@ -43,9 +43,10 @@ def bound(a, W, y_ref, terms, out):
     return b + (2.0 ** -8 * np.abs(y_ref) + 2.0 ** -134 if out == BF else 0.0)
 
 
-def check(y, a, W, terms, out, what=""):
+def check(y, a, W, terms, out, what="", lost=0.0):
+    """lost: how far the path holds each value of a (absolutely), which adds lost sum |w|."""
     ref = a @ W.T
-    err, b = np.abs(f64(y) - ref), bound(a, W, ref, terms, out)
+    err, b = np.abs(f64(y) - ref), bound(a, W, ref, terms, out) + lost * np.abs(W).sum(axis=1)
     print(what, "worst error / bound", float(np.max(err / np.maximum(b, 1e-300))) if err.size else 0.0)
     assert np.all(err <= b)
 
@@ -257,7 +258,10 @@ def test_gemm_extreme_scales(device, n):
         for dtype in (BF, F32):
             x = torch.from_numpy(rng.standard_normal((n, d)) * a).to(dtype)
             y = gq.mxfp4_gemm(x.to(device), u8(Q[0], device), u8(S1, device), out_dtype=F32)
-            check(y, f64(x), W, d * 3, F32, f"s={s} {dtype}")
+            # the third plane of a float32 ends at the smallest bfloat16, 2^-133: x 2^-149-grid
+            # bits below it are cut, so a value is held to within 2^-133 (nothing is cut, and
+            # the term is far below the bound, where |x| >= 2^-110)
+            check(y, f64(x), W, d * 3, F32, f"s={s} {dtype}", lost=2.0 ** -133 if dtype == F32 else 0.0)
 
 
 def test_float32_planes_are_exact(device):

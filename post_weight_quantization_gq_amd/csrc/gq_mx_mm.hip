@@ -207,10 +207,10 @@ struct MxGeo {
     static constexpr size_t BYTES = (size_t)(RING * STAGE + 3 * SROWS) * 16;
 };
 
-template <int MODE, int P, int BM, int BN, int WM>
-__global__ __launch_bounds__(256) void k_mx_tile(MxTile p) {
+template <int MODE, int P, int BM, int BN, int WM, int NW>
+__global__ __launch_bounds__(64 * NW) void k_mx_tile(MxTile p) {
     typedef MxGeo<MODE, BM, BN> G;
-    constexpr int WN = 4 / WM, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+    constexpr int WN = NW / WM, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
     constexpr int R = G::RING, SPAN = G::SPAN;
     static_assert(MODE != MX_GEMM_DX || TN == 128, "a wave of the gradient takes 128 columns");
     extern __shared__ u32x4 mx_lds[];
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxTile p) {
     const __amdgpu_buffer_rsrc_t xsr =
         MODE == MX_GEMM_MX ? mx_rsrc(p.AS + at.t0 * p.sb, at.rows * p.sb) : sr;
 
-    constexpr int XPW = G::X / 4, WPW = G::W / 4;          // slots a wave copies
+    constexpr int XPW = G::X / NW, WPW = G::W / NW;          // slots a wave copies
     constexpr int XI = (XPW + 63) / 64, WI = (WPW + 63) / 64;
     constexpr int LOADS = XI + WI + (MODE == MX_GEMM_MX ? 2 : 1);
     uint32_t xv[XI], xc[XI], wv[WI];
@@ -286,21 +286,24 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxTile p) {
             const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + o0 * p.qb + j0 / 2, left * p.qb - j0 / 2);
             const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + o0 * p.sb + j0 / 32, left * p.sb - j0 / 32);
 #pragma unroll
-            for (int i = 0; i < WI; ++i) mx_dma(q, wb + wave * WPW + i * 64, wv[i], 0);
-            if (lane < 16) mx_dma(z, wb + G::W + wave * 16, (uint32_t)((wave * 16 + lane) * p.sb), 0);
+            for (int i = 0; i < WI; ++i)
+                if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(q, wb + wave * WPW + i * 64, wv[i], 0);
+            constexpr int SR = 64 / NW;
+            if (lane < SR) mx_dma(z, wb + G::W + wave * SR, (uint32_t)((wave * SR + lane) * p.sb), 0);
         } else {
             const int ks = s / P;
             const uint32_t wo = (uint32_t)ks * (16u * G::WSPR);
 #pragma unroll
-            for (int i = 0; i < WI; ++i) mx_dma(wr, wb + wave * WPW + i * 64, wv[i], wo);
+            for (int i = 0; i < WI; ++i)
+                if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(wr, wb + wave * WPW + i * 64, wv[i], wo);
             // a share of the next span's scales
             const int span = ks / SPAN + 1, part = ks % SPAN;
             u32x4* sb = sc_lds + (span % 3) * G::SROWS;
-            constexpr int WR = BN / SPAN / 4;
+            constexpr int WR = BN / SPAN / NW;
             const int row = part * (BN / SPAN) + wave * WR;
             if (lane < WR) mx_dma(sr, sb + row, (uint32_t)((row + lane) * p.sb) + 16u * span, 0);
             if constexpr (MODE == MX_GEMM_MX) {
-                constexpr int XR = BM / SPAN / 4;
+                constexpr int XR = BM / SPAN / NW;
                 const int xrow = part * (BM / SPAN) + wave * XR;
                 if (lane < XR) mx_dma(xsr, sb + BN + xrow, (uint32_t)((xrow + lane) * p.sb) + 16u * span, 0);
             }
@@ -317,10 +320,10 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxTile p) {
         // the first span's scales whole
         const int span = s_lo / P / SPAN;
         u32x4* sb = sc_lds + (span % 3) * G::SROWS;
-        constexpr int WR = BN / 4;
+        constexpr int WR = BN / NW;
         if (lane < WR) mx_dma(sr, sb + wave * WR, (uint32_t)((wave * WR + lane) * p.sb) + 16u * span, 0);
         if constexpr (MODE == MX_GEMM_MX) {
-            constexpr int XR = BM / 4;
+            constexpr int XR = BM / NW;
             if (lane < XR) mx_dma(xsr, sb + BN + wave * XR, (uint32_t)((wave * XR + lane) * p.sb) + 16u * span, 0);
         }
     }
@@ -523,9 +526,9 @@ size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t 
     return P.stage_bytes + P.part_bytes;
 }
 
-template <int MODE, int P, int BM, int BN, int WM>
+template <int MODE, int P, int BM, int BN, int WM, int NW = 4>
 static hipError_t mx_launch(const MxTile& t, int split, hipStream_t st) {
-    const void* k = (const void*)k_mx_tile<MODE, P, BM, BN, WM>;
+    const void* k = (const void*)k_mx_tile<MODE, P, BM, BN, WM, NW>;
     const size_t lds = MxGeo<MODE, BM, BN>::BYTES;
     hipError_t e = ensure_dynamic_lds(k, lds);
     if (e != hipSuccess) return e;
@@ -533,7 +536,7 @@ static hipError_t mx_launch(const MxTile& t, int split, hipStream_t st) {
     const int64_t tiles = rows * ((t.m + BN - 1) / BN);
     const int64_t grid = (tiles + 7) / 8 * 8;
     if (grid > 0x7fffffffll) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_mx_tile<MODE, P, BM, BN, WM>), dim3((unsigned)grid, (unsigned)split), dim3(256), lds, st, t);
+    hipLaunchKernelGGL((k_mx_tile<MODE, P, BM, BN, WM, NW>), dim3((unsigned)grid, (unsigned)split), dim3(64 * NW), lds, st, t);
     GQ_LAUNCH_CHECK();
     return hipSuccess;
 }
@@ -542,13 +545,13 @@ template <int MODE, int P>
 static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t st) {
     if constexpr (MODE == MX_GEMM_DX) {
         switch (pl.bm) {
-            case 256: return mx_launch<MODE, P, 256, 256, 2>(t, pl.split, st);
+            case 256: return mx_launch<MODE, P, 256, 256, 4, 8>(t, pl.split, st);
             case 128: return mx_launch<MODE, P, 128, 128, 4>(t, pl.split, st);
             default: return mx_launch<MODE, P, 64, 128, 4>(t, pl.split, st);
         }
     } else {
         switch (pl.bm) {
-            case 256: return mx_launch<MODE, P, 256, 256, 2>(t, pl.split, st);
+            case 256: return mx_launch<MODE, P, 256, 256, 4, 8>(t, pl.split, st);
             case 128: return mx_launch<MODE, P, 128, 128, 2>(t, pl.split, st);
             case 64: return mx_launch<MODE, P, 64, 128, 1>(t, pl.split, st);
             default: return mx_launch<MODE, P, 32, 128, 1>(t, pl.split, st);

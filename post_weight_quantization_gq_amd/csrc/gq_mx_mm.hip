@@ -207,10 +207,33 @@ struct MxGeo {
     static constexpr size_t BYTES = (size_t)(RING * STAGE + 3 * SROWS) * 16;
 };
 
+// The fragments of half a stage, and an accumulator.
+template <int MODE, int FM, int FN> struct MxHalf;
+template <int FM, int FN> struct MxHalf<MX_GEMM, FM, FN> {
+    typedef f32x16 Acc;
+    static constexpr int T = 32, V = 16, READS = 2 * FM + 2 * FN, PRODUCTS = 2 * FM * FN;
+    u32x4 x[FM][2];
+    u32x2 w[FN];
+    uint32_t ws[FN];
+};
+template <int FM, int FN> struct MxHalf<MX_GEMM_MX, FM, FN> {
+    typedef f32x16 Acc;
+    static constexpr int T = 32, V = 16, READS = 2 * FM + 2 * FN, PRODUCTS = FM * FN;
+    u32x4 x[FM], w[FN];
+    uint32_t xs[FM], ws[FN];
+};
+template <int FM, int FN> struct MxHalf<MX_GEMM_DX, FM, FN> {
+    typedef f32x4 Acc;
+    static constexpr int T = 16, V = 4, READS = FM + 16, PRODUCTS = FM * FN;
+    u32x4 x[FM];
+    uint32_t w[8], ws[8];
+};
+
 template <int MODE, int P, int BM, int BN, int WM, int NW>
-__global__ __launch_bounds__(64 * NW) void k_mx_tile(MxTile p) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM == 256 && NW == 4 ? 1 : 8))) void k_mx_tile(MxTile p) {
     typedef MxGeo<MODE, BM, BN> G;
-    constexpr int WN = NW / WM, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+    constexpr int WN = NW / WM, TM = BM / WM, TN = BN / WN;
+    constexpr int T = MODE == MX_GEMM_DX ? 16 : 32, FM = TM / T, FN = TN / T;
     constexpr int R = G::RING, SPAN = G::SPAN;
     static_assert(MODE != MX_GEMM_DX || TN == 128, "a wave of the gradient takes 128 columns");
     extern __shared__ u32x4 mx_lds[];
@@ -218,7 +241,7 @@ __global__ __launch_bounds__(64 * NW) void k_mx_tile(MxTile p) {
 
     const MxPlace at = mx_place(p, BM, (int)((p.m + BN - 1) / BN));
     if (!at.ok) return;
-    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & (T - 1), g = lane / T;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const int64_t j0 = (int64_t)at.col * BN;
@@ -310,12 +333,6 @@ __global__ __launch_bounds__(64 * NW) void k_mx_tile(MxTile p) {
         }
     };
 
-    f32x4 acc[FN][FM];
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-#pragma unroll
-        for (int q = 0; q < FM; ++q) acc[f][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-
     if constexpr (MODE != MX_GEMM_DX) {
         // the first span's scales whole
         const int span = s_lo / P / SPAN;
@@ -327,118 +344,158 @@ __global__ __launch_bounds__(64 * NW) void k_mx_tile(MxTile p) {
             if (lane < XR) mx_dma(xsr, sb + BN + wave * XR, (uint32_t)((wave * XR + lane) * p.sb) + 16u * span, 0);
         }
     }
-    for (int s = s_lo; s < s_lo + R - 1 && s < s_hi; ++s) issue(s);
 
+    // ---- the contraction, half a stage at a time: while one half's products run, the other
+    // half's fragments are read, so the loop holds two halves and the accumulators
+    typedef MxHalf<MODE, FM, FN> Half;
+    typename Half::Acc acc[FN][FM];
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int q = 0; q < FM; ++q)
+#pragma unroll
+            for (int v = 0; v < Half::V; ++v) acc[f][q][v] = 0.f;
     const uint8_t* const lds = (const uint8_t*)mx_lds;
-    for (int s = s_lo; s < s_hi; ++s) {
-        // all but the loads of the R - 2 stages after this one have landed
-        if (s + R - 2 < s_hi) mx_wait_vmcnt<LOADS * (R - 2)>();
+    auto read = [&](int s, auto half, Half& o) {
+        constexpr int h = decltype(half)::value;
+        const int xb = (s % R) * G::STAGE * 16, wb = xb + G::X * 16, ks = s / P;
+        if constexpr (MODE == MX_GEMM) {
+            // lane (r, g): values 32 g .. of the stage's 64, 16 h .. of them in this half
+            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 2 * (ks % SPAN) + g;
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                const int row = wn * TN + 32 * f + r;
+                o.w[f] = *(const u32x2*)(lds + wb + row * 32 + 16 * (g ^ ((r >> 3) & 1)) + 8 * h);
+                o.ws[f] = lds[sb + row * 16];
+            }
+#pragma unroll
+            for (int q = 0; q < FM; ++q)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    o.x[q][u] = *(const u32x4*)(lds + xb + (wm * TM + 32 * q + r) * 128 + 16 * ((4 * g + 2 * h + u) ^ ((r >> 1) & 7)));
+        } else if constexpr (MODE == MX_GEMM_MX) {
+            // lane (r, g): block 2 h + g of the stage's four
+            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 4 * (ks % SPAN) + 2 * h + g;
+#pragma unroll
+            for (int q = 0; q < FM; ++q) {
+                const int row = wm * TM + 32 * q + r;
+                o.x[q] = *(const u32x4*)(lds + xb + row * 64 + 16 * ((2 * h + g) ^ ((r >> 2) & 3)));
+                o.xs[q] = lds[sb + (BN + row) * 16];
+            }
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                const int row = wn * TN + 32 * f + r;
+                o.w[f] = *(const u32x4*)(lds + wb + row * 64 + 16 * ((2 * h + g) ^ ((r >> 2) & 3)));
+                o.ws[f] = lds[sb + row * 16];
+            }
+        } else {
+            // lane (r, g): rows 16 g + 8 h .. + 7 of the stage's 64, columns 8 r .. of the wave's 128
+            const int sb = wb + G::W * 16 + wn * 4 + (r >> 2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = 16 * g + 8 * h + i;
+                if constexpr (BN == 256)
+                    o.w[i] = *(const uint32_t*)(lds + wb + (row ^ (g >> 1)) * 128 + 16 * ((wn * 4 + (r >> 2)) ^ (4 * (g & 1))) + 4 * (r & 3));
+                else
+                    o.w[i] = *(const uint32_t*)(lds + wb + (row ^ g) * 64 + 4 * r);
+                o.ws[i] = lds[sb + row * 16];
+            }
+#pragma unroll
+            for (int q = 0; q < FM; ++q)
+                o.x[q] = *(const u32x4*)(lds + xb + (wm * TM + 16 * q + r) * 128 + 16 * ((2 * g + h) ^ ((r >> 1) & 7)));
+        }
+    };
+    auto multiply = [&](const Half& o) {
+        if constexpr (MODE == MX_GEMM) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    const uint32_t w = o.w[f][u];
+                    const float sc = mx_scale(o.ws[f]);
+                    const u32x4 a{mx_bf16<0>(w, sc), mx_bf16<1>(w, sc), mx_bf16<2>(w, sc), mx_bf16<3>(w, sc)};
+#pragma unroll
+                    for (int q = 0; q < FM; ++q)
+                        acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(o.x[q][u]), acc[f][q], 0, 0, 0);
+                }
+        } else if constexpr (MODE == MX_GEMM_MX) {
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                const i32x8 a{(int)o.w[f][0], (int)o.w[f][1], (int)o.w[f][2], (int)o.w[f][3], 0, 0, 0, 0};
+#pragma unroll
+                for (int q = 0; q < FM; ++q) {
+                    const i32x8 b{(int)o.x[q][0], (int)o.x[q][1], (int)o.x[q][2], (int)o.x[q][3], 0, 0, 0, 0};
+                    acc[f][q] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[f][q], 4, 4, 0, (int)o.ws[f], 0, (int)o.xs[q]);
+                }
+            }
+        } else {
+            // byte b of the words: columns 8 r + 2 b and 8 r + 2 b + 1
+            auto two = [&](auto byte) {
+                constexpr int b = decltype(byte)::value;
+                u32x4 lo, hi;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u = mx_bf16<b>(o.w[2 * i], mx_scale(o.ws[2 * i]));
+                    const uint32_t v = mx_bf16<b>(o.w[2 * i + 1], mx_scale(o.ws[2 * i + 1]));
+                    lo[i] = __builtin_amdgcn_perm(v, u, 0x05040100u);
+                    hi[i] = __builtin_amdgcn_perm(v, u, 0x07060302u);
+                }
+#pragma unroll
+                for (int q = 0; q < FM; ++q) {
+                    acc[2 * b][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(lo), as_bf16x8(o.x[q]), acc[2 * b][q], 0, 0, 0);
+                    acc[2 * b + 1][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(hi), as_bf16x8(o.x[q]), acc[2 * b + 1][q], 0, 0, 0);
+                }
+            };
+            two(std::integral_constant<int, 0>{});
+            two(std::integral_constant<int, 1>{});
+            two(std::integral_constant<int, 2>{});
+            two(std::integral_constant<int, 3>{});
+        }
+    };
+    auto interleave = [&]() {                    // a few products after each few reads
+        constexpr int RD = Half::READS, MM = Half::PRODUCTS, N = RD < MM ? RD : MM;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, RD / N, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, MM / N, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const std::integral_constant<int, 0> first{};
+    const std::integral_constant<int, 1> second{};
+
+    for (int s = s_lo; s < s_lo + R && s < s_hi; ++s) issue(s);
+    if (s_lo < s_hi) {
+        if (s_lo + R <= s_hi) mx_wait_vmcnt<LOADS * (R - 1)>();
         else mx_wait_vmcnt<0>();
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if (s + R - 1 < s_hi) issue(s + R - 1);
-
-        const int xb = (s % R) * G::STAGE * 16, wb = xb + G::X * 16;
-        const int ks = s / P;
-        if constexpr (MODE == MX_GEMM) {
-            u32x2 wq[FN];
-            float ws[FN];
-            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 2 * (ks % SPAN) + (g >> 1);
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                const int row = wn * TN + 16 * f + r;
-                wq[f] = *(const u32x2*)(lds + wb + row * 32 + 16 * ((g >> 1) ^ ((r >> 3) & 1)) + 8 * (g & 1));
-                ws[f] = mx_scale(lds[sb + row * 16]);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                u32x4 x[FM];
-#pragma unroll
-                for (int q = 0; q < FM; ++q)
-                    x[q] = *(const u32x4*)(lds + xb + (wm * TM + 16 * q + r) * 128 + 16 * ((2 * g + j) ^ ((r >> 1) & 7)));
-#pragma unroll
-                for (int f = 0; f < FN; ++f) {
-                    const uint32_t w = wq[f][j];
-                    const u32x4 a{mx_bf16<0>(w, ws[f]), mx_bf16<1>(w, ws[f]), mx_bf16<2>(w, ws[f]),
-                                  mx_bf16<3>(w, ws[f])};
-#pragma unroll
-                    for (int q = 0; q < FM; ++q)
-                        acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(x[q]),
-                                                                           acc[f][q], 0, 0, 0);
-                }
-            }
-        } else if constexpr (MODE == MX_GEMM_MX) {
-            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 4 * (ks % SPAN) + g;
-            u32x4 x[FM];
-            int xs[FM];
-#pragma unroll
-            for (int q = 0; q < FM; ++q) {
-                const int row = wm * TM + 16 * q + r;
-                x[q] = *(const u32x4*)(lds + xb + row * 64 + 16 * (g ^ ((r >> 2) & 3)));
-                xs[q] = lds[sb + (BN + row) * 16];
-            }
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                const int row = wn * TN + 16 * f + r;
-                const u32x4 w = *(const u32x4*)(lds + wb + row * 64 + 16 * (g ^ ((r >> 2) & 3)));
-                const int ws = lds[sb + row * 16];
-                const i32x8 a{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-#pragma unroll
-                for (int q = 0; q < FM; ++q) {
-                    const i32x8 b{(int)x[q][0], (int)x[q][1], (int)x[q][2], (int)x[q][3], 0, 0, 0, 0};
-                    acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[f][q], 4, 4, 0, ws, 0, xs[q]);
-                }
-            }
-        } else {
-            const int sb = wb + G::W * 16 + wn * 4 + (r >> 2);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                u32x4 x[FM];
-#pragma unroll
-                for (int q = 0; q < FM; ++q)
-                    x[q] = *(const u32x4*)(lds + xb + (wm * TM + 16 * q + r) * 128 + 16 * ((2 * g + j) ^ ((r >> 1) & 7)));
-                uint32_t w[8];
-                float ws[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int o = 16 * g + 8 * j + i;
-                    if constexpr (BN == 256)
-                        w[i] = *(const uint32_t*)(lds + wb + (o ^ (g >> 1)) * 128 + 16 * ((wn * 4 + (r >> 2)) ^ (4 * (g & 1))) + 4 * (r & 3));
-                    else
-                        w[i] = *(const uint32_t*)(lds + wb + (o ^ g) * 64 + 4 * r);
-                    ws[i] = mx_scale(lds[sb + o * 16]);
-                }
-                // byte b of the words: columns 8 r + 2 b and 8 r + 2 b + 1 of the wave's 128
-                auto two = [&](auto byte) {
-                    constexpr int b = decltype(byte)::value;
-                    u32x4 lo, hi;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t u = mx_bf16<b>(w[2 * i], ws[2 * i]), v = mx_bf16<b>(w[2 * i + 1], ws[2 * i + 1]);
-                        lo[i] = __builtin_amdgcn_perm(v, u, 0x05040100u);
-                        hi[i] = __builtin_amdgcn_perm(v, u, 0x07060302u);
-                    }
-#pragma unroll
-                    for (int q = 0; q < FM; ++q) {
-                        acc[2 * b][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(lo), as_bf16x8(x[q]), acc[2 * b][q], 0, 0, 0);
-                        acc[2 * b + 1][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(hi), as_bf16x8(x[q]), acc[2 * b + 1][q], 0, 0, 0);
-                    }
-                };
-                two(std::integral_constant<int, 0>{});
-                two(std::integral_constant<int, 1>{});
-                two(std::integral_constant<int, 2>{});
-                two(std::integral_constant<int, 3>{});
-            }
+        Half A, B;
+        read(s_lo, first, A);
+        for (int s = s_lo; s < s_hi; ++s) {
+            read(s, second, B);
+            multiply(A);
+            interleave();
+            if (s + R - 1 < s_hi) mx_wait_vmcnt<LOADS * (R - 2)>();      // stage s + 1 has landed
+            else mx_wait_vmcnt<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();        // and this one's slot has been read by every wave
+            __builtin_amdgcn_sched_barrier(0);
+            if (s + R < s_hi) issue(s + R);
+            read(s + 1, first, A);               // past the last stage: read and not used
+            multiply(B);
+            interleave();
         }
     }
     mx_wait_vmcnt<0>();          // no load into this block's LDS may land after it ends
 
-    // ---- store: lane (r, g) holds row 16 q + r and columns 4 g + v of each 16 (MODE 2: 8 (4 g + v) + f)
+    // ---- store.  16 x 16 products: lane (r, g) holds row r and columns 4 g + v; 32 x 32:
+    // row r and columns 8 (v / 4) + 4 g + v % 4.  The gradient's fragment f is column 8 c + f.
     float* part = p.part ? p.part + (int64_t)blockIdx.y * p.n * p.m : nullptr;
 #pragma unroll
     for (int q = 0; q < FM; ++q) {
-        const int row = wm * TM + 16 * q + r;
+        const int row = wm * TM + Half::T * q + r;
         if (row >= at.rows) continue;
         const int64_t base = (at.t0 + row) * p.m;
         if constexpr (MODE == MX_GEMM_DX) {
@@ -452,11 +509,13 @@ __global__ __launch_bounds__(64 * NW) void k_mx_tile(MxTile p) {
             }
         } else {
 #pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                const int64_t j = j0 + wn * TN + 16 * f + 4 * g;
-                const float o[4] = {acc[f][q][0], acc[f][q][1], acc[f][q][2], acc[f][q][3]};
-                if (j < p.m) mx_store<4>(p, part, base + j, j, o);
-            }
+            for (int f = 0; f < FN; ++f)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int64_t j = j0 + wn * TN + 32 * f + 8 * v + 4 * g;
+                    const float o[4] = {acc[f][q][4 * v], acc[f][q][4 * v + 1], acc[f][q][4 * v + 2], acc[f][q][4 * v + 3]};
+                    if (j < p.m) mx_store<4>(p, part, base + j, j, o);
+                }
         }
     }
 }
@@ -551,7 +610,9 @@ static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t 
         }
     } else {
         switch (pl.bm) {
-            case 256: return mx_launch<MODE, P, 256, 256, 4, 8>(t, pl.split, st);
+            case 256:
+                if constexpr (MODE == MX_GEMM_MX) return mx_launch<MODE, P, 256, 256, 2>(t, pl.split, st);
+                else return mx_launch<MODE, P, 256, 256, 4, 8>(t, pl.split, st);
             case 128: return mx_launch<MODE, P, 128, 128, 2>(t, pl.split, st);
             case 64: return mx_launch<MODE, P, 64, 128, 1>(t, pl.split, st);
             default: return mx_launch<MODE, P, 32, 128, 1>(t, pl.split, st);

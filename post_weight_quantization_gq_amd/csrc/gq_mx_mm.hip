@@ -194,15 +194,15 @@ __device__ __forceinline__ void mx_store(const MxTile& p, float* part, int64_t a
 // Geometry of a stage in 16-byte LDS slots.
 template <int MODE, int BM, int BN>
 struct MxGeo {
-    static constexpr int RING = (MODE != MX_GEMM_MX && BM == 256) ? 3 : 4;
-    static constexpr int XSPR = MODE == MX_GEMM_MX ? 4 : 8;        // slots a row of activations
+    static constexpr int RING = MODE == MX_GEMM_MX ? (BM >= 128 ? 2 : 3) : (BM == 256 ? 3 : 4);
+    static constexpr int XSPR = 8;                                 // slots a row of activations
     static constexpr int WROWS = MODE == MX_GEMM_DX ? 64 : BN;
-    static constexpr int WSPR = MODE == MX_GEMM ? 2 : (MODE == MX_GEMM_MX ? 4 : BN / 32);
+    static constexpr int WSPR = MODE == MX_GEMM ? 2 : (MODE == MX_GEMM_MX ? 8 : BN / 32);
     static constexpr int X = BM * XSPR, W = WROWS * WSPR;
     static constexpr int SRING = MODE == MX_GEMM_DX ? 64 : 0;      // scales that travel in the ring
     static constexpr int STAGE = X + W + SRING;
     // stages that one 16-byte piece of a row's scales serves, and its three buffers
-    static constexpr int SPAN = MODE == MX_GEMM ? 8 : 4;
+    static constexpr int SPAN = MODE == MX_GEMM ? 8 : 2;
     static constexpr int SROWS = MODE == MX_GEMM_DX ? 0 : (MODE == MX_GEMM ? BN : BN + BM);
     static constexpr size_t BYTES = (size_t)(RING * STAGE + 3 * SROWS) * 16;
 };
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
         const int slot = wave * XPW + i * 64 + lane, row = slot / G::XSPR, c = slot % G::XSPR;
-        const int chunk = MODE == MX_GEMM_MX ? c ^ ((row >> 2) & 3) : c ^ ((row >> 1) & 7);
+        const int chunk = c ^ ((row >> 1) & 7);
         xc[i] = 16u * chunk;
         xv[i] = (uint32_t)(row * p.a_row) + 16u * chunk;
     }
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         const int slot = wave * WPW + i * 64 + lane;
         int row = slot / G::WSPR, c = slot % G::WSPR;
         if constexpr (MODE == MX_GEMM) c ^= (row >> 3) & 1;
-        if constexpr (MODE == MX_GEMM_MX) c ^= (row >> 2) & 3;
+        if constexpr (MODE == MX_GEMM_MX) c ^= (row >> 1) & 7;
         if constexpr (MODE == MX_GEMM_DX && BN == 256) {
             row ^= (row >> 5) & 1;
             c ^= 4 * ((row >> 4) & 1);
@@ -374,19 +374,28 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
                 for (int u = 0; u < 2; ++u)
                     o.x[q][u] = *(const u32x4*)(lds + xb + (wm * TM + 32 * q + r) * 128 + 16 * ((4 * g + 2 * h + u) ^ ((r >> 1) & 7)));
         } else if constexpr (MODE == MX_GEMM_MX) {
-            // lane (r, g): block 2 h + g of the stage's four
-            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 4 * (ks % SPAN) + 2 * h + g;
+            // lane (r, g): block 2 h + g of the stage's eight
+            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 8 * (ks % SPAN) + 2 * h + g;
 #pragma unroll
             for (int q = 0; q < FM; ++q) {
                 const int row = wm * TM + 32 * q + r;
-                o.x[q] = *(const u32x4*)(lds + xb + row * 64 + 16 * ((2 * h + g) ^ ((r >> 2) & 3)));
+                o.x[q] = *(const u32x4*)(lds + xb + row * 128 + 16 * ((2 * h + g) ^ ((r >> 1) & 7)));
                 o.xs[q] = lds[sb + (BN + row) * 16];
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
                 const int row = wn * TN + 32 * f + r;
-                o.w[f] = *(const u32x4*)(lds + wb + row * 64 + 16 * ((2 * h + g) ^ ((r >> 2) & 3)));
+                o.w[f] = *(const u32x4*)(lds + wb + row * 128 + 16 * ((2 * h + g) ^ ((r >> 1) & 7)));
                 o.ws[f] = lds[sb + row * 16];
+            }
+            if constexpr (h >= 2) {
+                // an odd number of 128s ends in half a stage: its other half has zero codes of
+                // x against the next row's weights, whose scales must not be NaN
+                const bool past = 128 * s + 64 >= (int)p.a_bytes;
+#pragma unroll
+                for (int q = 0; q < FM; ++q) o.xs[q] = past ? 127u : o.xs[q];
+#pragma unroll
+                for (int f = 0; f < FN; ++f) o.ws[f] = past ? 127u : o.ws[f];
             }
         } else {
             // lane (r, g): rows 16 g + 8 h .. + 7 of the stage's 64, columns 8 r .. of the wave's 128
@@ -477,6 +486,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             read(s, second, B);
             multiply(A);
             interleave();
+            if constexpr (MODE == MX_GEMM_MX) {
+                // four quarters of 64 values
+                read(s, std::integral_constant<int, 2>{}, A);
+                multiply(B);
+                interleave();
+                read(s, std::integral_constant<int, 3>{}, B);
+                multiply(A);
+                interleave();
+            }
             if (s + R - 1 < s_hi) mx_wait_vmcnt<LOADS * (R - 2)>();      // stage s + 1 has landed
             else mx_wait_vmcnt<0>();
             __builtin_amdgcn_sched_barrier(0);
@@ -560,8 +578,8 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
     P.planes = a_bf16 ? 1 : 3;
     P.staged = op != MX_GEMM_MX && (!a_bf16 || k % 8 != 0);
     const int64_t k64 = op == MX_GEMM_DX ? (k + 63) / 64 : 2 * mx_groups(k);
-    P.stages = (int)(op == MX_GEMM_MX ? mx_groups(k) : k64 * P.planes);
-    P.unit = op == MX_GEMM ? 8 * P.planes : (op == MX_GEMM_MX ? 4 : P.planes);
+    P.stages = (int)(op == MX_GEMM_MX ? (mx_groups(k) + 1) / 2 : k64 * P.planes);
+    P.unit = op == MX_GEMM ? 8 * P.planes : (op == MX_GEMM_MX ? 2 : P.planes);
     P.stage_bytes = P.staged ? mx_al256((size_t)n * k64 * 64 * P.planes * 2) : 0;
     const int64_t per = (n + experts - 1) / experts;
     P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 ? 64 : 32));

@@ -262,7 +262,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     const uint8_t* const Qe = p.Q + (int64_t)at.e * p.d_out * p.qb;
     const uint8_t* const Se = p.S + (int64_t)at.e * p.d_out * p.sb;
     const int64_t wrows = p.m - j0 < BN ? p.m - j0 : BN;
-    const __amdgpu_buffer_rsrc_t wr = mx_rsrc(Qe + j0 * p.qb, wrows * p.qb);
     const __amdgpu_buffer_rsrc_t sr = mx_rsrc(Se + j0 * p.sb, wrows * p.sb);
     const __amdgpu_buffer_rsrc_t xsr =
         MODE == MX_GEMM_MX ? mx_rsrc(p.AS + at.t0 * p.sb, at.rows * p.sb) : sr;
@@ -270,12 +269,16 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     constexpr int XPW = G::X / NW, WPW = G::W / NW;          // slots a wave copies
     constexpr int XI = (XPW + 63) / 64, WI = (WPW + 63) / 64;
     constexpr int LOADS = XI + WI + (MODE == MX_GEMM_MX ? 2 : 1);
-    uint32_t xv[XI], xc[XI], wv[WI];
+    uint32_t xv[XI], wv[WI];
+    int xe[2];                                             // a chunk's first stage past the row
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
         const int slot = wave * XPW + i * 64 + lane, row = slot / G::XSPR, c = slot % G::XSPR;
         const int chunk = c ^ ((row >> 1) & 7);
-        xc[i] = 16u * chunk;
+        if (i < 2) {
+            const int64_t e = (p.a_bytes - 16 * chunk + 16 * G::XSPR - 1) / (16 * G::XSPR);
+            xe[i] = e < s_hi ? (int)e : s_hi;
+        }
         xv[i] = (uint32_t)(row * p.a_row) + 16u * chunk;
     }
 #pragma unroll
@@ -292,45 +295,56 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         wv[i] = (uint32_t)(row * p.qb) + 16u * c;
     }
 
-    auto issue = [&](int s) {
-        u32x4* base = mx_lds + (s % R) * G::STAGE;
-        const uint32_t xo = (uint32_t)s * (16u * G::XSPR);
-        const bool tail = (int64_t)xo + 16 * G::XSPR > p.a_bytes;
-#pragma unroll
-        for (int i = 0; i < XI; ++i) {
-            uint32_t v = xv[i];
-            if (tail && (int64_t)xo + xc[i] >= p.a_bytes) v = 0xC0000000u;     // reads as zeros
-            if (XPW % 64 == 0 || lane < XPW % 64) mx_dma(xr, base + wave * XPW + i * 64, v, xo);
-        }
-        u32x4* wb = base + G::X;
+    // The loads of stage s, in two parts: a few scales (by some of the lanes), and the codes and
+    // activations, one load at a time.  Past this split's last stage they read nothing and clear
+    // a slot that is not read, so that the counts of loads in flight stay what they are.
+    auto issue_scales = [&](int s) {
+        const int ks = s / P;
         if constexpr (MODE == MX_GEMM_DX) {
-            const int ks = s / P;
             const int64_t o0 = (int64_t)ks * 64, left = p.d_out - o0 < 64 ? p.d_out - o0 : 64;
-            const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + o0 * p.qb + j0 / 2, left * p.qb - j0 / 2);
-            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + o0 * p.sb + j0 / 32, left * p.sb - j0 / 32);
-#pragma unroll
-            for (int i = 0; i < WI; ++i)
-                if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(q, wb + wave * WPW + i * 64, wv[i], 0);
+            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + o0 * p.sb + j0 / 32, s < s_hi ? left * p.sb - j0 / 32 : 0);
+            u32x4* wb = mx_lds + (s % R) * G::STAGE + G::X;
             constexpr int SR = 64 / NW;
             if (lane < SR) mx_dma(z, wb + G::W + wave * SR, (uint32_t)((wave * SR + lane) * p.sb), 0);
         } else {
-            const int ks = s / P;
-            const uint32_t wo = (uint32_t)ks * (16u * G::WSPR);
-#pragma unroll
-            for (int i = 0; i < WI; ++i)
-                if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(wr, wb + wave * WPW + i * 64, wv[i], wo);
-            // a share of the next span's scales
+            // a share of the next span's
             const int span = ks / SPAN + 1, part = ks % SPAN;
             u32x4* sb = sc_lds + (span % 3) * G::SROWS;
+            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + j0 * p.sb, s < s_hi ? wrows * p.sb : 0);
             constexpr int WR = BN / SPAN / NW;
             const int row = part * (BN / SPAN) + wave * WR;
-            if (lane < WR) mx_dma(sr, sb + row, (uint32_t)((row + lane) * p.sb) + 16u * span, 0);
+            if (lane < WR) mx_dma(z, sb + row, (uint32_t)((row + lane) * p.sb) + 16u * span, 0);
             if constexpr (MODE == MX_GEMM_MX) {
+                const __amdgpu_buffer_rsrc_t xz = mx_rsrc(p.AS + at.t0 * p.sb, s < s_hi ? at.rows * p.sb : 0);
                 constexpr int XR = BM / SPAN / NW;
                 const int xrow = part * (BM / SPAN) + wave * XR;
-                if (lane < XR) mx_dma(xsr, sb + BN + xrow, (uint32_t)((xrow + lane) * p.sb) + 16u * span, 0);
+                if (lane < XR) mx_dma(xz, sb + BN + xrow, (uint32_t)((xrow + lane) * p.sb) + 16u * span, 0);
             }
         }
+    };
+    auto issue_one = [&](int s, int i) {         // load i of XI + WI
+        u32x4* base = mx_lds + (s % R) * G::STAGE;
+        if (i < XI) {
+            const uint32_t v = s < xe[i & 1] ? xv[i] : 0xC0000000u;          // past the row: zeros
+            if (XPW % 64 == 0 || lane < XPW % 64) mx_dma(xr, base + wave * XPW + i * 64, v, (uint32_t)s * (16u * G::XSPR));
+        } else {
+            i -= XI;
+            u32x4* wb = base + G::X + wave * WPW + i * 64;
+            const int ks = s / P;
+            if constexpr (MODE == MX_GEMM_DX) {
+                const int64_t o0 = (int64_t)ks * 64, left = p.d_out - o0 < 64 ? p.d_out - o0 : 64;
+                const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + o0 * p.qb + j0 / 2, s < s_hi ? left * p.qb - j0 / 2 : 0);
+                if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(q, wb, wv[i], 0);
+            } else {
+                const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + j0 * p.qb, s < s_hi ? wrows * p.qb : 0);
+                if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(q, wb, wv[i], (uint32_t)ks * (16u * G::WSPR));
+            }
+        }
+    };
+    auto issue = [&](int s) {
+        issue_scales(s);
+#pragma unroll
+        for (int i = 0; i < XI + WI; ++i) issue_one(s, i);
     };
 
     if constexpr (MODE != MX_GEMM_DX) {
@@ -461,22 +475,28 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             two(std::integral_constant<int, 3>{});
         }
     };
-    auto interleave = [&]() {                    // a few products after each few reads
-        constexpr int RD = Half::READS, MM = Half::PRODUCTS, N = RD < MM ? RD : MM;
+    // the order of a part's instructions: its reads (and LD loads) spread over the first
+    // products, so that they have arrived when the part ends
+    auto interleave = [&](auto loads) {
+        if constexpr (MODE == MX_GEMM_DX) { __builtin_amdgcn_sched_barrier(0); return; }
+        constexpr int LD = decltype(loads)::value, RD = Half::READS, MM = Half::PRODUCTS;
+        constexpr int N = (MM + 1) / 2;
+        constexpr int PR = (RD + N - 1) / N;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, RD / N, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, MM / N, 0);
+        for (int i = 0; i < MM; ++i) {
+            if (i < N) __builtin_amdgcn_sched_group_barrier(0x100, PR, 0);
+            if (LD > 0) __builtin_amdgcn_sched_group_barrier(0x020, (LD + MM - 1) / MM, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    const std::integral_constant<int, 0> first{};
+    const std::integral_constant<int, 0> first{}, none{};
     const std::integral_constant<int, 1> second{};
 
-    for (int s = s_lo; s < s_lo + R && s < s_hi; ++s) issue(s);
     if (s_lo < s_hi) {
-        if (s_lo + R <= s_hi) mx_wait_vmcnt<LOADS * (R - 1)>();
-        else mx_wait_vmcnt<0>();
+#pragma unroll
+        for (int i = 0; i < R; ++i) issue(s_lo + i);
+        mx_wait_vmcnt<LOADS * (R - 1)>();
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -485,25 +505,26 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         for (int s = s_lo; s < s_hi; ++s) {
             read(s, second, B);
             multiply(A);
-            interleave();
+            interleave(none);
             if constexpr (MODE == MX_GEMM_MX) {
                 // four quarters of 64 values
                 read(s, std::integral_constant<int, 2>{}, A);
                 multiply(B);
-                interleave();
+                interleave(none);
                 read(s, std::integral_constant<int, 3>{}, B);
                 multiply(A);
-                interleave();
+                interleave(none);
             }
-            if (s + R - 1 < s_hi) mx_wait_vmcnt<LOADS * (R - 2)>();      // stage s + 1 has landed
-            else mx_wait_vmcnt<0>();
+            mx_wait_vmcnt<LOADS * (R - 2)>();    // stage s + 1 has landed
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_barrier();        // and this one's slot has been read by every wave
             __builtin_amdgcn_sched_barrier(0);
-            if (s + R < s_hi) issue(s + R);
+            issue_scales(s + R);
+#pragma unroll
+            for (int i = 0; i < XI + WI; ++i) issue_one(s + R, i);
             read(s + 1, first, A);               // past the last stage: read and not used
             multiply(B);
-            interleave();
+            interleave(std::integral_constant<int, XI + WI>{});
         }
     }
     mx_wait_vmcnt<0>();          // no load into this block's LDS may land after it ends

@@ -582,63 +582,101 @@ def mxfp4_row_scales(d: int) -> int:
 
 
 @contextlib.contextmanager
-def _on(t, stream):
-    """The stream pointer of a call on t's device: that device is current, and what the call
-    allocates belongs to the stream it runs on (its memory is reused in that stream's order)."""
-    with torch.cuda.device(t.device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        else:
-            if stream.device != t.device:
-                raise GQError(GQ_EINVAL, f"stream of {stream.device} for tensors on {t.device}")
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+def _other_place(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
 
 
-def _mx_packed(Q, S, d, lead, names=("Q", "S")):
-    """Shapes of packed rows of d values, the leading dimensions being `lead`."""
-    rb, rs = mxfp4_row_bytes(d), mxfp4_row_scales(d)
-    if rb == 0:
+def _place(t, stream):
+    """(context, stream pointer) of a call on t's device: inside the context that device is
+    current, and what the call allocates belongs to the stream it runs on (its memory is reused
+    in that stream's order).  Without a stream to change to, the context does nothing."""
+    index = t.device.index
+    if stream is None:
+        if index == torch._C._cuda_getDevice():
+            return _NOWHERE, torch._C._cuda_getCurrentRawStream(index)
+        stream = torch.cuda.current_stream(index)
+    elif stream.device != t.device:
+        raise GQError(GQ_EINVAL, f"stream of {stream.device} for tensors on {t.device}")
+    return _other_place(t.device, stream), stream.cuda_stream
+
+
+_NOWHERE = contextlib.nullcontext()
+_MX_DTYPES = {torch.float32: GQ_F32, torch.bfloat16: GQ_BF16}
+
+
+def _mx_tensor(t, name, device, shape=None, dtypes=_MX_DTYPES):
+    """One argument's checks, in the order of the other entry points': shape, then a contiguous
+    GPU tensor of an allowed dtype on `device` (None: any)."""
+    if shape is not None and t.shape != shape:
+        raise GQError(GQ_ESHAPE, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise GQError(GQ_EINVAL, f"{name} must be a GPU tensor")
+    if not t.is_contiguous():
+        raise GQError(GQ_EINVAL, f"{name} must be contiguous")
+    if t.dtype not in dtypes:
+        raise GQError(GQ_EDTYPE, f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise GQError(GQ_EINVAL, f"{name} is on {t.device}, the other tensors on {device}")
+
+
+_U8, _I64 = (torch.uint8,), (torch.int64,)
+_MX_MAX_D = 1 << 20
+
+
+def _mx_width(d):
+    """(bytes of codes, bytes of scales) of a packed row of d values."""
+    if d < 1 or d > _MX_MAX_D:
         raise GQError(GQ_ESHAPE if d < 1 else GQ_ENOTIMPL, f"rows of {d} values: 1 to 2^20")
-    _shape(Q, (*lead, rb), names[0])
-    _shape(S, (*lead, rs), names[1])
-    for t, name in ((Q, names[0]), (S, names[1])):
-        if t is not None:
-            _dev(t, name, torch.uint8)
+    groups = -(-d // 128)
+    return 64 * groups, 4 * groups
 
 
 def mxfp4_quantize(x, Q=None, S=None, stream=None):
     """x [..][d] float32 or bfloat16 -> (Q [..][64 ceil(d / 128)], S [..][4 ceil(d / 128)])
     uint8: 4-bit codes and a scale byte for each block of 32 along the last dimension."""
-    lib = library()
+    lib = _lib or library()
     if x.dim() < 1:
         raise GQError(GQ_ESHAPE, "x needs a last dimension to quantise along")
-    lead, d = tuple(x.shape[:-1]), x.shape[-1]
-    _mx_packed(Q, S, d, lead)
-    dt = _dt(_dev(x, "x"))
-    _same_device(x, Q, S)
-    with _on(x, stream) as st:
+    lead, d = x.shape[:-1], x.shape[-1]
+    rb, rs = _mx_width(d)
+    if Q is not None:
+        _mx_tensor(Q, "Q", x.device, (*lead, rb), _U8)
+    if S is not None:
+        _mx_tensor(S, "S", x.device, (*lead, rs), _U8)
+    _mx_tensor(x, "x", None)
+    where, st = _place(x, stream)
+    with where:
         if Q is None:
-            Q = torch.empty((*lead, mxfp4_row_bytes(d)), dtype=torch.uint8, device=x.device)
+            Q = torch.empty((*lead, rb), dtype=torch.uint8, device=x.device)
         if S is None:
-            S = torch.empty((*lead, mxfp4_row_scales(d)), dtype=torch.uint8, device=x.device)
-        _check(lib.mxfp4_quantize(_ptr(x), dt, x.numel() // d, d, _ptr(Q), _ptr(S), st))
+            S = torch.empty((*lead, rs), dtype=torch.uint8, device=x.device)
+        status = lib.mxfp4_quantize(x.data_ptr(), _MX_DTYPES[x.dtype], x.numel() // d, d, Q.data_ptr(),
+                                    S.data_ptr(), st)
+    if status:
+        _check(status)
     return Q, S
 
 
 def mxfp4_dequantize(Q, S, d: int, dtype=torch.bfloat16, y=None, stream=None) -> torch.Tensor:
     """The values [..][d] that packed rows stand for, in float32 or bfloat16."""
-    lib = library()
-    lead = tuple(Q.shape[:-1])
-    _mx_packed(Q, S, d, lead)
-    _shape(y, (*lead, d), "y")
+    lib = _lib or library()
+    lead = Q.shape[:-1]
+    rb, rs = _mx_width(d)
+    if dtype not in _MX_DTYPES:
+        raise GQError(GQ_EDTYPE, f"unsupported dtype {dtype}")
+    _mx_tensor(Q, "Q", None, (*lead, rb), _U8)
+    _mx_tensor(S, "S", Q.device, (*lead, rs), _U8)
     if y is not None:
-        _dev(y, "y", dtype)
-    _same_device(Q, S, y)
-    with _on(Q, stream) as st:
+        _mx_tensor(y, "y", Q.device, (*lead, d), (dtype,))
+    where, st = _place(Q, stream)
+    with where:
         if y is None:
             y = torch.empty((*lead, d), dtype=dtype, device=Q.device)
-        _check(lib.mxfp4_dequantize(_ptr(Q), _ptr(S), y.numel() // d, d, _ptr(y), _dt(y), st))
+        status = lib.mxfp4_dequantize(Q.data_ptr(), S.data_ptr(), y.numel() // d, d, y.data_ptr(),
+                                      _MX_DTYPES[dtype], st)
+    if status:
+        _check(status)
     return y
 
 
@@ -654,45 +692,56 @@ def mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts=1, dtype=GQ_BF16) -> in
     return int(library().mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts, dtype))
 
 
-def _mx_weight(Q, S, d_in, offsets):
+def _mx_weight(Q, S, d_in, offsets, device):
     """(experts, d_out) of a packed weight, one ([d_out][..]) or, with offsets, several
     ([experts][d_out][..])."""
+    rb, rs = _mx_width(d_in)
     if Q.dim() != (2 if offsets is None else 3):
         raise GQError(GQ_ESHAPE, "Q must be [d_out][row bytes], or [experts][d_out][row bytes] "
                                  "with offsets")
-    _mx_packed(Q, S, d_in, tuple(Q.shape[:-1]))
+    lead = Q.shape[:-1]
+    if offsets is not None and offsets.shape != (lead[0] + 1,):
+        raise GQError(GQ_ESHAPE, f"offsets must have shape {(lead[0] + 1,)}, got {tuple(offsets.shape)}")
+    _shape(Q, (*lead, rb), "Q")
+    _shape(S, (*lead, rs), "S")
+    _mx_tensor(Q, "Q", device, None, _U8)
+    _mx_tensor(S, "S", device, None, _U8)
     if offsets is None:
-        return 1, Q.shape[0]
-    if offsets.dtype != torch.int64:
-        raise GQError(GQ_EDTYPE, f"offsets must be int64, got {offsets.dtype}")
-    _shape(offsets, (Q.shape[0] + 1,), "offsets")
-    _dev(offsets, "offsets")
-    return Q.shape[0], Q.shape[1]
+        return 1, lead[0]
+    _mx_tensor(offsets, "offsets", device, None, _I64)
+    return lead
 
 
-def _mx_run(name, x, x_args, size_dt, n, d_in, d_out, width, Q, S, experts, offsets, y, out_dtype,
-            ws, stream):
-    """The part that the three products share: output, workspace and the call itself.  Only
-    with an output of its own does a grouped product need y's rows past the last expert: they
-    are zeroed."""
-    lib = library()
-    if y is not None and out_dtype is not None and y.dtype != out_dtype:
-        raise GQError(GQ_EDTYPE, f"y is {y.dtype}, out_dtype {out_dtype}")
-    _shape(y, (n, width), "y")
+def _mx_product(fn, size, x, first, size_args, n, width, Q, S, last, experts, offsets, y, out_dtype,
+                ws, stream):
+    """What the three products share: output, workspace and the call itself.  A grouped
+    product's own output has zeros in the rows past the last expert's."""
+    where, st = _place(x, stream)
+    device = x.device
     if y is not None:
-        _dev(y, "y")
-    _same_device(x, Q, S, offsets, y, ws if isinstance(ws, torch.Tensor) else None)
-    with _on(x, stream) as st:
+        if out_dtype is not None and y.dtype != out_dtype:
+            raise GQError(GQ_EDTYPE, f"y is {y.dtype}, out_dtype {out_dtype}")
+        _mx_tensor(y, "y", device, (n, width))
+    elif out_dtype not in _MX_DTYPES:
+        raise GQError(GQ_EDTYPE, f"unsupported dtype {out_dtype}")
+    with where:
         if y is None:
             new = torch.empty if offsets is None else torch.zeros
-            y = new((n, width), dtype=out_dtype, device=x.device)
+            y = new((n, width), dtype=out_dtype, device=device)
+        wp, wn = None, 0
         if ws is None:
-            ws = _ws(int(getattr(lib, name + "_workspace_size")(n, d_in, d_out, experts, *size_dt)),
-                     x.device)
-        wp, wn = _ws_arg(ws)
-        _check(getattr(lib, name)(*x_args, _ptr(Q), _ptr(S),
-                                  d_in if name == "mxfp4_gemm_dx" else d_out, experts,
-                                  _ptr(offsets), _ptr(y), _dt(y), wp, wn, st))
+            wn = size(*size_args)
+            if wn:
+                ws = torch.empty(wn, dtype=torch.uint8, device=device)
+                wp = ws.data_ptr()
+        elif ws is not False:
+            _mx_tensor(ws, "ws", device, None, _U8)
+            wp, wn = ws.data_ptr(), ws.numel()
+        status = fn(*first, Q.data_ptr(), S.data_ptr(), last, experts,
+                    None if offsets is None else offsets.data_ptr(), y.data_ptr(),
+                    _MX_DTYPES[y.dtype], wp, wn, st)
+    if status:
+        _check(status)
     return y
 
 
@@ -700,33 +749,39 @@ def mxfp4_gemm(x, Q, S, offsets=None, y=None, out_dtype=None, ws=None, stream=No
     """y [n][d_out] = x W^T for x [n][d_in] (float32 or bfloat16) and the packed weight (Q, S)
     of mxfp4_quantize.  With offsets (int64 [experts + 1] on the device) rows offsets[e] ..
     offsets[e + 1] - 1 of x are multiplied by weight e of Q [experts][d_out][row bytes], and
-    the rows past offsets[experts] of a given y keep their values (of a new one: zeros).
+    the other rows of a given y keep their values (of a new one: zeros).
     out_dtype: float32 or bfloat16, x's unless given."""
+    lib = _lib or library()
     if x.dim() != 2:
         raise GQError(GQ_ESHAPE, "x must be [n][d_in]")
     n, d_in = x.shape
-    experts, d_out = _mx_weight(Q, S, d_in, offsets)
-    dt = _dt(_dev(x, "x"))
+    experts, d_out = _mx_weight(Q, S, d_in, offsets, x.device)
+    _mx_tensor(x, "x", None)
+    dt = _MX_DTYPES[x.dtype]
     if y is None and out_dtype is None:
         out_dtype = x.dtype
-    return _mx_run("mxfp4_gemm", x, (_ptr(x), dt, n, d_in), (dt,), n, d_in, d_out, d_out, Q, S,
-                   experts, offsets, y, out_dtype, ws, stream)
+    return _mx_product(lib.mxfp4_gemm, lib.mxfp4_gemm_workspace_size, x, (x.data_ptr(), dt, n, d_in),
+                       (n, d_in, d_out, experts, dt), n, d_out, Q, S, d_out, experts, offsets, y,
+                       out_dtype, ws, stream)
 
 
 def mxfp4_gemm_mx(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,
                   stream=None) -> torch.Tensor:
     """mxfp4_gemm with the activations packed by mxfp4_quantize as well: XQ [n][row bytes],
     XS [n][row scales].  out_dtype: bfloat16 unless given."""
+    lib = _lib or library()
     if XQ.dim() != 2:
         raise GQError(GQ_ESHAPE, "XQ must be [n][row bytes]")
     n = XQ.shape[0]
-    experts, d_out = _mx_weight(Q, S, d_in, offsets)
-    _mx_packed(XQ, XS, d_in, (n,), ("XQ", "XS"))
-    _same_device(XQ, XS)
+    rb, rs = _mx_width(d_in)
+    experts, d_out = _mx_weight(Q, S, d_in, offsets, XQ.device)
+    _mx_tensor(XQ, "XQ", None, (n, rb), _U8)
+    _mx_tensor(XS, "XS", XQ.device, (n, rs), _U8)
     if y is None and out_dtype is None:
         out_dtype = torch.bfloat16
-    return _mx_run("mxfp4_gemm_mx", XQ, (_ptr(XQ), _ptr(XS), n, d_in), (), n, d_in, d_out, d_out,
-                   Q, S, experts, offsets, y, out_dtype, ws, stream)
+    return _mx_product(lib.mxfp4_gemm_mx, lib.mxfp4_gemm_mx_workspace_size, XQ,
+                       (XQ.data_ptr(), XS.data_ptr(), n, d_in), (n, d_in, d_out, experts), n, d_out,
+                       Q, S, d_out, experts, offsets, y, out_dtype, ws, stream)
 
 
 def mxfp4_gemm_dx(g, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,
@@ -734,16 +789,18 @@ def mxfp4_gemm_dx(g, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=N
     """dx [n][d_in] = g W for the output's gradient g [n][d_out] (float32 or bfloat16): the
     gradient of mxfp4_gemm's x (and, straight through the rounding, of the values that
     mxfp4_gemm_mx's were packed from).  Grouped by offsets like mxfp4_gemm."""
+    lib = _lib or library()
     if g.dim() != 2:
         raise GQError(GQ_ESHAPE, "g must be [n][d_out]")
     n = g.shape[0]
-    experts, d_out = _mx_weight(Q, S, d_in, offsets)
-    _shape(g, (n, d_out), "g")
-    dt = _dt(_dev(g, "g"))
+    experts, d_out = _mx_weight(Q, S, d_in, offsets, g.device)
+    _mx_tensor(g, "g", None, (n, d_out))
+    dt = _MX_DTYPES[g.dtype]
     if y is None and out_dtype is None:
         out_dtype = g.dtype
-    return _mx_run("mxfp4_gemm_dx", g, (_ptr(g), dt, n, d_out), (dt,), n, d_in, d_out, d_in, Q, S,
-                   experts, offsets, y, out_dtype, ws, stream)
+    return _mx_product(lib.mxfp4_gemm_dx, lib.mxfp4_gemm_dx_workspace_size, g,
+                       (g.data_ptr(), dt, n, d_out), (n, d_in, d_out, experts, dt), n, d_in, Q, S,
+                       d_in, experts, offsets, y, out_dtype, ws, stream)
 
 
 STAGES = ("group_scale", "fisher_mfma", "fisher_finalize", "fisher_plain", "lnq_prepare",

@@ -69,6 +69,9 @@ __device__ __forceinline__ void mx_wait_vmcnt() {
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
 }
 
+// lgkmcnt(0) alone
+__device__ __forceinline__ void mx_wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+
 __device__ __forceinline__ void mx_dma(__amdgpu_buffer_rsrc_t r, u32x4* dst, uint32_t voff, uint32_t soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mx_lds_t)dst, 16, voff, soff, 0, 0);
 }
@@ -478,7 +481,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     // the order of a part's instructions: its reads (and LD loads) spread over the first
     // products, so that they have arrived when the part ends
     auto interleave = [&](auto loads) {
-        if constexpr (MODE == MX_GEMM_DX) { __builtin_amdgcn_sched_barrier(0); return; }
+        if constexpr (MODE == MX_GEMM_DX) return;      // (the transposes leave the scheduler no slack: 390 us ordered, 371 free)
         constexpr int LD = decltype(loads)::value, RD = Half::READS, MM = Half::PRODUCTS;
         constexpr int N = (MM + 1) / 2;
         constexpr int PR = (RD + N - 1) / N;
@@ -559,6 +562,137 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: the weight is streamed once, each wave on its own.  A block takes 16 MT output
+// columns of one weight and up to 16 rows of activations at a time; its waves share out the
+// contraction and their sums are added in the waves' order at the end.  A wave copies pieces of
+// KU groups of 128 values of its 16 MT weight rows into LDS of its own, one piece ahead: read
+// straight into registers, 16 consecutive lanes would touch 16 rows and take four times the
+// address cycles.  Lane (r, b) then holds block b of a group of column r's weight (16 bytes),
+// dequantised in place to the products' left operand, and the same 32 values of row r of the
+// activations; the order of the values within a product is free.
+// ---------------------------------------------------------------------------
+template <int MODE, int P, int MT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
+    constexpr int KU = P == 3 ? 2 : 4;           // (three planes of x fill the registers sooner)
+    constexpr int SPR = 4 * KU, WS = 16 * MT * SPR, PIECE = WS + 64, LOADS = WS / 64 + 1;
+    extern __shared__ u32x4 mx_lds[];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, b = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    u32x4* const ring = mx_lds + wave * 2 * PIECE;
+    auto sums = [&](int w, int t) { return (float*)(mx_lds + w * 2 * PIECE) + 256 * t; };    // over the rings at the end
+    const int e = blockIdx.y;
+    const int64_t j0 = (int64_t)blockIdx.x * (16 * MT);
+    int64_t lo = 0, hi = p.n;
+    if (p.offsets) mx_expert_rows(p.offsets, e, p.n, lo, hi);
+    const int groups = (int)(p.qb / 64), pieces = (groups + KU - 1) / KU;
+    const int shares = WAVES * (int)gridDim.z, per = (pieces + shares - 1) / shares;
+    const int c0 = ((int)blockIdx.z * WAVES + wave) * per;
+    const int c1 = c0 + per < pieces ? c0 + per : pieces;
+
+    const int64_t wrows = p.m - j0 < 16 * MT ? p.m - j0 : 16 * MT, row0 = (int64_t)e * p.d_out + j0;
+    auto swizzle = [](int row) { return KU == 4 ? row & 15 : (row >> 1) & 7; };
+    uint32_t wv[WS / 64];
+#pragma unroll
+    for (int i = 0; i < WS / 64; ++i) {
+        const int slot = i * 64 + lane, row = slot / SPR;
+        wv[i] = (uint32_t)(row * p.qb) + 16u * ((slot % SPR) ^ swizzle(row));
+    }
+    auto copy = [&](int c) {                     // past the last piece: clears, reads nothing
+        u32x4* to = ring + (c & 1) * PIECE;
+        const __amdgpu_buffer_rsrc_t wr = mx_rsrc(p.Q + row0 * p.qb, c < c1 ? wrows * p.qb : 0);
+        const __amdgpu_buffer_rsrc_t sr = mx_rsrc(p.S + row0 * p.sb, c < c1 ? wrows * p.sb : 0);
+#pragma unroll
+        for (int i = 0; i < WS / 64; ++i) mx_dma(wr, to + 64 * i, wv[i], (uint32_t)c * (16u * SPR));
+        mx_dma(sr, to + WS, lane < 16 * MT ? (uint32_t)(lane * p.sb) : 0xC0000000u, (uint32_t)c * (4u * KU));
+    };
+
+    for (int64_t t0 = lo; t0 < hi; t0 += 16) {
+        const int rows = (int)(hi - t0 < 16 ? hi - t0 : 16);
+        const int64_t xrow = t0 + (r < rows ? r : rows - 1);
+        const uint8_t* const xp = p.A + xrow * p.a_row;
+        const uint8_t* const xsp = MODE == MX_GEMM_MX ? p.AS + xrow * p.sb : nullptr;
+        f32x4 acc[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (t0 > lo) __syncthreads();            // the sums of the rows before have been read
+        if (c0 < c1) copy(c0);
+        for (int c = c0; c < c1; ++c) {
+            // this piece's activations, then the next piece's copies: once those alone are in
+            // flight, both this piece's copies and its activations have arrived
+            u32x4 x[KU][MODE == MX_GEMM_MX ? 1 : 4 * P];
+            uint32_t xs[KU];
+#pragma unroll
+            for (int h = 0; h < KU; ++h) {
+                const int g = KU * c + h;                     // (past the last: zeros)
+                if constexpr (MODE == MX_GEMM_MX) {
+                    const u32x4 v = *(const u32x4*)(xp + (g < groups ? 64 * g : 0) + 16 * b);
+                    x[h][0] = g < groups ? v : u32x4{0u, 0u, 0u, 0u};
+                    xs[h] = *(const uint32_t*)(xsp + (g < groups ? 4 * g : 0));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int q = 0; q < P; ++q) {
+                            // values 128 g + 32 b + 8 j .. of plane q
+                            const int at = ((2 * g + (b >> 1)) * P + q) * 128 + 64 * (b & 1) + 16 * j;
+                            const u32x4 v = *(const u32x4*)(xp + (at < p.a_bytes ? at : 0));
+                            x[h][j * P + q] = at < p.a_bytes ? v : u32x4{0u, 0u, 0u, 0u};
+                        }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            copy(c + 1);
+            mx_wait_vmcnt<LOADS>();
+            __builtin_amdgcn_sched_barrier(0);
+            const uint8_t* const at = (const uint8_t*)(ring + (c & 1) * PIECE);
+#pragma unroll
+            for (int h = 0; h < KU; ++h) {
+                const bool own = KU * c + h < groups;         // else codes and scales of the next row
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const int row = 16 * t + r;
+                    const u32x4 w = *(const u32x4*)(at + 16 * (row * SPR + ((4 * h + b) ^ swizzle(row))));
+                    const uint32_t sb = at[16 * (WS + row) + 4 * h + b], sc = own ? sb : 127u;
+                    if constexpr (MODE == MX_GEMM_MX) {
+                        const i32x8 wa{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+                        const i32x8 xa{(int)x[h][0][0], (int)x[h][0][1], (int)x[h][0][2], (int)x[h][0][3], 0, 0, 0, 0};
+                        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, xa, acc[t], 4, 4, 0, (int)sc, 0, (int)((xs[h] >> (8 * b)) & 255u));
+                    } else {
+                        const float f = mx_scale(sc);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const u32x4 wa{mx_bf16<0>(w[j], f), mx_bf16<1>(w[j], f), mx_bf16<2>(w[j], f), mx_bf16<3>(w[j], f)};
+#pragma unroll
+                            for (int q = 0; q < P; ++q)
+                                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wa), as_bf16x8(x[h][j * P + q]), acc[t], 0, 0, 0);
+                        }
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            mx_wait_lds();                       // read, before its half of the ring is copied into
+        }
+        mx_wait_vmcnt<0>();                      // no copy into the ring may land later
+#pragma unroll
+        for (int t = 0; t < MT; ++t) *(f32x4*)(sums(wave, t) + 4 * lane) = acc[t];
+        __syncthreads();
+        // output (row i / (16 MT), column i % (16 MT)) is in lane 16 (column / 4) + row, element column % 4
+        for (int i = tid; i < 256 * MT; i += 64 * WAVES) {
+            const int row = i / (16 * MT), c = i - row * (16 * MT), t = c >> 4;
+            const int from = 4 * (16 * ((c & 15) >> 2) + row) + (c & 3);
+            if (row >= rows || j0 + c >= p.m) continue;
+            float v = sums(0, t)[from];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) v += sums(w, t)[from];
+            const int64_t at = (t0 + row) * p.m + j0 + c;
+            if (p.part) p.part[(int64_t)blockIdx.z * p.n * p.m + at] = v;
+            else if (p.y_bf16) ((uint16_t*)p.y)[at] = (uint16_t)f32_to_bf16_bits(v);
+            else ((float*)p.y)[at] = v;
+        }
+    }
+}
+
 // y = the sum of a split contraction's parts, in their order; rows that belong to an expert
 // (all of them without offsets).
 __global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part, int split, int64_t n,
@@ -570,8 +704,18 @@ __global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part,
         mx_expert_rows(offsets, 0, n, lo, a);
         mx_expert_rows(offsets, experts - 1, n, b, hi);
     }
-    const int64_t first = lo * m, end = hi * m, all = n * m;
-    for (int64_t t = first + (int64_t)blockIdx.x * 256 + threadIdx.x; t < end; t += (int64_t)gridDim.x * 256) {
+    const int64_t first = lo * m, end = hi * m, all = n * m, stride = (int64_t)gridDim.x * 256;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (all % 4 == 0 && m % 4 == 0 && ((uintptr_t)y & (y_bf16 ? 7u : 15u)) == 0) {
+        for (int64_t t = first + 4 * id; t < end; t += 4 * stride) {
+            f32x4 s = *(const f32x4*)(part + t);
+            for (int k = 1; k < split; ++k) s += *(const f32x4*)(part + k * all + t);
+            if (y_bf16) *(u32x2*)((uint16_t*)y + t) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+            else *(f32x4*)((float*)y + t) = s;
+        }
+        return;
+    }
+    for (int64_t t = first + id; t < end; t += stride) {
         float s = part[t];
         for (int k = 1; k < split; ++k) s += part[k * all + t];
         if (y_bf16) ((uint16_t*)y)[t] = (uint16_t)f32_to_bf16_bits(s);
@@ -588,7 +732,8 @@ static size_t mx_al256(size_t x) { return (x + 255) & ~(size_t)255; }
 struct MxPlan {
     bool staged;                  // activations are copied into planes first
     int planes;
-    int bm, bn, split;
+    bool stream;                  // few rows a weight
+    int bm, bn, split, waves;
     int stages, unit;
     size_t stage_bytes, part_bytes;
 };
@@ -603,15 +748,28 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
     P.unit = op == MX_GEMM ? 8 * P.planes : (op == MX_GEMM_MX ? 2 : P.planes);
     P.stage_bytes = P.staged ? mx_al256((size_t)n * k64 * 64 * P.planes * 2) : 0;
     const int64_t per = (n + experts - 1) / experts;
-    P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 ? 64 : 32));
-    P.bn = P.bm == 256 ? 256 : 128;
-    if (op == MX_GEMM_DX && P.bm == 32) P.bm = 64;
+    P.stream = op != MX_GEMM_DX && per <= 16;
     P.split = 1;
-    const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;
-    const int64_t tiles = rows * ((m + P.bn - 1) / P.bn);
-    const int units = (P.stages + P.unit - 1) / P.unit;
-    if (tiles < 256) {
-        int64_t s = 512 / tiles;
+    int64_t blocks, units;
+    if (P.stream) {
+        const int64_t live = experts > 1 ? (experts < n ? experts : n) : 1;      // experts with rows, at most
+        P.bm = 16;
+        P.bn = live * ((m + 31) / 32) >= 512 ? 32 : 16;
+        const int ku = P.planes == 3 ? 2 : 4;
+        units = (mx_groups(k) + ku - 1) / ku;
+        P.waves = units >= 8 ? 8 : 4;
+        blocks = live * ((m + P.bn - 1) / P.bn);
+        units /= P.waves;
+    } else {
+        P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 ? 64 : 32));
+        P.bn = P.bm == 256 ? 256 : 128;
+        if (op == MX_GEMM_DX && P.bm == 32) P.bm = 64;
+        const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;
+        blocks = rows * ((m + P.bn - 1) / P.bn);
+        units = (P.stages + P.unit - 1) / P.unit;
+    }
+    if (blocks < 256) {
+        int64_t s = 512 / blocks;
         s = s < units ? s : units;
         P.split = (int)(s < 1 ? 1 : (s > 16 ? 16 : s));
     }
@@ -639,8 +797,26 @@ static hipError_t mx_launch(const MxTile& t, int split, hipStream_t st) {
     return hipSuccess;
 }
 
+template <int MODE, int P, int MT, int WAVES>
+static hipError_t mx_launch_stream(const MxTile& t, const MxPlan& pl, hipStream_t st) {
+    constexpr int KU = P == 3 ? 2 : 4;
+    const size_t lds = (size_t)WAVES * 2 * (16 * MT * 4 * KU + 64) * 16;
+    const hipError_t e = ensure_dynamic_lds((const void*)k_mx_stream<MODE, P, MT, WAVES>, lds);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)((t.m + 16 * MT - 1) / (16 * MT)), (unsigned)t.experts, (unsigned)pl.split);
+    hipLaunchKernelGGL((k_mx_stream<MODE, P, MT, WAVES>), grid, dim3(64 * WAVES), lds, st, t);
+    GQ_LAUNCH_CHECK();
+    return hipSuccess;
+}
+
 template <int MODE, int P>
 static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t st) {
+    if constexpr (MODE != MX_GEMM_DX) {
+        if (pl.stream && pl.waves == 8)
+            return pl.bn == 32 ? mx_launch_stream<MODE, P, 2, 8>(t, pl, st) : mx_launch_stream<MODE, P, 1, 8>(t, pl, st);
+        if (pl.stream)
+            return pl.bn == 32 ? mx_launch_stream<MODE, P, 2, 4>(t, pl, st) : mx_launch_stream<MODE, P, 1, 4>(t, pl, st);
+    }
     if constexpr (MODE == MX_GEMM_DX) {
         switch (pl.bm) {
             case 256: return mx_launch<MODE, P, 256, 256, 4, 8>(t, pl.split, st);

@@ -58,6 +58,7 @@ struct MxTile {
     int experts;
     int64_t n, m, d_out;          // rows, output columns, rows of one weight
     int stages;                   // stages of the whole contraction
+    int kpad;                     // its length padded to whole groups (MX_GEMM, MX_GEMM_MX)
     int unit;                     // a split's range is a multiple of this many stages
     void* y;
     int y_bf16, y_vec;            // y_vec: runs of 4 (MODE 2: 8) outputs may be stored whole
@@ -194,23 +195,39 @@ __device__ __forceinline__ void mx_store(const MxTile& p, float* part, int64_t a
     }
 }
 
-// Geometry of a stage in 16-byte LDS slots.
-template <int MODE, int BM, int BN>
+// Geometry of a stage in 16-byte LDS slots.  KS (MX_GEMM): pieces of 64 values a stage.  With
+// one, the planes of float32 activations are stages of their own (and the weight is read for
+// each); with four, a stage holds them all.
+template <int MODE, int P, int BM, int BN, int KS>
 struct MxGeo {
-    static constexpr int RING = MODE == MX_GEMM_MX ? (BM >= 128 ? 2 : 3) : (BM == 256 ? 3 : 4);
-    static constexpr int XSPR = 8;                                 // slots a row of activations
+    static constexpr int RING = MODE == MX_GEMM_MX ? (BM >= 128 ? 2 : 3) : (KS > 1 ? 2 : (BM == 256 ? 3 : 4));
+    static constexpr int PS = KS > 1 ? P : 1;                      // planes within a stage
+    static constexpr int PA = KS > 1 ? 1 : P;                      // stages for one piece of the weight
+    static constexpr int XSPR = MODE == MX_GEMM ? 8 * KS * PS : 8; // slots a row of activations
     static constexpr int WROWS = MODE == MX_GEMM_DX ? 64 : BN;
-    static constexpr int WSPR = MODE == MX_GEMM ? 2 : (MODE == MX_GEMM_MX ? 8 : BN / 32);
+    static constexpr int WSPR = MODE == MX_GEMM ? 2 * KS : (MODE == MX_GEMM_MX ? 8 : BN / 32);
     static constexpr int X = BM * XSPR, W = WROWS * WSPR;
     static constexpr int SRING = MODE == MX_GEMM_DX ? 64 : 0;      // scales that travel in the ring
     static constexpr int STAGE = X + W + SRING;
     // stages that one 16-byte piece of a row's scales serves, and its three buffers
-    static constexpr int SPAN = MODE == MX_GEMM ? 8 : 2;
+    static constexpr int SPAN = MODE == MX_GEMM ? 8 / KS : 2;
     static constexpr int SROWS = MODE == MX_GEMM_DX ? 0 : (MODE == MX_GEMM ? BN : BN + BM);
+    static constexpr int PARTS = MODE == MX_GEMM ? 2 * KS * PS : (MODE == MX_GEMM_MX ? 4 : 2);
     static constexpr size_t BYTES = (size_t)(RING * STAGE + 3 * SROWS) * 16;
+    // a row's chunks are moved about so that the 16 rows of a fragment read spread over the banks
+    static __device__ __forceinline__ int xswz(int row) { return KS > 1 ? row & 15 : (row >> 1) & 7; }
 };
 
-// The fragments of half a stage, and an accumulator.
+// f(integral_constant 0) .. f(integral_constant N - 1)
+template <int N, class F>
+__device__ __forceinline__ void mx_each(F f) {
+    if constexpr (N > 0) {
+        mx_each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
+
+// The fragments of a part of a stage, and an accumulator.
 template <int MODE, int FM, int FN> struct MxHalf;
 template <int FM, int FN> struct MxHalf<MX_GEMM, FM, FN> {
     typedef f32x16 Acc;
@@ -232,12 +249,12 @@ template <int FM, int FN> struct MxHalf<MX_GEMM_DX, FM, FN> {
     uint32_t w[8], ws[8];
 };
 
-template <int MODE, int P, int BM, int BN, int WM, int NW>
+template <int MODE, int P, int BM, int BN, int WM, int NW, int KS>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM == 256 && NW == 4 ? 1 : 8))) void k_mx_tile(MxTile p) {
-    typedef MxGeo<MODE, BM, BN> G;
+    typedef MxGeo<MODE, P, BM, BN, KS> G;
     constexpr int WN = NW / WM, TM = BM / WM, TN = BN / WN;
     constexpr int T = MODE == MX_GEMM_DX ? 16 : 32, FM = TM / T, FN = TN / T;
-    constexpr int R = G::RING, SPAN = G::SPAN;
+    constexpr int R = G::RING, SPAN = G::SPAN, PA = G::PA;
     static_assert(MODE != MX_GEMM_DX || TN == 128, "a wave of the gradient takes 128 columns");
     extern __shared__ u32x4 mx_lds[];
     u32x4* const sc_lds = mx_lds + R * G::STAGE;
@@ -273,12 +290,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     constexpr int XI = (XPW + 63) / 64, WI = (WPW + 63) / 64;
     constexpr int LOADS = XI + WI + (MODE == MX_GEMM_MX ? 2 : 1);
     uint32_t xv[XI], wv[WI];
-    int xe[2];                                             // a chunk's first stage past the row
+    constexpr int XE = KS > 1 ? XI : (XI < 2 ? XI : 2);    // (chunks repeat every other load otherwise)
+    int xe[XE];                                            // a chunk's first stage past the row
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
         const int slot = wave * XPW + i * 64 + lane, row = slot / G::XSPR, c = slot % G::XSPR;
-        const int chunk = c ^ ((row >> 1) & 7);
-        if (i < 2) {
+        const int chunk = c ^ G::xswz(row);
+        if (i < XE) {
             const int64_t e = (p.a_bytes - 16 * chunk + 16 * G::XSPR - 1) / (16 * G::XSPR);
             xe[i] = e < s_hi ? (int)e : s_hi;
         }
@@ -288,7 +306,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     for (int i = 0; i < WI; ++i) {
         const int slot = wave * WPW + i * 64 + lane;
         int row = slot / G::WSPR, c = slot % G::WSPR;
-        if constexpr (MODE == MX_GEMM) c ^= (row >> 3) & 1;
+        if constexpr (MODE == MX_GEMM) c ^= KS > 1 ? (row >> 1) & 7 : (row >> 3) & 1;
         if constexpr (MODE == MX_GEMM_MX) c ^= (row >> 1) & 7;
         if constexpr (MODE == MX_GEMM_DX && BN == 256) {
             row ^= (row >> 5) & 1;
@@ -302,7 +320,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     // activations, one load at a time.  Past this split's last stage they read nothing and clear
     // a slot that is not read, so that the counts of loads in flight stay what they are.
     auto issue_scales = [&](int s) {
-        const int ks = s / P;
+        const int ks = s / PA;
         if constexpr (MODE == MX_GEMM_DX) {
             const int64_t o0 = (int64_t)ks * 64, left = p.d_out - o0 < 64 ? p.d_out - o0 : 64;
             const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + o0 * p.sb + j0 / 32, s < s_hi ? left * p.sb - j0 / 32 : 0);
@@ -328,12 +346,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     auto issue_one = [&](int s, int i) {         // load i of XI + WI
         u32x4* base = mx_lds + (s % R) * G::STAGE;
         if (i < XI) {
-            const uint32_t v = s < xe[i & 1] ? xv[i] : 0xC0000000u;          // past the row: zeros
+            const uint32_t v = s < xe[i % XE] ? xv[i] : 0xC0000000u;          // past the row: zeros
             if (XPW % 64 == 0 || lane < XPW % 64) mx_dma(xr, base + wave * XPW + i * 64, v, (uint32_t)s * (16u * G::XSPR));
         } else {
             i -= XI;
             u32x4* wb = base + G::X + wave * WPW + i * 64;
-            const int ks = s / P;
+            const int ks = s / PA;
             if constexpr (MODE == MX_GEMM_DX) {
                 const int64_t o0 = (int64_t)ks * 64, left = p.d_out - o0 < 64 ? p.d_out - o0 : 64;
                 const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + o0 * p.qb + j0 / 2, s < s_hi ? left * p.qb - j0 / 2 : 0);
@@ -352,7 +370,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 
     if constexpr (MODE != MX_GEMM_DX) {
         // the first span's scales whole
-        const int span = s_lo / P / SPAN;
+        const int span = s_lo / PA / SPAN;
         u32x4* sb = sc_lds + (span % 3) * G::SROWS;
         constexpr int WR = BN / NW;
         if (lane < WR) mx_dma(sr, sb + wave * WR, (uint32_t)((wave * WR + lane) * p.sb) + 16u * span, 0);
@@ -362,8 +380,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         }
     }
 
-    // ---- the contraction, half a stage at a time: while one half's products run, the other
-    // half's fragments are read, so the loop holds two halves and the accumulators
+    // ---- the contraction, a part of a stage at a time: while one part's products run, the next
+    // part's fragments are read, so the loop holds two parts and the accumulators
     typedef MxHalf<MODE, FM, FN> Half;
     typename Half::Acc acc[FN][FM];
 #pragma unroll
@@ -373,23 +391,29 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 #pragma unroll
             for (int v = 0; v < Half::V; ++v) acc[f][q][v] = 0.f;
     const uint8_t* const lds = (const uint8_t*)mx_lds;
-    auto read = [&](int s, auto half, Half& o) {
-        constexpr int h = decltype(half)::value;
-        const int xb = (s % R) * G::STAGE * 16, wb = xb + G::X * 16, ks = s / P;
+    auto read = [&](int s, auto part, Half& o) {
+        constexpr int h = decltype(part)::value;
+        const int xb = (s % R) * G::STAGE * 16, wb = xb + G::X * 16, ks = s / PA;
         if constexpr (MODE == MX_GEMM) {
-            // lane (r, g): values 32 g .. of the stage's 64, 16 h .. of them in this half
-            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 2 * (ks % SPAN) + g;
+            // part h: values 16 hh .. of the 32 that lane (r, g) has of piece kk, in plane q
+            constexpr int kk = h / (2 * G::PS), q0 = h / 2 % G::PS, hh = h % 2;
+            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 2 * KS * (ks % SPAN) + 2 * kk + g;
+            const int wc = KS > 1 ? (2 * kk + g) ^ ((r >> 1) & 7) : g ^ ((r >> 3) & 1);
+            // an odd number of 128s ends in half a stage: its other half has zeros of x against
+            // the next row's weights, whose scales must not be NaN
+            const bool past = KS > 1 && 4 * kk >= 2 * KS && 64 * KS * ks + 64 * kk >= p.kpad;
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
                 const int row = wn * TN + 32 * f + r;
-                o.w[f] = *(const u32x2*)(lds + wb + row * 32 + 16 * (g ^ ((r >> 3) & 1)) + 8 * h);
-                o.ws[f] = lds[sb + row * 16];
+                o.w[f] = *(const u32x2*)(lds + wb + row * (16 * G::WSPR) + 16 * wc + 8 * hh);
+                const uint32_t sc = lds[sb + row * 16];
+                o.ws[f] = past ? 127u : sc;
             }
 #pragma unroll
             for (int q = 0; q < FM; ++q)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-                    o.x[q][u] = *(const u32x4*)(lds + xb + (wm * TM + 32 * q + r) * 128 + 16 * ((4 * g + 2 * h + u) ^ ((r >> 1) & 7)));
+                    o.x[q][u] = *(const u32x4*)(lds + xb + (wm * TM + 32 * q + r) * (16 * G::XSPR) + 16 * ((8 * (kk * G::PS + q0) + 4 * g + 2 * hh + u) ^ G::xswz(r)));
         } else if constexpr (MODE == MX_GEMM_MX) {
             // lane (r, g): block 2 h + g of the stage's eight
             const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 8 * (ks % SPAN) + 2 * h + g;
@@ -408,7 +432,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             if constexpr (h >= 2) {
                 // an odd number of 128s ends in half a stage: its other half has zero codes of
                 // x against the next row's weights, whose scales must not be NaN
-                const bool past = 128 * s + 64 >= (int)p.a_bytes;
+                const bool past = 256 * s + 128 >= p.kpad;
 #pragma unroll
                 for (int q = 0; q < FM; ++q) o.xs[q] = past ? 127u : o.xs[q];
 #pragma unroll
@@ -494,7 +518,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         __builtin_amdgcn_sched_barrier(0);
     };
     const std::integral_constant<int, 0> first{}, none{};
-    const std::integral_constant<int, 1> second{};
 
     if (s_lo < s_hi) {
 #pragma unroll
@@ -506,18 +529,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         Half A, B;
         read(s_lo, first, A);
         for (int s = s_lo; s < s_hi; ++s) {
-            read(s, second, B);
-            multiply(A);
-            interleave(none);
-            if constexpr (MODE == MX_GEMM_MX) {
-                // four quarters of 64 values
-                read(s, std::integral_constant<int, 2>{}, A);
-                multiply(B);
-                interleave(none);
-                read(s, std::integral_constant<int, 3>{}, B);
+            mx_each<G::PARTS / 2 - 1>([&](auto i) {
+                constexpr int h = 2 * decltype(i)::value;
+                read(s, std::integral_constant<int, h + 1>{}, B);
                 multiply(A);
                 interleave(none);
-            }
+                read(s, std::integral_constant<int, h + 2>{}, A);
+                multiply(B);
+                interleave(none);
+            });
+            read(s, std::integral_constant<int, G::PARTS - 1>{}, B);
+            multiply(A);
+            interleave(none);
             mx_wait_vmcnt<LOADS * (R - 2)>();    // stage s + 1 has landed
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_barrier();        // and this one's slot has been read by every wave
@@ -709,7 +732,15 @@ __global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part,
     if (all % 4 == 0 && m % 4 == 0 && ((uintptr_t)y & (y_bf16 ? 7u : 15u)) == 0) {
         for (int64_t t = first + 4 * id; t < end; t += 4 * stride) {
             f32x4 s = *(const f32x4*)(part + t);
-            for (int k = 1; k < split; ++k) s += *(const f32x4*)(part + k * all + t);
+            int k = 1;
+            for (; k + 4 <= split; k += 4) {     // four loads in flight, added in their order
+                f32x4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = *(const f32x4*)(part + (k + i) * all + t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s += v[i];
+            }
+            for (; k < split; ++k) s += *(const f32x4*)(part + k * all + t);
             if (y_bf16) *(u32x2*)((uint16_t*)y + t) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
             else *(f32x4*)((float*)y + t) = s;
         }
@@ -744,17 +775,16 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
     P.planes = a_bf16 ? 1 : 3;
     P.staged = op != MX_GEMM_MX && (!a_bf16 || k % 8 != 0);
     const int64_t k64 = op == MX_GEMM_DX ? (k + 63) / 64 : 2 * mx_groups(k);
-    P.stages = (int)(op == MX_GEMM_MX ? (mx_groups(k) + 1) / 2 : k64 * P.planes);
-    P.unit = op == MX_GEMM ? 8 * P.planes : (op == MX_GEMM_MX ? 2 : P.planes);
     P.stage_bytes = P.staged ? mx_al256((size_t)n * k64 * 64 * P.planes * 2) : 0;
     const int64_t per = (n + experts - 1) / experts;
     P.stream = op != MX_GEMM_DX && per <= 16;
     P.split = 1;
+    P.stages = P.unit = 0;
     int64_t blocks, units;
     if (P.stream) {
         const int64_t live = experts > 1 ? (experts < n ? experts : n) : 1;      // experts with rows, at most
         P.bm = 16;
-        P.bn = live * ((m + 31) / 32) >= 512 ? 32 : 16;
+        P.bn = live * ((m + 31) / 32) >= 256 ? 32 : 16;
         const int ku = P.planes == 3 ? 2 : 4;
         units = (mx_groups(k) + ku - 1) / ku;
         P.waves = units >= 8 ? 8 : 4;
@@ -766,6 +796,10 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
         if (op == MX_GEMM_DX && P.bm == 32) P.bm = 64;
         const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;
         blocks = rows * ((m + P.bn - 1) / P.bn);
+        // few rows of x: stages of 256 values, so that a weight row is read by whole lines
+        const bool deep = op == MX_GEMM && (P.bm == 32 || (P.bm == 64 && P.planes == 1));
+        P.stages = (int)(op == MX_GEMM_MX || deep ? (mx_groups(k) + 1) / 2 : k64 * P.planes);
+        P.unit = op == MX_GEMM_DX ? P.planes : (op == MX_GEMM_MX || deep ? 2 : 8 * P.planes);
         units = (P.stages + P.unit - 1) / P.unit;
     }
     if (blocks < 256) {
@@ -782,17 +816,17 @@ size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t 
     return P.stage_bytes + P.part_bytes;
 }
 
-template <int MODE, int P, int BM, int BN, int WM, int NW = 4>
+template <int MODE, int P, int BM, int BN, int WM, int NW = 4, int KS = 1>
 static hipError_t mx_launch(const MxTile& t, int split, hipStream_t st) {
-    const void* k = (const void*)k_mx_tile<MODE, P, BM, BN, WM, NW>;
-    const size_t lds = MxGeo<MODE, BM, BN>::BYTES;
+    const void* k = (const void*)k_mx_tile<MODE, P, BM, BN, WM, NW, KS>;
+    const size_t lds = MxGeo<MODE, P, BM, BN, KS>::BYTES;
     hipError_t e = ensure_dynamic_lds(k, lds);
     if (e != hipSuccess) return e;
     const int64_t rows = (t.n + BM - 1) / BM + (t.offsets ? t.experts : 0);
     const int64_t tiles = rows * ((t.m + BN - 1) / BN);
     const int64_t grid = (tiles + 7) / 8 * 8;
     if (grid > 0x7fffffffll) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_mx_tile<MODE, P, BM, BN, WM, NW>), dim3((unsigned)grid, (unsigned)split), dim3(64 * NW), lds, st, t);
+    hipLaunchKernelGGL((k_mx_tile<MODE, P, BM, BN, WM, NW, KS>), dim3((unsigned)grid, (unsigned)split), dim3(64 * NW), lds, st, t);
     GQ_LAUNCH_CHECK();
     return hipSuccess;
 }
@@ -829,8 +863,8 @@ static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t 
                 if constexpr (MODE == MX_GEMM_MX) return mx_launch<MODE, P, 256, 256, 2>(t, pl.split, st);
                 else return mx_launch<MODE, P, 256, 256, 4, 8>(t, pl.split, st);
             case 128: return mx_launch<MODE, P, 128, 128, 2>(t, pl.split, st);
-            case 64: return mx_launch<MODE, P, 64, 128, 1>(t, pl.split, st);
-            default: return mx_launch<MODE, P, 32, 128, 1>(t, pl.split, st);
+            case 64: return mx_launch<MODE, P, 64, 128, 1, 4, MODE == MX_GEMM && P == 1 ? 4 : 1>(t, pl.split, st);
+            default: return mx_launch<MODE, P, 32, 128, 1, 4, MODE == MX_GEMM ? 4 : 1>(t, pl.split, st);
         }
     }
 }
@@ -844,7 +878,7 @@ hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
     t.AS = c.as;
     t.a_row = t.a_bytes = c.op == MX_GEMM_MX ? mx_row_bytes(k) : 2 * k;
     if (pl.staged) {
-        const int64_t pieces = pl.stages / pl.planes;
+        const int64_t pieces = c.op == MX_GEMM_DX ? (k + 63) / 64 : 2 * mx_groups(k);
         t.A = (const uint8_t*)ws;
         t.a_row = t.a_bytes = pieces * pl.planes * 128;
         const int64_t blocks = (c.n * pieces * 64 + 255) / 256;
@@ -863,6 +897,7 @@ hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
     t.m = m;
     t.d_out = c.d_out;
     t.stages = pl.stages;
+    t.kpad = (int)(128 * mx_groups(k));
     t.unit = pl.unit;
     t.y = c.y;
     t.y_bf16 = c.y_bf16;

@@ -200,7 +200,7 @@ __device__ __forceinline__ void mx_store(const MxTile& p, float* part, int64_t a
 // each); with four, a stage holds them all.
 template <int MODE, int P, int BM, int BN, int KS>
 struct MxGeo {
-    static constexpr int RING = MODE == MX_GEMM_MX ? (BM >= 128 ? 2 : 3) : (KS > 1 ? 2 : (BM == 256 ? 3 : 4));
+    static constexpr int RING = MODE == MX_GEMM_MX ? (BM >= 128 ? 2 : 3) : (KS > 1 ? 2 : (BM * BN > 128 * 128 ? 3 : 4));
     static constexpr int PS = KS > 1 ? P : 1;                      // planes within a stage
     static constexpr int PA = KS > 1 ? 1 : P;                      // stages for one piece of the weight
     static constexpr int XSPR = MODE == MX_GEMM ? 8 * KS * PS : 8; // slots a row of activations
@@ -231,20 +231,20 @@ __device__ __forceinline__ void mx_each(F f) {
 template <int MODE, int FM, int FN> struct MxHalf;
 template <int FM, int FN> struct MxHalf<MX_GEMM, FM, FN> {
     typedef f32x16 Acc;
-    static constexpr int T = 32, V = 16, READS = 2 * FM + 2 * FN, PRODUCTS = 2 * FM * FN;
+    static constexpr int T = 32, V = 16, STEPS = 2 * FM + FN, PRODUCTS = 2 * FM * FN;
     u32x4 x[FM][2];
     u32x2 w[FN];
     uint32_t ws[FN];
 };
 template <int FM, int FN> struct MxHalf<MX_GEMM_MX, FM, FN> {
     typedef f32x16 Acc;
-    static constexpr int T = 32, V = 16, READS = 2 * FM + 2 * FN, PRODUCTS = FM * FN;
+    static constexpr int T = 32, V = 16, STEPS = FM + FN, PRODUCTS = FM * FN;
     u32x4 x[FM], w[FN];
     uint32_t xs[FM], ws[FN];
 };
 template <int FM, int FN> struct MxHalf<MX_GEMM_DX, FM, FN> {
     typedef f32x4 Acc;
-    static constexpr int T = 16, V = 4, READS = FM + 16, PRODUCTS = FM * FN;
+    static constexpr int T = 16, V = 4, STEPS = FM + 8, PRODUCTS = FM * FN;
     u32x4 x[FM];
     uint32_t w[8], ws[8];
 };
@@ -391,7 +391,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 #pragma unroll
             for (int v = 0; v < Half::V; ++v) acc[f][q][v] = 0.f;
     const uint8_t* const lds = (const uint8_t*)mx_lds;
-    auto read = [&](int s, auto part, Half& o) {
+    // read k (of Half::STEPS) of part h of stage s: one fragment, with its scale
+    auto read_one = [&](int s, auto part, Half& o, int k) {
         constexpr int h = decltype(part)::value;
         const int xb = (s % R) * G::STAGE * 16, wb = xb + G::X * 16, ks = s / PA;
         if constexpr (MODE == MX_GEMM) {
@@ -402,155 +403,130 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             // an odd number of 128s ends in half a stage: its other half has zeros of x against
             // the next row's weights, whose scales must not be NaN
             const bool past = KS > 1 && 4 * kk >= 2 * KS && 64 * KS * ks + 64 * kk >= p.kpad;
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                const int row = wn * TN + 32 * f + r;
-                o.w[f] = *(const u32x2*)(lds + wb + row * (16 * G::WSPR) + 16 * wc + 8 * hh);
+            if (k < FN) {
+                const int row = wn * TN + 32 * k + r;
+                o.w[k] = *(const u32x2*)(lds + wb + row * (16 * G::WSPR) + 16 * wc + 8 * hh);
                 const uint32_t sc = lds[sb + row * 16];
-                o.ws[f] = past ? 127u : sc;
+                o.ws[k] = past ? 127u : sc;
+            } else {
+                const int q = (k - FN) / 2, u = (k - FN) % 2;
+                o.x[q][u] = *(const u32x4*)(lds + xb + (wm * TM + 32 * q + r) * (16 * G::XSPR) + 16 * ((8 * (kk * G::PS + q0) + 4 * g + 2 * hh + u) ^ G::xswz(r)));
             }
-#pragma unroll
-            for (int q = 0; q < FM; ++q)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    o.x[q][u] = *(const u32x4*)(lds + xb + (wm * TM + 32 * q + r) * (16 * G::XSPR) + 16 * ((8 * (kk * G::PS + q0) + 4 * g + 2 * hh + u) ^ G::xswz(r)));
         } else if constexpr (MODE == MX_GEMM_MX) {
-            // lane (r, g): block 2 h + g of the stage's eight
+            // lane (r, g): block 2 h + g of the stage's eight; past an odd number of 128s as above
             const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 8 * (ks % SPAN) + 2 * h + g;
-#pragma unroll
-            for (int q = 0; q < FM; ++q) {
-                const int row = wm * TM + 32 * q + r;
-                o.x[q] = *(const u32x4*)(lds + xb + row * 128 + 16 * ((2 * h + g) ^ ((r >> 1) & 7)));
-                o.xs[q] = lds[sb + (BN + row) * 16];
-            }
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                const int row = wn * TN + 32 * f + r;
-                o.w[f] = *(const u32x4*)(lds + wb + row * 128 + 16 * ((2 * h + g) ^ ((r >> 1) & 7)));
-                o.ws[f] = lds[sb + row * 16];
-            }
-            if constexpr (h >= 2) {
-                // an odd number of 128s ends in half a stage: its other half has zero codes of
-                // x against the next row's weights, whose scales must not be NaN
-                const bool past = 256 * s + 128 >= p.kpad;
-#pragma unroll
-                for (int q = 0; q < FM; ++q) o.xs[q] = past ? 127u : o.xs[q];
-#pragma unroll
-                for (int f = 0; f < FN; ++f) o.ws[f] = past ? 127u : o.ws[f];
+            const bool past = h >= 2 && 256 * s + 128 >= p.kpad;
+            const bool isx = k < FM;
+            const int row = isx ? wm * TM + 32 * k + r : wn * TN + 32 * (k - FM) + r;
+            const u32x4 v = *(const u32x4*)(lds + (isx ? xb : wb) + row * 128 + 16 * ((2 * h + g) ^ ((r >> 1) & 7)));
+            const uint32_t sc = lds[sb + (isx ? BN + row : row) * 16];
+            if (isx) {
+                o.x[k] = v;
+                o.xs[k] = past ? 127u : sc;
+            } else {
+                o.w[k - FM] = v;
+                o.ws[k - FM] = past ? 127u : sc;
             }
         } else {
             // lane (r, g): rows 16 g + 8 h .. + 7 of the stage's 64, columns 8 r .. of the wave's 128
-            const int sb = wb + G::W * 16 + wn * 4 + (r >> 2);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 16 * g + 8 * h + i;
+            if (k < 8) {
+                const int sb = wb + G::W * 16 + wn * 4 + (r >> 2);
+                const int row = 16 * g + 8 * h + k;
                 if constexpr (BN == 256)
-                    o.w[i] = *(const uint32_t*)(lds + wb + (row ^ (g >> 1)) * 128 + 16 * ((wn * 4 + (r >> 2)) ^ (4 * (g & 1))) + 4 * (r & 3));
+                    o.w[k] = *(const uint32_t*)(lds + wb + (row ^ (g >> 1)) * 128 + 16 * ((wn * 4 + (r >> 2)) ^ (4 * (g & 1))) + 4 * (r & 3));
                 else
-                    o.w[i] = *(const uint32_t*)(lds + wb + (row ^ g) * 64 + 4 * r);
-                o.ws[i] = lds[sb + row * 16];
-            }
-#pragma unroll
-            for (int q = 0; q < FM; ++q)
+                    o.w[k] = *(const uint32_t*)(lds + wb + (row ^ g) * 64 + 4 * r);
+                o.ws[k] = lds[sb + row * 16];
+            } else {
+                const int q = k - 8;
                 o.x[q] = *(const u32x4*)(lds + xb + (wm * TM + 16 * q + r) * 128 + 16 * ((2 * g + h) ^ ((r >> 1) & 7)));
+            }
         }
     };
-    auto multiply = [&](const Half& o) {
+    auto read = [&](int s, auto part, Half& o) {
+#pragma unroll
+        for (int k = 0; k < Half::STEPS; ++k) read_one(s, part, o, k);
+    };
+    // product i (of Half::PRODUCTS) of a part; `a`: the dequantised weights of the last ones
+    u32x4 a[2];
+    auto product = [&](const Half& o, auto index) {
+        constexpr int i = decltype(index)::value;
         if constexpr (MODE == MX_GEMM) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int f = 0; f < FN; ++f) {
-                    const uint32_t w = o.w[f][u];
-                    const float sc = mx_scale(o.ws[f]);
-                    const u32x4 a{mx_bf16<0>(w, sc), mx_bf16<1>(w, sc), mx_bf16<2>(w, sc), mx_bf16<3>(w, sc)};
-#pragma unroll
-                    for (int q = 0; q < FM; ++q)
-                        acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(o.x[q][u]), acc[f][q], 0, 0, 0);
-                }
-        } else if constexpr (MODE == MX_GEMM_MX) {
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                const i32x8 a{(int)o.w[f][0], (int)o.w[f][1], (int)o.w[f][2], (int)o.w[f][3], 0, 0, 0, 0};
-#pragma unroll
-                for (int q = 0; q < FM; ++q) {
-                    const i32x8 b{(int)o.x[q][0], (int)o.x[q][1], (int)o.x[q][2], (int)o.x[q][3], 0, 0, 0, 0};
-                    acc[f][q] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[f][q], 4, 4, 0, (int)o.ws[f], 0, (int)o.xs[q]);
-                }
+            constexpr int u = i / (FM * FN), f = i / FM % FN, q = i % FM;
+            if constexpr (q == 0) {
+                const uint32_t w = o.w[f][u];
+                const float sc = mx_scale(o.ws[f]);
+                a[0] = u32x4{mx_bf16<0>(w, sc), mx_bf16<1>(w, sc), mx_bf16<2>(w, sc), mx_bf16<3>(w, sc)};
             }
+            acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a[0]), as_bf16x8(o.x[q][u]), acc[f][q], 0, 0, 0);
+        } else if constexpr (MODE == MX_GEMM_MX) {
+            constexpr int f = i / FM, q = i % FM;
+            const i32x8 w{(int)o.w[f][0], (int)o.w[f][1], (int)o.w[f][2], (int)o.w[f][3], 0, 0, 0, 0};
+            const i32x8 x{(int)o.x[q][0], (int)o.x[q][1], (int)o.x[q][2], (int)o.x[q][3], 0, 0, 0, 0};
+            acc[f][q] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc[f][q], 4, 4, 0, (int)o.ws[f], 0, (int)o.xs[q]);
         } else {
             // byte b of the words: columns 8 r + 2 b and 8 r + 2 b + 1
-            auto two = [&](auto byte) {
-                constexpr int b = decltype(byte)::value;
-                u32x4 lo, hi;
+            constexpr int b = i / (2 * FM), q = i / 2 % FM, odd = i % 2;
+            if constexpr (i % (2 * FM) == 0) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t u = mx_bf16<b>(o.w[2 * i], mx_scale(o.ws[2 * i]));
-                    const uint32_t v = mx_bf16<b>(o.w[2 * i + 1], mx_scale(o.ws[2 * i + 1]));
-                    lo[i] = __builtin_amdgcn_perm(v, u, 0x05040100u);
-                    hi[i] = __builtin_amdgcn_perm(v, u, 0x07060302u);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t u = mx_bf16<b>(o.w[2 * k], mx_scale(o.ws[2 * k]));
+                    const uint32_t v = mx_bf16<b>(o.w[2 * k + 1], mx_scale(o.ws[2 * k + 1]));
+                    a[0][k] = __builtin_amdgcn_perm(v, u, 0x05040100u);
+                    a[1][k] = __builtin_amdgcn_perm(v, u, 0x07060302u);
                 }
-#pragma unroll
-                for (int q = 0; q < FM; ++q) {
-                    acc[2 * b][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(lo), as_bf16x8(o.x[q]), acc[2 * b][q], 0, 0, 0);
-                    acc[2 * b + 1][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(hi), as_bf16x8(o.x[q]), acc[2 * b + 1][q], 0, 0, 0);
-                }
-            };
-            two(std::integral_constant<int, 0>{});
-            two(std::integral_constant<int, 1>{});
-            two(std::integral_constant<int, 2>{});
-            two(std::integral_constant<int, 3>{});
+            }
+            acc[2 * b + odd][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[odd]), as_bf16x8(o.x[q]), acc[2 * b + odd][q], 0, 0, 0);
         }
     };
-    // the order of a part's instructions: its reads (and LD loads) spread over the first
-    // products, so that they have arrived when the part ends
-    auto interleave = [&](auto loads) {
-        if constexpr (MODE == MX_GEMM_DX) return;      // (the transposes leave the scheduler no slack: 390 us ordered, 371 free)
-        constexpr int LD = decltype(loads)::value, RD = Half::READS, MM = Half::PRODUCTS;
-        constexpr int N = (MM + 1) / 2;
-        constexpr int PR = (RD + N - 1) / N;
+    // Products of `cur` while part `part` of stage s is read into `nxt` and loads l0 .. l1 - 1 of
+    // stage sl are issued: the reads beside the first products, so that they have arrived when
+    // the part ends, and the loads evenly, at the rate at which they are taken.
+    auto run = [&](const Half& cur, int s, auto part, Half& nxt, int sl, auto l0, auto l1) {
+        constexpr int MM = Half::PRODUCTS, L0 = decltype(l0)::value, LN = decltype(l1)::value - L0;
+        constexpr int RP = (2 * Half::STEPS + MM - 1) / MM;                   // reads beside a product
+        mx_each<MM>([&](auto index) {
+            constexpr int i = decltype(index)::value;
 #pragma unroll
-        for (int i = 0; i < MM; ++i) {
-            if (i < N) __builtin_amdgcn_sched_group_barrier(0x100, PR, 0);
-            if (LD > 0) __builtin_amdgcn_sched_group_barrier(0x020, (LD + MM - 1) / MM, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+            for (int k = RP * i; k < RP * (i + 1); ++k)
+                if (k < Half::STEPS) read_one(s, part, nxt, k);
+            product(cur, index);
+#pragma unroll
+            for (int l = i * LN / MM; l < (i + 1) * LN / MM; ++l) issue_one(sl, L0 + l);
+            if constexpr (MODE != MX_GEMM_DX) __builtin_amdgcn_sched_barrier(0);
+        });
     };
-    const std::integral_constant<int, 0> first{}, none{};
 
+    constexpr int ALL = XI + WI, LATE = MODE == MX_GEMM_MX ? ALL / 2 : 0, SOON = ALL - LATE;
+    const std::integral_constant<int, 0> zero{};
+    const std::integral_constant<int, SOON> soon{};
+    const std::integral_constant<int, ALL> all{};
     if (s_lo < s_hi) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) issue(s_lo + i);
-        mx_wait_vmcnt<LOADS * (R - 1)>();
+        for (int i = 0; i < R - 1; ++i) issue(s_lo + i);
+        issue_scales(s_lo + R - 1);
+#pragma unroll
+        for (int i = 0; i < SOON; ++i) issue_one(s_lo + R - 1, i);
+        mx_wait_vmcnt<LOADS * (R - 2) + LOADS - LATE>();
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         Half A, B;
-        read(s_lo, first, A);
+        read(s_lo, zero, A);
         for (int s = s_lo; s < s_hi; ++s) {
+            // the rest of the last stage's loads go out with the first part
+            run(A, s, std::integral_constant<int, 1>{}, B, s + R - 1, soon, all);
             mx_each<G::PARTS / 2 - 1>([&](auto i) {
                 constexpr int h = 2 * decltype(i)::value;
-                read(s, std::integral_constant<int, h + 1>{}, B);
-                multiply(A);
-                interleave(none);
-                read(s, std::integral_constant<int, h + 2>{}, A);
-                multiply(B);
-                interleave(none);
+                run(B, s, std::integral_constant<int, h + 2>{}, A, 0, zero, zero);
+                run(A, s, std::integral_constant<int, h + 3>{}, B, 0, zero, zero);
             });
-            read(s, std::integral_constant<int, G::PARTS - 1>{}, B);
-            multiply(A);
-            interleave(none);
             mx_wait_vmcnt<LOADS * (R - 2)>();    // stage s + 1 has landed
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_barrier();        // and this one's slot has been read by every wave
             __builtin_amdgcn_sched_barrier(0);
             issue_scales(s + R);
-#pragma unroll
-            for (int i = 0; i < XI + WI; ++i) issue_one(s + R, i);
-            read(s + 1, first, A);               // past the last stage: read and not used
-            multiply(B);
-            interleave(std::integral_constant<int, XI + WI>{});
+            run(B, s + 1, zero, A, s + R, zero, soon);       // past the last stage: read and not used
         }
     }
     mx_wait_vmcnt<0>();          // no load into this block's LDS may land after it ends
@@ -802,10 +778,13 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
         P.unit = op == MX_GEMM_DX ? P.planes : (op == MX_GEMM_MX || deep ? 2 : 8 * P.planes);
         units = (P.stages + P.unit - 1) / P.unit;
     }
+    if (units < 1) units = 1;
     if (blocks < 256) {
-        int64_t s = 512 / blocks;
+        int64_t s = (P.stream ? 512 : 256) / blocks;
         s = s < units ? s : units;
-        P.split = (int)(s < 1 ? 1 : (s > 16 ? 16 : s));
+        s = s < 1 ? 1 : (s > 16 ? 16 : s);
+        const int64_t each = (units + s - 1) / s;        // no part without work
+        P.split = (int)((units + each - 1) / each);
     }
     P.part_bytes = P.split > 1 ? mx_al256((size_t)P.split * n * m * 4) : 0;
     return P;

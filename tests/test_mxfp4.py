@@ -65,6 +65,21 @@ def test_sizes():
     assert gq.mxfp4_gemm_dx_workspace_size(8, 4096, 4096, 0) == 0
 
 
+def test_workspaces_over_the_sizes():
+    """Every size has a plan (the host's arithmetic alone), small ones and float32 ones too."""
+    for n in (1, 2, 15, 16, 17, 33, 64, 65, 129, 1000, 100000):
+        for d_in in (1, 31, 128, 129, 1000, 1 << 20):
+            for d_out in (1, 16, 1000, 70000):
+                for experts in (1, 3, 4096):
+                    for dt in (gq.GQ_BF16, gq.GQ_F32):
+                        a = gq.mxfp4_gemm_workspace_size(n, d_in, d_out, experts, dt)
+                        b = gq.mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts, dt)
+                        assert a % 256 == 0 and b % 256 == 0
+                        if dt == gq.GQ_F32:          # three planes of two bytes
+                            assert a >= 6 * n * d_in and b >= 6 * n * d_out
+                    assert gq.mxfp4_gemm_mx_workspace_size(n, d_in, d_out, experts) % 256 == 0
+
+
 def _err():
     return gq.library().gq_last_error().decode()
 

@@ -21,25 +21,49 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void k_mx_stage(const void* __restrict__ x, int64_t n, int64_t k,
                                                  int64_t pieces, uint16_t* __restrict__ out) {
     constexpr int P = BF16 ? 1 : 3;
-    const int64_t total = n * pieces * 64;
+    // a lane takes 8 values; 8 lanes a piece
+    const int64_t total = n * pieces * 8;
+    const bool vec = !BF16 && k % 4 == 0 && ((uintptr_t)x & 15u) == 0;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
-        const int64_t piece = t >> 6, r = piece / pieces;
-        const int64_t i = (piece - r * pieces) * 64 + (t & 63);
-        uint16_t* o = out + piece * P * 64 + (t & 63);
+        const int64_t piece = t >> 3, r = piece / pieces;
+        const int64_t i = (piece - r * pieces) * 64 + (t & 7) * 8, at = r * k + i;
+        u32x4* o = (u32x4*)(out + piece * P * 64 + (t & 7) * 8);
         if constexpr (BF16) {
-            o[0] = i < k ? ((const uint16_t*)x)[r * k + i] : (uint16_t)0;
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = i + 2 * e < k ? ((const uint16_t*)x)[at + 2 * e] : 0u;
+                const uint32_t hi = i + 2 * e + 1 < k ? ((const uint16_t*)x)[at + 2 * e + 1] : 0u;
+                w[e] = lo | (hi << 16);
+            }
+            o[0] = w;
         } else {
-            const float v = i < k ? ((const float*)x)[r * k + i] : 0.f;
-            const uint32_t b = __float_as_uint(v);
-            uint32_t h = b & 0xffff0000u;
-            float rest = 0.f;
-            if ((b & 0x7f800000u) != 0x7f800000u) rest = v - __uint_as_float(h);
-            else if (b & 0x007fffffu) h |= 0x00400000u;            // a NaN stays one
-            const uint32_t m = __float_as_uint(rest) & 0xffff0000u;
-            const float low = rest - __uint_as_float(m);
-            o[0] = (uint16_t)(h >> 16);
-            o[64] = (uint16_t)(m >> 16);
-            o[128] = (uint16_t)(__float_as_uint(low) >> 16);
+            float v[8];
+            if (vec && i + 8 <= k) {
+                const f32x4 a = *(const f32x4*)((const float*)x + at), b = *(const f32x4*)((const float*)x + at + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = i + e < k ? ((const float*)x)[at + e] : 0.f;
+            }
+            uint32_t w[3][8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t b = __float_as_uint(v[e]);
+                uint32_t h = b & 0xffff0000u;
+                float rest = 0.f;
+                if ((b & 0x7f800000u) != 0x7f800000u) rest = v[e] - __uint_as_float(h);
+                else if (b & 0x007fffffu) h |= 0x00400000u;            // a NaN stays one
+                const uint32_t m = __float_as_uint(rest) & 0xffff0000u;
+                w[0][e] = h >> 16;
+                w[1][e] = m >> 16;
+                w[2][e] = __float_as_uint(rest - __uint_as_float(m)) >> 16;
+            }
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+                o[8 * q] = u32x4{w[q][0] | (w[q][1] << 16), w[q][2] | (w[q][3] << 16),
+                                 w[q][4] | (w[q][5] << 16), w[q][6] | (w[q][7] << 16)};
         }
     }
 }
@@ -197,7 +221,7 @@ __device__ __forceinline__ void mx_store(const MxTile& p, float* part, int64_t a
 
 // Geometry of a stage in 16-byte LDS slots.  KS (MX_GEMM): pieces of 64 values a stage.  With
 // one, the planes of float32 activations are stages of their own (and the weight is read for
-// each); with four, a stage holds them all.
+// each); with more, a stage holds them all.
 template <int MODE, int P, int BM, int BN, int KS>
 struct MxGeo {
     static constexpr int RING = MODE == MX_GEMM_MX ? (BM >= 128 ? 2 : 3) : (KS > 1 ? 2 : (BM * BN > 128 * 128 ? 3 : 4));
@@ -216,6 +240,9 @@ struct MxGeo {
     static constexpr size_t BYTES = (size_t)(RING * STAGE + 3 * SROWS) * 16;
     // a row's chunks are moved about so that the 16 rows of a fragment read spread over the banks
     static __device__ __forceinline__ int xswz(int row) { return KS > 1 ? row & 15 : (row >> 1) & 7; }
+    static __device__ __forceinline__ int wswz(int row) {          // (of MX_GEMM)
+        return KS == 4 ? (row >> 1) & 7 : (KS == 2 ? (row >> 2) & 3 : (row >> 3) & 1);
+    }
 };
 
 // f(integral_constant 0) .. f(integral_constant N - 1)
@@ -306,7 +333,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     for (int i = 0; i < WI; ++i) {
         const int slot = wave * WPW + i * 64 + lane;
         int row = slot / G::WSPR, c = slot % G::WSPR;
-        if constexpr (MODE == MX_GEMM) c ^= KS > 1 ? (row >> 1) & 7 : (row >> 3) & 1;
+        if constexpr (MODE == MX_GEMM) c ^= G::wswz(row);
         if constexpr (MODE == MX_GEMM_MX) c ^= (row >> 1) & 7;
         if constexpr (MODE == MX_GEMM_DX && BN == 256) {
             row ^= (row >> 5) & 1;
@@ -399,10 +426,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             // part h: values 16 hh .. of the 32 that lane (r, g) has of piece kk, in plane q
             constexpr int kk = h / (2 * G::PS), q0 = h / 2 % G::PS, hh = h % 2;
             const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 2 * KS * (ks % SPAN) + 2 * kk + g;
-            const int wc = KS > 1 ? (2 * kk + g) ^ ((r >> 1) & 7) : g ^ ((r >> 3) & 1);
+            const int wc = (2 * kk + g) ^ G::wswz(r);
             // an odd number of 128s ends in half a stage: its other half has zeros of x against
             // the next row's weights, whose scales must not be NaN
-            const bool past = KS > 1 && 4 * kk >= 2 * KS && 64 * KS * ks + 64 * kk >= p.kpad;
+            const bool past = KS == 4 && kk >= 2 && 256 * ks + 128 >= p.kpad;
             if (k < FN) {
                 const int row = wn * TN + 32 * k + r;
                 o.w[k] = *(const u32x2*)(lds + wb + row * (16 * G::WSPR) + 16 * wc + 8 * hh);
@@ -767,15 +794,20 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
         blocks = live * ((m + P.bn - 1) / P.bn);
         units /= P.waves;
     } else {
-        P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 ? 64 : 32));
-        P.bn = P.bm == 256 ? 256 : 128;
-        if (op == MX_GEMM_DX && P.bm == 32) P.bm = 64;
-        const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;
-        blocks = rows * ((m + P.bn - 1) / P.bn);
-        // few rows of x: stages of 256 values, so that a weight row is read by whole lines
-        const bool deep = op == MX_GEMM && (P.bm == 32 || (P.bm == 64 && P.planes == 1));
-        P.stages = (int)(op == MX_GEMM_MX || deep ? (mx_groups(k) + 1) / 2 : k64 * P.planes);
-        P.unit = op == MX_GEMM_DX ? P.planes : (op == MX_GEMM_MX || deep ? 2 : 8 * P.planes);
+        // the largest tile that the rows of a weight fill and that gives most compute units
+        // one, else the smallest of them
+        P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 || op == MX_GEMM_DX ? 64 : 32));
+        for (;; P.bm /= 2) {
+            P.bn = P.bm == 256 ? 256 : 128;
+            const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;
+            blocks = rows * ((m + P.bn - 1) / P.bn);
+            if (P.bm <= 64 || blocks >= 192) break;
+        }
+        // few rows of x: stages of 256 (128: three planes of them) values, so that a weight row
+        // is read by whole lines
+        const int deep = op != MX_GEMM || P.bm > 64 ? 1 : (P.bm == 64 && P.planes == 3 ? 2 : 4);
+        P.stages = (int)(op == MX_GEMM_MX ? (mx_groups(k) + 1) / 2 : (deep == 1 ? k64 * P.planes : (k64 + deep - 1) / deep));
+        P.unit = op == MX_GEMM_DX ? P.planes : (op == MX_GEMM_MX ? 2 : (deep == 1 ? 8 * P.planes : 8 / deep));
         units = (P.stages + P.unit - 1) / P.unit;
     }
     if (units < 1) units = 1;
@@ -842,7 +874,7 @@ static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t 
                 if constexpr (MODE == MX_GEMM_MX) return mx_launch<MODE, P, 256, 256, 2>(t, pl.split, st);
                 else return mx_launch<MODE, P, 256, 256, 4, 8>(t, pl.split, st);
             case 128: return mx_launch<MODE, P, 128, 128, 2>(t, pl.split, st);
-            case 64: return mx_launch<MODE, P, 64, 128, 1, 4, MODE == MX_GEMM && P == 1 ? 4 : 1>(t, pl.split, st);
+            case 64: return mx_launch<MODE, P, 64, 128, 1, 4, MODE == MX_GEMM ? (P == 1 ? 4 : 2) : 1>(t, pl.split, st);
             default: return mx_launch<MODE, P, 32, 128, 1, 4, MODE == MX_GEMM ? 4 : 1>(t, pl.split, st);
         }
     }
@@ -860,7 +892,7 @@ hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
         const int64_t pieces = c.op == MX_GEMM_DX ? (k + 63) / 64 : 2 * mx_groups(k);
         t.A = (const uint8_t*)ws;
         t.a_row = t.a_bytes = pieces * pl.planes * 128;
-        const int64_t blocks = (c.n * pieces * 64 + 255) / 256;
+        const int64_t blocks = (c.n * pieces * 8 + 255) / 256;
         const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
         if (c.a_bf16) hipLaunchKernelGGL(k_mx_stage<true>, grid, dim3(256), 0, st, c.a, c.n, k, pieces, (uint16_t*)ws);
         else hipLaunchKernelGGL(k_mx_stage<false>, grid, dim3(256), 0, st, c.a, c.n, k, pieces, (uint16_t*)ws);

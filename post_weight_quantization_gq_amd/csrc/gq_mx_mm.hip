@@ -267,7 +267,6 @@ template <int FM, int FN> struct MxHalf<MX_GEMM_MX, FM, FN> {
     typedef f32x16 Acc;
     static constexpr int T = 32, V = 16, STEPS = FM + FN, PRODUCTS = FM * FN;
     u32x4 x[FM], w[FN];
-    uint32_t xs[FM], ws[FN];
 };
 template <int FM, int FN> struct MxHalf<MX_GEMM_DX, FM, FN> {
     typedef f32x4 Acc;
@@ -418,6 +417,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 #pragma unroll
             for (int v = 0; v < Half::V; ++v) acc[f][q][v] = 0.f;
     const uint8_t* const lds = (const uint8_t*)mx_lds;
+    // MX_GEMM_MX: a row's eight scale bytes of a stage, and the two words that this lane's four
+    // are bytes 0 and 2 of (block 2 h + g: word h / 2, byte 2 (h % 2)), which the products select
+    u32x2 raw[MODE == MX_GEMM_MX ? FM + FN : 1];
+    uint32_t scale[MODE == MX_GEMM_MX ? FM + FN : 1][2];
+    auto take_scales = [&](int s) {
+        if constexpr (MODE == MX_GEMM_MX) {
+            // a contraction of an odd number of 128s ends in half a stage: its other half has
+            // zeros of x against the next row's weights, whose scales must not be NaN
+            const bool past = 256 * s + 128 >= p.kpad;
+#pragma unroll
+            for (int k = 0; k < FM + FN; ++k) {
+                scale[k][0] = __builtin_amdgcn_alignbit(raw[k][1], raw[k][0], 8 * g);
+                scale[k][1] = past ? 0x7f7f7f7fu : raw[k][1] >> (8 * g);
+            }
+        }
+    };
     // read k (of Half::STEPS) of part h of stage s: one fragment, with its scale
     auto read_one = [&](int s, auto part, Half& o, int k) {
         constexpr int h = decltype(part)::value;
@@ -440,20 +455,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
                 o.x[q][u] = *(const u32x4*)(lds + xb + (wm * TM + 32 * q + r) * (16 * G::XSPR) + 16 * ((8 * (kk * G::PS + q0) + 4 * g + 2 * hh + u) ^ G::xswz(r)));
             }
         } else if constexpr (MODE == MX_GEMM_MX) {
-            // lane (r, g): block 2 h + g of the stage's eight; past an odd number of 128s as above
-            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 8 * (ks % SPAN) + 2 * h + g;
-            const bool past = h >= 2 && 256 * s + 128 >= p.kpad;
+            // lane (r, g): block 2 h + g of the stage's eight; with the first part, all eight scales
             const bool isx = k < FM;
             const int row = isx ? wm * TM + 32 * k + r : wn * TN + 32 * (k - FM) + r;
             const u32x4 v = *(const u32x4*)(lds + (isx ? xb : wb) + row * 128 + 16 * ((2 * h + g) ^ ((r >> 1) & 7)));
-            const uint32_t sc = lds[sb + (isx ? BN + row : row) * 16];
-            if (isx) {
-                o.x[k] = v;
-                o.xs[k] = past ? 127u : sc;
-            } else {
-                o.w[k - FM] = v;
-                o.ws[k - FM] = past ? 127u : sc;
-            }
+            if (isx) o.x[k] = v;
+            else o.w[k - FM] = v;
+            if constexpr (h == 0)
+                raw[k] = *(const u32x2*)(lds + (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS + (isx ? BN + row : row)) * 16 + 8 * (ks % SPAN));
         } else {
             // lane (r, g): rows 16 g + 8 h .. + 7 of the stage's 64, columns 8 r .. of the wave's 128
             if (k < 8) {
@@ -476,7 +485,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     };
     // product i (of Half::PRODUCTS) of a part; `a`: the dequantised weights of the last ones
     u32x4 a[2];
-    auto product = [&](const Half& o, auto index) {
+    auto product = [&](const Half& o, auto part, auto index) {
         constexpr int i = decltype(index)::value;
         if constexpr (MODE == MX_GEMM) {
             constexpr int u = i / (FM * FN), f = i / FM % FN, q = i % FM;
@@ -490,7 +499,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             constexpr int f = i / FM, q = i % FM;
             const i32x8 w{(int)o.w[f][0], (int)o.w[f][1], (int)o.w[f][2], (int)o.w[f][3], 0, 0, 0, 0};
             const i32x8 x{(int)o.x[q][0], (int)o.x[q][1], (int)o.x[q][2], (int)o.x[q][3], 0, 0, 0, 0};
-            acc[f][q] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc[f][q], 4, 4, 0, (int)o.ws[f], 0, (int)o.xs[q]);
+            constexpr int h = decltype(part)::value, byte = 2 * (h % 2);
+            acc[f][q] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc[f][q], 4, 4, byte, (int)scale[FM + f][h / 2], byte, (int)scale[q][h / 2]);
         } else {
             // byte b of the words: columns 8 r + 2 b and 8 r + 2 b + 1
             constexpr int b = i / (2 * FM), q = i / 2 % FM, odd = i % 2;
@@ -506,10 +516,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             acc[2 * b + odd][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[odd]), as_bf16x8(o.x[q]), acc[2 * b + odd][q], 0, 0, 0);
         }
     };
-    // Products of `cur` while part `part` of stage s is read into `nxt` and loads l0 .. l1 - 1 of
+    // Products of `cur` (part `own`) while part `part` of stage s is read into `nxt` and loads l0 .. l1 - 1 of
     // stage sl are issued: the reads beside the first products, so that they have arrived when
     // the part ends, and the loads evenly, at the rate at which they are taken.
-    auto run = [&](const Half& cur, int s, auto part, Half& nxt, int sl, auto l0, auto l1) {
+    auto run = [&](const Half& cur, auto own, int s, auto part, Half& nxt, int sl, auto l0, auto l1) {
         constexpr int MM = Half::PRODUCTS, L0 = decltype(l0)::value, LN = decltype(l1)::value - L0;
         constexpr int RP = (2 * Half::STEPS + MM - 1) / MM;                   // reads beside a product
         mx_each<MM>([&](auto index) {
@@ -517,7 +527,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 #pragma unroll
             for (int k = RP * i; k < RP * (i + 1); ++k)
                 if (k < Half::STEPS) read_one(s, part, nxt, k);
-            product(cur, index);
+            product(cur, own, index);
 #pragma unroll
             for (int l = i * LN / MM; l < (i + 1) * LN / MM; ++l) issue_one(sl, L0 + l);
             if constexpr (MODE != MX_GEMM_DX) __builtin_amdgcn_sched_barrier(0);
@@ -540,20 +550,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         __builtin_amdgcn_sched_barrier(0);
         Half A, B;
         read(s_lo, zero, A);
+        take_scales(s_lo);
         for (int s = s_lo; s < s_hi; ++s) {
             // the rest of the last stage's loads go out with the first part
-            run(A, s, std::integral_constant<int, 1>{}, B, s + R - 1, soon, all);
+            run(A, zero, s, std::integral_constant<int, 1>{}, B, s + R - 1, soon, all);
             mx_each<G::PARTS / 2 - 1>([&](auto i) {
                 constexpr int h = 2 * decltype(i)::value;
-                run(B, s, std::integral_constant<int, h + 2>{}, A, 0, zero, zero);
-                run(A, s, std::integral_constant<int, h + 3>{}, B, 0, zero, zero);
+                run(B, std::integral_constant<int, h + 1>{}, s, std::integral_constant<int, h + 2>{}, A, 0, zero, zero);
+                run(A, std::integral_constant<int, h + 2>{}, s, std::integral_constant<int, h + 3>{}, B, 0, zero, zero);
             });
             mx_wait_vmcnt<LOADS * (R - 2)>();    // stage s + 1 has landed
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_barrier();        // and this one's slot has been read by every wave
             __builtin_amdgcn_sched_barrier(0);
             issue_scales(s + R);
-            run(B, s + 1, zero, A, s + R, zero, soon);       // past the last stage: read and not used
+            run(B, std::integral_constant<int, G::PARTS - 1>{}, s + 1, zero, A, s + R, zero, soon);  // past the last stage: read and not used
+            take_scales(s + 1);
         }
     }
     mx_wait_vmcnt<0>();          // no load into this block's LDS may land after it ends

@@ -85,7 +85,7 @@ struct MxTile {
     int kpad;                     // its length padded to whole groups (MX_GEMM, MX_GEMM_MX)
     int unit;                     // a split's range is a multiple of this many stages
     void* y;
-    int y_bf16, y_vec;            // y_vec: runs of 4 (MODE 2: 8) outputs may be stored whole
+    int y_bf16, y_vec;            // y_vec: rows of outputs (parts) start and end at 16-byte borders
     float* part;                  // partial sums [split][n][m], or null
 };
 
@@ -186,37 +186,6 @@ __device__ __forceinline__ MxPlace mx_place(const MxTile& p, int bm, int ncol) {
     r.rows = p.n - r.t0 < bm ? p.n - r.t0 : bm;
     r.ok = true;
     return r;
-}
-
-// N consecutive outputs from column j of a row of m (at: their index)
-template <int N>
-__device__ __forceinline__ void mx_store(const MxTile& p, float* part, int64_t at, int64_t j,
-                                         const float (&v)[N]) {
-    const bool whole = j + N <= p.m;
-    if (part || !p.y_bf16) {
-        float* o = (part ? part : (float*)p.y) + at;
-        if (whole && p.y_vec) {
-#pragma unroll
-            for (int k = 0; k < N; k += 4) *(f32x4*)(o + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (j + k < p.m) o[k] = v[k];
-        }
-    } else {
-        uint16_t* o = (uint16_t*)p.y + at;
-        if (whole && p.y_vec) {
-            if constexpr (N == 4)
-                *(u32x2*)o = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-            else
-                *(u32x4*)o = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (j + k < p.m) o[k] = (uint16_t)f32_to_bf16_bits(v[k]);
-        }
-    }
 }
 
 // Geometry of a stage in 16-byte LDS slots.  KS (MX_GEMM): pieces of 64 values a stage.  With
@@ -568,34 +537,55 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             take_scales(s + 1);
         }
     }
-    mx_wait_vmcnt<0>();          // no load into this block's LDS may land after it ends
+    mx_wait_vmcnt<0>();          // no load may land in the LDS later
+    __syncthreads();
 
-    // ---- store.  16 x 16 products: lane (r, g) holds row r and columns 4 g + v; 32 x 32:
-    // row r and columns 8 (v / 4) + 4 g + v % 4.  The gradient's fragment f is column 8 c + f.
-    float* part = p.part ? p.part + (int64_t)blockIdx.y * p.n * p.m : nullptr;
+    // ---- store, T rows of a wave's tile at a time, by way of LDS of its own: in the
+    // accumulators a lane's neighbours are other rows, in memory they are a row's columns.
+    // 16 x 16 products: lane (r, g) holds row r and columns 4 g + v (the gradient's fragment f:
+    // column 8 c + f); 32 x 32: row r and columns 8 (v / 4) + 4 g + v % 4.
+    float* const part = p.part ? p.part + (int64_t)blockIdx.y * p.n * p.m : nullptr;
+    const int wide = part || !p.y_bf16 ? 4 : 2, pitch = TN * wide + 16;
+    uint8_t* const own = (uint8_t*)mx_lds + wave * (T * (TN * 4 + 16));
+    uint8_t* const out = part ? (uint8_t*)part : (uint8_t*)p.y;
+    auto put = [&](int col, f32x4 v) {           // four columns of row r
+        if (wide == 4) *(f32x4*)(own + r * pitch + 4 * col) = v;
+        else *(u32x2*)(own + r * pitch + 2 * col) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    };
+    const int64_t jw = j0 + wn * TN;
+    const int cols = (int)(p.m - jw < TN ? p.m - jw : TN);        // can be negative
 #pragma unroll
     for (int q = 0; q < FM; ++q) {
-        const int row = wm * TM + Half::T * q + r;
-        if (row >= at.rows) continue;
-        const int64_t base = (at.t0 + row) * p.m;
         if constexpr (MODE == MX_GEMM_DX) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t j = j0 + wn * TN + 8 * (4 * g + v);
-                float o[8];
+            for (int v = 0; v < 4; ++v)
 #pragma unroll
-                for (int f = 0; f < 8; ++f) o[f] = acc[f][q][v];
-                if (j < p.m) mx_store<8>(p, part, base + j, j, o);
-            }
+                for (int f = 0; f < 8; f += 4)
+                    put(8 * (4 * g + v) + f, f32x4{acc[f][q][v], acc[f + 1][q][v], acc[f + 2][q][v], acc[f + 3][q][v]});
         } else {
 #pragma unroll
             for (int f = 0; f < FN; ++f)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int64_t j = j0 + wn * TN + 32 * f + 8 * v + 4 * g;
-                    const float o[4] = {acc[f][q][4 * v], acc[f][q][4 * v + 1], acc[f][q][4 * v + 2], acc[f][q][4 * v + 3]};
-                    if (j < p.m) mx_store<4>(p, part, base + j, j, o);
-                }
+                for (int v = 0; v < 16; v += 4)
+                    put(32 * f + 2 * v + 4 * g, f32x4{acc[f][q][v], acc[f][q][v + 1], acc[f][q][v + 2], acc[f][q][v + 3]});
+        }
+        const int row0 = wm * TM + T * q, left = (int)at.rows - row0;
+        if (p.y_vec) {
+            const int lanes = TN * wide / 16;                    // of a row: a power of two
+            for (int i = lane; i < T * lanes; i += 64) {
+                const int row = i / lanes, b = 16 * (i - row * lanes);
+                const u32x4 v = *(const u32x4*)(own + row * pitch + b);
+                if (row < left && b < cols * wide)
+                    *(u32x4*)(out + ((at.t0 + row0 + row) * p.m + jw) * wide + b) = v;
+            }
+        } else {
+            for (int i = lane; i < T * TN; i += 64) {
+                const int row = i / TN, c = i - row * TN;
+                if (row >= left || c >= cols) continue;
+                const int64_t to = (at.t0 + row0 + row) * p.m + jw + c;
+                if (wide == 4) ((float*)out)[to] = *(const float*)(own + row * pitch + 4 * c);
+                else ((uint16_t*)out)[to] = *(const uint16_t*)(own + row * pitch + 2 * c);
+            }
         }
     }
 }
@@ -842,7 +832,11 @@ size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t 
 template <int MODE, int P, int BM, int BN, int WM, int NW = 4, int KS = 1>
 static hipError_t mx_launch(const MxTile& t, int split, hipStream_t st) {
     const void* k = (const void*)k_mx_tile<MODE, P, BM, BN, WM, NW, KS>;
-    const size_t lds = MxGeo<MODE, P, BM, BN, KS>::BYTES;
+    // the stages and scales, later the outputs on their way
+    constexpr int T = MODE == MX_GEMM_DX ? 16 : 32, TN = BN / (NW / WM);
+    constexpr size_t OUT = (size_t)NW * T * (TN * 4 + 16), IN = MxGeo<MODE, P, BM, BN, KS>::BYTES;
+    constexpr size_t lds = IN > OUT ? IN : OUT;
+    static_assert(lds <= 160 * 1024, "LDS of a compute unit");
     hipError_t e = ensure_dynamic_lds(k, lds);
     if (e != hipSuccess) return e;
     const int64_t rows = (t.n + BM - 1) / BM + (t.offsets ? t.experts : 0);
@@ -924,10 +918,8 @@ hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
     t.unit = pl.unit;
     t.y = c.y;
     t.y_bf16 = c.y_bf16;
-    const int run = c.op == MX_GEMM_DX ? 8 : 4;
     t.part = pl.split > 1 ? (float*)((char*)ws + pl.stage_bytes) : nullptr;
-    // a run's vector stores: whole runs in every row, and an aligned base (float32 runs go by 4)
-    t.y_vec = m % run == 0 && (t.part || ((uintptr_t)c.y & (c.y_bf16 ? 2u * run - 1u : 15u)) == 0);
+    t.y_vec = t.part ? m % 4 == 0 : m % (c.y_bf16 ? 8 : 4) == 0 && ((uintptr_t)c.y & 15u) == 0;
     hipError_t e;
     switch (c.op) {
         case MX_GEMM: e = pl.planes == 1 ? mx_launch_size<MX_GEMM, 1>(t, pl, st) : mx_launch_size<MX_GEMM, 3>(t, pl, st); break;

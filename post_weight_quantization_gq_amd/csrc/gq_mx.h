@@ -18,10 +18,9 @@ __device__ __forceinline__ uint32_t mx_bf16(uint32_t q, float scale) {
     return __builtin_bit_cast(uint32_t, r);
 }
 
-// a code's value (scale 1)
-__device__ __forceinline__ float mx_value(uint32_t q) {
-    const float m = (q & 4u) ? (float)(2u + (q & 1u)) * ((q & 2u) ? 2.f : 1.f) : 0.5f * (float)(q & 3u);
-    return (q & 8u) ? -m : m;
+// a / b for a, b >= 0: 64-bit division is some hundred instructions, and few sizes need it
+__device__ __forceinline__ int64_t mx_div(int64_t a, int64_t b) {
+    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 }  // namespace gq

@@ -40,7 +40,9 @@ __device__ __forceinline__ void mx_load8(const void* p, int64_t row0, int64_t i,
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = i + k < d ? load_elem<BF16>(p, row0 + i + k) : 0.f;
+        for (int k = 0; k < 8; ++k) v[k] = load_elem<BF16>(p, i + k < d ? row0 + i + k : row0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = i + k < d ? v[k] : 0.f;
     }
 }
 
@@ -51,7 +53,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ x,
                                                     uint8_t* __restrict__ S) {
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (t >= pieces) return;             // pieces is a multiple of 16: blocks stay whole
-    const int64_t r = t / ppr;
+    const int64_t r = mx_div(t, ppr);
     const int64_t i = (t - r * ppr) * 8;
     float v[8];
     mx_load8<BF16, VEC>(x, r * d, i, d, v);
@@ -88,7 +90,7 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const uint32_t* __restric
                                                       void* __restrict__ y) {
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (t >= pieces) return;
-    const int64_t r = t / ppr;
+    const int64_t r = mx_div(t, ppr);
     const int64_t i = (t - r * ppr) * 8;
     if (i >= d) return;
     const uint32_t q = Q[t];

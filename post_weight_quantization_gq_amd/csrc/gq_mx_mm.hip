@@ -25,16 +25,17 @@ __global__ __launch_bounds__(256) void k_mx_stage(const void* __restrict__ x, in
     const int64_t total = n * pieces * 8;
     const bool vec = !BF16 && k % 4 == 0 && ((uintptr_t)x & 15u) == 0;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
-        const int64_t piece = t >> 3, r = piece / pieces;
+        const int64_t piece = t >> 3, r = mx_div(piece, pieces);
         const int64_t i = (piece - r * pieces) * 64 + (t & 7) * 8, at = r * k + i;
         u32x4* o = (u32x4*)(out + piece * P * 64 + (t & 7) * 8);
         if constexpr (BF16) {
             u32x4 w;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = i + 2 * e < k ? ((const uint16_t*)x)[at + 2 * e] : 0u;
-                const uint32_t hi = i + 2 * e + 1 < k ? ((const uint16_t*)x)[at + 2 * e + 1] : 0u;
-                w[e] = lo | (hi << 16);
+                // (loaded without a condition: past the row, the row's first value)
+                const uint32_t lo = ((const uint16_t*)x)[i + 2 * e < k ? at + 2 * e : r * k];
+                const uint32_t hi = ((const uint16_t*)x)[i + 2 * e + 1 < k ? at + 2 * e + 1 : r * k];
+                w[e] = (i + 2 * e < k ? lo : 0u) | (i + 2 * e + 1 < k ? hi << 16 : 0u);
             }
             o[0] = w;
         } else {
@@ -45,7 +46,9 @@ __global__ __launch_bounds__(256) void k_mx_stage(const void* __restrict__ x, in
                 for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = i + e < k ? ((const float*)x)[at + e] : 0.f;
+                for (int e = 0; e < 8; ++e) v[e] = ((const float*)x)[i + e < k ? at + e : r * k];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = i + e < k ? v[e] : 0.f;
             }
             uint32_t w[3][8];
 #pragma unroll

@@ -803,10 +803,10 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
         // one, else the smallest of them
         P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 || op == MX_GEMM_DX ? 64 : 32));
         for (;; P.bm /= 2) {
-            P.bn = P.bm == 256 ? 256 : 128;
+            P.bn = P.bm == 256 || op == MX_GEMM_DX ? 256 : 128;
             const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;
             blocks = rows * ((m + P.bn - 1) / P.bn);
-            if (P.bm <= 64 || blocks >= 192) break;
+            if (P.bm <= 64 || blocks >= (op == MX_GEMM_DX ? 48 : 192)) break;
         }
         // few rows of x: stages of 256 (128: three planes of them) values, so that a weight row
         // is read by whole lines
@@ -874,8 +874,8 @@ static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t 
     if constexpr (MODE == MX_GEMM_DX) {
         switch (pl.bm) {
             case 256: return mx_launch<MODE, P, 256, 256, 4, 8>(t, pl.split, st);
-            case 128: return mx_launch<MODE, P, 128, 128, 4>(t, pl.split, st);
-            default: return mx_launch<MODE, P, 64, 128, 4>(t, pl.split, st);
+            case 128: return mx_launch<MODE, P, 128, 256, 4, 8>(t, pl.split, st);
+            default: return mx_launch<MODE, P, 64, 256, 2>(t, pl.split, st);
         }
     } else {
         switch (pl.bm) {

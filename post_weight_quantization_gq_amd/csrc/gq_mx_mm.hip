@@ -520,10 +520,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
+        // a wave whose rows all lie past the tile's own only copies
+        const bool idle = wm * TM >= at.rows;
+        for (int s = s_lo; idle && s < s_hi; ++s) {
+#pragma unroll
+            for (int i = SOON; i < ALL; ++i) issue_one(s + R - 1, i);
+            mx_wait_vmcnt<LOADS * (R - 2)>();
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            issue_scales(s + R);
+#pragma unroll
+            for (int i = 0; i < SOON; ++i) issue_one(s + R, i);
+        }
         Half A, B;
-        read(s_lo, zero, A);
-        take_scales(s_lo);
-        for (int s = s_lo; s < s_hi; ++s) {
+        if (!idle) {
+            read(s_lo, zero, A);
+            take_scales(s_lo);
+        }
+        for (int s = s_lo; !idle && s < s_hi; ++s) {
             // the rest of the last stage's loads go out with the first part
             run(A, zero, s, std::integral_constant<int, 1>{}, B, s + R - 1, soon, all);
             mx_each<G::PARTS / 2 - 1>([&](auto i) {
@@ -785,12 +800,17 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
     const int64_t k64 = op == MX_GEMM_DX ? (k + 63) / 64 : 2 * mx_groups(k);
     P.stage_bytes = P.staged ? mx_al256((size_t)n * k64 * 64 * P.planes * 2) : 0;
     const int64_t per = (n + experts - 1) / experts;
-    P.stream = op != MX_GEMM_DX && per <= 16;
+    // Streaming saves the tiles' split and its sum (one token 4096 -> 4096: 9.7 us a call, 13.7 by
+    // tiles); where tiles need no split they are as fast or faster (8192 -> 28672: 31 and 29), and
+    // with more activations than a wave's registers take in passing too (16 rows of 14336: 18 and
+    // 14 us; 16 of 4096 in float32: 19 and 17; packed 16 of 28672: 25 and 24).
+    const int64_t live = experts > 1 ? (experts < n ? experts : n) : 1;          // experts with rows, at most
+    const int64_t room = op == MX_GEMM_MX ? 1 << 18 : (a_bf16 ? 1 << 17 : 3 << 14);
+    P.stream = op != MX_GEMM_DX && per <= 16 && per * k <= room && live * ((m + 127) / 128) < 192;
     P.split = 1;
     P.stages = P.unit = 0;
     int64_t blocks, units;
     if (P.stream) {
-        const int64_t live = experts > 1 ? (experts < n ? experts : n) : 1;      // experts with rows, at most
         P.bm = 16;
         P.bn = live * ((m + 31) / 32) >= 256 ? 32 : 16;
         const int ku = P.planes == 3 ? 2 : 4;
@@ -806,7 +826,7 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
             P.bn = P.bm == 256 || op == MX_GEMM_DX ? 256 : 128;
             const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;
             blocks = rows * ((m + P.bn - 1) / P.bn);
-            if (P.bm <= 64 || blocks >= (op == MX_GEMM_DX ? 48 : 192)) break;
+            if (P.bm <= 64 || blocks >= (op == MX_GEMM_DX ? 48 : (P.planes == 3 && P.bm == 256 ? 64 : 192))) break;
         }
         // few rows of x: stages of 256 (128: three planes of them) values, so that a weight row
         // is read by whole lines

@@ -92,14 +92,32 @@ struct MxTile {
     float* part;                  // partial sums [split][n][m], or null
 };
 
+// At most N loads in flight, and this wave's LDS accesses done.  The copies into LDS are loads
+// whose arrival only this counter tells, so no access moves across the wait.
 template <int N>
 __device__ __forceinline__ void mx_wait_vmcnt() {
+    static_assert(N >= 0 && N < 64, "a 6-bit counter");
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+    asm volatile("" ::: "memory");
 }
 
 // lgkmcnt(0) alone
-__device__ __forceinline__ void mx_wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+__device__ __forceinline__ void mx_wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+    asm volatile("" ::: "memory");
+}
 
+__device__ __forceinline__ void mx_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// One wave copies 64 x 16 bytes into LDS from `dst` on; lane l's come from r at voff + soff
+// (zeros out of r's range).
 __device__ __forceinline__ void mx_dma(__amdgpu_buffer_rsrc_t r, u32x4* dst, uint32_t voff, uint32_t soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mx_lds_t)dst, 16, voff, soff, 0, 0);
 }
@@ -517,18 +535,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 #pragma unroll
         for (int i = 0; i < SOON; ++i) issue_one(s_lo + R - 1, i);
         mx_wait_vmcnt<LOADS * (R - 2) + LOADS - LATE>();
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
+        mx_barrier();
         // a wave whose rows all lie past the tile's own only copies
         const bool idle = wm * TM >= at.rows;
         for (int s = s_lo; idle && s < s_hi; ++s) {
 #pragma unroll
             for (int i = SOON; i < ALL; ++i) issue_one(s + R - 1, i);
             mx_wait_vmcnt<LOADS * (R - 2)>();
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
+            mx_barrier();
             issue_scales(s + R);
 #pragma unroll
             for (int i = 0; i < SOON; ++i) issue_one(s + R, i);
@@ -547,9 +561,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
                 run(A, std::integral_constant<int, h + 2>{}, s, std::integral_constant<int, h + 3>{}, B, 0, zero, zero);
             });
             mx_wait_vmcnt<LOADS * (R - 2)>();    // stage s + 1 has landed
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_barrier();        // and this one's slot has been read by every wave
-            __builtin_amdgcn_sched_barrier(0);
+            mx_barrier();                        // and this one's slot has been read by every wave
             issue_scales(s + R);
             run(B, std::integral_constant<int, G::PARTS - 1>{}, s + 1, zero, A, s + R, zero, soon);  // past the last stage: read and not used
             take_scales(s + 1);

@@ -590,8 +590,8 @@ def _other_place(device, stream):
 def _place(t, stream):
     """(context, stream pointer) of a call on t's device: inside the context that device is
     current, and what the call allocates belongs to the stream it runs on (its memory is reused
-    in that stream's order).  Without a stream to change to, the context does nothing."""
-    index = t.device.index
+    in that stream's order).  Without a device or stream to change to, the context does nothing."""
+    index = t.get_device()
     if stream is None:
         if index == torch._C._cuda_getDevice():
             return _NOWHERE, torch._C._cuda_getCurrentRawStream(index)
@@ -605,19 +605,22 @@ _NOWHERE = contextlib.nullcontext()
 _MX_DTYPES = {torch.float32: GQ_F32, torch.bfloat16: GQ_BF16}
 
 
-def _mx_tensor(t, name, device, shape=None, dtypes=_MX_DTYPES):
-    """One argument's checks, in the order of the other entry points': shape, then a contiguous
-    GPU tensor of an allowed dtype on `device` (None: any)."""
-    if shape is not None and t.shape != shape:
+def _mx_shape(t, shape, name):
+    if t.shape != shape:
         raise GQError(GQ_ESHAPE, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _mx_tensor(t, name, index, dtypes=_MX_DTYPES):
+    """A contiguous GPU tensor of an allowed dtype, on GPU `index`."""
+    if t.get_device() == index and index >= 0 and t.is_contiguous() and t.dtype in dtypes:
+        return
     if not t.is_cuda:
         raise GQError(GQ_EINVAL, f"{name} must be a GPU tensor")
     if not t.is_contiguous():
         raise GQError(GQ_EINVAL, f"{name} must be contiguous")
     if t.dtype not in dtypes:
         raise GQError(GQ_EDTYPE, f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise GQError(GQ_EINVAL, f"{name} is on {t.device}, the other tensors on {device}")
+    raise GQError(GQ_EINVAL, f"{name} is on {t.device}, the call's first tensor is not")
 
 
 _U8, _I64 = (torch.uint8,), (torch.int64,)
@@ -640,17 +643,18 @@ def mxfp4_quantize(x, Q=None, S=None, stream=None):
         raise GQError(GQ_ESHAPE, "x needs a last dimension to quantise along")
     lead, d = x.shape[:-1], x.shape[-1]
     rb, rs = _mx_width(d)
-    if Q is not None:
-        _mx_tensor(Q, "Q", x.device, (*lead, rb), _U8)
-    if S is not None:
-        _mx_tensor(S, "S", x.device, (*lead, rs), _U8)
-    _mx_tensor(x, "x", None)
+    index = x.get_device()
+    for t, width, name in ((Q, rb, "Q"), (S, rs, "S")):
+        if t is not None:
+            _mx_shape(t, (*lead, width), name)
+            _mx_tensor(t, name, index, _U8)
+    _mx_tensor(x, "x", index)
     where, st = _place(x, stream)
     with where:
         if Q is None:
-            Q = torch.empty((*lead, rb), dtype=torch.uint8, device=x.device)
+            Q = x.new_empty((*lead, rb), dtype=torch.uint8)
         if S is None:
-            S = torch.empty((*lead, rs), dtype=torch.uint8, device=x.device)
+            S = x.new_empty((*lead, rs), dtype=torch.uint8)
         status = lib.mxfp4_quantize(x.data_ptr(), _MX_DTYPES[x.dtype], x.numel() // d, d, Q.data_ptr(),
                                     S.data_ptr(), st)
     if status:
@@ -665,14 +669,18 @@ def mxfp4_dequantize(Q, S, d: int, dtype=torch.bfloat16, y=None, stream=None) ->
     rb, rs = _mx_width(d)
     if dtype not in _MX_DTYPES:
         raise GQError(GQ_EDTYPE, f"unsupported dtype {dtype}")
-    _mx_tensor(Q, "Q", None, (*lead, rb), _U8)
-    _mx_tensor(S, "S", Q.device, (*lead, rs), _U8)
+    index = Q.get_device()
+    _mx_shape(Q, (*lead, rb), "Q")
+    _mx_shape(S, (*lead, rs), "S")
     if y is not None:
-        _mx_tensor(y, "y", Q.device, (*lead, d), (dtype,))
+        _mx_shape(y, (*lead, d), "y")
+        _mx_tensor(y, "y", index, (dtype,))
+    _mx_tensor(Q, "Q", index, _U8)
+    _mx_tensor(S, "S", index, _U8)
     where, st = _place(Q, stream)
     with where:
         if y is None:
-            y = torch.empty((*lead, d), dtype=dtype, device=Q.device)
+            y = Q.new_empty((*lead, d), dtype=dtype)
         status = lib.mxfp4_dequantize(Q.data_ptr(), S.data_ptr(), y.numel() // d, d, y.data_ptr(),
                                       _MX_DTYPES[dtype], st)
     if status:
@@ -692,51 +700,49 @@ def mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts=1, dtype=GQ_BF16) -> in
     return int(library().mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts, dtype))
 
 
-def _mx_weight(Q, S, d_in, offsets, device):
+def _mx_weight(Q, S, d_in, offsets, index):
     """(experts, d_out) of a packed weight, one ([d_out][..]) or, with offsets, several
     ([experts][d_out][..])."""
     rb, rs = _mx_width(d_in)
-    if Q.dim() != (2 if offsets is None else 3):
+    lead = Q.shape[:-1]
+    if len(lead) != (1 if offsets is None else 2):
         raise GQError(GQ_ESHAPE, "Q must be [d_out][row bytes], or [experts][d_out][row bytes] "
                                  "with offsets")
-    lead = Q.shape[:-1]
-    if offsets is not None and offsets.shape != (lead[0] + 1,):
-        raise GQError(GQ_ESHAPE, f"offsets must have shape {(lead[0] + 1,)}, got {tuple(offsets.shape)}")
-    _shape(Q, (*lead, rb), "Q")
-    _shape(S, (*lead, rs), "S")
-    _mx_tensor(Q, "Q", device, None, _U8)
-    _mx_tensor(S, "S", device, None, _U8)
-    if offsets is None:
-        return 1, lead[0]
-    _mx_tensor(offsets, "offsets", device, None, _I64)
-    return lead
+    _mx_shape(Q, (*lead, rb), "Q")
+    _mx_shape(S, (*lead, rs), "S")
+    if offsets is not None:
+        _mx_shape(offsets, (lead[0] + 1,), "offsets")
+        _mx_tensor(offsets, "offsets", index, _I64)
+    _mx_tensor(Q, "Q", index, _U8)
+    _mx_tensor(S, "S", index, _U8)
+    return (1, lead[0]) if offsets is None else lead
 
 
 def _mx_product(fn, size, x, first, size_args, n, width, Q, S, last, experts, offsets, y, out_dtype,
                 ws, stream):
     """What the three products share: output, workspace and the call itself.  A grouped
     product's own output has zeros in the rows past the last expert's."""
-    where, st = _place(x, stream)
-    device = x.device
+    index = x.get_device()
     if y is not None:
         if out_dtype is not None and y.dtype != out_dtype:
             raise GQError(GQ_EDTYPE, f"y is {y.dtype}, out_dtype {out_dtype}")
-        _mx_tensor(y, "y", device, (n, width))
+        _mx_shape(y, (n, width), "y")
+        _mx_tensor(y, "y", index)
     elif out_dtype not in _MX_DTYPES:
         raise GQError(GQ_EDTYPE, f"unsupported dtype {out_dtype}")
+    wp, wn = None, 0
+    if ws is not None and ws is not False:
+        _mx_tensor(ws, "ws", index, _U8)
+        wp, wn = ws.data_ptr(), ws.numel()
+    where, st = _place(x, stream)
     with where:
         if y is None:
-            new = torch.empty if offsets is None else torch.zeros
-            y = new((n, width), dtype=out_dtype, device=device)
-        wp, wn = None, 0
+            y = (x.new_empty if offsets is None else x.new_zeros)((n, width), dtype=out_dtype)
         if ws is None:
             wn = size(*size_args)
             if wn:
-                ws = torch.empty(wn, dtype=torch.uint8, device=device)
+                ws = x.new_empty(wn, dtype=torch.uint8)
                 wp = ws.data_ptr()
-        elif ws is not False:
-            _mx_tensor(ws, "ws", device, None, _U8)
-            wp, wn = ws.data_ptr(), ws.numel()
         status = fn(*first, Q.data_ptr(), S.data_ptr(), last, experts,
                     None if offsets is None else offsets.data_ptr(), y.data_ptr(),
                     _MX_DTYPES[y.dtype], wp, wn, st)
@@ -755,8 +761,9 @@ def mxfp4_gemm(x, Q, S, offsets=None, y=None, out_dtype=None, ws=None, stream=No
     if x.dim() != 2:
         raise GQError(GQ_ESHAPE, "x must be [n][d_in]")
     n, d_in = x.shape
-    experts, d_out = _mx_weight(Q, S, d_in, offsets, x.device)
-    _mx_tensor(x, "x", None)
+    index = x.get_device()
+    experts, d_out = _mx_weight(Q, S, d_in, offsets, index)
+    _mx_tensor(x, "x", index)
     dt = _MX_DTYPES[x.dtype]
     if y is None and out_dtype is None:
         out_dtype = x.dtype
@@ -774,9 +781,12 @@ def mxfp4_gemm_mx(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None,
         raise GQError(GQ_ESHAPE, "XQ must be [n][row bytes]")
     n = XQ.shape[0]
     rb, rs = _mx_width(d_in)
-    experts, d_out = _mx_weight(Q, S, d_in, offsets, XQ.device)
-    _mx_tensor(XQ, "XQ", None, (n, rb), _U8)
-    _mx_tensor(XS, "XS", XQ.device, (n, rs), _U8)
+    index = XQ.get_device()
+    _mx_shape(XQ, (n, rb), "XQ")
+    _mx_shape(XS, (n, rs), "XS")
+    experts, d_out = _mx_weight(Q, S, d_in, offsets, index)
+    _mx_tensor(XQ, "XQ", index, _U8)
+    _mx_tensor(XS, "XS", index, _U8)
     if y is None and out_dtype is None:
         out_dtype = torch.bfloat16
     return _mx_product(lib.mxfp4_gemm_mx, lib.mxfp4_gemm_mx_workspace_size, XQ,
@@ -793,8 +803,10 @@ def mxfp4_gemm_dx(g, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=N
     if g.dim() != 2:
         raise GQError(GQ_ESHAPE, "g must be [n][d_out]")
     n = g.shape[0]
-    experts, d_out = _mx_weight(Q, S, d_in, offsets, g.device)
-    _mx_tensor(g, "g", None, (n, d_out))
+    index = g.get_device()
+    experts, d_out = _mx_weight(Q, S, d_in, offsets, index)
+    _mx_shape(g, (n, d_out), "g")
+    _mx_tensor(g, "g", index)
     dt = _MX_DTYPES[g.dtype]
     if y is None and out_dtype is None:
         out_dtype = g.dtype

@@ -271,12 +271,17 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     constexpr int WN = NW / WM, TM = BM / WM, TN = BN / WN;
     constexpr int T = MODE == MX_GEMM_DX ? 16 : 32, FM = TM / T, FN = TN / T;
     constexpr int R = G::RING, SPAN = G::SPAN, PA = G::PA;
-    static_assert(MODE != MX_GEMM_DX || TN == 128, "a wave of the gradient takes 128 columns");
+    static_assert(MODE != MX_GEMM_DX || (TN == 128 && BN == 256), "a wave of the gradient takes 128 columns");
     extern __shared__ u32x4 mx_lds[];
     u32x4* const sc_lds = mx_lds + R * G::STAGE;
 
-    const MxPlace at = mx_place(p, BM, (int)((p.m + BN - 1) / BN));
+    MxPlace at = mx_place(p, BM, (int)((p.m + BN - 1) / BN));
     if (!at.ok) return;
+    // (the same in every lane; said so, or the descriptors built from it are looped over lanes)
+    at.e = __builtin_amdgcn_readfirstlane(at.e);
+    at.col = __builtin_amdgcn_readfirstlane(at.col);
+    at.rows = __builtin_amdgcn_readfirstlane((int)at.rows);
+    at.t0 = (int64_t)__builtin_amdgcn_readfirstlane((int)at.t0);            // below 2^31
     const int tid = threadIdx.x, lane = tid & 63, r = lane & (T - 1), g = lane / T;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
@@ -324,11 +329,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         int row = slot / G::WSPR, c = slot % G::WSPR;
         if constexpr (MODE == MX_GEMM) c ^= G::wswz(row);
         if constexpr (MODE == MX_GEMM_MX) c ^= (row >> 1) & 7;
-        if constexpr (MODE == MX_GEMM_DX && BN == 256) {
+        if constexpr (MODE == MX_GEMM_DX) {
             row ^= (row >> 5) & 1;
             c ^= 4 * ((row >> 4) & 1);
         }
-        if constexpr (MODE == MX_GEMM_DX && BN == 128) row ^= (row >> 4) & 3;
         wv[i] = (uint32_t)(row * p.qb) + 16u * c;
     }
 
@@ -423,49 +427,60 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             }
         }
     };
+    // Where this lane reads within a stage: what depends on the lane, once; the rest of an address
+    // is the stage's start and a constant, which the instruction holds.
+    constexpr int XV = MODE == MX_GEMM ? (KS > 1 ? 8 : 4) : (MODE == MX_GEMM_MX ? 4 : 2);
+    constexpr int WV = MODE == MX_GEMM ? KS : (MODE == MX_GEMM_MX ? 4 : 2);
+    int lx[XV], lw[WV], ls;
+#pragma unroll
+    for (int v = 0; v < XV; ++v) {
+        // the chunk (its low four bits where a row has more than 8): values of part h
+        const int chunk = MODE == MX_GEMM ? 8 * (v >> 2) + 4 * g + (v & 3) : (MODE == MX_GEMM_MX ? 2 * v + g : 2 * g + v);
+        lx[v] = (wm * TM + r) * (16 * G::XSPR) + 16 * (chunk ^ G::xswz(r));
+    }
+#pragma unroll
+    for (int v = 0; v < WV; ++v) {
+        if constexpr (MODE == MX_GEMM) lw[v] = (wn * TN + r) * (16 * G::WSPR) + 16 * ((2 * v + g) ^ G::wswz(r));
+        else if constexpr (MODE == MX_GEMM_MX) lw[v] = (wn * TN + r) * 128 + 16 * ((2 * v + g) ^ ((r >> 1) & 7));
+        else lw[v] = (16 * g + (v ^ (g >> 1))) * 128 + 16 * ((wn * 4 + (r >> 2)) ^ (4 * (g & 1))) + 4 * (r & 3);
+    }
+    if constexpr (MODE == MX_GEMM) ls = (wn * TN + r) * 16 + g;
+    else if constexpr (MODE == MX_GEMM_MX) ls = r * 16;
+    else ls = 16 * g * 16 + wn * 4 + (r >> 2);
     // read k (of Half::STEPS) of part h of stage s: one fragment, with its scale
     auto read_one = [&](int s, auto part, Half& o, int k) {
         constexpr int h = decltype(part)::value;
         const int xb = (s % R) * G::STAGE * 16, wb = xb + G::X * 16, ks = s / PA;
+        const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16;
         if constexpr (MODE == MX_GEMM) {
-            // part h: values 16 hh .. of the 32 that lane (r, g) has of piece kk, in plane q
-            constexpr int kk = h / (2 * G::PS), q0 = h / 2 % G::PS, hh = h % 2;
-            const int sb = (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS) * 16 + 2 * KS * (ks % SPAN) + 2 * kk + g;
-            const int wc = (2 * kk + g) ^ G::wswz(r);
+            // part h: values 16 hh .. of the 32 that lane (r, g) has of piece kk, in plane q0
+            constexpr int kk = h / (2 * G::PS), q0 = h / 2 % G::PS, hh = h % 2, at = kk * G::PS + q0;
             // an odd number of 128s ends in half a stage: its other half has zeros of x against
             // the next row's weights, whose scales must not be NaN
             const bool past = KS == 4 && kk >= 2 && 256 * ks + 128 >= p.kpad;
             if (k < FN) {
-                const int row = wn * TN + 32 * k + r;
-                o.w[k] = *(const u32x2*)(lds + wb + row * (16 * G::WSPR) + 16 * wc + 8 * hh);
-                const uint32_t sc = lds[sb + row * 16];
+                o.w[k] = *(const u32x2*)(lds + (wb + lw[kk]) + (k * 32 * 16 * G::WSPR + 8 * hh));
+                const uint32_t sc = *(lds + (sb + 2 * KS * (ks % SPAN) + ls) + (k * 32 * 16 + 2 * kk));
                 o.ws[k] = past ? 127u : sc;
             } else {
                 const int q = (k - FN) / 2, u = (k - FN) % 2;
-                o.x[q][u] = *(const u32x4*)(lds + xb + (wm * TM + 32 * q + r) * (16 * G::XSPR) + 16 * ((8 * (kk * G::PS + q0) + 4 * g + 2 * hh + u) ^ G::xswz(r)));
+                o.x[q][u] = *(const u32x4*)(lds + (xb + lx[4 * (at % 2) + 2 * hh + u]) + (q * 32 * 16 * G::XSPR + at / 2 * 256));
             }
         } else if constexpr (MODE == MX_GEMM_MX) {
             // lane (r, g): block 2 h + g of the stage's eight; with the first part, all eight scales
-            const bool isx = k < FM;
-            const int row = isx ? wm * TM + 32 * k + r : wn * TN + 32 * (k - FM) + r;
-            const u32x4 v = *(const u32x4*)(lds + (isx ? xb : wb) + row * 128 + 16 * ((2 * h + g) ^ ((r >> 1) & 7)));
-            if (isx) o.x[k] = v;
-            else o.w[k - FM] = v;
-            if constexpr (h == 0)
-                raw[k] = *(const u32x2*)(lds + (R * G::STAGE + ((ks / SPAN) % 3) * G::SROWS + (isx ? BN + row : row)) * 16 + 8 * (ks % SPAN));
+            if (k < FM) o.x[k] = *(const u32x4*)(lds + (xb + lx[h]) + k * 32 * 128);
+            else o.w[k - FM] = *(const u32x4*)(lds + (wb + lw[h]) + (k - FM) * 32 * 128);
+            if constexpr (h == 0) {
+                const int row0 = k < FM ? BN + wm * TM : wn * TN;
+                raw[k] = *(const u32x2*)(lds + (sb + 8 * (ks % SPAN) + row0 * 16 + ls) + (k < FM ? k : k - FM) * 32 * 16);
+            }
         } else {
             // lane (r, g): rows 16 g + 8 h .. + 7 of the stage's 64, columns 8 r .. of the wave's 128
             if (k < 8) {
-                const int sb = wb + G::W * 16 + wn * 4 + (r >> 2);
-                const int row = 16 * g + 8 * h + k;
-                if constexpr (BN == 256)
-                    o.w[k] = *(const uint32_t*)(lds + wb + (row ^ (g >> 1)) * 128 + 16 * ((wn * 4 + (r >> 2)) ^ (4 * (g & 1))) + 4 * (r & 3));
-                else
-                    o.w[k] = *(const uint32_t*)(lds + wb + (row ^ g) * 64 + 4 * r);
-                o.ws[k] = lds[sb + row * 16];
+                o.w[k] = *(const uint32_t*)(lds + (wb + lw[k % 2]) + (8 * h + (k & ~1)) * 128);
+                o.ws[k] = *(lds + (wb + ls) + (G::W * 16 + (8 * h + k) * 16));
             } else {
-                const int q = k - 8;
-                o.x[q] = *(const u32x4*)(lds + xb + (wm * TM + 16 * q + r) * 128 + 16 * ((2 * g + h) ^ ((r >> 1) & 7)));
+                o.x[k - 8] = *(const u32x4*)(lds + (xb + lx[h]) + (k - 8) * 16 * 128);
             }
         }
     };

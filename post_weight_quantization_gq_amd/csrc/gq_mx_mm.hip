@@ -122,9 +122,11 @@ __device__ __forceinline__ void mx_dma(__amdgpu_buffer_rsrc_t r, u32x4* dst, uin
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mx_lds_t)dst, 16, voff, soff, 0, 0);
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const uint8_t* p, int64_t bytes) {
-    const uint32_t nb = bytes < 0 ? 0u : (bytes > 0xffffffffll ? 0xffffffffu : (uint32_t)bytes);
-    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)nb, 0x00020000);
+// `rows` rows of `row` bytes from p on, the first `skip` bytes left out (none where `on` is
+// false: every load reads zeros).  A tile's rows come to less than 2^31 bytes (256 of 2^20
+// values in three planes), so 32 bits hold it, which the scalar unit compares and selects.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const uint8_t* p, int rows, int64_t row, bool on = true, int skip = 0) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, on ? rows * (int)row - skip : 0, 0x00020000);
 }
 
 // Rows of expert e, clamped to [0, n].
@@ -138,7 +140,8 @@ __device__ __forceinline__ void mx_expert_rows(const int64_t* offsets, int e, in
 
 struct MxPlace {
     int e;
-    int64_t t0, rows;             // first row of the tile, rows of it
+    int64_t t0;                   // first row of the tile
+    int rows;                     // rows of it
     int col;                      // column tile
     bool ok;
 };
@@ -194,7 +197,7 @@ __device__ __forceinline__ MxPlace mx_place(const MxTile& p, int bm, int ncol) {
                 int64_t lo, hi;
                 mx_expert_rows(p.offsets, r.e, p.n, lo, hi);
                 r.t0 = lo + (row - before) * bm;
-                r.rows = hi - r.t0 < bm ? hi - r.t0 : bm;
+                r.rows = (int)(hi - r.t0 < bm ? hi - r.t0 : bm);
                 r.ok = row >= before && r.rows > 0;     // (offsets out of order could count wrongly)
                 return r;
             }
@@ -204,7 +207,7 @@ __device__ __forceinline__ MxPlace mx_place(const MxTile& p, int bm, int ncol) {
     }
     r.e = 0;
     r.t0 = row * bm;
-    r.rows = p.n - r.t0 < bm ? p.n - r.t0 : bm;
+    r.rows = (int)(p.n - r.t0 < bm ? p.n - r.t0 : bm);
     r.ok = true;
     return r;
 }
@@ -280,7 +283,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     // (the same in every lane; said so, or the descriptors built from it are looped over lanes)
     at.e = __builtin_amdgcn_readfirstlane(at.e);
     at.col = __builtin_amdgcn_readfirstlane(at.col);
-    at.rows = __builtin_amdgcn_readfirstlane((int)at.rows);
+    at.rows = __builtin_amdgcn_readfirstlane(at.rows);
     at.t0 = (int64_t)__builtin_amdgcn_readfirstlane((int)at.t0);            // below 2^31
     const int tid = threadIdx.x, lane = tid & 63, r = lane & (T - 1), g = lane / T;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -299,13 +302,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     }
 
     // ---- sources
-    const __amdgpu_buffer_rsrc_t xr = mx_rsrc(p.A + at.t0 * p.a_row, at.rows * p.a_row);
+    const __amdgpu_buffer_rsrc_t xr = mx_rsrc(p.A + at.t0 * p.a_row, at.rows, p.a_row);
     const uint8_t* const Qe = p.Q + (int64_t)at.e * p.d_out * p.qb;
     const uint8_t* const Se = p.S + (int64_t)at.e * p.d_out * p.sb;
-    const int64_t wrows = p.m - j0 < BN ? p.m - j0 : BN;
-    const __amdgpu_buffer_rsrc_t sr = mx_rsrc(Se + j0 * p.sb, wrows * p.sb);
+    const int wrows = (int)(p.m - j0 < BN ? p.m - j0 : BN);
+    const __amdgpu_buffer_rsrc_t sr = mx_rsrc(Se + j0 * p.sb, wrows, p.sb);
     const __amdgpu_buffer_rsrc_t xsr =
-        MODE == MX_GEMM_MX ? mx_rsrc(p.AS + at.t0 * p.sb, at.rows * p.sb) : sr;
+        MODE == MX_GEMM_MX ? mx_rsrc(p.AS + at.t0 * p.sb, at.rows, p.sb) : sr;
 
     constexpr int XPW = G::X / NW, WPW = G::W / NW;          // slots a wave copies
     constexpr int XI = (XPW + 63) / 64, WI = (WPW + 63) / 64;
@@ -336,27 +339,28 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         wv[i] = (uint32_t)(row * p.qb) + 16u * c;
     }
 
+    constexpr int SR = 64 / NW;                            // MX_GEMM_DX: rows whose scales a wave copies
+    const uint32_t sv = (uint32_t)(wave * SR + lane) * (uint32_t)p.sb;
     // The loads of stage s, in two parts: a few scales (by some of the lanes), and the codes and
     // activations, one load at a time.  Past this split's last stage they read nothing and clear
     // a slot that is not read, so that the counts of loads in flight stay what they are.
     auto issue_scales = [&](int s) {
         const int ks = s / PA;
         if constexpr (MODE == MX_GEMM_DX) {
-            const int64_t o0 = (int64_t)ks * 64, left = p.d_out - o0 < 64 ? p.d_out - o0 : 64;
-            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + o0 * p.sb + j0 / 32, s < s_hi ? left * p.sb - j0 / 32 : 0);
+            const int o0 = ks * 64, left = (int)p.d_out - o0 < 64 ? (int)p.d_out - o0 : 64;
+            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + o0 * p.sb + j0 / 32, left, p.sb, s < s_hi, (int)(j0 / 32));
             u32x4* wb = mx_lds + (s % R) * G::STAGE + G::X;
-            constexpr int SR = 64 / NW;
-            if (lane < SR) mx_dma(z, wb + G::W + wave * SR, (uint32_t)((wave * SR + lane) * p.sb), 0);
+            if (lane < SR) mx_dma(z, wb + G::W + wave * SR, sv, 0);
         } else {
             // a share of the next span's
             const int span = ks / SPAN + 1, part = ks % SPAN;
             u32x4* sb = sc_lds + (span % 3) * G::SROWS;
-            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + j0 * p.sb, s < s_hi ? wrows * p.sb : 0);
+            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + j0 * p.sb, wrows, p.sb, s < s_hi);
             constexpr int WR = BN / SPAN / NW;
             const int row = part * (BN / SPAN) + wave * WR;
             if (lane < WR) mx_dma(z, sb + row, (uint32_t)((row + lane) * p.sb) + 16u * span, 0);
             if constexpr (MODE == MX_GEMM_MX) {
-                const __amdgpu_buffer_rsrc_t xz = mx_rsrc(p.AS + at.t0 * p.sb, s < s_hi ? at.rows * p.sb : 0);
+                const __amdgpu_buffer_rsrc_t xz = mx_rsrc(p.AS + at.t0 * p.sb, at.rows, p.sb, s < s_hi);
                 constexpr int XR = BM / SPAN / NW;
                 const int xrow = part * (BM / SPAN) + wave * XR;
                 if (lane < XR) mx_dma(xz, sb + BN + xrow, (uint32_t)((xrow + lane) * p.sb) + 16u * span, 0);
@@ -373,11 +377,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             u32x4* wb = base + G::X + wave * WPW + i * 64;
             const int ks = s / PA;
             if constexpr (MODE == MX_GEMM_DX) {
-                const int64_t o0 = (int64_t)ks * 64, left = p.d_out - o0 < 64 ? p.d_out - o0 : 64;
-                const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + o0 * p.qb + j0 / 2, s < s_hi ? left * p.qb - j0 / 2 : 0);
+                const int o0 = ks * 64, left = (int)p.d_out - o0 < 64 ? (int)p.d_out - o0 : 64;
+                const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + o0 * p.qb + j0 / 2, left, p.qb, s < s_hi, (int)(j0 / 2));
                 if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(q, wb, wv[i], 0);
             } else {
-                const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + j0 * p.qb, s < s_hi ? wrows * p.qb : 0);
+                const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + j0 * p.qb, wrows, p.qb, s < s_hi);
                 if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(q, wb, wv[i], (uint32_t)ks * (16u * G::WSPR));
             }
         }
@@ -614,7 +618,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
                 for (int v = 0; v < 16; v += 4)
                     put(32 * f + 2 * v + 4 * g, f32x4{acc[f][q][v], acc[f][q][v + 1], acc[f][q][v + 2], acc[f][q][v + 3]});
         }
-        const int row0 = wm * TM + T * q, left = (int)at.rows - row0;
+        const int row0 = wm * TM + T * q, left = at.rows - row0;
         if (p.y_vec) {
             const int lanes = TN * wide / 16;                    // of a row: a power of two
             for (int i = lane; i < T * lanes; i += 64) {
@@ -663,7 +667,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
     const int c0 = ((int)blockIdx.z * WAVES + wave) * per;
     const int c1 = c0 + per < pieces ? c0 + per : pieces;
 
-    const int64_t wrows = p.m - j0 < 16 * MT ? p.m - j0 : 16 * MT, row0 = (int64_t)e * p.d_out + j0;
+    const int wrows = (int)(p.m - j0 < 16 * MT ? p.m - j0 : 16 * MT);
+    const int64_t row0 = (int64_t)e * p.d_out + j0;
     auto swizzle = [](int row) { return KU == 4 ? row & 15 : (row >> 1) & 7; };
     uint32_t wv[WS / 64];
 #pragma unroll
@@ -673,8 +678,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
     }
     auto copy = [&](int c) {                     // past the last piece: clears, reads nothing
         u32x4* to = ring + (c & 1) * PIECE;
-        const __amdgpu_buffer_rsrc_t wr = mx_rsrc(p.Q + row0 * p.qb, c < c1 ? wrows * p.qb : 0);
-        const __amdgpu_buffer_rsrc_t sr = mx_rsrc(p.S + row0 * p.sb, c < c1 ? wrows * p.sb : 0);
+        const __amdgpu_buffer_rsrc_t wr = mx_rsrc(p.Q + row0 * p.qb, wrows, p.qb, c < c1);
+        const __amdgpu_buffer_rsrc_t sr = mx_rsrc(p.S + row0 * p.sb, wrows, p.sb, c < c1);
 #pragma unroll
         for (int i = 0; i < WS / 64; ++i) mx_dma(wr, to + 64 * i, wv[i], (uint32_t)c * (16u * SPR));
         mx_dma(sr, to + WS, lane < 16 * MT ? (uint32_t)(lane * p.sb) : 0xC0000000u, (uint32_t)c * (4u * KU));

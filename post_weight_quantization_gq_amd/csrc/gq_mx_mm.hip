@@ -1,4 +1,30 @@
 // Products with MXFP4 weights on gfx950.
+//
+//   MX_GEMM     y[t][j]  = sum_i x[t][i] w[j][i]     x bfloat16, or float32 in three planes
+//   MX_GEMM_MX  the same, x in MXFP4 too
+//   MX_GEMM_DX  dx[t][i] = sum_j g[t][j] w[j][i]     g as x
+//
+// w = 2^(s - 127) c with c of two significant bits is exact in bfloat16 (down to its subnormal
+// range, which the matrix cores keep), so the first and last are bfloat16 products of weights
+// converted in registers, one instruction for two values; the second is the matrix cores' own
+// scaled product.  All sums are float32; every order of summation depends on sizes alone.
+//
+// Three ways, chosen by mx_plan:
+//   k_mx_tile    tiles of activations' rows by output columns, both operands copied by
+//                asynchronous loads into a ring of LDS stages.  Bound by the matrix cores for
+//                many rows, by the weight's bytes for few.
+//   k_mx_stream  up to 16 rows of a small weight: waves that stream it each on its own.
+//   k_mx_join    the sum of a contraction split over blocks, where tiles are too few.
+// Several weights ("experts") are tiles of one launch; their row counts stay on the device.
+//
+// One MI355X, whole calls (kernels under a profiler: a few per cent more, by the clock):
+//   4096 rows, 11008 -> 4096, bfloat16      283 us   1.31 PFLOP/s (the library's bfloat16
+//                                                    matrix product reaches 1.20 to 1.29)
+//   8192 rows, 28672 -> 8192, both MXFP4    826 us   4.7 PFLOP/s (the instruction alone: 7.3)
+//   gradient, 4096 rows, 11008 -> 4096      307 us   1.20 PFLOP/s
+//   1 row, 4096 -> 4096                     5.1 us on the GPU (9 MB)
+//   8 rows, 28672 -> 8192, both MXFP4       27 us    4.6 TB/s (a large copy: 5.0)
+//   96 rows over 64 experts, 2048 -> 1408   16 us    4.4 TB/s
 #include "gq_common.h"
 #include "gq_internal.h"
 #include "gq_mx.h"
@@ -73,6 +99,37 @@ __global__ __launch_bounds__(256) void k_mx_stage(const void* __restrict__ x, in
 
 // ---------------------------------------------------------------------------
 // The tiled product.
+//
+// Tile and wave.  A wave's products need (rows + columns) fragments from LDS for rows x columns
+// products, so waves are as large as the accumulators allow: 256 x 256 tiles of 4 waves of
+// 128 x 128 (MX_GEMM_MX, 256 accumulator registers) or 8 waves of 64 x 128 (two to a SIMD; the
+// bfloat16 products take four times the cycles for the same LDS bytes, and two waves hide each
+// other's waits: 712 -> 336 us when they came).  A stage is 64 values of the contraction for the
+// bfloat16 products (a 128-byte line of each row of x) and 256 for the fp4 one (a line of codes;
+// with 128 the half lines were fetched twice: 1176 -> 1087 us).
+//
+// Loop.  A stage is used in parts; while a part's products run, the next part's fragments are
+// read, and the loads of a later stage go out one beside each product or two: issued together
+// they hold the wave up for longer than the part lasts (1031 -> 986 us).  One barrier a stage:
+// after it the stage's slot is refilled.  Loads past the end read nothing, so the waits count
+// the same number of loads throughout.
+//
+// Scales.  They stay where the caller has them, a row's bytes in a row: 16 bytes of each row are
+// fetched at a time (512 values), each stage bringing its share of the next such span, into one
+// of three buffers.  The fp4 products take a row's eight scales of a stage by one read and select
+// bytes in the instruction (1011 -> 940 us against a read for each).
+//
+// Gradient.  The contraction runs over the weight's rows, but its codes lie along the columns: a
+// lane reads 8 columns (4 bytes) of 8 rows, converts pairs along the columns and exchanges halves
+// of two rows' words, which gives 8 fragments of 8 rows each.  Conversions and exchanges are one
+// instruction each a product, which with the addresses fills the vector unit (half the cycles)
+// beside the matrix cores (half): this bounds it.
+//
+// Outputs leave by way of LDS as whole lines; stored from the accumulators, each store touched 32
+// rows (fp4 prompt 1006 -> 918 us, 32 experts 155 -> 128 us).
+//
+// What bounds the large tiles now is power: the clock falls to 1.75 GHz (fp4) and 1.87 GHz
+// (bfloat16) of 2.4 with the matrix cores busy 57 and 63 per cent of the cycles.
 // ---------------------------------------------------------------------------
 struct MxTile {
     const uint8_t* A;             // rows of the activations (bfloat16, or codes)
@@ -640,7 +697,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: the weight is streamed once, each wave on its own.  A block takes 16 MT output
+// Few rows: the weight is streamed once, each wave on its own, without a barrier before the end
+// (one row 4096 -> 4096: 5.1 us; by tiles 8.0 and 4.0 for the sum of the split).  A block takes 16 MT output
 // columns of one weight and up to 16 rows of activations at a time; its waves share out the
 // contraction and their sums are added in the waves' order at the end.  A wave copies pieces of
 // KU groups of 128 values of its 16 MT weight rows into LDS of its own, one piece ahead: read
@@ -772,7 +830,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
 }
 
 // y = the sum of a split contraction's parts, in their order; rows that belong to an expert
-// (all of them without offsets).
+// (all of them without offsets).  2 to 4 us, most of it the launch, for up to 16 parts of a few
+// hundred kilobytes.
 __global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part, int split, int64_t n,
                                                 int64_t m, const int64_t* __restrict__ offsets,
                                                 int experts, void* __restrict__ y, int y_bf16) {
@@ -851,8 +910,13 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
         blocks = live * ((m + P.bn - 1) / P.bn);
         units /= P.waves;
     } else {
-        // the largest tile that the rows of a weight fill and that gives most compute units
-        // one, else the smallest of them
+        // The largest tile that the rows of a weight fill and that gives most compute units
+        // one, else the smallest: 1024 rows 4096 -> 4096 take 40 us by 128 x 128 and 54 by
+        // 256 x 256 split in four, 2048 rows 81 and 79; fp4 17 and 41, 26 and 44.  In float32
+        // (three times the products, so the split's sum weighs less) large tiles pay from 64
+        // on: 1024 rows 104 us and 130 by 128 x 128, 512 rows 79 and 59 by 64 x 128.  The
+        // gradient's smaller tiles convert the same weights for fewer products: it takes the
+        // largest from 48 on (512 rows of 4096 x 4096: 45 us, 60 by 128 x 256).
         P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 || op == MX_GEMM_DX ? 64 : 32));
         for (;; P.bm /= 2) {
             P.bn = P.bm == 256 || op == MX_GEMM_DX ? 256 : 128;
@@ -860,8 +924,8 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
             blocks = rows * ((m + P.bn - 1) / P.bn);
             if (P.bm <= 64 || blocks >= (op == MX_GEMM_DX ? 48 : (P.planes == 3 && P.bm == 256 ? 64 : 192))) break;
         }
-        // few rows of x: stages of 256 (128: three planes of them) values, so that a weight row
-        // is read by whole lines
+        // Few rows of x: stages of 256 (128: three planes of them) values, so that a weight row
+        // is read by whole lines (24 rows 14336 -> 4096: 15.6 -> 12.9 us).
         const int deep = op != MX_GEMM || P.bm > 64 ? 1 : (P.bm == 64 && P.planes == 3 ? 2 : 4);
         P.stages = (int)(op == MX_GEMM_MX ? (mx_groups(k) + 1) / 2 : (deep == 1 ? k64 * P.planes : (k64 + deep - 1) / deep));
         P.unit = op == MX_GEMM_DX ? P.planes : (op == MX_GEMM_MX ? 2 : (deep == 1 ? 8 * P.planes : 8 / deep));
@@ -983,7 +1047,7 @@ hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
     }
     if (e != hipSuccess) return e;
     if (t.part) {
-        const int64_t blocks = (c.n * m + 255) / 256;
+        const int64_t blocks = (c.n * m + 1023) / 1024;          // (four outputs a lane)
         hipLaunchKernelGGL(k_mx_join, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, t.part, pl.split,
                            c.n, m, c.offsets, c.experts, c.y, (int)c.y_bf16);
         GQ_LAUNCH_CHECK();

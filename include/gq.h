@@ -389,7 +389,7 @@ int64_t mxfp4_row_scales(int64_t d);
  * block of zeros has s = 0); each value over 2^(s - 127) is rounded to the nearest magnitude, ties to
  * the even index, 6 above it (the block's maximum lies in [4, 8) scale units).  A sign is
  * kept, also of a value that rounds to zero.  A block with a NaN or an infinity has s = 255
- * and codes 0.  x element-aligned.
+ * and codes 0.  x element-aligned; x, Q and S must not overlap (GQ_EINVAL).
  * Weights (once per layer, rows = d_out, d = d_in; several experts' weights are one call
  * with rows = experts * d_out) and activations (per call, rows = tokens) are packed alike.
  */
@@ -414,7 +414,7 @@ gq_status mxfp4_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, int
  * `experts` weights one after another, offsets (device int64 [experts + 1]) is
  * nondecreasing within [0, n], and rows offsets[e] .. offsets[e + 1] - 1 are multiplied by
  * weight e (none where the two are equal).  Rows before offsets[0] and from
- * offsets[experts] on are neither read nor written.  The library cannot refuse bad offsets
+ * offsets[experts] on take no part and their outputs are not written.  The library cannot refuse bad offsets
  * (they are on the device): each is clamped to [0, n] and an expert whose end lies before its
  * start has no rows, so nothing is read or written out of range; rows that two experts
  * claim, or that bad offsets leave over, hold unspecified values.
@@ -429,7 +429,7 @@ gq_status mxfp4_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, int
  * Alignment: x and g 16-byte aligned where they are bfloat16 and their rows are a multiple
  * of 8 elements, else element-aligned; y and dx element-aligned.  ws as for every entry
  * point, of at least the matching size (which can be 0).  y and dx must not overlap the
- * inputs or ws.  1 <= experts <= 4096 (GQ_ENOTIMPL beyond), n < 2^31.
+ * inputs or ws, nor ws the inputs (GQ_EINVAL).  1 <= experts <= 4096 (GQ_ENOTIMPL beyond), n < 2^31.
  */
 size_t mxfp4_gemm_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts,
                                  gq_dtype x_dt);

@@ -802,6 +802,11 @@ int64_t mxfp4_row_scales(int64_t d) {
 
 static bool mx_el_al(const void* p, gq_dtype t) { return ((uintptr_t)p & (t == GQ_BF16 ? 1u : 3u)) == 0; }
 
+static bool mx_overlap(const void* p, size_t np, const void* q, size_t nq) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return np && nq && a < b + nq && b < a + np;
+}
+
 static gq_status mx_rows_check(const void* x, gq_dtype dt, int64_t rows, int64_t d,
                                const uint8_t* Q, const uint8_t* S) {
     if (!dtype_ok(dt)) return fail(GQ_EDTYPE, "unsupported dtype %d", (int)dt);
@@ -813,6 +818,10 @@ static gq_status mx_rows_check(const void* x, gq_dtype dt, int64_t rows, int64_t
     if (!x || !Q || !S) return fail(GQ_EINVAL, "null values, Q or S");
     if (!al16(Q) || ((uintptr_t)S & 3u) || !mx_el_al(x, dt))
         return fail(GQ_EINVAL, "Q must be 16-byte, S 4-byte aligned and the values element-aligned");
+    const size_t n = (size_t)rows, x_len = n * d * (dt == GQ_BF16 ? 2 : 4);
+    const size_t q_len = n * gq::mx_row_bytes(d), s_len = n * gq::mx_row_scales(d);
+    if (mx_overlap(x, x_len, Q, q_len) || mx_overlap(x, x_len, S, s_len) || mx_overlap(Q, q_len, S, s_len))
+        return fail(GQ_EINVAL, "the values, Q and S must not overlap");
     return GQ_OK;
 }
 
@@ -883,8 +892,22 @@ static gq_status mx_product(gq::MxOp op, const void* a, const uint8_t* as, gq_dt
                     "with rows of no multiple of 8), the output element- and ws 256-byte aligned");
     hipStream_t st = (hipStream_t)stream;
     const bool ab = a_dt == GQ_BF16;
+    const size_t need = gq::mx_gemm_workspace(op, ab, n, d_in, d_out, experts);
+    {
+        const size_t rows = (size_t)n, wrows = (size_t)experts * d_out;
+        const size_t a_len = op == gq::MX_GEMM_MX ? rows * gq::mx_row_bytes(k) : rows * k * (ab ? 2 : 4);
+        const size_t as_len = op == gq::MX_GEMM_MX ? rows * gq::mx_row_scales(k) : 0;
+        const size_t y_len = rows * (op == gq::MX_GEMM_DX ? d_in : d_out) * (y_dt == GQ_BF16 ? 2 : 4);
+        const size_t q_len = wrows * gq::mx_row_bytes(d_in), s_len = wrows * gq::mx_row_scales(d_in);
+        const size_t o_len = offsets ? (size_t)(experts + 1) * 8 : 0, w_len = ws ? need : 0;
+        const struct { const void* p; size_t n; } in[] = {{a, a_len}, {as, as_len}, {Q, q_len}, {S, s_len}, {offsets, o_len}};
+        for (const auto& i : in)
+            if (mx_overlap(y, y_len, i.p, i.n) || mx_overlap(ws, w_len, i.p, i.n))
+                return fail(GQ_EINVAL, "the output and ws must not overlap the inputs");
+        if (mx_overlap(y, y_len, ws, w_len)) return fail(GQ_EINVAL, "the output must not overlap ws");
+    }
     Scratch s;
-    gq_status rc = s.acquire(ws, ws_bytes, gq::mx_gemm_workspace(op, ab, n, d_in, d_out, experts), st);
+    gq_status rc = s.acquire(ws, ws_bytes, need, st);
     if (rc != GQ_OK) return rc;
     const gq::MxCall c{op, a, as, ab, n, d_in, d_out, Q, S, experts, offsets, y, y_dt == GQ_BF16};
     hipError_t e = gq::mx_gemm_run(c, s.ptr, st);

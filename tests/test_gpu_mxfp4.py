@@ -445,3 +445,105 @@ def test_refusals_on_the_device(device):
     need = gq.mxfp4_gemm_workspace_size(8, 256, 64, 1, gq.GQ_F32)
     if need:
         assert status(gq.mxfp4_gemm, x.float(), Q, S, ws=torch.empty(need - 1, dtype=torch.uint8, device=device)) == 1
+
+
+def test_output_on_the_input_is_refused(device):
+    x = torch.randn(40, 128, device=device)
+    Q, S = gq.mxfp4_quantize(torch.randn(128, 128, device=device))
+    for fn in (lambda: gq.mxfp4_gemm(x, Q, S, y=x), lambda: gq.mxfp4_gemm_dx(x, Q, S, 128, y=x)):
+        with pytest.raises(gq.GQError) as e:
+            fn()
+        assert e.value.status == 1 and "overlap" in e.value.message
+
+
+@pytest.mark.parametrize("n", [3, 40, 200])
+def test_views_off_the_vector_borders(device, n):
+    """Outputs, and float32 inputs, that start one element off a 16-byte border."""
+    d, m = 256, 64
+    rng = np.random.default_rng(n)
+    Q, S, W = random_weight(rng, 1, m, d)
+    Qd, Sd = u8(Q[0], device), u8(S[0], device)
+    flat = torch.randn(1 + n * d, device=device)
+    x = flat[1:].view(n, d)
+    for out in (BF, F32):
+        buf = torch.full((2 + n * m,), 5.0, dtype=out, device=device)
+        gq.mxfp4_gemm(x, Qd, Sd, y=buf[1:1 + n * m].view(n, m))
+        assert float(buf[0]) == 5.0 and float(buf[-1]) == 5.0
+        check(buf[1:1 + n * m].view(n, m), f64(x), W[0], 3 * d, out)
+        buf = torch.full((2 + n * d,), 5.0, dtype=out, device=device)
+        g = torch.randn(1 + n * m, device=device)[1:].view(n, m)
+        gq.mxfp4_gemm_dx(g, Qd, Sd, d, y=buf[1:1 + n * d].view(n, d))
+        assert float(buf[0]) == 5.0 and float(buf[-1]) == 5.0
+        check(buf[1:1 + n * d].view(n, d), f64(g), np.ascontiguousarray(W[0].T), 3 * m, out)
+
+
+@pytest.mark.parametrize("op", ["gemm", "gemm_mx", "gemm_dx"])
+@pytest.mark.parametrize("E,n", [(130, 600), (130, 4500), (64, 640)])
+def test_many_and_skewed_experts(device, op, E, n):
+    """More experts than a wave counts at once, most of them empty, one with most of the rows."""
+    d, m = 160, 96
+    rng = np.random.default_rng(E + n)
+    counts = np.zeros(E, np.int64)
+    counts[rng.choice(E, 9, replace=False)] = rng.integers(1, n // 20, 9)
+    counts[E // 2] += n - counts.sum() - 5
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    Q, S, W = random_weight(rng, E, m, d)
+    off = torch.from_numpy(offsets).to(device)
+    k, width = (m, d) if op == "gemm_dx" else (d, m)
+    y = torch.full((n, width), -1.0, device=device)
+    if op == "gemm_mx":
+        XQ, XS, X = random_weight(rng, 1, n, d)
+        a = X[0]
+        gq.mxfp4_gemm_mx(u8(XQ[0], device), u8(XS[0], device), u8(Q, device), u8(S, device), d, offsets=off, y=y)
+    else:
+        x = torch.from_numpy(rng.standard_normal((n, k))).to(BF)
+        a = f64(x)
+        if op == "gemm":
+            gq.mxfp4_gemm(x.to(device), u8(Q, device), u8(S, device), offsets=off, y=y)
+        else:
+            gq.mxfp4_gemm_dx(x.to(device), u8(Q, device), u8(S, device), d, offsets=off, y=y)
+    assert (y[offsets[-1]:] == -1.0).all()
+    for e in np.nonzero(counts)[0]:
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        check(y[r], a[r], np.ascontiguousarray(W[e].T) if op == "gemm_dx" else W[e], k, F32, f"expert {e}")
+
+
+def test_rows_past_32_bits(device):
+    """Activations of more than 2^31 elements and 4 GiB: the last rows are those of a call on them
+    alone (to the sums' rounding), and packing them equals packing the last rows alone."""
+    n, d, m, t = 140000, 16384, 48, 40
+    gen = torch.Generator(device=device)
+    gen.manual_seed(1)
+    x = torch.randn((n, d), generator=gen, device=device, dtype=BF)
+    W = torch.randn((m, d), generator=gen, device=device)
+    Q, S = gq.mxfp4_quantize(W)
+    w = O.mx_values(Q.cpu().numpy(), S.cpu().numpy(), d)
+    y = gq.mxfp4_gemm(x, Q, S, out_dtype=F32)
+    check(y[-t:], f64(x[-t:]), w, d, F32, "gemm")
+    XQ, XS = gq.mxfp4_quantize(x)
+    TQ, TS = gq.mxfp4_quantize(x[-t:].contiguous())
+    assert torch.equal(XQ[-t:], TQ) and torch.equal(XS[-t:], TS)
+    z = gq.mxfp4_gemm_mx(XQ, XS, Q, S, d, out_dtype=F32)
+    check(z[-t:], O.mx_values(TQ.cpu().numpy(), TS.cpu().numpy(), d), w, d, F32, "gemm_mx")
+    del XQ, XS, x
+    g = torch.randn((n, m), generator=gen, device=device, dtype=BF)
+    dx = gq.mxfp4_gemm_dx(g, Q, S, d)                  # 2.3e9 outputs
+    check(dx[-t:], f64(g[-t:]), np.ascontiguousarray(w.T), m, BF, "gemm_dx")
+    del dx
+
+
+def test_weights_past_32_bits(device):
+    """Codes of more than 4 GiB: the last expert's product."""
+    E, m, d, n = 36, 16384, 16384, 24
+    Q = torch.randint(0, 256, (E, m, d // 2), dtype=torch.uint8, device=device)
+    S = torch.randint(110, 125, (E, m, d // 32), dtype=torch.uint8, device=device)
+    off = torch.tensor([0] * E + [n], device=device)
+    x = torch.randn(n, d, device=device, dtype=BF)
+    y = gq.mxfp4_gemm(x, Q, S, offsets=off, out_dtype=F32)
+    rows = torch.arange(0, m, 1031)
+    w = O.mx_values(Q[-1, rows].cpu().numpy(), S[-1, rows].cpu().numpy(), d)
+    check(y[:, rows], f64(x), w, d, F32)
+    dx = gq.mxfp4_gemm_dx(y.to(BF), Q, S, d, offsets=off, out_dtype=F32)
+    cols = slice(d - 64, d)
+    wc = gq.mxfp4_dequantize(Q[-1].contiguous(), S[-1].contiguous(), d, dtype=F32)[:, cols]
+    check(dx[:, cols], f64(y.to(BF)), np.ascontiguousarray(f64(wc).T), m, F32)

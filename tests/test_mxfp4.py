@@ -100,6 +100,7 @@ def test_quantize_argument_errors():
         assert fn(Q=FAKE_ODD) == B.GQ_EINVAL and "aligned" in _err()
         assert fn(S=ctypes.c_void_p(0x10002)) == B.GQ_EINVAL
         assert fn(x=ctypes.c_void_p(0x10001)) == B.GQ_EINVAL
+        assert fn() == B.GQ_EINVAL and "overlap" in _err()         # all one address
         assert fn(rows=0, x=None, Q=None, S=None) == B.GQ_OK
 
 
@@ -139,6 +140,17 @@ def test_product_argument_errors(name):
     assert call(y=ctypes.c_void_p(0x10001)) == B.GQ_EINVAL
     assert call(y=ctypes.c_void_p(0x10002), ydt=0) == B.GQ_EINVAL
     assert call(ws=FAKE_ODD, wsb=1 << 30) == B.GQ_EINVAL and "ws" in _err()
+    # the output on the inputs (every pointer here is the same address)
+    assert call() == B.GQ_EINVAL and "overlap" in _err()
+    far = [ctypes.c_void_p(i << 32) for i in range(1, 6)]
+    assert call(x=far[0], xs=far[1], Q=far[2], S=far[3], y=far[0]) == B.GQ_EINVAL and "overlap" in _err()
+    assert call(x=far[0], xs=far[1], Q=far[2], S=far[3], y=ctypes.c_void_p((3 << 32) + 256)) == B.GQ_EINVAL
+    assert call(x=far[0], xs=far[1], Q=far[2], S=far[3], y=far[4], experts=1, offsets=far[4]) == B.GQ_EINVAL
+    if name != "mxfp4_gemm_mx":                       # float32: a workspace, here too small, then on x
+        assert call(x=far[0], dt=0, Q=far[2], S=far[3], y=far[4], ws=far[1], wsb=16) == B.GQ_EINVAL
+        assert "too small" in _err()
+        assert call(x=far[0], dt=0, Q=far[2], S=far[3], y=far[4], ws=far[0], wsb=1 << 30) == B.GQ_EINVAL
+        assert "overlap" in _err()
     assert call(n=0, x=None, Q=None, S=None, y=None) == B.GQ_OK
     # no rows and bad sizes: still refused
     assert call(n=0, k=0) == B.GQ_ESHAPE

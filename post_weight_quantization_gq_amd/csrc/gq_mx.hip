@@ -17,40 +17,8 @@
 
 namespace gq {
 
-// 8 consecutive values of a row of d, from element i of it (p: the row's start); VEC: the
-// row's 8-value pieces are whole and 16-byte aligned, else values past d read as 0.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void mx_load8(const void* p, int64_t row0, int64_t i, int64_t d,
-                                         float (&v)[8]) {
-    if constexpr (VEC) {
-        if (i < d) {
-            if constexpr (BF16) {
-                const u32x4 w = *(const u32x4*)((const uint16_t*)p + row0 + i);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[2 * k] = __uint_as_float(w[k] << 16);
-                    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-                }
-            } else {
-                const f32x4 a = *(const f32x4*)((const float*)p + row0 + i);
-                const f32x4 b = *(const f32x4*)((const float*)p + row0 + i + 4);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) { v[k] = a[k]; v[4 + k] = b[k]; }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = load_elem<BF16>(p, i + k < d ? row0 + i + k : row0);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = i + k < d ? v[k] : 0.f;
-    }
-}
-
 // Lane t of the grid takes the 8-value piece t of the padded rows (16 pieces a group of 128).
-template <bool BF16, bool VEC>
+template <bool BF16>
 __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ x, int64_t pieces,
                                                     int64_t d, int ppr, uint32_t* __restrict__ Q,
                                                     uint8_t* __restrict__ S) {
@@ -58,8 +26,8 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ x,
     if (t >= pieces) return;             // pieces is a multiple of 16: blocks stay whole
     const int64_t r = mx_div(t, ppr);
     const int64_t i = (t - r * ppr) * 8;
-    float v[8];
-    mx_load8<BF16, VEC>(x, r * d, i, d, v);
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (i < d) mx_load8<BF16>(x, r * d, i, d, v);
     // the maximum by magnitude as its bits: they order like the values, NaN above infinity
     uint32_t top = 0u;
 #pragma unroll
@@ -86,7 +54,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const void* __restrict__ x,
     if ((t & 3) == 0) S[t >> 2] = (uint8_t)(i < d ? s : 127u);
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16>
 __global__ __launch_bounds__(256) void k_mx_dequantize(const uint32_t* __restrict__ Q,
                                                       const uint8_t* __restrict__ S,
                                                       int64_t pieces, int64_t d, int ppr,
@@ -103,8 +71,8 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const uint32_t* __restric
         const u32x4 w{mx_bf16<0>(q, scale), mx_bf16<1>(q, scale), mx_bf16<2>(q, scale),
                       mx_bf16<3>(q, scale)};
         uint16_t* o = (uint16_t*)y + at;
-        if constexpr (VEC) {
-            *(u32x4*)o = w;
+        if (i + 8 <= d) {
+            *(u32x4_any*)o = w;
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -117,9 +85,9 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const uint32_t* __restric
         const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 3);
         const float v[8] = {a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
         float* o = (float*)y + at;
-        if constexpr (VEC) {
-            *(f32x4*)o = f32x4{v[0], v[1], v[2], v[3]};
-            *(f32x4*)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        if (i + 8 <= d) {
+            *(f32x4_any*)o = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4_any*)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -133,13 +101,10 @@ hipError_t mx_quantize_run(const void* x, bool x_bf16, int64_t rows, int64_t d, 
     StageTimer tm(ST_LUT_PACK, st);
     const int ppr = (int)(16 * mx_groups(d));
     const int64_t pieces = rows * ppr;
-    const bool vec = d % 8 == 0 && ((uintptr_t)x & 15u) == 0;
     const dim3 grid((unsigned)((pieces + 255) / 256)), block(256);
     uint32_t* q = (uint32_t*)Q;
-    if (x_bf16 && vec) hipLaunchKernelGGL((k_mx_quantize<true, true>), grid, block, 0, st, x, pieces, d, ppr, q, S);
-    else if (x_bf16) hipLaunchKernelGGL((k_mx_quantize<true, false>), grid, block, 0, st, x, pieces, d, ppr, q, S);
-    else if (vec) hipLaunchKernelGGL((k_mx_quantize<false, true>), grid, block, 0, st, x, pieces, d, ppr, q, S);
-    else hipLaunchKernelGGL((k_mx_quantize<false, false>), grid, block, 0, st, x, pieces, d, ppr, q, S);
+    if (x_bf16) hipLaunchKernelGGL(k_mx_quantize<true>, grid, block, 0, st, x, pieces, d, ppr, q, S);
+    else hipLaunchKernelGGL(k_mx_quantize<false>, grid, block, 0, st, x, pieces, d, ppr, q, S);
     GQ_LAUNCH_CHECK();
     return hipSuccess;
 }
@@ -149,13 +114,10 @@ hipError_t mx_dequantize_run(const uint8_t* Q, const uint8_t* S, int64_t rows, i
     StageTimer tm(ST_LUT_PACK, st);
     const int ppr = (int)(16 * mx_groups(d));
     const int64_t pieces = rows * ppr;
-    const bool vec = d % 8 == 0 && ((uintptr_t)y & 15u) == 0;
     const dim3 grid((unsigned)((pieces + 255) / 256)), block(256);
     const uint32_t* q = (const uint32_t*)Q;
-    if (y_bf16 && vec) hipLaunchKernelGGL((k_mx_dequantize<true, true>), grid, block, 0, st, q, S, pieces, d, ppr, y);
-    else if (y_bf16) hipLaunchKernelGGL((k_mx_dequantize<true, false>), grid, block, 0, st, q, S, pieces, d, ppr, y);
-    else if (vec) hipLaunchKernelGGL((k_mx_dequantize<false, true>), grid, block, 0, st, q, S, pieces, d, ppr, y);
-    else hipLaunchKernelGGL((k_mx_dequantize<false, false>), grid, block, 0, st, q, S, pieces, d, ppr, y);
+    if (y_bf16) hipLaunchKernelGGL(k_mx_dequantize<true>, grid, block, 0, st, q, S, pieces, d, ppr, y);
+    else hipLaunchKernelGGL(k_mx_dequantize<false>, grid, block, 0, st, q, S, pieces, d, ppr, y);
     GQ_LAUNCH_CHECK();
     return hipSuccess;
 }

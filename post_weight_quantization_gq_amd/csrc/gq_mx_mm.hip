@@ -49,33 +49,18 @@ __global__ __launch_bounds__(256) void k_mx_stage(const void* __restrict__ x, in
     constexpr int P = BF16 ? 1 : 3;
     // a lane takes 8 values; 8 lanes a piece
     const int64_t total = n * pieces * 8;
-    const bool vec = !BF16 && k % 4 == 0 && ((uintptr_t)x & 15u) == 0;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
         const int64_t piece = t >> 3, r = mx_div(piece, pieces);
-        const int64_t i = (piece - r * pieces) * 64 + (t & 7) * 8, at = r * k + i;
+        const int64_t i = (piece - r * pieces) * 64 + (t & 7) * 8;
         u32x4* o = (u32x4*)(out + piece * P * 64 + (t & 7) * 8);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (i < k) mx_load8<BF16>(x, r * k, i, k, v);
         if constexpr (BF16) {
             u32x4 w;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // (loaded without a condition: past the row, the row's first value)
-                const uint32_t lo = ((const uint16_t*)x)[i + 2 * e < k ? at + 2 * e : r * k];
-                const uint32_t hi = ((const uint16_t*)x)[i + 2 * e + 1 < k ? at + 2 * e + 1 : r * k];
-                w[e] = (i + 2 * e < k ? lo : 0u) | (i + 2 * e + 1 < k ? hi << 16 : 0u);
-            }
+            for (int e = 0; e < 4; ++e) w[e] = (__float_as_uint(v[2 * e]) >> 16) | (__float_as_uint(v[2 * e + 1]) & 0xffff0000u);
             o[0] = w;
         } else {
-            float v[8];
-            if (vec && i + 8 <= k) {
-                const f32x4 a = *(const f32x4*)((const float*)x + at), b = *(const f32x4*)((const float*)x + at + 4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = ((const float*)x)[i + e < k ? at + e : r * k];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = i + e < k ? v[e] : 0.f;
-            }
             uint32_t w[3][8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -1047,7 +1032,7 @@ hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
     }
     if (e != hipSuccess) return e;
     if (t.part) {
-        const int64_t blocks = (c.n * m + 1023) / 1024;          // (four outputs a lane)
+        const int64_t blocks = (c.n * m + 255) / 256 / (m % 4 == 0 ? 4 : 1) + 1;      // four outputs a lane, or one
         hipLaunchKernelGGL(k_mx_join, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, t.part, pl.split,
                            c.n, m, c.offsets, c.experts, c.y, (int)c.y_bf16);
         GQ_LAUNCH_CHECK();

@@ -130,7 +130,7 @@ struct MxTile {
     int kpad;                     // its length padded to whole groups (MX_GEMM, MX_GEMM_MX)
     int unit;                     // a split's range is a multiple of this many stages
     void* y;
-    int y_bf16, y_vec;            // y_vec: rows of outputs (parts) start and end at 16-byte borders
+    int y_bf16;
     float* part;                  // partial sums [split][n][m], or null
 };
 
@@ -661,21 +661,19 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
                     put(32 * f + 2 * v + 4 * g, f32x4{acc[f][q][v], acc[f][q][v + 1], acc[f][q][v + 2], acc[f][q][v + 3]});
         }
         const int row0 = wm * TM + T * q, left = at.rows - row0;
-        if (p.y_vec) {
-            const int lanes = TN * wide / 16;                    // of a row: a power of two
-            for (int i = lane; i < T * lanes; i += 64) {
-                const int row = i / lanes, b = 16 * (i - row * lanes);
-                const u32x4 v = *(const u32x4*)(own + row * pitch + b);
-                if (row < left && b < cols * wide)
-                    *(u32x4*)(out + ((at.t0 + row0 + row) * p.m + jw) * wide + b) = v;
-            }
-        } else {
-            for (int i = lane; i < T * TN; i += 64) {
-                const int row = i / TN, c = i - row * TN;
-                if (row >= left || c >= cols) continue;
-                const int64_t to = (at.t0 + row0 + row) * p.m + jw + c;
-                if (wide == 4) ((float*)out)[to] = *(const float*)(own + row * pitch + 4 * c);
-                else ((uint16_t*)out)[to] = *(const uint16_t*)(own + row * pitch + 2 * c);
+        const int lanes = TN * wide / 16;                        // of a row: a power of two
+        for (int i = lane; i < T * lanes; i += 64) {
+            const int row = i / lanes, at16 = 16 * (i - row * lanes), some = cols * wide - at16;
+            const u32x4 v = *(const u32x4*)(own + row * pitch + at16);
+            if (row >= left || some <= 0) continue;
+            uint8_t* const to = out + ((at.t0 + row0 + row) * p.m + jw) * wide + at16;
+            if (some >= 16) {
+                *(u32x4_any*)to = v;
+            } else {                             // the row ends within these 16 bytes
+                for (int c = 0; c < some; c += wide) {
+                    if (wide == 4) *(uint32_t*)(to + c) = v[c / 4];
+                    else *(uint16_t*)(to + c) = (uint16_t)(v[c / 4] >> (8 * (c & 2)));
+                }
             }
         }
     }
@@ -1023,7 +1021,6 @@ hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
     t.y = c.y;
     t.y_bf16 = c.y_bf16;
     t.part = pl.split > 1 ? (float*)((char*)ws + pl.stage_bytes) : nullptr;
-    t.y_vec = t.part ? m % 4 == 0 : m % (c.y_bf16 ? 8 : 4) == 0 && ((uintptr_t)c.y & 15u) == 0;
     hipError_t e;
     switch (c.op) {
         case MX_GEMM: e = pl.planes == 1 ? mx_launch_size<MX_GEMM, 1>(t, pl, st) : mx_launch_size<MX_GEMM, 3>(t, pl, st); break;

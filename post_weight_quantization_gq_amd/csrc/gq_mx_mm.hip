@@ -662,20 +662,24 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         }
         const int row0 = wm * TM + T * q, left = at.rows - row0;
         const int lanes = TN * wide / 16;                        // of a row: a power of two
-        for (int i = lane; i < T * lanes; i += 64) {
-            const int row = i / lanes, at16 = 16 * (i - row * lanes), some = cols * wide - at16;
-            const u32x4 v = *(const u32x4*)(own + row * pitch + at16);
-            if (row >= left || some <= 0) continue;
-            uint8_t* const to = out + ((at.t0 + row0 + row) * p.m + jw) * wide + at16;
-            if (some >= 16) {
-                *(u32x4_any*)to = v;
-            } else {                             // the row ends within these 16 bytes
-                for (int c = 0; c < some; c += wide) {
-                    if (wide == 4) *(uint32_t*)(to + c) = v[c / 4];
-                    else *(uint16_t*)(to + c) = (uint16_t)(v[c / 4] >> (8 * (c & 2)));
+        auto store = [&](auto ends) {                            // ends: rows may end inside 16 bytes
+            for (int i = lane; i < T * lanes; i += 64) {
+                const int row = i / lanes, at16 = 16 * (i - row * lanes), some = cols * wide - at16;
+                const u32x4 v = *(const u32x4*)(own + row * pitch + at16);
+                if (row >= left || some <= 0) continue;
+                uint8_t* const to = out + ((at.t0 + row0 + row) * p.m + jw) * wide + at16;
+                if (!decltype(ends)::value || some >= 16) {
+                    *(u32x4_any*)to = v;
+                } else {
+                    for (int c = 0; c < some; c += wide) {
+                        if (wide == 4) *(uint32_t*)(to + c) = v[c / 4];
+                        else *(uint16_t*)(to + c) = (uint16_t)(v[c / 4] >> (8 * (c & 2)));
+                    }
                 }
             }
-        }
+        };
+        if (cols * wide % 16 == 0) store(std::false_type{});
+        else store(std::true_type{});
     }
 }
 

@@ -904,7 +904,14 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
         // on: 1024 rows 104 us and 130 by 128 x 128, 512 rows 79 and 59 by 64 x 128.  The
         // gradient's smaller tiles convert the same weights for fewer products: it takes the
         // largest from 48 on (512 rows of 4096 x 4096: 45 us, 60 by 128 x 256).
-        P.bm = per > 128 ? 256 : (per > 64 ? 128 : (per > 32 || op == MX_GEMM_DX ? 64 : 32));
+        // Experts in fp4 have last tiles that are part empty, and after a short contraction a
+        // compute unit's one large tile has its start and its stores to itself: up to 1024 rows
+        // an expert and 2048 values take tiles of at most 128 x 128 (24000 rows over 64 experts
+        // 2048 -> 1408: 84 us, 105 by 256 x 256; 16384 rows: 66 and 80; but 8 experts 2048 ->
+        // 4096 of 2048 rows each 141 and 144, 16 experts 1024 -> 4096 of 1875 rows 197 and 186, one
+        // weight 2048 -> 2048 with 8192 rows 32 and 30, 16 of 8192 -> 8192 with 137 rows 220 and 190).
+        const bool small = op == MX_GEMM_MX && experts > 1 && per <= 1024 && k <= 2048;
+        P.bm = per > 128 && !small ? 256 : (per > 64 ? 128 : (per > 32 || op == MX_GEMM_DX ? 64 : 32));
         for (;; P.bm /= 2) {
             P.bn = P.bm == 256 || op == MX_GEMM_DX ? 256 : 128;
             const int64_t rows = experts > 1 ? n / P.bm + (experts < n ? experts : n) : (n + P.bm - 1) / P.bm;

@@ -508,6 +508,38 @@ def test_many_and_skewed_experts(device, op, E, n):
         check(y[r], a[r], np.ascontiguousarray(W[e].T) if op == "gemm_dx" else W[e], k, F32, f"expert {e}")
 
 
+@pytest.mark.parametrize("op", ["gemm", "gemm_mx", "gemm_dx"])
+@pytest.mark.parametrize("d_in", [2100, 1200])
+def test_experts_of_large_tiles(device, op, d_in):
+    """Ragged experts with enough rows and columns for the largest tiles, and (fp4, up to 2048
+    values) for the smaller ones that short contractions take; a contraction of an odd number of
+    128s; an output width that is no multiple of 8."""
+    offsets, d_out = [5, 900, 901, 2090], 4603
+    n, E = 2100, 3
+    rng = np.random.default_rng(d_in)
+    Q, S, W = random_weight(rng, E, d_out, d_in)
+    off = torch.tensor(offsets, dtype=torch.int64, device=device)
+    Qd, Sd = u8(Q, device), u8(S, device)
+    k, m = (d_out, d_in) if op == "gemm_dx" else (d_in, d_out)
+    y = torch.full((n, m), -77.0, dtype=BF, device=device)
+    if op == "gemm_mx":
+        XQ, XS, X = random_weight(rng, 1, n, d_in)
+        a = X[0]
+        gq.mxfp4_gemm_mx(u8(XQ[0], device), u8(XS[0], device), Qd, Sd, d_in, offsets=off, y=y)
+    else:
+        x = torch.from_numpy(rng.standard_normal((n, k))).to(BF)
+        a = f64(x)
+        if op == "gemm":
+            gq.mxfp4_gemm(x.to(device), Qd, Sd, offsets=off, y=y)
+        else:
+            gq.mxfp4_gemm_dx(x.to(device), Qd, Sd, d_in, offsets=off, y=y)
+    v = f64(y)
+    assert (v[:5] == -77.0).all() and (v[2090:] == -77.0).all()
+    for e in range(E):
+        r = slice(offsets[e], offsets[e + 1])
+        check(y[r], a[r], np.ascontiguousarray(W[e].T) if op == "gemm_dx" else W[e], k, BF, f"expert {e}")
+
+
 def test_rows_past_32_bits(device):
     """Activations of more than 2^31 elements and 4 GiB: the last rows are those of a call on them
     alone (to the sums' rounding), and packing them equals packing the last rows alone."""

@@ -937,9 +937,27 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
     return P;
 }
 
+// Rows that a product of one weight by plan P takes first, by full rounds of large tiles (one for
+// each compute unit), where the others would be up to half a round more: those are then a product
+// of their own, by smaller tiles or a split (4352 rows 4096 -> 4096: 130 us, 184 at once; float32
+// 343 and 546, fp4 57 and 69, gradient 158 and 225).  Half a round at once takes the same or less
+// from there on (6144 rows, half: 186 and 186; 6656: 221 and 191; gradient 231 and 226).
+static int64_t mx_head(const MxPlan& P, MxOp op, int64_t n, int64_t d_in, int64_t d_out) {
+    if (P.stream || P.bm < 256) return n;
+    const int64_t cols = ((op == MX_GEMM_DX ? d_in : d_out) + 255) / 256, tiles = (n + 255) / 256 * cols;
+    const int64_t head = (tiles - 1) / 256 * 256 / cols;          // row tiles
+    return head * cols >= 192 && tiles - head * cols <= 128 ? head * 256 : n;
+}
+
 size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts) {
     const MxPlan P = mx_plan(op, a_bf16, n, d_in, d_out, experts);
-    return P.stage_bytes + P.part_bytes;
+    size_t part = P.part_bytes;
+    const int64_t head = experts == 1 ? mx_head(P, op, n, d_in, d_out) : n;
+    if (head < n) {              // (a call with offsets takes all rows at once)
+        const size_t rest = mx_plan(op, a_bf16, n - head, d_in, d_out, 1).part_bytes;
+        part = part > rest ? part : rest;
+    }
+    return P.stage_bytes + part;
 }
 
 template <int MODE, int P, int BM, int BN, int WM, int NW = 4, int KS = 1>
@@ -1001,16 +1019,16 @@ static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t 
 
 hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
     StageTimer tm(ST_LUT_GEMV, st);
-    const MxPlan pl = mx_plan(c.op, c.a_bf16, c.n, c.d_in, c.d_out, c.experts);
+    const MxPlan whole = mx_plan(c.op, c.a_bf16, c.n, c.d_in, c.d_out, c.experts);
     const int64_t k = c.op == MX_GEMM_DX ? c.d_out : c.d_in, m = c.op == MX_GEMM_DX ? c.d_in : c.d_out;
     MxTile t{};
     t.A = (const uint8_t*)c.a;
     t.AS = c.as;
     t.a_row = t.a_bytes = c.op == MX_GEMM_MX ? mx_row_bytes(k) : 2 * k;
-    if (pl.staged) {
+    if (whole.staged) {
         const int64_t pieces = c.op == MX_GEMM_DX ? (k + 63) / 64 : 2 * mx_groups(k);
         t.A = (const uint8_t*)ws;
-        t.a_row = t.a_bytes = pieces * pl.planes * 128;
+        t.a_row = t.a_bytes = pieces * whole.planes * 128;
         const int64_t blocks = (c.n * pieces * 8 + 255) / 256;
         const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
         if (c.a_bf16) hipLaunchKernelGGL(k_mx_stage<true>, grid, dim3(256), 0, st, c.a, c.n, k, pieces, (uint16_t*)ws);
@@ -1023,29 +1041,39 @@ hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
     t.sb = mx_row_scales(c.d_in);
     t.offsets = c.offsets;
     t.experts = c.experts;
-    t.n = c.n;
     t.m = m;
     t.d_out = c.d_out;
-    t.stages = pl.stages;
     t.kpad = (int)(128 * mx_groups(k));
-    t.unit = pl.unit;
     t.y = c.y;
     t.y_bf16 = c.y_bf16;
-    t.part = pl.split > 1 ? (float*)((char*)ws + pl.stage_bytes) : nullptr;
-    hipError_t e;
-    switch (c.op) {
-        case MX_GEMM: e = pl.planes == 1 ? mx_launch_size<MX_GEMM, 1>(t, pl, st) : mx_launch_size<MX_GEMM, 3>(t, pl, st); break;
-        case MX_GEMM_MX: e = mx_launch_size<MX_GEMM_MX, 1>(t, pl, st); break;
-        default: e = pl.planes == 1 ? mx_launch_size<MX_GEMM_DX, 1>(t, pl, st) : mx_launch_size<MX_GEMM_DX, 3>(t, pl, st); break;
-    }
-    if (e != hipSuccess) return e;
-    if (t.part) {
-        const int64_t blocks = (c.n * m + 255) / 256 / (m % 4 == 0 ? 4 : 1) + 1;      // four outputs a lane, or one
-        hipLaunchKernelGGL(k_mx_join, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, t.part, pl.split,
-                           c.n, m, c.offsets, c.experts, c.y, (int)c.y_bf16);
-        GQ_LAUNCH_CHECK();
-    }
-    return hipSuccess;
+    // the next `rows` rows of t
+    auto product = [&](int64_t rows) -> hipError_t {
+        const MxPlan pl = rows == c.n ? whole : mx_plan(c.op, c.a_bf16, rows, c.d_in, c.d_out, 1);
+        t.n = rows;
+        t.stages = pl.stages;
+        t.unit = pl.unit;
+        t.part = pl.split > 1 ? (float*)((char*)ws + whole.stage_bytes) : nullptr;
+        hipError_t e;
+        switch (c.op) {
+            case MX_GEMM: e = pl.planes == 1 ? mx_launch_size<MX_GEMM, 1>(t, pl, st) : mx_launch_size<MX_GEMM, 3>(t, pl, st); break;
+            case MX_GEMM_MX: e = mx_launch_size<MX_GEMM_MX, 1>(t, pl, st); break;
+            default: e = pl.planes == 1 ? mx_launch_size<MX_GEMM_DX, 1>(t, pl, st) : mx_launch_size<MX_GEMM_DX, 3>(t, pl, st); break;
+        }
+        if (e != hipSuccess) return e;
+        if (t.part) {
+            const int64_t blocks = (rows * m + 255) / 256 / (m % 4 == 0 ? 4 : 1) + 1;  // four outputs a lane, or one
+            hipLaunchKernelGGL(k_mx_join, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, t.part, pl.split,
+                               rows, m, c.offsets, c.experts, t.y, (int)c.y_bf16);
+            GQ_LAUNCH_CHECK();
+        }
+        t.A += rows * t.a_row;
+        if (t.AS) t.AS += rows * t.sb;
+        t.y = (char*)t.y + rows * m * (c.y_bf16 ? 2 : 4);
+        return hipSuccess;
+    };
+    const int64_t head = c.offsets ? c.n : mx_head(whole, c.op, c.n, c.d_in, c.d_out);
+    const hipError_t e = product(head);
+    return e != hipSuccess || head == c.n ? e : product(c.n - head);
 }
 
 }  // namespace gq

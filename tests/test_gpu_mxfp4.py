@@ -540,6 +540,48 @@ def test_experts_of_large_tiles(device, op, d_in):
         check(y[r], a[r], np.ascontiguousarray(W[e].T) if op == "gemm_dx" else W[e], k, BF, f"expert {e}")
 
 
+@pytest.mark.parametrize("op", ["gemm", "gemm_mx", "gemm_dx"])
+@pytest.mark.parametrize("n,k", [(4200, 333), (3856, 1100), (3861, 1104)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_behind_full_rounds_of_tiles(device, op, n, k, dtype):
+    """17 columns of large tiles: 3840 rows fill a round of them, the others are a product of
+    their own (360 rows by tiles, 16 streamed or split, 21 split).  The same from a captured
+    graph, and as one expert that leaves rows at both ends alone, which is not divided."""
+    m = 4200
+    rng = np.random.default_rng(n + k)
+    d_in, d_out = (m, k) if op == "gemm_dx" else (k, m)
+    Q, S, W = random_weight(rng, 1, d_out, d_in)
+    Qd, Sd = u8(Q[0], device), u8(S[0], device)
+    V = np.ascontiguousarray(W[0].T) if op == "gemm_dx" else W[0]
+    if op == "gemm_mx":
+        XQ, XS, X = random_weight(rng, 1, n, k)
+        a, xq, xs, terms = X[0], u8(XQ[0], device), u8(XS[0], device), k
+        call = lambda Q, S, **o: gq.mxfp4_gemm_mx(xq, xs, Q, S, d_in, **o)
+    else:
+        x = torch.from_numpy(rng.standard_normal((n, k))).to(dtype)
+        a, x, terms = f64(x), x.to(device), k * (1 if dtype == BF else 3)
+        if op == "gemm":
+            call = lambda Q, S, **o: gq.mxfp4_gemm(x, Q, S, **o)
+        else:
+            call = lambda Q, S, **o: gq.mxfp4_gemm_dx(x, Q, S, d_in, **o)
+    y = torch.full((n, m), -77.0, dtype=dtype, device=device)
+    call(Qd, Sd, y=y)
+    check(y, a, V, terms, dtype, "all rows")
+    z = torch.zeros_like(y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(Qd, Sd, y=z)
+    for _ in range(3):
+        z.zero_()
+        g.replay()
+        assert torch.equal(y, z)
+    off = torch.tensor([7, n - 9], dtype=torch.int64, device=device)
+    z.fill_(-77.0)
+    call(Qd[None], Sd[None], y=z, offsets=off)
+    assert (z[:7] == -77.0).all() and (z[n - 9:] == -77.0).all()
+    check(z[7:n - 9], a[7:n - 9], V, terms, dtype, "one expert")
+
+
 def test_rows_past_32_bits(device):
     """Activations of more than 2^31 elements and 4 GiB: the last rows are those of a call on them
     alone (to the sums' rounding), and packing them equals packing the last rows alone."""

@@ -928,6 +928,11 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
     if (units < 1) units = 1;
     if (blocks < 256) {
         int64_t s = (P.stream ? 512 : 256) / blocks;
+        // 129 to 170 large tiles of the gradient in thirds take two rounds of three: worth the sum
+        // from 96 stages on (8192 -> 2048, 5060 rows: 198 us, 224 whole; float32, 2500 rows of
+        // 4096 -> 4096: 295 and 356; but 4096 -> 2048 in bfloat16 123 and 118; the product itself,
+        // 4096 -> 2048 in float32, 312 and 298).
+        if (op == MX_GEMM_DX && P.bm == 256 && experts == 1 && P.stages >= 96 && blocks > 128 && blocks <= 170) s = 3;
         s = s < units ? s : units;
         s = s < 1 ? 1 : (s > 16 ? 16 : s);
         const int64_t each = (units + s - 1) / s;        // no part without work

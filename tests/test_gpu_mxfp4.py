@@ -582,6 +582,17 @@ def test_rows_behind_full_rounds_of_tiles(device, op, n, k, dtype):
     check(z[7:n - 9], a[7:n - 9], V, terms, dtype, "one expert")
 
 
+@pytest.mark.parametrize("dtype,d_out", [(BF, 6200), (F32, 2060), (BF, 2060)])
+def test_gradient_of_a_weight_in_thirds(device, dtype, d_out):
+    """144 large tiles: long contractions are split in three, the last of 2060 values is not."""
+    n, d_in = 2244, 4096
+    rng = np.random.default_rng(d_out)
+    Q, S, W = random_weight(rng, 1, d_out, d_in)
+    g = torch.from_numpy(rng.standard_normal((n, d_out))).to(dtype)
+    dx = gq.mxfp4_gemm_dx(g.to(device), u8(Q[0], device), u8(S[0], device), d_in)
+    check(dx, f64(g), np.ascontiguousarray(W[0].T), d_out * (1 if dtype == BF else 3), dtype)
+
+
 def test_rows_past_32_bits(device):
     """Activations of more than 2^31 elements and 4 GiB: the last rows are those of a call on them
     alone (to the sums' rounding), and packing them equals packing the last rows alone."""

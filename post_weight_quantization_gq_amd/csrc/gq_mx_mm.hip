@@ -259,7 +259,10 @@ __device__ __forceinline__ MxPlace mx_place(const MxTile& p, int bm, int ncol) {
 // each); with more, a stage holds them all.
 template <int MODE, int P, int BM, int BN, int KS>
 struct MxGeo {
-    static constexpr int RING = MODE == MX_GEMM_MX ? (BM >= 128 ? 2 : 3) : (KS > 1 ? 2 : (BM * BN > 128 * 128 ? 3 : 4));
+    // 128 x 128 tiles: three, so that a compute unit holds two blocks (2048 rows 4096 -> 4096: 69
+    // us, 81 with four; 6000 rows over 64 experts 2048 -> 1408: 68 and 94; two: 69 and 70, but
+    // 1024 rows 11008 -> 4096 121 and 102)
+    static constexpr int RING = MODE == MX_GEMM_MX ? (BM >= 128 ? 2 : 3) : (KS > 1 ? 2 : (MODE == MX_GEMM_DX && BM == 64 ? 4 : 3));
     static constexpr int PS = KS > 1 ? P : 1;                      // planes within a stage
     static constexpr int PA = KS > 1 ? 1 : P;                      // stages for one piece of the weight
     static constexpr int XSPR = MODE == MX_GEMM ? 8 * KS * PS : 8; // slots a row of activations
@@ -935,6 +938,10 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
         if (op == MX_GEMM_DX && P.bm == 256 && experts == 1 && P.stages >= 96 && blocks > 128 && blocks <= 170) s = 3;
         s = s < units ? s : units;
         s = s < 1 ? 1 : (s > 16 ? 16 : s);
+        // A part's sums are written and read at about 4 TB/s; a stage of a tile takes 0.6 to 1.7 us:
+        // no part that costs more than it saves (gradient of 1024 -> 256, 4000 rows: 32 -> 16 us)
+        const int64_t t = P.bm == 256 ? 17 : (P.bm == 128 ? (op == MX_GEMM_DX ? 11 : 7) : 6);
+        while (!P.stream && s > 1 && s * s * n * m * 20 > P.stages * (s - 1) * t * 1000000) --s;
         const int64_t each = (units + s - 1) / s;        // no part without work
         P.split = (int)((units + each - 1) / each);
     }

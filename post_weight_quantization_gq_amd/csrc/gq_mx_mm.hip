@@ -902,9 +902,9 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
     } else {
         // The largest tile that the rows of a weight fill and that gives most compute units
         // one, else the smallest: 1024 rows 4096 -> 4096 take 40 us by 128 x 128 and 54 by
-        // 256 x 256 split in four, 2048 rows 81 and 79; fp4 17 and 41, 26 and 44.  In float32
+        // 256 x 256 split in four, 2048 rows 69 and 79; fp4 17 and 41, 26 and 44.  In float32
         // (three times the products, so the split's sum weighs less) large tiles pay from 64
-        // on: 1024 rows 104 us and 130 by 128 x 128, 512 rows 79 and 59 by 64 x 128.  The
+        // on: 1024 rows 104 us and 126 by 128 x 128, 512 rows 79 and 59 by 64 x 128.  The
         // gradient's smaller tiles convert the same weights for fewer products: it takes the
         // largest from 48 on (512 rows of 4096 x 4096: 45 us, 60 by 128 x 256).
         // Experts in fp4 have last tiles that are part empty, and after a short contraction a

@@ -379,7 +379,8 @@ gq_status lut_gemv(const uint32_t* Q, const float* C, int64_t d_out, int64_t d_i
  * size functions return 0 for d < 1 or d > 2^20.
  *
  * Every Q is 16-byte and every S 4-byte aligned.  d_in, d_out and d are at most 2^20
- * (GQ_ENOTIMPL beyond).  n = 0 and rows = 0 are valid and do nothing.
+ * (GQ_ENOTIMPL beyond).  n = 0 and rows = 0 are valid and do nothing.  mxfp4_quantize and
+ * mxfp4_dequantize take up to 2^40 values rows * d (GQ_ENOTIMPL beyond).
  */
 int64_t mxfp4_row_bytes(int64_t d);
 int64_t mxfp4_row_scales(int64_t d);

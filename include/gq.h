@@ -430,7 +430,9 @@ gq_status mxfp4_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, int
  * Alignment: x and g 16-byte aligned where they are bfloat16 and their rows are a multiple
  * of 8 elements, else element-aligned; y and dx element-aligned.  ws as for every entry
  * point, of at least the matching size (which can be 0).  y and dx must not overlap the
- * inputs or ws, nor ws the inputs (GQ_EINVAL).  1 <= experts <= 4096 (GQ_ENOTIMPL beyond), n < 2^31.
+ * inputs or ws, nor ws the inputs (GQ_EINVAL).  1 <= experts <= 4096, n < 2^31
+ * (GQ_ENOTIMPL beyond).  2^31 - 2^21 rows or more, and experts of 2^29 columns or more together,
+ * can be more tiles than a launch takes (GQ_ENOTIMPL).
  */
 size_t mxfp4_gemm_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts,
                                  gq_dtype x_dt);

@@ -892,6 +892,9 @@ static gq_status mx_product(gq::MxOp op, const void* a, const uint8_t* as, gq_dt
                     "with rows of no multiple of 8), the output element- and ws 256-byte aligned");
     hipStream_t st = (hipStream_t)stream;
     const bool ab = a_dt == GQ_BF16;
+    if (!gq::mx_gemm_fits(op, ab, n, d_in, d_out, experts, offsets != nullptr))
+        return fail(GQ_ENOTIMPL, "n=%lld d_in=%lld d_out=%lld experts=%d: more tiles than a launch takes",
+                    (long long)n, (long long)d_in, (long long)d_out, experts);
     const size_t need = gq::mx_gemm_workspace(op, ab, n, d_in, d_out, experts);
     {
         const size_t rows = (size_t)n, wrows = (size_t)experts * d_out;

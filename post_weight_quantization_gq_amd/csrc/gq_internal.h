@@ -160,6 +160,7 @@ struct MxCall {
     bool y_bf16;
 };
 size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts);
+bool mx_gemm_fits(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets);
 hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st);
 
 // GANQ-style assignment (gq_ganq.hip)

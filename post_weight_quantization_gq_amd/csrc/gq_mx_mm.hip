@@ -972,6 +972,29 @@ size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t 
     return P.stage_bytes + part;
 }
 
+// Blocks of a launch of tiles of bm x bn: with offsets every expert can have a part-empty one
+static int64_t mx_blocks(int64_t n, int64_t m, int bm, int bn, int64_t part_empty) {
+    return (((n + bm - 1) / bm + part_empty) * ((m + bn - 1) / bn) + 7) / 8 * 8;
+}
+
+// A launch has fewer than 2^32 lanes: close to 2^31 rows of few columns, or thousands of experts with
+// 2^18 columns each, would take more.
+constexpr int64_t MX_MAX_LANES = ((int64_t)1 << 32) - 1;
+
+bool mx_gemm_fits(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets) {
+    const int64_t m = op == MX_GEMM_DX ? d_in : d_out;
+    if ((n / 32 + 1 + experts) * ((m + 127) / 128) < (int64_t)1 << 22) return true;   // by any tiles
+    const MxPlan whole = mx_plan(op, a_bf16, n, d_in, d_out, experts);
+    const int64_t head = offsets ? n : mx_head(whole, op, n, d_in, d_out);
+    for (int64_t rows : {head, n - head}) {
+        if (rows == 0) continue;
+        const MxPlan P = rows == n ? whole : mx_plan(op, a_bf16, rows, d_in, d_out, 1);
+        const int lanes = P.bm == 256 ? (op == MX_GEMM_MX ? 256 : 512) : (P.bm == 128 && op == MX_GEMM_DX ? 512 : 256);
+        if (!P.stream && mx_blocks(rows, m, P.bm, P.bn, offsets ? experts : 0) * lanes > MX_MAX_LANES) return false;
+    }
+    return true;
+}
+
 template <int MODE, int P, int BM, int BN, int WM, int NW = 4, int KS = 1>
 static hipError_t mx_launch(const MxTile& t, int split, hipStream_t st) {
     const void* k = (const void*)k_mx_tile<MODE, P, BM, BN, WM, NW, KS>;
@@ -982,10 +1005,8 @@ static hipError_t mx_launch(const MxTile& t, int split, hipStream_t st) {
     static_assert(lds <= 160 * 1024, "LDS of a compute unit");
     hipError_t e = ensure_dynamic_lds(k, lds);
     if (e != hipSuccess) return e;
-    const int64_t rows = (t.n + BM - 1) / BM + (t.offsets ? t.experts : 0);
-    const int64_t tiles = rows * ((t.m + BN - 1) / BN);
-    const int64_t grid = (tiles + 7) / 8 * 8;
-    if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+    const int64_t grid = mx_blocks(t.n, t.m, BM, BN, t.offsets ? t.experts : 0);
+    if (grid * (64 * NW) > MX_MAX_LANES) return hipErrorInvalidValue;     // (refused before)
     hipLaunchKernelGGL((k_mx_tile<MODE, P, BM, BN, WM, NW, KS>), dim3((unsigned)grid, (unsigned)split), dim3(64 * NW), lds, st, t);
     GQ_LAUNCH_CHECK();
     return hipSuccess;

@@ -2,6 +2,7 @@
 // handling and the launch sequences of the GuidedQuant Fisher and of LNQ.
 #include "gq_common.h"
 #include "gq_internal.h"
+#include "gq_mx.h"
 #include "gq.h"
 
 static_assert((int)gq::ST_COUNT == (int)GQ_STAGE_COUNT, "stage ids of gq.h and the library differ");

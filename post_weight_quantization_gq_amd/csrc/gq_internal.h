@@ -134,35 +134,6 @@ hipError_t lut_pack_run(const uint8_t* P, int64_t d_out, int64_t d_in, int bits,
 hipError_t lut_gemv_run(const uint32_t* Q, const float* C, int64_t d_out, int64_t d_in, int bits,
                         const void* x, bool x_bf16, int batch, float* y, hipStream_t st);
 
-// MXFP4 rows and products (gq_mx.hip, gq_mx_mm.hip)
-constexpr int64_t MX_MAX_D = (int64_t)1 << 20;      // widest row
-constexpr int MX_MAX_EXPERTS = 4096;
-__host__ __device__ inline int64_t mx_groups(int64_t d) { return (d + 127) / 128; }
-__host__ __device__ inline int64_t mx_row_bytes(int64_t d) { return 64 * mx_groups(d); }
-__host__ __device__ inline int64_t mx_row_scales(int64_t d) { return 4 * mx_groups(d); }
-hipError_t mx_quantize_run(const void* x, bool x_bf16, int64_t rows, int64_t d, uint8_t* Q,
-                           uint8_t* S, hipStream_t st);
-hipError_t mx_dequantize_run(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t d, void* y,
-                             bool y_bf16, hipStream_t st);
-
-enum MxOp { MX_GEMM = 0, MX_GEMM_MX = 1, MX_GEMM_DX = 2 };
-// One product: a [n][k] (bfloat16, float32, or MXFP4 with as) by W [experts][d_out][d_in].
-struct MxCall {
-    MxOp op;
-    const void* a;
-    const uint8_t* as;            // scales of a (MX_GEMM_MX)
-    bool a_bf16;
-    int64_t n, d_in, d_out;
-    const uint8_t *Q, *S;
-    int experts;
-    const int64_t* offsets;       // null: one weight for all rows
-    void* y;
-    bool y_bf16;
-};
-size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts);
-bool mx_gemm_fits(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets);
-hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st);
-
 // GANQ-style assignment (gq_ganq.hip)
 struct GanqWs {
     double* A;                    // F' then its Cholesky factor L (lower) [groups][d][d]

@@ -11,8 +11,6 @@
 //
 // 8192 x 28672 bfloat16 values to MXFP4 and back: 222 us, 4.8 TB/s (a large copy on this card:
 // 5.0); one row of 4096: 1.8 us each way, the launch.
-#include "gq_common.h"
-#include "gq_internal.h"
 #include "gq_mx.h"
 
 namespace gq {

@@ -25,8 +25,6 @@
 //   1 row, 4096 -> 4096                     5.1 us on the GPU (9 MB)
 //   8 rows, 28672 -> 8192, both MXFP4       27 us    4.6 TB/s (a large copy: 5.0)
 //   96 rows over 64 experts, 2048 -> 1408   16 us    4.4 TB/s
-#include "gq_common.h"
-#include "gq_internal.h"
 #include "gq_mx.h"
 
 #include <type_traits>

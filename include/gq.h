@@ -514,8 +514,8 @@ typedef enum {
     GQ_STAGE_LNQ_SMALL,         /* sums and counters */
     GQ_STAGE_FISHER_PACK,       /* feature-major bf16 operands of the Fisher contraction */
     GQ_STAGE_LNQ_DELTA,         /* Gram and residual updates from the changed coordinates */
-    GQ_STAGE_LUT_PACK,          /* code packing: lookup-table codes, and MXFP4 both ways */
-    GQ_STAGE_LUT_GEMV,          /* products with packed weights: lookup-table and MXFP4 */
+    GQ_STAGE_LUT_PACK,          /* code packing for the lookup-table product */
+    GQ_STAGE_LUT_GEMV,          /* the lookup-table product */
     GQ_STAGE_FISHER_H2D,        /* host-to-device copies of the streamed Fisher (copy stream) */
     GQ_STAGE_GANQ_CHOL,         /* Cholesky factor of F' for the back-substitution assignment */
     GQ_STAGE_GANQ_PASS,         /* the back-substitution assignment */
@@ -526,6 +526,21 @@ void gq_timing_enable(int mask);
 gq_status gq_timing_read(double* ms, int64_t* launches);
 /* Short name of a stage ("" for an unknown id); static storage. */
 const char* gq_stage_name(int stage);
+
+/*
+ * The MXFP4 entry points have stages of their own, beside those above, whose number is the
+ * length of the callers' arrays.  Their bits of gq_timing_enable's mask are
+ * 1 << (GQ_STAGE_COUNT + gq_mxfp4_stage); gq_timing_read_mxfp4 reads and clears them as
+ * gq_timing_read does the others (neither clears what the other reads), into
+ * ms[GQ_MXFP4_STAGE_COUNT] and launches[GQ_MXFP4_STAGE_COUNT].
+ */
+typedef enum {
+    GQ_MXFP4_STAGE_PACK = 0,    /* rows: quantisation and reading back */
+    GQ_MXFP4_STAGE_GEMM,        /* the products and the gradient */
+    GQ_MXFP4_STAGE_COUNT
+} gq_mxfp4_stage;
+
+gq_status gq_timing_read_mxfp4(double* ms, int64_t* launches);
 
 #ifdef __cplusplus
 }

@@ -39,9 +39,9 @@ EXPORTS = (
     "mxfp4_row_bytes", "mxfp4_row_scales", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_gemm_workspace_size", "mxfp4_gemm", "mxfp4_gemm_mx_workspace_size", "mxfp4_gemm_mx",
     "mxfp4_gemm_dx_workspace_size", "mxfp4_gemm_dx",
-    "gq_timing_enable", "gq_timing_read", "gq_stage_name",
+    "gq_timing_enable", "gq_timing_read", "gq_timing_read_mxfp4", "gq_stage_name",
 )
-STAGE_COUNT = 18
+STAGE_COUNT, MXFP4_STAGE_COUNT = 18, 2
 
 
 class GQError(RuntimeError):
@@ -114,6 +114,7 @@ _SIGS = {
                                      _vp, _sz, _vp]),
     "gq_timing_enable": (None, [ctypes.c_int]),
     "gq_timing_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
+    "gq_timing_read_mxfp4": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gq_stage_name": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -818,7 +819,7 @@ def mxfp4_gemm_dx(g, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=N
 STAGES = ("group_scale", "fisher_mfma", "fisher_finalize", "fisher_plain", "lnq_prepare",
           "lnq_resid", "lnq_init", "lnq_gram", "lnq_solve", "lnq_sweep", "lnq_small",
           "fisher_pack", "lnq_delta", "lut_pack", "lut_gemv", "fisher_h2d", "ganq_chol",
-          "ganq_pass")
+          "ganq_pass", "mxfp4_pack", "mxfp4_gemm")     # the last two are read on their own
 
 
 def gq_timing_enable(on=True) -> None:
@@ -839,9 +840,15 @@ def gq_timing_enable(on=True) -> None:
 
 
 def gq_timing_read() -> dict:
-    """{stage name: (milliseconds, launch sequences)} since the last read; clears."""
+    """{stage name: (milliseconds, launch sequences)} since the last read; clears.  The MXFP4
+    stages (mxfp4_pack, mxfp4_gemm) are in it where they were timed."""
     lib = library()
     ms = (ctypes.c_double * STAGE_COUNT)()
     cnt = (_i64 * STAGE_COUNT)()
     _check(lib.gq_timing_read(ms, cnt))
-    return {lib.gq_stage_name(i).decode(): (ms[i], cnt[i]) for i in range(STAGE_COUNT)}
+    times = {lib.gq_stage_name(i).decode(): (ms[i], cnt[i]) for i in range(STAGE_COUNT)}
+    ms = (ctypes.c_double * MXFP4_STAGE_COUNT)()
+    cnt = (_i64 * MXFP4_STAGE_COUNT)()
+    _check(lib.gq_timing_read_mxfp4(ms, cnt))
+    times.update((name, (ms[i], cnt[i])) for i, name in enumerate(STAGES[STAGE_COUNT:]) if cnt[i])
+    return times

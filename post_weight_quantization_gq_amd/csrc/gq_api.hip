@@ -205,18 +205,17 @@ gq_status check_options(const gq_lnq_options& o, int64_t d_in) {
     return GQ_OK;
 }
 
-}  // namespace
+// Stages of gq_timing_read, then those of gq_timing_read_mxfp4.
+constexpr int ALL_STAGES = GQ_STAGE_COUNT + GQ_MXFP4_STAGE_COUNT;
+static_assert((int)gq::ST_MXFP4_PACK == GQ_STAGE_COUNT + GQ_MXFP4_STAGE_PACK &&
+              (int)gq::ST_MXFP4_GEMM == GQ_STAGE_COUNT + GQ_MXFP4_STAGE_GEMM, "MXFP4 stage ids");
 
-extern "C" {
-
-int gq_abi_version(void) { return GQ_ABI_VERSION; }
-
-void gq_timing_enable(int mask) { gq::g_timing.store(mask & ((1 << GQ_STAGE_COUNT) - 1)); }
-
-gq_status gq_timing_read(double* ms, int64_t* launches) {
+// What the recorded events came to since they were last taken, for `count` stages from `first` on.
+gq_status timing_take(int first, int count, double* ms, int64_t* launches) {
     if (!ms || !launches) return fail(GQ_EINVAL, "null ms or launches");
+    static double total[ALL_STAGES];
+    static int64_t times[ALL_STAGES];
     std::lock_guard<std::mutex> lk(gq::g_tmu);
-    for (int i = 0; i < GQ_STAGE_COUNT; ++i) { ms[i] = 0.0; launches[i] = 0; }
     gq_status rc = GQ_OK;
     if (gq::g_err) rc = fail(GQ_EHIP, "an event record failed while timing");
     for (const gq::Mark& m : gq::g_marks) {
@@ -226,15 +225,37 @@ gq_status gq_timing_read(double* ms, int64_t* launches) {
         if (e != hipSuccess) {
             rc = hip_fail(e, "gq_timing_read");
         } else {
-            ms[m.stage] += (double)t;
-            launches[m.stage] += 1;
+            total[m.stage] += (double)t;
+            times[m.stage] += 1;
         }
         gq::g_pool.push_back(m.start);
         gq::g_pool.push_back(m.stop);
     }
     gq::g_marks.clear();
     gq::g_err = false;
+    for (int i = 0; i < count; ++i) {
+        ms[i] = total[first + i];
+        launches[i] = times[first + i];
+        total[first + i] = 0.0;
+        times[first + i] = 0;
+    }
     return rc;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gq_abi_version(void) { return GQ_ABI_VERSION; }
+
+void gq_timing_enable(int mask) { gq::g_timing.store(mask & ((1 << ALL_STAGES) - 1)); }
+
+gq_status gq_timing_read(double* ms, int64_t* launches) {
+    return timing_take(0, GQ_STAGE_COUNT, ms, launches);
+}
+
+gq_status gq_timing_read_mxfp4(double* ms, int64_t* launches) {
+    return timing_take(GQ_STAGE_COUNT, GQ_MXFP4_STAGE_COUNT, ms, launches);
 }
 
 const char* gq_stage_name(int stage) {

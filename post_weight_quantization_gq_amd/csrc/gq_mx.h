@@ -5,6 +5,9 @@
 
 namespace gq {
 
+// timer stages, behind those of the other entry points (gq_mxfp4_stage of gq.h)
+constexpr Stage ST_MXFP4_PACK = (Stage)(ST_COUNT + 0), ST_MXFP4_GEMM = (Stage)(ST_COUNT + 1);
+
 constexpr int64_t MX_MAX_D = (int64_t)1 << 20;      // widest row
 constexpr int MX_MAX_EXPERTS = 4096;
 __host__ __device__ inline int64_t mx_groups(int64_t d) { return (d + 127) / 128; }

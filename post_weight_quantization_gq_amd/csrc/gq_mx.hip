@@ -109,7 +109,7 @@ static hipError_t mx_rows_each(int64_t rows, int ppr, F f) {
 
 hipError_t mx_quantize_run(const void* x, bool x_bf16, int64_t rows, int64_t d, uint8_t* Q,
                            uint8_t* S, hipStream_t st) {
-    StageTimer tm(ST_LUT_PACK, st);
+    StageTimer tm(ST_MXFP4_PACK, st);
     const int ppr = (int)(16 * mx_groups(d));
     return mx_rows_each(rows, ppr, [&](int64_t r, int64_t n) {
         const int64_t pieces = n * ppr;
@@ -124,7 +124,7 @@ hipError_t mx_quantize_run(const void* x, bool x_bf16, int64_t rows, int64_t d, 
 
 hipError_t mx_dequantize_run(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t d, void* y,
                              bool y_bf16, hipStream_t st) {
-    StageTimer tm(ST_LUT_PACK, st);
+    StageTimer tm(ST_MXFP4_PACK, st);
     const int ppr = (int)(16 * mx_groups(d));
     return mx_rows_each(rows, ppr, [&](int64_t r, int64_t n) {
         const int64_t pieces = n * ppr;

@@ -1049,7 +1049,7 @@ static hipError_t mx_launch_size(const MxTile& t, const MxPlan& pl, hipStream_t 
 }
 
 hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st) {
-    StageTimer tm(ST_LUT_GEMV, st);
+    StageTimer tm(ST_MXFP4_GEMM, st);
     const MxPlan whole = mx_plan(c.op, c.a_bf16, c.n, c.d_in, c.d_out, c.experts);
     const int64_t k = c.op == MX_GEMM_DX ? c.d_out : c.d_in, m = c.op == MX_GEMM_DX ? c.d_in : c.d_out;
     MxTile t{};

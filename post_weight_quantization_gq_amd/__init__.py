@@ -10,7 +10,7 @@ from .binding import (  # noqa: F401
     grid_quantize, lut_packed_row_words,
     lut_pack_codes, lut_gemv, mxfp4_row_bytes, mxfp4_row_scales, mxfp4_quantize,
     mxfp4_dequantize, mxfp4_gemm, mxfp4_gemm_mx, mxfp4_gemm_dx, mxfp4_gemm_workspace_size,
-    mxfp4_gemm_mx_workspace_size, mxfp4_gemm_dx_workspace_size, gq_fisher_accumulate_host, fisher_stream_workspace_size,
+    mxfp4_gemm_mx_workspace_size, mxfp4_gemm_dx_workspace_size, mxfp4_plan, gq_fisher_accumulate_host, fisher_stream_workspace_size,
     ganq_workspace_size, ganq_quantize, ganq_factor_damped,
     fisher_workspace_size,
     lnq_workspace_size, gq_timing_enable, gq_timing_read, EXPORTS, GQ_F32, GQ_BF16,

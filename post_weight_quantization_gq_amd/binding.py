@@ -38,7 +38,7 @@ EXPORTS = (
     "ganq_workspace_size", "ganq_quantize", "ganq_factor_damped",
     "mxfp4_row_bytes", "mxfp4_row_scales", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_gemm_workspace_size", "mxfp4_gemm", "mxfp4_gemm_mx_workspace_size", "mxfp4_gemm_mx",
-    "mxfp4_gemm_dx_workspace_size", "mxfp4_gemm_dx",
+    "mxfp4_gemm_dx_workspace_size", "mxfp4_gemm_dx", "mxfp4_plan",
     "gq_timing_enable", "gq_timing_read", "gq_timing_read_mxfp4", "gq_stage_name",
 )
 STAGE_COUNT, MXFP4_STAGE_COUNT = 18, 2
@@ -112,6 +112,8 @@ _SIGS = {
     "mxfp4_gemm_dx_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
     "mxfp4_gemm_dx": (ctypes.c_int, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _i32,
                                      _vp, _sz, _vp]),
+    "mxfp4_plan": (ctypes.c_int, [_i32, _i32, _i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_i32),
+                                  ctypes.POINTER(_i64)]),
     "gq_timing_enable": (None, [ctypes.c_int]),
     "gq_timing_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gq_timing_read_mxfp4": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
@@ -699,6 +701,17 @@ def mxfp4_gemm_mx_workspace_size(n, d_in, d_out, experts=1) -> int:
 
 def mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts=1, dtype=GQ_BF16) -> int:
     return int(library().mxfp4_gemm_dx_workspace_size(n, d_in, d_out, experts, dtype))
+
+
+def mxfp4_plan(op: str, n, d_in, d_out, experts=None, dtype=GQ_BF16) -> dict:
+    """How a product ("gemm", "gemm_mx" or "gemm_dx") of these sizes is done: planes, streamed,
+    rows and cols of a tile, waves of a block, split; first_rows < n where a call is divided in
+    two products (the plan is the first's).  experts: None for one weight, else their number."""
+    plan, first = (_i32 * 6)(), _i64()
+    _check(library().mxfp4_plan(("gemm", "gemm_mx", "gemm_dx").index(op), dtype, n, d_in, d_out,
+                                experts or 1, experts is not None, plan, ctypes.byref(first)))
+    names = ("planes", "streamed", "rows", "cols", "waves", "split")
+    return dict(zip(names, plan), first_rows=first.value)
 
 
 def _mx_weight(Q, S, d_in, offsets, index):

@@ -888,10 +888,9 @@ size_t mxfp4_gemm_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int3
     return mx_workspace(gq::MX_GEMM_DX, g_dt, n, d_in, d_out, experts);
 }
 
-static gq_status mx_product(gq::MxOp op, const void* a, const uint8_t* as, gq_dtype a_dt, int64_t n,
-                            int64_t d_in, const uint8_t* Q, const uint8_t* S, int64_t d_out,
-                            int32_t experts, const int64_t* offsets, void* y, gq_dtype y_dt,
-                            void* ws, size_t ws_bytes, void* stream, const char* name) {
+// Types and sizes of a product, in the order of the checks of every entry point.
+static gq_status mx_sizes_check(gq_dtype a_dt, gq_dtype y_dt, int64_t n, int64_t d_in, int64_t d_out,
+                                int32_t experts) {
     if (!dtype_ok(a_dt) || !dtype_ok(y_dt)) return fail(GQ_EDTYPE, "unsupported dtype");
     if (n < 0 || d_in < 1 || d_out < 1)
         return fail(GQ_ESHAPE, "n=%lld d_in=%lld d_out=%lld", (long long)n, (long long)d_in,
@@ -900,6 +899,15 @@ static gq_status mx_product(gq::MxOp op, const void* a, const uint8_t* as, gq_dt
     if (!mx_sizes_ok(n, d_in, d_out, experts))
         return fail(GQ_ENOTIMPL, "n=%lld d_in=%lld d_out=%lld experts=%d: at most 2^31 - 1, 2^20, "
                     "2^20 and 4096", (long long)n, (long long)d_in, (long long)d_out, experts);
+    return GQ_OK;
+}
+
+static gq_status mx_product(gq::MxOp op, const void* a, const uint8_t* as, gq_dtype a_dt, int64_t n,
+                            int64_t d_in, const uint8_t* Q, const uint8_t* S, int64_t d_out,
+                            int32_t experts, const int64_t* offsets, void* y, gq_dtype y_dt,
+                            void* ws, size_t ws_bytes, void* stream, const char* name) {
+    gq_status rc = mx_sizes_check(a_dt, y_dt, n, d_in, d_out, experts);
+    if (rc != GQ_OK) return rc;
     if (experts > 1 && !offsets) return fail(GQ_EINVAL, "several experts need offsets");
     if ((uintptr_t)offsets & 7u) return fail(GQ_EINVAL, "offsets must be 8-byte aligned");
     if (n == 0) return GQ_OK;
@@ -932,11 +940,26 @@ static gq_status mx_product(gq::MxOp op, const void* a, const uint8_t* as, gq_dt
         if (mx_overlap(y, y_len, ws, w_len)) return fail(GQ_EINVAL, "the output must not overlap ws");
     }
     Scratch s;
-    gq_status rc = s.acquire(ws, ws_bytes, need, st);
+    rc = s.acquire(ws, ws_bytes, need, st);
     if (rc != GQ_OK) return rc;
     const gq::MxCall c{op, a, as, ab, n, d_in, d_out, Q, S, experts, offsets, y, y_dt == GQ_BF16};
     hipError_t e = gq::mx_gemm_run(c, s.ptr, st);
     return e == hipSuccess ? GQ_OK : hip_fail(e, name);
+}
+
+gq_status mxfp4_plan(int32_t op, gq_dtype a_dt, int64_t n, int64_t d_in, int64_t d_out,
+                     int32_t experts, int32_t grouped, int32_t plan[6], int64_t* first_rows) {
+    if (op < gq::MX_GEMM || op > gq::MX_GEMM_DX) return fail(GQ_EINVAL, "op=%d outside [0, 2]", op);
+    if (!plan || !first_rows) return fail(GQ_EINVAL, "null plan or first_rows");
+    if (op == gq::MX_GEMM_MX) a_dt = GQ_BF16;
+    gq_status rc = mx_sizes_check(a_dt, GQ_F32, n, d_in, d_out, experts);
+    if (rc != GQ_OK) return rc;
+    if (n < 1) return fail(GQ_ESHAPE, "n=%lld: no rows, no plan", (long long)n);
+    if (experts > 1 && !grouped) return fail(GQ_EINVAL, "several experts need offsets");
+    int32_t v[6];
+    *first_rows = gq::mx_gemm_plan((gq::MxOp)op, a_dt == GQ_BF16, n, d_in, d_out, experts, grouped != 0, v);
+    for (int i = 0; i < 6; ++i) plan[i] = v[i];
+    return GQ_OK;
 }
 
 gq_status mxfp4_gemm(const void* x, gq_dtype x_dt, int64_t n, int64_t d_in, const uint8_t* Q,

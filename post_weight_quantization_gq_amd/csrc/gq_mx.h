@@ -34,6 +34,8 @@ struct MxCall {
 };
 size_t mx_gemm_workspace(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts);
 bool mx_gemm_fits(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets);
+// planes, streamed, rows and columns of a tile, waves, split; returns the rows that the first product takes
+int64_t mx_gemm_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets, int32_t (&plan)[6]);
 hipError_t mx_gemm_run(const MxCall& c, void* ws, hipStream_t st);
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));

@@ -979,6 +979,19 @@ static int64_t mx_blocks(int64_t n, int64_t m, int bm, int bn, int64_t part_empt
 // 2^18 columns each, would take more.
 constexpr int64_t MX_MAX_LANES = ((int64_t)1 << 32) - 1;
 
+static int mx_waves(const MxPlan& P, MxOp op) {
+    return P.stream ? P.waves : ((P.bm == 256 && op != MX_GEMM_MX) || (P.bm == 128 && op == MX_GEMM_DX) ? 8 : 4);
+}
+
+int64_t mx_gemm_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets, int32_t (&plan)[6]) {
+    MxPlan P = mx_plan(op, a_bf16, n, d_in, d_out, experts);
+    const int64_t head = offsets ? n : mx_head(P, op, n, d_in, d_out);
+    if (head < n) P = mx_plan(op, a_bf16, head, d_in, d_out, 1);
+    const int32_t v[6] = {P.planes, P.stream, P.bm, P.bn, mx_waves(P, op), P.split};
+    for (int i = 0; i < 6; ++i) plan[i] = v[i];
+    return head;
+}
+
 bool mx_gemm_fits(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets) {
     const int64_t m = op == MX_GEMM_DX ? d_in : d_out;
     if ((n / 32 + 1 + experts) * ((m + 127) / 128) < (int64_t)1 << 22) return true;   // by any tiles
@@ -987,8 +1000,7 @@ bool mx_gemm_fits(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_out, 
     for (int64_t rows : {head, n - head}) {
         if (rows == 0) continue;
         const MxPlan P = rows == n ? whole : mx_plan(op, a_bf16, rows, d_in, d_out, 1);
-        const int lanes = P.bm == 256 ? (op == MX_GEMM_MX ? 256 : 512) : (P.bm == 128 && op == MX_GEMM_DX ? 512 : 256);
-        if (!P.stream && mx_blocks(rows, m, P.bm, P.bn, offsets ? experts : 0) * lanes > MX_MAX_LANES) return false;
+        if (!P.stream && mx_blocks(rows, m, P.bm, P.bn, offsets ? experts : 0) * 64 * mx_waves(P, op) > MX_MAX_LANES) return false;
     }
     return true;
 }

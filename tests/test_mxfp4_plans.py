@@ -6,6 +6,8 @@ import pytest
 import post_weight_quantization_gq_amd as gq
 from post_weight_quantization_gq_amd import binding as B
 
+from _mx_cases import CASES, kernels
+
 
 def _far(i):
     return ctypes.c_void_p(i << 56)         # apart, aligned, never dereferenced
@@ -46,3 +48,44 @@ def test_fewer_tiles_are_taken(name, n, k, m, experts, offsets):
     for dt in (gq.GQ_F32, gq.GQ_BF16):
         status, message = _product(name, n, d_in, d_out, experts, offsets, dt)
         assert status == B.GQ_EINVAL and "overlap" in message, message
+
+
+def test_the_kernels_cases_reach_every_kernel():
+    """Whatever a sweep over rows, widths, experts and types can choose is run by a case of the
+    kernels' tests."""
+    covered = set().union(*(kernels(*c) for c in CASES))
+    rows = (1, 2, 8, 15, 16, 17, 24, 32, 33, 64, 65, 100, 128, 129, 200, 256, 257, 333, 512, 700, 1024,
+            1500, 2048, 3000, 4096, 6000, 8192, 20000)
+    widths = (1, 32, 64, 200, 512, 640, 1000, 1100, 2048, 4096, 5000, 8192, 11008, 14336, 28672, 100000)
+    missing = {}
+    for op, dtype in (("gemm", "bf16"), ("gemm", "f32"), ("gemm_mx", "mx"), ("gemm_dx", "bf16"),
+                      ("gemm_dx", "f32")):
+        for n in rows:
+            for d_in in widths:
+                for d_out in widths:
+                    for experts in (None, 1, 2, 8, 64, 300):
+                        case = (op, dtype, n, d_in, d_out, experts)
+                        for k in kernels(*case) - covered:
+                            missing.setdefault(k, case)
+    assert not missing
+
+
+def test_plan_refusals():
+    lib = gq.library()
+    plan, first = (ctypes.c_int32 * 6)(), ctypes.c_int64()
+
+    def status(op=0, dt=1, n=8, d_in=128, d_out=128, experts=1, grouped=0, plan=plan, first=ctypes.byref(first)):
+        return lib.mxfp4_plan(op, dt, n, d_in, d_out, experts, grouped, plan, first)
+
+    assert status() == B.GQ_OK and first.value == 8 and list(plan)[:2] == [1, 1]
+    assert status(op=3) == B.GQ_EINVAL and status(op=-1) == B.GQ_EINVAL
+    assert status(dt=2) == B.GQ_EDTYPE and status(op=1, dt=2) == B.GQ_OK
+    assert status(n=0) == B.GQ_ESHAPE and status(d_in=0) == B.GQ_ESHAPE and status(d_out=-1) == B.GQ_ESHAPE
+    assert status(n=1 << 31) == B.GQ_ENOTIMPL and status(d_in=(1 << 20) + 1) == B.GQ_ENOTIMPL
+    assert status(experts=0) == B.GQ_EINVAL and status(experts=2) == B.GQ_EINVAL
+    assert status(experts=2, grouped=1) == B.GQ_OK and status(experts=4097, grouped=1) == B.GQ_ENOTIMPL
+    assert status(plan=None) == B.GQ_EINVAL and status(first=None) == B.GQ_EINVAL
+    with pytest.raises(ValueError):
+        gq.mxfp4_plan("gemv", 8, 128, 128)
+    with pytest.raises(gq.GQError):
+        gq.mxfp4_plan("gemm", 8, 0, 128)

@@ -1,5 +1,11 @@
 """GPU tests of every kernel, tile and split of the MXFP4 products (the sizes of _mx_cases).
 
+Selection.  Each output has one nonzero weight, a power of two, so it is one activation times it:
+exact in float32, however the terms are ordered or split (float32 activations are the sum of three
+bfloat16 planes of 8 bits each, and so is every partial sum), and rounded once to bfloat16.  The
+outputs have to be equal: a plane, a stage, a scale or a block lost, stale or in the wrong place
+shows as such, which a bound over sums of thousands of terms would not see.
+
 Dense.  Random codes under random scales against float64, by the bound of the other MXFP4 tests:
 T terms, products exact, every float32 addition off by at most 2^-23 of a partial sum that is at
 most A = sum |a w|: |y - y64| <= (T + 8) 2^-23 A, T = K, or 3 K for three planes (whose sizes sum
@@ -54,6 +60,25 @@ def _codes(gen, shape, d, device):
     return codes
 
 
+def _selecting_weight(gen, op, E, d_out, d_in, device):
+    """Packed weights in which each output (a row, for the gradient a column) has one nonzero, a
+    power of two: (Q, S, index [E][outputs] of the contraction, value [E][outputs] float64)."""
+    codes = torch.zeros((E, d_out, 128 * -(-d_in // 128)), dtype=torch.uint8, device=device)
+    S = _scales(gen, (E, d_out), d_in, device)
+    K, m = (d_out, d_in) if op == "gemm_dx" else (d_in, d_out)
+    # spread evenly over the contraction, from a random start, in a random order
+    at = (torch.arange(m, device=device) * K // m + torch.randint(0, K, (E, 1), generator=gen, device=device)) % K
+    at = at[:, torch.randperm(m, generator=gen, device=device)]
+    pick = torch.tensor([1, 2, 4, 6], dtype=torch.uint8, device=device)        # 0.5, 1, 2, 4
+    code = pick[torch.randint(0, 4, (E, m), generator=gen, device=device)]
+    code += 8 * torch.randint(0, 2, (E, m), generator=gen, device=device).to(torch.uint8)
+    e, o = torch.arange(E, device=device)[:, None], torch.arange(m, device=device)[None]
+    row, col = (at, o.expand(E, m)) if op == "gemm_dx" else (o.expand(E, m), at)
+    codes[e, row, col] = code
+    value = VALUES.to(device)[(code & 7).long()] * (1 - 2 * (code >> 3).long())
+    return _pack(codes), S, at, value * _power(S[e, row, col // 32].long() - 127)
+
+
 def _offsets(gen_np, n, E):
     """Rows before the first expert, empty experts, one with many, rows behind the last."""
     lo, hi = min(2, n // 4), n - min(3, n // 4)
@@ -66,10 +91,10 @@ def _offsets(gen_np, n, E):
 class _Call:
     """Activations, offsets and the call of a case for given weights."""
 
-    def __init__(self, case, device):
+    def __init__(self, case, device, exact):
         self.op, self.dtype, self.n, self.d_in, self.d_out, self.experts = case
         self.E = self.experts or 1
-        seed = sum((i + 1) * v for i, v in enumerate((self.n, self.d_in, self.d_out, self.E)))
+        seed = sum((i + 1) * v for i, v in enumerate((self.n, self.d_in, self.d_out, self.E))) + exact
         self.gen = torch.Generator(device=device)
         self.gen.manual_seed(seed)
         gen, n = self.gen, self.n
@@ -80,10 +105,18 @@ class _Call:
         self.off = torch.tensor(self.at, device=device) if self.experts else None
         if self.dtype == "mx":
             codes = _codes(gen, (n,), self.K, device)
+            if exact:
+                codes[..., :self.K] |= 1                                   # no zeros
             self.x = _pack(codes), _scales(gen, (n,), self.K, device)
             self.a = _decode(*self.x, self.K)
             return
-        x = torch.randn((n, self.K), generator=gen, device=device)
+        if exact:        # every bit of the mantissa in use
+            bits = 24 if self.dtype == "f32" else 8
+            x = torch.randint(1 << (bits - 1), 1 << bits, (n, self.K), generator=gen, device=device).double()
+            x *= 1 - 2 * torch.randint(0, 2, (n, self.K), generator=gen, device=device)
+            x *= _power(torch.randint(-40, 20, (n, self.K), generator=gen, device=device))
+        else:
+            x = torch.randn((n, self.K), generator=gen, device=device)
         self.x = x.to(F32 if self.dtype == "f32" else BF)
         self.a = self.x.double()
 
@@ -104,8 +137,20 @@ class _Call:
 
 
 @pytest.mark.parametrize("case", CASES, ids=_ids)
+def test_one_term_a_product_is_exact(device, case):
+    c = _Call(case, device, exact=True)
+    Q, S, index, value = _selecting_weight(c.gen, c.op, c.E, c.d_out, c.d_in, device)
+    for out in (F32, BF):
+        y = c.run(Q, S, out)
+        for e, r in c.parts():
+            want = c.a[r][:, index[e]] * value[e]
+            assert torch.equal(want.to(F32).double(), want)              # one float32 value
+            assert torch.equal(y[r], want.to(F32).to(out)), (out, e)
+
+
+@pytest.mark.parametrize("case", CASES, ids=_ids)
 def test_dense_against_float64(device, case):
-    c = _Call(case, device)
+    c = _Call(case, device, exact=False)
     codes = _codes(c.gen, (c.E, c.d_out), c.d_in, device)
     Q, S = _pack(codes), _scales(c.gen, (c.E, c.d_out), c.d_in, device, low=-4, high=5)
     del codes

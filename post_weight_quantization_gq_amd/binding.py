@@ -765,16 +765,56 @@ def _mx_product(fn, size, x, first, size_args, n, width, Q, S, last, experts, of
     return y
 
 
+class _MxProduct(torch.autograd.Function):
+    """mxfp4_gemm as a function of x or, with `back`, mxfp4_gemm_dx as one of g: the weight is
+    fixed and both are linear, so each one's gradient is the other."""
+
+    @staticmethod
+    def forward(ctx, a, Q, S, d_in, offsets, out_dtype, ws, back):
+        ctx.save_for_backward(Q, S, offsets)
+        ctx.d_in, ctx.dtype, ctx.back = d_in, a.dtype, back
+        if back:
+            return mxfp4_gemm_dx(a, Q, S, d_in, offsets=offsets, out_dtype=out_dtype, ws=ws)
+        return mxfp4_gemm(a, Q, S, offsets=offsets, out_dtype=out_dtype, ws=ws)
+
+    @staticmethod
+    def backward(ctx, grad):
+        Q, S, offsets = ctx.saved_tensors
+        grad = grad.contiguous()
+        if grad.data_ptr() & 15:           # a part of a larger gradient, off the rows' alignment
+            grad = grad.clone()
+        if ctx.back:
+            d = mxfp4_gemm(grad, Q, S, offsets=offsets, out_dtype=ctx.dtype)
+        else:
+            d = mxfp4_gemm_dx(grad, Q, S, ctx.d_in, offsets=offsets, out_dtype=ctx.dtype)
+        return d, None, None, None, None, None, None, None
+
+
+def _mx_recorded(a, name, Q, S, d_in, offsets, y, out_dtype, ws, stream, back):
+    """A product of activations that require a gradient, as autograd records it: its backward
+    pass runs on the stream of the call."""
+    if y is not None:
+        raise GQError(GQ_EINVAL, f"{name} requires a gradient, which a given y would not carry: "
+                                 "call without y, or under torch.no_grad()")
+    _mx_tensor(a, name, a.get_device())
+    where, _ = _place(a, stream)
+    with where:
+        return _MxProduct.apply(a, Q, S, d_in, offsets, out_dtype, ws, back)
+
+
 def mxfp4_gemm(x, Q, S, offsets=None, y=None, out_dtype=None, ws=None, stream=None) -> torch.Tensor:
     """y [n][d_out] = x W^T for x [n][d_in] (float32 or bfloat16) and the packed weight (Q, S)
     of mxfp4_quantize.  With offsets (int64 [experts + 1] on the device) rows offsets[e] ..
     offsets[e + 1] - 1 of x are multiplied by weight e of Q [experts][d_out][row bytes], and
     the other rows of a given y keep their values (of a new one: zeros).
-    out_dtype: float32 or bfloat16, x's unless given."""
+    out_dtype: float32 or bfloat16, x's unless given.
+    Where x requires a gradient, autograd gets it by mxfp4_gemm_dx (and y cannot be given)."""
     lib = _lib or library()
     if x.dim() != 2:
         raise GQError(GQ_ESHAPE, "x must be [n][d_in]")
     n, d_in = x.shape
+    if x.requires_grad and torch.is_grad_enabled():
+        return _mx_recorded(x, "x", Q, S, d_in, offsets, y, out_dtype, ws, stream, False)
     index = x.get_device()
     experts, d_out = _mx_weight(Q, S, d_in, offsets, index)
     _mx_tensor(x, "x", index)
@@ -789,7 +829,8 @@ def mxfp4_gemm(x, Q, S, offsets=None, y=None, out_dtype=None, ws=None, stream=No
 def mxfp4_gemm_mx(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,
                   stream=None) -> torch.Tensor:
     """mxfp4_gemm with the activations packed by mxfp4_quantize as well: XQ [n][row bytes],
-    XS [n][row scales].  out_dtype: bfloat16 unless given."""
+    XS [n][row scales].  out_dtype: bfloat16 unless given.  Bytes carry no gradient: autograd
+    does not reach what they were packed from (mxfp4_gemm_dx is the product's part of it)."""
     lib = _lib or library()
     if XQ.dim() != 2:
         raise GQError(GQ_ESHAPE, "XQ must be [n][row bytes]")
@@ -812,10 +853,13 @@ def mxfp4_gemm_dx(g, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=N
                   stream=None) -> torch.Tensor:
     """dx [n][d_in] = g W for the output's gradient g [n][d_out] (float32 or bfloat16): the
     gradient of mxfp4_gemm's x (and, straight through the rounding, of the values that
-    mxfp4_gemm_mx's were packed from).  Grouped by offsets like mxfp4_gemm."""
+    mxfp4_gemm_mx's were packed from).  Grouped by offsets like mxfp4_gemm.
+    Where g requires a gradient, autograd gets it by mxfp4_gemm (and y cannot be given)."""
     lib = _lib or library()
     if g.dim() != 2:
         raise GQError(GQ_ESHAPE, "g must be [n][d_out]")
+    if g.requires_grad and torch.is_grad_enabled():
+        return _mx_recorded(g, "g", Q, S, d_in, offsets, y, out_dtype, ws, stream, True)
     n = g.shape[0]
     index = g.get_device()
     experts, d_out = _mx_weight(Q, S, d_in, offsets, index)

@@ -186,24 +186,56 @@ struct MxPlace {
     bool ok;
 };
 
+// Tiles of bm rows that expert e's rows make, the first `skip` left out.
+__device__ __forceinline__ int mx_row_tiles(const MxTile& p, int bm, int e, int skip = 0) {
+    if (e >= p.experts) return 0;
+    int64_t lo, hi;
+    mx_expert_rows(p.offsets, e, p.n, lo, hi);
+    lo += (int64_t)skip * bm;
+    return hi > lo ? (int)((hi - lo + bm - 1) / bm) : 0;
+}
+
+// Row tile `row` of the experts' (without the first `skip` of each) in their order, counted from
+// the offsets by each wave for itself, 64 experts at a time; not ok past the last one.
+__device__ __forceinline__ void mx_row_tile(const MxTile& p, int bm, int row, MxPlace& r, int skip = 0) {
+    const int lane = threadIdx.x & 63;
+    r.ok = false;
+    int first = 0;
+    for (int b = 0; b < p.experts; b += 64) {
+        const int c = mx_row_tiles(p, bm, b + lane, skip);
+        if (skip && !__ballot(c > 0)) continue;
+        int s = c;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(s, o, 64);
+            if (lane >= o) s += v;
+        }
+        const unsigned long long hit = __ballot(first + s > row);
+        if (hit) {
+            const int l = __ffsll((unsigned long long)hit) - 1;
+            r.e = __builtin_amdgcn_readfirstlane(b + l);
+            const int before = __builtin_amdgcn_readfirstlane(first + __shfl(s - c, l, 64));
+            int64_t lo, hi;
+            mx_expert_rows(p.offsets, r.e, p.n, lo, hi);
+            r.t0 = lo + (int64_t)(skip + row - before) * bm;
+            r.rows = (int)(hi - r.t0 < bm ? hi - r.t0 : bm);
+            r.ok = row >= before && r.rows > 0;     // (offsets out of order could count wrongly)
+            return;
+        }
+        first += __builtin_amdgcn_readfirstlane(__shfl(s, 63, 64));
+    }
+}
+
 // Block hw -> its tile.  XCD x (= hw % 8) takes a contiguous eighth of the tiles, which run
 // row-tile fastest within groups of 8 row tiles, so the blocks that one L2 serves at a time
-// share both operands.  With several experts the row tiles are counted from the offsets,
-// by each wave for itself.
+// share both operands.
 __device__ __forceinline__ MxPlace mx_place(const MxTile& p, int bm, int ncol) {
-    const int lane = threadIdx.x & 63;
-    auto tiles = [&](int e) -> int {
-        if (e >= p.experts) return 0;
-        int64_t lo, hi;
-        mx_expert_rows(p.offsets, e, p.n, lo, hi);
-        return hi > lo ? (int)((hi - lo + bm - 1) / bm) : 0;
-    };
     MxPlace r;
     r.ok = false;
     int64_t nrow;
     if (p.offsets) {
         int c = 0;
-        for (int b = 0; b < p.experts; b += 64) c += tiles(b + lane);
+        for (int b = 0; b < p.experts; b += 64) c += mx_row_tiles(p, bm, b + (threadIdx.x & 63));
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) c += __shfl_xor(c, o, 64);
         nrow = __builtin_amdgcn_readfirstlane(c);
@@ -217,32 +249,10 @@ __device__ __forceinline__ MxPlace mx_place(const MxTile& p, int bm, int ncol) {
     const int64_t g = lin / (H * ncol), rest = lin - g * (H * ncol);
     const int64_t left = nrow - g * H;
     const int64_t h = left < H ? left : H;
-    int64_t row = g * H + rest % h;
+    const int64_t row = g * H + rest % h;
     r.col = (int)(rest / h);
     if (p.offsets) {
-        int first = 0;
-        for (int b = 0; b < p.experts; b += 64) {
-            const int c = tiles(b + lane);
-            int s = c;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int v = __shfl_up(s, o, 64);
-                if (lane >= o) s += v;
-            }
-            const unsigned long long hit = __ballot(first + s > (int)row);
-            if (hit) {
-                const int l = __ffsll((unsigned long long)hit) - 1;
-                r.e = __builtin_amdgcn_readfirstlane(b + l);
-                const int before = __builtin_amdgcn_readfirstlane(first + __shfl(s - c, l, 64));
-                int64_t lo, hi;
-                mx_expert_rows(p.offsets, r.e, p.n, lo, hi);
-                r.t0 = lo + (row - before) * bm;
-                r.rows = (int)(hi - r.t0 < bm ? hi - r.t0 : bm);
-                r.ok = row >= before && r.rows > 0;     // (offsets out of order could count wrongly)
-                return r;
-            }
-            first += __builtin_amdgcn_readfirstlane(__shfl(s, 63, 64));
-        }
+        mx_row_tile(p, bm, (int)row, r);
         return r;
     }
     r.e = 0;
@@ -687,14 +697,24 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
 // ---------------------------------------------------------------------------
 // Few rows: the weight is streamed once, each wave on its own, without a barrier before the end
 // (one row 4096 -> 4096: 5.1 us; by tiles 8.0 and 4.0 for the sum of the split).  A block takes 16 MT output
-// columns of one weight and up to 16 rows of activations at a time; its waves share out the
-// contraction and their sums are added in the waves' order at the end.  A wave copies pieces of
+// columns of one weight and 16 rows of activations at a time; its waves share out the contraction and
+// their sums are added in the waves' order at the end.  A wave copies pieces of
 // KU groups of 128 values of its 16 MT weight rows into LDS of its own, one piece ahead: read
 // straight into registers, 16 consecutive lanes would touch 16 rows and take four times the
 // address cycles.  Lane (r, b) then holds block b of a group of column r's weight (16 bytes),
 // dequantised in place to the products' left operand, and the same 32 values of row r of the
 // activations; the order of the values within a product is free.
+//
+// The plan knows the mean of the experts' rows alone.  An expert's block takes its first two groups of
+// 16 rows, and what experts have beyond those is spread over blocks of its own, up to one a compute
+// unit, that find their groups from the offsets.  3040 rows, 190 experts of 8192 -> 128: evenly
+// routed 52 us, by a lognormal of 0.7 63, all to one expert 63; with every group left to its
+// expert's block 52, 92 and 1930.  Where no expert has more than 32 of over 32 rows those blocks end at
+// once, which takes 0 to 1 us (128 rows, 8 of 4096 -> 1024: 10.9 us, 10.1 without).  With one group
+// or four a block: 63 and 76 us by the lognormal, but 128 rows, 8 of 4096 -> 1024 14.7 and 13.4 (two: 13.4).
 // ---------------------------------------------------------------------------
+constexpr int MX_FIRST = 2;
+
 template <int MODE, int P, int MT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
     constexpr int KU = P == 3 ? 2 : 4;           // (three planes of x fill the registers sooner)
@@ -704,17 +724,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     u32x4* const ring = mx_lds + wave * 2 * PIECE;
     auto sums = [&](int w, int t) { return (float*)(mx_lds + w * 2 * PIECE) + 256 * t; };    // over the rings at the end
-    const int e = blockIdx.y;
     const int64_t j0 = (int64_t)blockIdx.x * (16 * MT);
-    int64_t lo = 0, hi = p.n;
-    if (p.offsets) mx_expert_rows(p.offsets, e, p.n, lo, hi);
     const int groups = (int)(p.qb / 64), pieces = (groups + KU - 1) / KU;
     const int shares = WAVES * (int)gridDim.z, per = (pieces + shares - 1) / shares;
     const int c0 = ((int)blockIdx.z * WAVES + wave) * per;
     const int c1 = c0 + per < pieces ? c0 + per : pieces;
 
     const int wrows = (int)(p.m - j0 < 16 * MT ? p.m - j0 : 16 * MT);
-    const int64_t row0 = (int64_t)e * p.d_out + j0;
     auto swizzle = [](int row) { return KU == 4 ? row & 15 : (row >> 1) & 7; };
     uint32_t wv[WS / 64];
 #pragma unroll
@@ -722,24 +738,40 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
         const int slot = i * 64 + lane, row = slot / SPR;
         wv[i] = (uint32_t)(row * p.qb) + 16u * ((slot % SPR) ^ swizzle(row));
     }
-    auto copy = [&](int c) {                     // past the last piece: clears, reads nothing
-        u32x4* to = ring + (c & 1) * PIECE;
-        const __amdgpu_buffer_rsrc_t wr = mx_rsrc(p.Q + row0 * p.qb, wrows, p.qb, c < c1);
-        const __amdgpu_buffer_rsrc_t sr = mx_rsrc(p.S + row0 * p.sb, wrows, p.sb, c < c1);
+    // This block's rows, 16 at a time: its expert's first MX_FIRST groups of them, or every step-th of
+    // the groups that experts have beyond those.
+    const int beyond = (int)blockIdx.y - p.experts, step = (int)gridDim.y - p.experts;
+    int64_t lo = 0, hi = p.n;
+    if (p.offsets && beyond < 0) mx_expert_rows(p.offsets, blockIdx.y, p.n, lo, hi);
+    for (int turn = 0;; ++turn) {
+        MxPlace place;
+        if (beyond < 0) {
+            place.e = blockIdx.y;
+            place.t0 = lo + 16 * turn;
+            place.rows = (int)(hi - place.t0 < 16 ? hi - place.t0 : 16);
+            place.ok = turn < MX_FIRST && place.rows > 0;
+        } else {
+            mx_row_tile(p, 16, beyond + turn * step, place, MX_FIRST);
+        }
+        if (!place.ok) return;
+        if (turn > 0) __syncthreads();           // the sums of the rows before have been read
+        const int rows = place.rows;
+        const int64_t t0 = place.t0, row0 = (int64_t)place.e * p.d_out + j0;
+        auto copy = [&](int c) {                     // past the last piece: clears, reads nothing
+            u32x4* to = ring + (c & 1) * PIECE;
+            const __amdgpu_buffer_rsrc_t wr = mx_rsrc(p.Q + row0 * p.qb, wrows, p.qb, c < c1);
+            const __amdgpu_buffer_rsrc_t sr = mx_rsrc(p.S + row0 * p.sb, wrows, p.sb, c < c1);
 #pragma unroll
-        for (int i = 0; i < WS / 64; ++i) mx_dma(wr, to + 64 * i, wv[i], (uint32_t)c * (16u * SPR));
-        mx_dma(sr, to + WS, lane < 16 * MT ? (uint32_t)(lane * p.sb) : 0xC0000000u, (uint32_t)c * (4u * KU));
-    };
+            for (int i = 0; i < WS / 64; ++i) mx_dma(wr, to + 64 * i, wv[i], (uint32_t)c * (16u * SPR));
+            mx_dma(sr, to + WS, lane < 16 * MT ? (uint32_t)(lane * p.sb) : 0xC0000000u, (uint32_t)c * (4u * KU));
+        };
 
-    for (int64_t t0 = lo; t0 < hi; t0 += 16) {
-        const int rows = (int)(hi - t0 < 16 ? hi - t0 : 16);
         const int64_t xrow = t0 + (r < rows ? r : rows - 1);
         const uint8_t* const xp = p.A + xrow * p.a_row;
         const uint8_t* const xsp = MODE == MX_GEMM_MX ? p.AS + xrow * p.sb : nullptr;
         f32x4 acc[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (t0 > lo) __syncthreads();            // the sums of the rows before have been read
         if (c0 < c1) copy(c0);
         for (int c = c0; c < c1; ++c) {
             // this piece's activations, then the next piece's copies: once those alone are in
@@ -772,12 +804,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
             const uint8_t* const at = (const uint8_t*)(ring + (c & 1) * PIECE);
 #pragma unroll
             for (int h = 0; h < KU; ++h) {
-                const bool own = KU * c + h < groups;         // else codes and scales of the next row
+                const bool has = KU * c + h < groups;         // else codes and scales of the next row
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     const int row = 16 * t + r;
                     const u32x4 w = *(const u32x4*)(at + 16 * (row * SPR + ((4 * h + b) ^ swizzle(row))));
-                    const uint32_t sb = at[16 * (WS + row) + 4 * h + b], sc = own ? sb : 127u;
+                    const uint32_t sb = at[16 * (WS + row) + 4 * h + b], sc = has ? sb : 127u;
                     if constexpr (MODE == MX_GEMM_MX) {
                         const i32x8 wa{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
                         const i32x8 xa{(int)x[h][0][0], (int)x[h][0][1], (int)x[h][0][2], (int)x[h][0][3], 0, 0, 0, 0};
@@ -1028,7 +1060,10 @@ static hipError_t mx_launch_stream(const MxTile& t, const MxPlan& pl, hipStream_
     const size_t lds = (size_t)WAVES * 2 * (16 * MT * 4 * KU + 64) * 16;
     const hipError_t e = ensure_dynamic_lds((const void*)k_mx_stream<MODE, P, MT, WAVES>, lds);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)((t.m + 16 * MT - 1) / (16 * MT)), (unsigned)t.experts, (unsigned)pl.split);
+    // a block for each expert, and for the groups beyond its own those of a compute unit each
+    const int64_t cols = (t.m + 16 * MT - 1) / (16 * MT), far = (t.n + 15) / 16 - MX_FIRST, room = 256 / (cols * pl.split);
+    const int64_t more = !t.offsets || far < 1 ? 0 : (room < 1 ? 1 : (room < far ? room : far));
+    const dim3 grid((unsigned)cols, (unsigned)(t.experts + more), (unsigned)pl.split);
     hipLaunchKernelGGL((k_mx_stream<MODE, P, MT, WAVES>), grid, dim3(64 * WAVES), lds, st, t);
     GQ_LAUNCH_CHECK();
     return hipSuccess;

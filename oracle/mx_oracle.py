@@ -1,4 +1,4 @@
-"""fp64 CPU oracle for the MXFP4 rows and products.
+"""fp64 CPU oracle for the MXFP4 rows.
 
 TEST INFRASTRUCTURE ONLY, like gq_oracle: NumPy, float64, the plain definitions of the OCP
 Microscaling format's e2m1 elements with e8m0 scales over blocks of 32.
@@ -8,7 +8,7 @@ multiple of 128 values; one scale byte a block, 127 past the last one.
 """
 import numpy as np
 
-__all__ = ["mx_quantize", "mx_values", "mx_gemm", "MX_GRID"]
+__all__ = ["mx_quantize", "mx_values", "MX_GRID"]
 
 MX_GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
@@ -49,14 +49,3 @@ def mx_values(Q, S, d):
     v = MX_GRID[code & 7] * np.where(code & 8, -1.0, 1.0)
     scale = np.where(S == 255, np.nan, np.ldexp(1.0, S.astype(np.int64) - 127))
     return v * np.repeat(scale, 32, axis=1)[:, :d]
-
-
-def mx_gemm(a, W, offsets=None, y=None):
-    """a W^T in float64, W [d_out][d_in]; with offsets W [experts][d_out][d_in] and the rows of
-    expert e from offsets[e] on, other rows as in y."""
-    if offsets is None:
-        return a @ W.T
-    y = np.array(y, np.float64)
-    for e in range(len(W)):
-        y[offsets[e]:offsets[e + 1]] = a[offsets[e]:offsets[e + 1]] @ W[e].T
-    return y

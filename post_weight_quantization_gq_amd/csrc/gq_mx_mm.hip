@@ -17,14 +17,15 @@
 //   k_mx_join    the sum of a contraction split over blocks, where tiles are too few.
 // Several weights ("experts") are tiles of one launch; their row counts stay on the device.
 //
-// One MI355X, whole calls (kernels under a profiler: a few per cent more, by the clock):
-//   4096 rows, 11008 -> 4096, bfloat16      283 us   1.31 PFLOP/s (the library's bfloat16
-//                                                    matrix product reaches 1.20 to 1.29)
-//   8192 rows, 28672 -> 8192, both MXFP4    826 us   4.7 PFLOP/s (the instruction alone: 7.3)
-//   gradient, 4096 rows, 11008 -> 4096      307 us   1.20 PFLOP/s
-//   1 row, 4096 -> 4096                     5.1 us on the GPU (9 MB)
-//   8 rows, 28672 -> 8192, both MXFP4       27 us    4.6 TB/s (a large copy: 5.0)
-//   96 rows over 64 experts, 2048 -> 1408   16 us    4.4 TB/s
+// MI355X, calls among others of their kind; large ones vary from card to card by their clock:
+//   4096 rows, 11008 -> 4096, bfloat16      282 to 295 us   1.25 to 1.31 PFLOP/s (the library's
+//                                           bfloat16 matrix product reaches 1.20 to 1.33)
+//   8192 rows, 28672 -> 8192, both MXFP4    840 to 885 us   4.3 to 4.6 PFLOP/s (the rows packed
+//                                           before; a loop of the instruction alone: 7.3)
+//   gradient, 4096 rows, 11008 -> 4096      307 to 320 us   1.15 to 1.20 PFLOP/s
+//   1 row, 4096 -> 4096                     9 us, 5.1 of them on the GPU (9 MB)
+//   8 rows, 28672 -> 8192, both MXFP4       27 to 29 us on the GPU, 4.3 to 4.6 TB/s (a large copy: 5.0)
+//   96 rows over 64 experts, 2048 -> 1408   16 us           4.4 TB/s
 #include "gq_mx.h"
 
 #include <type_traits>
@@ -105,14 +106,17 @@ __global__ __launch_bounds__(256) void k_mx_stage(const void* __restrict__ x, in
 // Gradient.  The contraction runs over the weight's rows, but its codes lie along the columns: a
 // lane reads 8 columns (4 bytes) of 8 rows, converts pairs along the columns and exchanges halves
 // of two rows' words, which gives 8 fragments of 8 rows each.  Conversions and exchanges are one
-// instruction each a product, which with the addresses fills the vector unit (half the cycles)
-// beside the matrix cores (half): this bounds it.
+// instruction each a product; with the addresses three vector instructions stand beside each product,
+// 38 per cent of a prompt's cycles next to the matrix cores' 49, and the waves wait for a quarter.
 //
 // Outputs leave by way of LDS as whole lines; stored from the accumulators, each store touched 32
 // rows (fp4 prompt 1006 -> 918 us, 32 experts 155 -> 128 us).
 //
-// What bounds the large tiles now is power: the clock falls to 1.75 GHz (fp4) and 1.87 GHz
-// (bfloat16) of 2.4 with the matrix cores busy 57 and 63 per cent of the cycles.
+// The large tiles of a prompt run at 1.6 to 1.75 GHz (fp4) and 1.8 to 1.87 GHz (bfloat16) of 2.4, with
+// the matrix cores busy 57 to 63 and 63 to 66 per cent of the cycles.  Power alone does not bound
+// them: loops of the instructions alone keep the matrix cores busy throughout at 1.75 and 2.0 GHz.  Nor
+// does LDS (20 and 34 per cent).  The waves wait 18 to 20 and 26 per cent of their cycles for loads, LDS
+// and the barrier; which of these leaves the matrix cores idle has not been separated.
 // ---------------------------------------------------------------------------
 struct MxTile {
     const uint8_t* A;             // rows of the activations (bfloat16, or codes)

@@ -549,7 +549,7 @@ gq_status gq_timing_read_mxfp4(double* ms, int64_t* launches);
  * activations are multiplied in, 1 for streamed weights (0: tiles), rows and columns of a
  * tile, waves of a block, parts that the contraction is split in.  *first_rows: rows of the
  * first of two products that a call is divided in, n where it is one (the plan is the
- * first's; the other's is that of n - *first_rows rows).  Statuses as the products'.
+ * first's; the other's is that of n - *first_rows rows).  n >= 1; else statuses as the products'.
  */
 gq_status mxfp4_plan(int32_t op, gq_dtype a_dt, int64_t n, int64_t d_in, int64_t d_out,
                      int32_t experts, int32_t grouped, int32_t plan[6], int64_t* first_rows);

@@ -956,6 +956,9 @@ gq_status mxfp4_plan(int32_t op, gq_dtype a_dt, int64_t n, int64_t d_in, int64_t
     if (rc != GQ_OK) return rc;
     if (n < 1) return fail(GQ_ESHAPE, "n=%lld: no rows, no plan", (long long)n);
     if (experts > 1 && !grouped) return fail(GQ_EINVAL, "several experts need offsets");
+    if (!gq::mx_gemm_fits((gq::MxOp)op, a_dt == GQ_BF16, n, d_in, d_out, experts, grouped != 0))
+        return fail(GQ_ENOTIMPL, "n=%lld d_in=%lld d_out=%lld experts=%d: more tiles than a launch takes",
+                    (long long)n, (long long)d_in, (long long)d_out, experts);
     int32_t v[6];
     *first_rows = gq::mx_gemm_plan((gq::MxOp)op, a_dt == GQ_BF16, n, d_in, d_out, experts, grouped != 0, v);
     for (int i = 0; i < 6; ++i) plan[i] = v[i];

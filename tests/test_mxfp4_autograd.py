@@ -182,6 +182,14 @@ def test_backward_on_another_stream_and_in_a_graph(device):
 
 
 @pytest.mark.gpu
+def test_no_rows(device):
+    Q, S = _weight(device, 64, 128)
+    x = torch.empty(0, 128, device=device, requires_grad=True)
+    gq.mxfp4_gemm(x, Q, S).sum().backward()
+    assert x.grad.shape == (0, 128)
+
+
+@pytest.mark.gpu
 def test_a_weight_changed_before_the_backward_pass_is_noticed(device):
     """The graph holds the weight's tensors: torch refuses a backward pass over changed ones."""
     Q, S = _weight(device, 64, 128)

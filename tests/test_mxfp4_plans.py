@@ -84,6 +84,7 @@ def test_plan_refusals():
     assert status(n=1 << 31) == B.GQ_ENOTIMPL and status(d_in=(1 << 20) + 1) == B.GQ_ENOTIMPL
     assert status(experts=0) == B.GQ_EINVAL and status(experts=2) == B.GQ_EINVAL
     assert status(experts=2, grouped=1) == B.GQ_OK and status(experts=4097, grouped=1) == B.GQ_ENOTIMPL
+    assert status(n=4096, d_out=1 << 19, experts=4096, grouped=1) == B.GQ_ENOTIMPL
     assert status(plan=None) == B.GQ_EINVAL and status(first=None) == B.GQ_EINVAL
     with pytest.raises(ValueError):
         gq.mxfp4_plan("gemv", 8, 128, 128)

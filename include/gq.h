@@ -451,6 +451,132 @@ gq_status mxfp4_gemm_dx(const void* g, gq_dtype g_dt, int64_t n, int64_t d_out, 
                         void* dx, gq_dtype dx_dt, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Products in 8-bit floating point with block scales, and the gated feed-forward block.
+ *
+ * Packed rows.  A row of d values is held as 8-bit floating point (e4m3 of the OCP 8-bit formats:
+ * a sign, four exponent and three mantissa bits, up to 448, no infinity), one byte a value, padded with
+ * zero codes to whole blocks of 128, fp8_row_bytes(d) = 128 ceil(d / 128) bytes; where d is a multiple
+ * of 128 that is the plain row-major layout.  Each block of 128 has a scale, fp8_row_scales(d) =
+ * 4 ceil(d / 512) of them a row (those past the last block stand for 1).
+ * Packed weights.  W [d_out][d_in] is held as d_out rows of codes with one scale for each block of
+ * 128 x 128: [ceil(d_out / 128)][ceil(d_in / 128)], nothing behind.  Several weights ("experts")
+ * lie one after another, their codes as well as their scales.
+ * Scales (s_dt of gq_scale).  GQ_SCALE_E8M0: a byte s for 2^(s - 127), 255 for NaN; the matrix cores apply
+ * it themselves.  GQ_SCALE_F32: a float32 number, any, as the 8-bit checkpoints that others publish have
+ * them.  The two operands of a product have scales of one type.
+ * Both size functions return 0 for d < 1 or d > 2^20.
+ *
+ * Limits of all entry points below: every d at most 2^20, n < 2^31, experts at most 4096
+ * (GQ_ENOTIMPL beyond; also where a call would be more tiles than a launch takes), rows * d at most
+ * 2^40.  n = 0 and rows = 0 are valid: the gradients of the weights are then zero, all else does nothing.
+ * Codes are 16-byte, the scales of rows 4-byte aligned, the scales of weights and all values
+ * element-aligned, ws 256-byte.  Outputs must not overlap the inputs, each other or ws (GQ_EINVAL).
+ */
+typedef enum { GQ_SCALE_E8M0 = 0, GQ_SCALE_F32 = 1 } gq_scale;
+
+int64_t fp8_row_bytes(int64_t d);
+int64_t fp8_row_scales(int64_t d);
+
+/*
+ * x [rows][d] (x_dt) -> Q, S.  Per block the scale is 2^e, the smallest with max|x| <= 448 2^e, e
+ * at least -127 (a block of zeros has that), in either type of scale; each value over it is rounded once, to the
+ * nearest code, ties to even, and keeps its sign.  A block with a NaN or an infinity has the scale NaN
+ * and codes 0.  fp8_quantize_weight does the same with blocks of 128 x 128 of each of `experts`
+ * weights W [d_out][d_in].
+ */
+gq_status fp8_quantize(const void* x, gq_dtype x_dt, int64_t rows, int64_t d, uint8_t* Q, void* S,
+                       gq_scale s_dt, void* stream);
+gq_status fp8_quantize_weight(const void* W, gq_dtype w_dt, int32_t experts, int64_t d_out,
+                              int64_t d_in, uint8_t* Q, void* S, gq_scale s_dt, void* stream);
+
+/*
+ * The values that codes stand for, y (y_dt): code times scale in float32, then in y_dt.  With scales that are powers
+ * of two that is exact in either type (a product below the type's normal range or over its largest value apart).
+ */
+gq_status fp8_dequantize(const uint8_t* Q, const void* S, gq_scale s_dt, int64_t rows, int64_t d,
+                         void* y, gq_dtype y_dt, void* stream);
+gq_status fp8_dequantize_weight(const uint8_t* Q, const void* S, gq_scale s_dt, int32_t experts,
+                                int64_t d_out, int64_t d_in, void* y, gq_dtype y_dt, void* stream);
+
+/*
+ * Products with a packed weight W [d_out][d_in]:
+ *   fp8_gemm     y [n][d_out] = x W^T, x [n][d_in] in packed rows (XQ, XS);
+ *   fp8_gemm_dx  dx [n][d_in] = g W, g [n][d_out] in packed rows (GQ, GS): with g the gradient of
+ *                fp8_gemm's output, that of the values that x was packed from (W itself is frozen).
+ * Experts and offsets as for mxfp4_gemm: rows offsets[e] .. offsets[e + 1] - 1 (device int64
+ * [experts + 1], nondecreasing within [0, n]) are multiplied by weight e, and the outputs of other rows are not
+ * written.  Offsets that are none of these are clamped, so nothing is read or written out of
+ * range; the rows that they concern hold unspecified values.
+ *
+ * Precision: products of codes are exact, sums float32.  With GQ_SCALE_E8M0 the sum is of terms with their scales;
+ * with GQ_SCALE_F32 each block's sum is multiplied by the product of its two scales, a float32 rounding each, and
+ * added.  y is rounded once to y_dt.  A NaN stays within its row of x (and, from a weight's block, its columns of y).
+ * The order of sums depends on the sizes alone, so equal calls give equal bits.
+ */
+size_t fp8_gemm_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts, gq_scale s_dt);
+gq_status fp8_gemm(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_in, const uint8_t* Q,
+                   const void* S, gq_scale s_dt, int64_t d_out, int32_t experts,
+                   const int64_t* offsets, void* y, gq_dtype y_dt, void* ws, size_t ws_bytes,
+                   void* stream);
+size_t fp8_gemm_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts, gq_scale s_dt);
+gq_status fp8_gemm_dx(const uint8_t* GQ, const void* GS, int64_t n, int64_t d_out, const uint8_t* Q,
+                      const void* S, gq_scale s_dt, int64_t d_in, int32_t experts,
+                      const int64_t* offsets, void* dx, gq_dtype dx_dt, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/*
+ * The gate of a feed-forward block, h [n][d_ff] = act(x G^T) (x U^T) element by element, with the
+ * weights of two projections G and U [d_ff][d_in]: both products, the activation and their product in
+ * one pass (the down projection after it is a product of its own).  act: z s(z) with the logistic
+ * function s; z P(z) with the normal distribution's P; and that with P by
+ * (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
+ *
+ * fp8_ffn_gate: x, G and U packed; h (h_dt) rounded once from float32.  fp8_ffn_gate_packed: h in
+ * packed rows HQ, HS (scales of type s_dt, as fp8_quantize makes them from h in float32), which
+ * fp8_gemm takes with the down projection's weight.
+ */
+typedef enum { GQ_ACT_SILU = 0, GQ_ACT_GELU = 1, GQ_ACT_GELU_TANH = 2 } gq_activation;
+
+size_t fp8_ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts, gq_scale s_dt);
+gq_status fp8_ffn_gate(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_in, const uint8_t* GQ,
+                       const void* GS, const uint8_t* UQ, const void* US, gq_scale s_dt, int64_t d_ff,
+                       gq_activation act, int32_t experts, const int64_t* offsets, void* h,
+                       gq_dtype h_dt, void* ws, size_t ws_bytes, void* stream);
+size_t fp8_ffn_gate_packed_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts, gq_scale s_dt);
+gq_status fp8_ffn_gate_packed(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_in,
+                              const uint8_t* GQ, const void* GS, const uint8_t* UQ, const void* US,
+                              gq_scale s_dt, int64_t d_ff, gq_activation act, int32_t experts,
+                              const int64_t* offsets, uint8_t* HQ, void* HS, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * The gate with bfloat16 x, G and U, as a calibration or training run has them, and its backward pass.
+ *   ffn_gate     h (h_dt), and where zg and zu are not NULL (both or neither) the two products
+ *                zg = x G^T and zu = x U^T [n][d_ff] in float32, which the backward pass takes;
+ *   ffn_gate_dz  dzg = dh zu act'(zg), dzu = dh act(zg), in bfloat16: the gradients of both projections'
+ *                outputs, which gq_fisher_accumulate takes with x; `count` values each;
+ *   ffn_gate_dx  dx [n][d_in] = dzg G + dzu U;
+ *   ffn_gate_dw  dG [d_ff][d_in] = dzg^T x, dU = dzu^T x (dw_dt), each expert's over its own rows
+ *                (zeros where it has none); with NULL for dG or dU that one is left out.
+ * Experts and offsets as above.  Sums are float32, outputs rounded once.  Operands are 16-byte aligned where their rows are a
+ * multiple of 8 values, else element-aligned (such operands are first copied, into ws).
+ */
+size_t ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts);
+gq_status ffn_gate(const void* x, int64_t n, int64_t d_in, const void* G, const void* U, int64_t d_ff,
+                   gq_activation act, int32_t experts, const int64_t* offsets, void* h,
+                   gq_dtype h_dt, float* zg, float* zu, void* ws, size_t ws_bytes, void* stream);
+gq_status ffn_gate_dz(const void* dh, gq_dtype dh_dt, const float* zg, const float* zu, int64_t count,
+                      gq_activation act, void* dzg, void* dzu, void* stream);
+size_t ffn_gate_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts);
+gq_status ffn_gate_dx(const void* dzg, const void* dzu, int64_t n, int64_t d_ff, const void* G,
+                      const void* U, int64_t d_in, int32_t experts, const int64_t* offsets, void* dx,
+                      gq_dtype dx_dt, void* ws, size_t ws_bytes, void* stream);
+size_t ffn_gate_dw_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts);
+gq_status ffn_gate_dw(const void* dzg, const void* dzu, int64_t n, int64_t d_ff, const void* x,
+                      int64_t d_in, int32_t experts, const int64_t* offsets, void* dG, void* dU,
+                      gq_dtype dw_dt, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * GANQ-style alternation.  The GANQ summary page ("Approach") solves each row by
  * alternating a closed-form least-squares codebook update with an assignment of
  * the indices by Cholesky / back-substitution.  Here: F'_g = L L^T (float64
@@ -541,6 +667,21 @@ typedef enum {
 } gq_mxfp4_stage;
 
 gq_status gq_timing_read_mxfp4(double* ms, int64_t* launches);
+
+/*
+ * Likewise the stages of the 8-bit products and the gated feed-forward block: bits
+ * 1 << (GQ_STAGE_COUNT + GQ_MXFP4_STAGE_COUNT + gq_product_stage), read by gq_timing_read_product into
+ * arrays of GQ_PRODUCT_STAGE_COUNT.
+ */
+typedef enum {
+    GQ_PRODUCT_STAGE_FP8_PACK = 0,  /* packed rows and weights, both directions */
+    GQ_PRODUCT_STAGE_FP8_GEMM,      /* fp8_gemm, fp8_gemm_dx */
+    GQ_PRODUCT_STAGE_FFN_GATE,      /* the gate, of either type */
+    GQ_PRODUCT_STAGE_FFN_BACK,      /* its backward pass */
+    GQ_PRODUCT_STAGE_COUNT
+} gq_product_stage;
+
+gq_status gq_timing_read_product(double* ms, int64_t* launches);
 
 /*
  * Diagnostics: how an MXFP4 product is done, from its sizes and types alone (no GPU is

@@ -23,6 +23,7 @@ GQ_ENOTPD, GQ_ENONFINITE, GQ_ENOTIMPL, GQ_ECHECK = 6, 7, 8, 9
 GQ_F32, GQ_BF16 = 0, 1
 GQ_INIT_QUANTILE, GQ_INIT_GIVEN, GQ_INIT_UNIFORM = 0, 1, 2
 GQ_GRAM_AUTO, GQ_GRAM_DENSE = 0, 1
+GQ_SCALE_E8M0, GQ_SCALE_F32 = 0, 1
 GQ_FISHER_CHECK_FINITE = 2
 ABI_VERSION = 8
 DEFAULT_BLOCK = 512
@@ -39,9 +40,16 @@ EXPORTS = (
     "mxfp4_row_bytes", "mxfp4_row_scales", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_gemm_workspace_size", "mxfp4_gemm", "mxfp4_gemm_mx_workspace_size", "mxfp4_gemm_mx",
     "mxfp4_gemm_dx_workspace_size", "mxfp4_gemm_dx", "mxfp4_plan",
-    "gq_timing_enable", "gq_timing_read", "gq_timing_read_mxfp4", "gq_stage_name",
+    "fp8_row_bytes", "fp8_row_scales", "fp8_quantize", "fp8_quantize_weight", "fp8_dequantize",
+    "fp8_dequantize_weight", "fp8_gemm_workspace_size", "fp8_gemm", "fp8_gemm_dx_workspace_size",
+    "fp8_gemm_dx", "fp8_ffn_gate_workspace_size", "fp8_ffn_gate",
+    "fp8_ffn_gate_packed_workspace_size", "fp8_ffn_gate_packed", "ffn_gate_workspace_size", "ffn_gate",
+    "ffn_gate_dz", "ffn_gate_dx_workspace_size", "ffn_gate_dx", "ffn_gate_dw_workspace_size",
+    "ffn_gate_dw",
+    "gq_timing_enable", "gq_timing_read", "gq_timing_read_mxfp4", "gq_timing_read_product",
+    "gq_stage_name",
 )
-STAGE_COUNT, MXFP4_STAGE_COUNT = 18, 2
+STAGE_COUNT, MXFP4_STAGE_COUNT, PRODUCT_STAGE_COUNT = 18, 2, 4
 
 
 class GQError(RuntimeError):
@@ -114,9 +122,38 @@ _SIGS = {
                                      _vp, _sz, _vp]),
     "mxfp4_plan": (ctypes.c_int, [_i32, _i32, _i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_i32),
                                   ctypes.POINTER(_i64)]),
+    "fp8_row_bytes": (_i64, [_i64]),
+    "fp8_row_scales": (_i64, [_i64]),
+    "fp8_quantize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _vp, _vp, _i32, _vp]),
+    "fp8_quantize_weight": (ctypes.c_int, [_vp, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _vp]),
+    "fp8_dequantize": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp]),
+    "fp8_dequantize_weight": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i64, _i64, _vp, _i32, _vp]),
+    "fp8_gemm_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "fp8_gemm": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _i32,
+                                _vp, _sz, _vp]),
+    "fp8_gemm_dx_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "fp8_gemm_dx": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _i32,
+                                   _vp, _sz, _vp]),
+    "fp8_ffn_gate_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "fp8_ffn_gate": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32,
+                                    _vp, _vp, _i32, _vp, _sz, _vp]),
+    "fp8_ffn_gate_packed_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "fp8_ffn_gate_packed": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i32,
+                                           _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "ffn_gate_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "ffn_gate": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _i32, _vp, _vp,
+                                _vp, _sz, _vp]),
+    "ffn_gate_dz": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
+    "ffn_gate_dx_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "ffn_gate_dx": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _vp,
+                                   _sz, _vp]),
+    "ffn_gate_dw_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "ffn_gate_dw": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _vp,
+                                   _sz, _vp]),
     "gq_timing_enable": (None, [ctypes.c_int]),
     "gq_timing_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gq_timing_read_mxfp4": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
+    "gq_timing_read_product": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gq_stage_name": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -873,10 +910,520 @@ def mxfp4_gemm_dx(g, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=N
                        d_in, experts, offsets, y, out_dtype, ws, stream)
 
 
+# ---- 8-bit rows and products, the gated feed-forward block ----------------------------------
+
+_FP8 = (torch.float8_e4m3fn,)
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_SCALES = {torch.uint8: GQ_SCALE_E8M0, torch.float32: GQ_SCALE_F32}
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def fp8_row_bytes(d: int) -> int:
+    return int(library().fp8_row_bytes(d))
+
+
+def fp8_row_scales(d: int) -> int:
+    return int(library().fp8_row_scales(d))
+
+
+def _fp8_width(d):
+    """(bytes of codes, scales) of a packed row of d values."""
+    if d < 1 or d > _MX_MAX_D:
+        raise GQError(GQ_ESHAPE if d < 1 else GQ_ENOTIMPL, f"rows of {d} values: 1 to 2^20")
+    return 128 * -(-d // 128), 4 * -(-d // 512)
+
+
+def _scale_type(scales):
+    if scales not in _SCALES:
+        raise GQError(GQ_EDTYPE, f"scales are uint8 (powers of two) or float32, not {scales}")
+    return _SCALES[scales]
+
+
+def _act_id(act):
+    if act not in _ACTS:
+        raise GQError(GQ_EINVAL, f"unknown activation {act!r}: {', '.join(_ACTS)}")
+    return _ACTS[act]
+
+
+def _pack(fn, x, codes, scale_shape, sizes, Q, S, scales, stream):
+    """What both quantisations share: x's checks, the outputs and the call."""
+    index = x.get_device()
+    if S is not None and scales is not None and S.dtype != scales:
+        raise GQError(GQ_EDTYPE, f"S is {S.dtype}, scales {scales}")
+    dt = torch.uint8 if S is None and scales is None else (scales if S is None else S.dtype)
+    st_dt = _scale_type(dt)
+    for t, shape, name, kinds in ((Q, codes, "Q", _FP8), (S, scale_shape, "S", _SCALES)):
+        if t is not None:
+            _mx_shape(t, shape, name)
+            _mx_tensor(t, name, index, kinds)
+    _mx_tensor(x, "x", index)
+    where, st = _place(x, stream)
+    with where:
+        if Q is None:
+            Q = x.new_empty(codes, dtype=_FP8[0])
+        if S is None:
+            S = x.new_empty(scale_shape, dtype=dt)
+        status = fn(x.data_ptr(), _MX_DTYPES[x.dtype], *sizes, Q.data_ptr(), S.data_ptr(), st_dt, st)
+    if status:
+        _check(status)
+    return Q, S
+
+
+def fp8_quantize(x, Q=None, S=None, scales=None, stream=None):
+    """x [..][d] float32 or bfloat16 -> packed rows (Q [..][128 ceil(d / 128)] float8_e4m3fn,
+    S [..][4 ceil(d / 512)]): 8-bit codes and a power-of-two scale for each block of 128 along
+    the last dimension.  scales: torch.uint8 (s for 2^(s - 127), unless given) or torch.float32."""
+    lib = _lib or library()
+    if x.dim() < 1:
+        raise GQError(GQ_ESHAPE, "x needs a last dimension to quantise along")
+    lead, d = x.shape[:-1], x.shape[-1]
+    rb, rs = _fp8_width(d)
+    return _pack(lib.fp8_quantize, x, (*lead, rb), (*lead, rs), (x.numel() // d, d), Q, S, scales, stream)
+
+
+def fp8_quantize_weight(W, Q=None, S=None, scales=None, stream=None):
+    """W [d_out][d_in] or [experts][d_out][d_in] -> a packed weight (Q [..][d_out][128 ceil(d_in /
+    128)] float8_e4m3fn, S [..][ceil(d_out / 128)][ceil(d_in / 128)]): a scale for each block of
+    128 x 128.  scales as for fp8_quantize."""
+    lib = _lib or library()
+    if W.dim() not in (2, 3):
+        raise GQError(GQ_ESHAPE, "W must be [d_out][d_in] or [experts][d_out][d_in]")
+    *lead, d_out, d_in = W.shape
+    rb, _ = _fp8_width(d_in)
+    experts = lead[0] if lead else 1
+    return _pack(lib.fp8_quantize_weight, W, (*lead, d_out, rb), (*lead, -(-d_out // 128), rb // 128),
+                 (experts, d_out, d_in), Q, S, scales, stream)
+
+
+def _unpack(fn, Q, S, sizes, shape, dtype, y, stream):
+    """What reading back rows and weights shares (Q's and S's shapes are checked)."""
+    if dtype not in _MX_DTYPES:
+        raise GQError(GQ_EDTYPE, f"unsupported dtype {dtype}")
+    index = Q.get_device()
+    if y is not None:
+        _mx_shape(y, shape, "y")
+        _mx_tensor(y, "y", index, (dtype,))
+    _mx_tensor(Q, "Q", index, _FP8)
+    _mx_tensor(S, "S", index, _SCALES)
+    where, st = _place(Q, stream)
+    with where:
+        if y is None:
+            y = Q.new_empty(shape, dtype=dtype)
+        status = fn(Q.data_ptr(), S.data_ptr(), _SCALES[S.dtype], *sizes, y.data_ptr(), _MX_DTYPES[dtype], st)
+    if status:
+        _check(status)
+    return y
+
+
+def fp8_dequantize(Q, S, d: int, dtype=torch.bfloat16, y=None, stream=None) -> torch.Tensor:
+    """The values [..][d] that packed rows stand for, in float32 or bfloat16."""
+    lib = _lib or library()
+    lead = Q.shape[:-1]
+    rb, rs = _fp8_width(d)
+    _mx_shape(Q, (*lead, rb), "Q")
+    _mx_shape(S, (*lead, rs), "S")
+    return _unpack(lib.fp8_dequantize, Q, S, (Q.numel() // rb, d), (*lead, d), dtype, y, stream)
+
+
+def fp8_dequantize_weight(Q, S, d_in: int, dtype=torch.bfloat16, y=None, stream=None) -> torch.Tensor:
+    """The values [d_out][d_in] or [experts][d_out][d_in] that a packed weight stands for."""
+    lib = _lib or library()
+    experts, d_out = _fp8_weight_shape(Q, S, d_in, None if Q.dim() == 2 else 1)
+    return _unpack(lib.fp8_dequantize_weight, Q, S, (experts, d_out, d_in), (*Q.shape[:-1], d_in), dtype, y, stream)
+
+
+def _fp8_weight_shape(Q, S, d_in, offsets):
+    """(experts, d_out) of a packed weight's shapes."""
+    rb, _ = _fp8_width(d_in)
+    lead = Q.shape[:-1]
+    if len(lead) != (1 if offsets is None else 2):
+        raise GQError(GQ_ESHAPE, "Q must be [d_out][row bytes], or [experts][d_out][row bytes] "
+                                 "with offsets")
+    _mx_shape(Q, (*lead, rb), "Q")
+    _mx_shape(S, (*lead[:-1], -(-lead[-1] // 128), rb // 128), "S")
+    return (1, lead[0]) if offsets is None else lead
+
+
+def _fp8_weight(Q, S, d_in, offsets, index, scales):
+    """(experts, d_out) of a packed weight whose scales are of the type of the rows' scales."""
+    found = _fp8_weight_shape(Q, S, d_in, offsets)
+    _mx_tensor(Q, "Q", index, _FP8)
+    _mx_tensor(S, "S", index, _SCALES)
+    if S.dtype != scales:
+        raise GQError(GQ_EDTYPE, f"the weight's scales are {S.dtype}, the rows' {scales}")
+    return found
+
+
+def _fp8_rows(Q, S, d, names):
+    """Rows of a packed operand."""
+    rb, rs = _fp8_width(d)
+    if Q.dim() != 2:
+        raise GQError(GQ_ESHAPE, f"{names[0]} must be [n][row bytes]")
+    n, index = Q.shape[0], Q.get_device()
+    _mx_shape(Q, (n, rb), names[0])
+    _mx_shape(S, (n, rs), names[1])
+    _mx_tensor(Q, names[0], index, _FP8)
+    _mx_tensor(S, names[1], index, _SCALES)
+    return n, index
+
+
+def _mm_offsets(offsets, experts, index):
+    if offsets is None:
+        return None
+    _mx_shape(offsets, (experts + 1,), "offsets")
+    _mx_tensor(offsets, "offsets", index, _I64)
+    return offsets.data_ptr()
+
+
+def _mm_output(y, out_dtype, shape, index):
+    if y is None:
+        if out_dtype not in _MX_DTYPES:
+            raise GQError(GQ_EDTYPE, f"unsupported dtype {out_dtype}")
+        return
+    if out_dtype is not None and y.dtype != out_dtype:
+        raise GQError(GQ_EDTYPE, f"y is {y.dtype}, out_dtype {out_dtype}")
+    _mx_shape(y, shape, "y")
+    _mx_tensor(y, "y", index)
+
+
+def _mm_scratch(x, ws, size, size_args):
+    """(tensor, pointer, bytes) of a call's workspace, inside its _place."""
+    if ws is False:
+        return None, None, 0
+    if ws is None:
+        need = size(*size_args)
+        if not need:
+            return None, None, 0
+        ws = x.new_empty(need, dtype=torch.uint8)
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _mm_product(x, first, offsets, shape, y, out_dtype, ws, size, size_args, call, stream):
+    """What products with one output share.  call(out, out dtype, ws, ws bytes, stream) makes it.
+    An output of its own has zeros in the rows of no expert."""
+    if ws is not None and ws is not False:
+        _mx_tensor(ws, "ws", x.get_device(), _U8)
+    where, st = _place(x, stream)
+    with where:
+        if y is None:
+            y = (x.new_empty if offsets is None else x.new_zeros)(shape, dtype=out_dtype)
+        keep, wp, wn = _mm_scratch(x, ws, size, size_args)
+        status = call(*first, y.data_ptr(), _MX_DTYPES[y.dtype], wp, wn, st)
+    if status:
+        _check(status)
+    return y
+
+
+def fp8_gemm_workspace_size(n, d_in, d_out, experts=1, scales=torch.uint8) -> int:
+    return int(library().fp8_gemm_workspace_size(n, d_in, d_out, experts, _scale_type(scales)))
+
+
+def fp8_gemm_dx_workspace_size(n, d_in, d_out, experts=1, scales=torch.uint8) -> int:
+    return int(library().fp8_gemm_dx_workspace_size(n, d_in, d_out, experts, _scale_type(scales)))
+
+
+def fp8_ffn_gate_workspace_size(n, d_in, d_ff, experts=1, scales=torch.uint8) -> int:
+    return int(library().fp8_ffn_gate_workspace_size(n, d_in, d_ff, experts, _scale_type(scales)))
+
+
+def fp8_ffn_gate_packed_workspace_size(n, d_in, d_ff, experts=1, scales=torch.uint8) -> int:
+    return int(library().fp8_ffn_gate_packed_workspace_size(n, d_in, d_ff, experts, _scale_type(scales)))
+
+
+def ffn_gate_workspace_size(n, d_in, d_ff, experts=1) -> int:
+    return int(library().ffn_gate_workspace_size(n, d_in, d_ff, experts))
+
+
+def ffn_gate_dx_workspace_size(n, d_in, d_ff, experts=1) -> int:
+    return int(library().ffn_gate_dx_workspace_size(n, d_in, d_ff, experts))
+
+
+def ffn_gate_dw_workspace_size(n, d_in, d_ff, experts=1) -> int:
+    return int(library().ffn_gate_dw_workspace_size(n, d_in, d_ff, experts))
+
+
+def fp8_gemm(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,
+             stream=None) -> torch.Tensor:
+    """y [n][d_out] = x W^T for x packed by fp8_quantize (XQ, XS) and W by fp8_quantize_weight
+    (Q, S), or by others: codes in rows of whole 128s and float32 scales [ceil(d_out / 128)]
+    [ceil(d_in / 128)].  Both have scales of one type.  With offsets (int64 [experts + 1] on the device)
+    rows offsets[e] .. offsets[e + 1] - 1 are multiplied by weight e of Q [experts][d_out][..],
+    and the other rows of a given y keep their values (of a new one: zeros).  out_dtype: bfloat16
+    unless given.  Codes carry no gradient: fp8_gemm_dx is the product's part of it."""
+    lib = _lib or library()
+    n, index = _fp8_rows(XQ, XS, d_in, ("XQ", "XS"))
+    experts, d_out = _fp8_weight(Q, S, d_in, offsets, index, XS.dtype)
+    op = _mm_offsets(offsets, experts, index)
+    if y is None and out_dtype is None:
+        out_dtype = torch.bfloat16
+    _mm_output(y, out_dtype, (n, d_out), index)
+    dt = _SCALES[S.dtype]
+    first = (XQ.data_ptr(), XS.data_ptr(), n, d_in, Q.data_ptr(), S.data_ptr(), dt, d_out, experts, op)
+    return _mm_product(XQ, first, offsets, (n, d_out), y, out_dtype, ws, lib.fp8_gemm_workspace_size,
+                       (n, d_in, d_out, experts, dt), lib.fp8_gemm, stream)
+
+
+def fp8_gemm_dx(GQ, GS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,
+                stream=None) -> torch.Tensor:
+    """dx [n][d_in] = g W for the output's gradient g [n][d_out] packed by fp8_quantize (GQ, GS) and
+    the weight (Q, S) of fp8_gemm: the gradient of the values that x was packed from, straight
+    through the rounding.  Grouped by offsets like fp8_gemm."""
+    lib = _lib or library()
+    experts, d_out = _fp8_weight_shape(Q, S, d_in, offsets)
+    n, index = _fp8_rows(GQ, GS, d_out, ("GQ", "GS"))
+    _fp8_weight(Q, S, d_in, offsets, index, GS.dtype)
+    op = _mm_offsets(offsets, experts, index)
+    if y is None and out_dtype is None:
+        out_dtype = torch.bfloat16
+    _mm_output(y, out_dtype, (n, d_in), index)
+    dt = _SCALES[S.dtype]
+    first = (GQ.data_ptr(), GS.data_ptr(), n, d_out, Q.data_ptr(), S.data_ptr(), dt, d_in, experts, op)
+    return _mm_product(GQ, first, offsets, (n, d_in), y, out_dtype, ws, lib.fp8_gemm_dx_workspace_size,
+                       (n, d_in, d_out, experts, dt), lib.fp8_gemm_dx, stream)
+
+
+def fp8_ffn_gate(XQ, XS, GQ, GS, UQ, US, d_in: int, act: str = "silu", offsets=None, y=None,
+                 out_dtype=None, packed: bool = False, HQ=None, HS=None, ws=None, stream=None):
+    """h [n][d_ff] = act(x G^T) (x U^T), element by element, for packed x, G and U (as fp8_gemm
+    takes them): the gate of a feed-forward block in one pass.  act: "silu", "gelu" or "gelu_tanh".
+    With packed, h comes as packed rows (HQ, HS) with scales of the operands' type, as fp8_gemm takes
+    them for the down projection (fp8_ffn_gate_packed); else as y in out_dtype (bfloat16 unless given).
+    Grouped by offsets like fp8_gemm; packed rows of no expert are zeros in new outputs."""
+    lib = _lib or library()
+    act = _act_id(act)
+    n, index = _fp8_rows(XQ, XS, d_in, ("XQ", "XS"))
+    experts, d_ff = _fp8_weight(GQ, GS, d_in, offsets, index, XS.dtype)
+    _mx_shape(UQ, GQ.shape, "UQ")
+    _mx_shape(US, GS.shape, "US")
+    _fp8_weight(UQ, US, d_in, offsets, index, XS.dtype)
+    op = _mm_offsets(offsets, experts, index)
+    dt = _SCALES[XS.dtype]
+    first = (XQ.data_ptr(), XS.data_ptr(), n, d_in, GQ.data_ptr(), GS.data_ptr(), UQ.data_ptr(),
+             US.data_ptr(), dt, d_ff, act, experts, op)
+    sizes = (n, d_in, d_ff, experts, dt)
+    if not packed:
+        if HQ is not None or HS is not None:
+            raise GQError(GQ_EINVAL, "HQ and HS are outputs of a packed call")
+        if y is None and out_dtype is None:
+            out_dtype = torch.bfloat16
+        _mm_output(y, out_dtype, (n, d_ff), index)
+        return _mm_product(XQ, first, offsets, (n, d_ff), y, out_dtype, ws, lib.fp8_ffn_gate_workspace_size,
+                           sizes, lib.fp8_ffn_gate, stream)
+    if y is not None or out_dtype is not None:
+        raise GQError(GQ_EINVAL, "a packed call's outputs are HQ and HS, not y")
+    hb, hs = _fp8_width(d_ff)
+    for t, shape, name, kinds in ((HQ, (n, hb), "HQ", _FP8), (HS, (n, hs), "HS", (XS.dtype,))):
+        if t is not None:
+            _mx_shape(t, shape, name)
+            _mx_tensor(t, name, index, kinds)
+    if ws is not None and ws is not False:
+        _mx_tensor(ws, "ws", index, _U8)
+    where, st = _place(XQ, stream)
+    with where:
+        new = XQ.new_empty if offsets is None else XQ.new_zeros
+        if HQ is None:
+            HQ = new((n, hb), dtype=torch.uint8).view(_FP8[0])
+        if HS is None:
+            HS = new((n, hs), dtype=XS.dtype)
+        keep, wp, wn = _mm_scratch(XQ, ws, lib.fp8_ffn_gate_packed_workspace_size, sizes)
+        status = lib.fp8_ffn_gate_packed(*first, HQ.data_ptr(), HS.data_ptr(), wp, wn, st)
+    if status:
+        _check(status)
+    return HQ, HS
+
+
+def _ffn_weights(G, U, offsets, index):
+    """(experts, d_ff, d_in) of the two projections of a gate."""
+    if G.dim() != (2 if offsets is None else 3):
+        raise GQError(GQ_ESHAPE, "G must be [d_ff][d_in], or [experts][d_ff][d_in] with offsets")
+    _mx_shape(U, G.shape, "U")
+    _mx_tensor(G, "G", index, _BF16)
+    _mx_tensor(U, "U", index, _BF16)
+    return (1, *G.shape) if offsets is None else tuple(G.shape)
+
+
+def _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream):
+    lib = _lib or library()
+    act = _act_id(act)
+    if x.dim() != 2:
+        raise GQError(GQ_ESHAPE, "x must be [n][d_in]")
+    n, index = x.shape[0], x.get_device()
+    experts, d_ff, d_in = _ffn_weights(G, U, offsets, index)
+    _mx_shape(x, (n, d_in), "x")
+    _mx_tensor(x, "x", index, _BF16)
+    op = _mm_offsets(offsets, experts, index)
+    if y is None and out_dtype is None:
+        out_dtype = x.dtype
+    _mm_output(y, out_dtype, (n, d_ff), index)
+    if ws is not None and ws is not False:
+        _mx_tensor(ws, "ws", index, _U8)
+    where, st = _place(x, stream)
+    with where:
+        new = x.new_empty if offsets is None else x.new_zeros
+        if y is None:
+            y = new((n, d_ff), dtype=out_dtype)
+        zg, zu = (new((n, d_ff), dtype=torch.float32) for _ in range(2)) if save else (None, None)
+        keep, wp, wn = _mm_scratch(x, ws, lib.ffn_gate_workspace_size, (n, d_in, d_ff, experts))
+        status = lib.ffn_gate(x.data_ptr(), n, d_in, G.data_ptr(), U.data_ptr(), d_ff, act, experts, op,
+                              y.data_ptr(), _MX_DTYPES[y.dtype], zg.data_ptr() if save else None,
+                              zu.data_ptr() if save else None, wp, wn, st)
+    if status:
+        _check(status)
+    return (y, zg, zu) if save else y
+
+
+class _FfnGate(torch.autograd.Function):
+    """ffn_gate as a function of x, G and U."""
+
+    @staticmethod
+    def forward(ctx, x, G, U, act, offsets, out_dtype, ws):
+        h, zg, zu = _ffn_forward(x, G, U, act, offsets, None, out_dtype, True, ws, None)
+        ctx.save_for_backward(x, G, U, zg, zu, offsets)
+        ctx.act = act
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        x, G, U, zg, zu, offsets = ctx.saved_tensors
+        dzg, dzu = ffn_gate_dz(dh.contiguous(), zg, zu, act=ctx.act)
+        need = ctx.needs_input_grad
+        dx = ffn_gate_dx(dzg, dzu, G, U, offsets=offsets) if need[0] else None
+        dG = dU = None
+        if need[1] or need[2]:
+            dG, dU = ffn_gate_dw(dzg, dzu, x, experts=None if offsets is None else G.shape[0],
+                                 offsets=offsets, which=(need[1], need[2]))
+        return dx, dG, dU, None, None, None, None
+
+
+def ffn_gate(x, G, U, act: str = "silu", offsets=None, y=None, out_dtype=None, save: bool = False,
+             ws=None, stream=None):
+    """h [n][d_ff] = act(x G^T) (x U^T), element by element, for bfloat16 x [n][d_in] and
+    weights G and U [d_ff][d_in]: the gate of a feed-forward block in one pass.  act: "silu",
+    "gelu" or "gelu_tanh".  With offsets (int64 [experts + 1] on the device) rows offsets[e] ..
+    offsets[e + 1] - 1 take weights e of G and U [experts][d_ff][d_in], and the other rows of a given y keep their
+    values (of a new one: zeros).  out_dtype: float32 or bfloat16, x's unless given.
+    With save: (h, zg, zu), zg = x G^T and zu = x U^T in float32, as ffn_gate_dz takes them.
+    Where x, G or U requires a gradient, autograd gets it by ffn_gate_dz, ffn_gate_dx and ffn_gate_dw (and
+    neither y nor save can be given)."""
+    if torch.is_grad_enabled() and (x.requires_grad or G.requires_grad or U.requires_grad):
+        if y is not None or save:
+            raise GQError(GQ_EINVAL, "x, G or U requires a gradient, which a given y or saved products would "
+                                     "not carry: call without them, or under torch.no_grad()")
+        _mx_tensor(x, "x", x.get_device(), _BF16)
+        where, _ = _place(x, stream)
+        with where:
+            return _FfnGate.apply(x, G, U, act, offsets, out_dtype, ws)
+    return _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream)
+
+
+def ffn_gate_dz(dh, zg, zu, act: str = "silu", dzg=None, dzu=None, stream=None):
+    """(dzg, dzu) bfloat16, the gradients of zg and zu (float32, as ffn_gate saves them) from
+    that of h = act(zg) zu (float32 or bfloat16); all of one shape.  gq_fisher_accumulate takes
+    them with x as the gradients of the two projections' outputs."""
+    lib = _lib or library()
+    act = _act_id(act)
+    index = dh.get_device()
+    for t, name in ((zg, "zg"), (zu, "zu")):
+        _mx_shape(t, dh.shape, name)
+        _mx_tensor(t, name, index, _F32)
+    for t, name in ((dzg, "dzg"), (dzu, "dzu")):
+        if t is not None:
+            _mx_shape(t, dh.shape, name)
+            _mx_tensor(t, name, index, _BF16)
+    _mx_tensor(dh, "dh", index)
+    where, st = _place(dh, stream)
+    with where:
+        if dzg is None:
+            dzg = dh.new_empty(dh.shape, dtype=torch.bfloat16)
+        if dzu is None:
+            dzu = dh.new_empty(dh.shape, dtype=torch.bfloat16)
+        status = lib.ffn_gate_dz(dh.data_ptr(), _MX_DTYPES[dh.dtype], zg.data_ptr(), zu.data_ptr(),
+                                 dh.numel(), act, dzg.data_ptr(), dzu.data_ptr(), st)
+    if status:
+        _check(status)
+    return dzg, dzu
+
+
+def _ffn_dz_pair(dzg, dzu):
+    """(n, d_ff, device) of the two projections' gradients."""
+    if dzg.dim() != 2:
+        raise GQError(GQ_ESHAPE, "dzg must be [n][d_ff]")
+    index = dzg.get_device()
+    _mx_shape(dzu, dzg.shape, "dzu")
+    _mx_tensor(dzg, "dzg", index, _BF16)
+    _mx_tensor(dzu, "dzu", index, _BF16)
+    return (*dzg.shape, index)
+
+
+def ffn_gate_dx(dzg, dzu, G, U, offsets=None, y=None, out_dtype=None, ws=None, stream=None) -> torch.Tensor:
+    """dx [n][d_in] = dzg G + dzu U, the gradient of ffn_gate's x (bfloat16 operands; out_dtype
+    bfloat16 unless given).  Grouped by offsets like ffn_gate."""
+    lib = _lib or library()
+    n, d_ff, index = _ffn_dz_pair(dzg, dzu)
+    experts, f, d_in = _ffn_weights(G, U, offsets, index)
+    if f != d_ff:
+        raise GQError(GQ_ESHAPE, f"dzg has {d_ff} columns, G {f} rows")
+    op = _mm_offsets(offsets, experts, index)
+    if y is None and out_dtype is None:
+        out_dtype = torch.bfloat16
+    _mm_output(y, out_dtype, (n, d_in), index)
+    first = (dzg.data_ptr(), dzu.data_ptr(), n, d_ff, G.data_ptr(), U.data_ptr(), d_in, experts, op)
+    return _mm_product(dzg, first, offsets, (n, d_in), y, out_dtype, ws, lib.ffn_gate_dx_workspace_size,
+                       (n, d_in, d_ff, experts), lib.ffn_gate_dx, stream)
+
+
+def ffn_gate_dw(dzg, dzu, x, experts=None, offsets=None, which=(True, True), dG=None, dU=None,
+                out_dtype=None, ws=None, stream=None):
+    """(dG, dU), the gradients of ffn_gate's weights: dzg^T x and dzu^T x [d_ff][d_in] or, with
+    `experts` and offsets, [experts][d_ff][d_in], each over its expert's rows (zeros where it has
+    none).  which: the ones wanted (None for the other).  out_dtype: bfloat16 unless given."""
+    lib = _lib or library()
+    n, d_ff, index = _ffn_dz_pair(dzg, dzu)
+    if x.dim() != 2:
+        raise GQError(GQ_ESHAPE, "x must be [n][d_in]")
+    if (experts is None) != (offsets is None):
+        raise GQError(GQ_EINVAL, "experts and offsets: both or neither")
+    d_in = x.shape[1]
+    _mx_shape(x, (n, d_in), "x")
+    _mx_tensor(x, "x", index, _BF16)
+    op = _mm_offsets(offsets, experts, index)
+    shape = (d_ff, d_in) if experts is None else (experts, d_ff, d_in)
+    out, dt = [dG, dU], out_dtype
+    for i, name in enumerate(("dG", "dU")):
+        if out[i] is not None:
+            if not which[i]:
+                raise GQError(GQ_EINVAL, f"{name} is given, but not asked for")
+            if dt is not None and out[i].dtype != dt:
+                raise GQError(GQ_EDTYPE, f"{name} is {out[i].dtype}, not {dt}")
+            dt = out[i].dtype
+            _mx_shape(out[i], shape, name)
+            _mx_tensor(out[i], name, index)
+    dt = torch.bfloat16 if dt is None else dt
+    if dt not in _MX_DTYPES:
+        raise GQError(GQ_EDTYPE, f"unsupported dtype {dt}")
+    if ws is not None and ws is not False:
+        _mx_tensor(ws, "ws", index, _U8)
+    where, st = _place(x, stream)
+    with where:
+        for i in range(2):
+            if which[i] and out[i] is None:
+                out[i] = x.new_empty(shape, dtype=dt)
+        keep, wp, wn = _mm_scratch(x, ws, lib.ffn_gate_dw_workspace_size, (n, d_in, d_ff, experts or 1))
+        status = lib.ffn_gate_dw(dzg.data_ptr(), dzu.data_ptr(), n, d_ff, x.data_ptr(), d_in, experts or 1, op,
+                                 out[0].data_ptr() if which[0] else None,
+                                 out[1].data_ptr() if which[1] else None, _MX_DTYPES[dt], wp, wn, st)
+    if status:
+        _check(status)
+    return tuple(out)
+
+
 STAGES = ("group_scale", "fisher_mfma", "fisher_finalize", "fisher_plain", "lnq_prepare",
           "lnq_resid", "lnq_init", "lnq_gram", "lnq_solve", "lnq_sweep", "lnq_small",
           "fisher_pack", "lnq_delta", "lut_pack", "lut_gemv", "fisher_h2d", "ganq_chol",
           "ganq_pass", "mxfp4_pack", "mxfp4_gemm")     # the last two are read on their own
+PRODUCT_STAGES = ("fp8_pack", "fp8_gemm", "ffn_gate", "ffn_back")    # behind them, read on their own too
 
 
 def gq_timing_enable(on=True) -> None:
@@ -892,13 +1439,13 @@ def gq_timing_enable(on=True) -> None:
         names = [on] if isinstance(on, str) else list(on)
         mask = 0
         for n in names:
-            mask |= 1 << STAGES.index(n)
+            mask |= 1 << (STAGES + PRODUCT_STAGES).index(n)
     library().gq_timing_enable(mask)
 
 
 def gq_timing_read() -> dict:
     """{stage name: (milliseconds, launch sequences)} since the last read; clears.  The MXFP4
-    stages (mxfp4_pack, mxfp4_gemm) are in it where they were timed."""
+    stages (mxfp4_pack, mxfp4_gemm) and PRODUCT_STAGES are in it where they were timed."""
     lib = library()
     ms = (ctypes.c_double * STAGE_COUNT)()
     cnt = (_i64 * STAGE_COUNT)()
@@ -908,4 +1455,8 @@ def gq_timing_read() -> dict:
     cnt = (_i64 * MXFP4_STAGE_COUNT)()
     _check(lib.gq_timing_read_mxfp4(ms, cnt))
     times.update((name, (ms[i], cnt[i])) for i, name in enumerate(STAGES[STAGE_COUNT:]) if cnt[i])
+    ms = (ctypes.c_double * PRODUCT_STAGE_COUNT)()
+    cnt = (_i64 * PRODUCT_STAGE_COUNT)()
+    _check(lib.gq_timing_read_product(ms, cnt))
+    times.update((name, (ms[i], cnt[i])) for i, name in enumerate(PRODUCT_STAGES) if cnt[i])
     return times

@@ -3,6 +3,7 @@
 #include "gq_common.h"
 #include "gq_internal.h"
 #include "gq_mx.h"
+#include "gq_mm.h"
 #include "gq.h"
 
 static_assert((int)gq::ST_COUNT == (int)GQ_STAGE_COUNT, "stage ids of gq.h and the library differ");
@@ -205,8 +206,15 @@ gq_status check_options(const gq_lnq_options& o, int64_t d_in) {
     return GQ_OK;
 }
 
-// Stages of gq_timing_read, then those of gq_timing_read_mxfp4.
-constexpr int ALL_STAGES = GQ_STAGE_COUNT + GQ_MXFP4_STAGE_COUNT;
+// Stages of gq_timing_read, then those of gq_timing_read_mxfp4 and of gq_timing_read_product.
+constexpr int PRODUCT_STAGES = GQ_STAGE_COUNT + GQ_MXFP4_STAGE_COUNT;      // the first of the last
+constexpr int ALL_STAGES = PRODUCT_STAGES + GQ_PRODUCT_STAGE_COUNT;
+static_assert((int)gq::ST_FP8_PACK == PRODUCT_STAGES + GQ_PRODUCT_STAGE_FP8_PACK &&
+              (int)gq::ST_FP8_GEMM == PRODUCT_STAGES + GQ_PRODUCT_STAGE_FP8_GEMM &&
+              (int)gq::ST_FFN_GATE == PRODUCT_STAGES + GQ_PRODUCT_STAGE_FFN_GATE &&
+              (int)gq::ST_FFN_BACK == PRODUCT_STAGES + GQ_PRODUCT_STAGE_FFN_BACK, "product stage ids");
+static_assert((int)gq::ACT_SILU == GQ_ACT_SILU && (int)gq::ACT_GELU == GQ_ACT_GELU &&
+              (int)gq::ACT_GELU_TANH == GQ_ACT_GELU_TANH, "activation ids");
 static_assert((int)gq::ST_MXFP4_PACK == GQ_STAGE_COUNT + GQ_MXFP4_STAGE_PACK &&
               (int)gq::ST_MXFP4_GEMM == GQ_STAGE_COUNT + GQ_MXFP4_STAGE_GEMM, "MXFP4 stage ids");
 
@@ -256,6 +264,10 @@ gq_status gq_timing_read(double* ms, int64_t* launches) {
 
 gq_status gq_timing_read_mxfp4(double* ms, int64_t* launches) {
     return timing_take(GQ_STAGE_COUNT, GQ_MXFP4_STAGE_COUNT, ms, launches);
+}
+
+gq_status gq_timing_read_product(double* ms, int64_t* launches) {
+    return timing_take(PRODUCT_STAGES, GQ_PRODUCT_STAGE_COUNT, ms, launches);
 }
 
 const char* gq_stage_name(int stage) {
@@ -985,6 +997,269 @@ gq_status mxfp4_gemm_dx(const void* g, gq_dtype g_dt, int64_t n, int64_t d_out, 
                         void* dx, gq_dtype dx_dt, void* ws, size_t ws_bytes, void* stream) {
     return mx_product(gq::MX_GEMM_DX, g, nullptr, g_dt, n, d_in, Q, S, d_out, experts, offsets, dx,
                       dx_dt, ws, ws_bytes, stream, "mxfp4_gemm_dx");
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit rows and products, the gated feed-forward block
+// ---------------------------------------------------------------------------
+int64_t fp8_row_bytes(int64_t d) { return d < 1 || d > gq::MX_MAX_D ? 0 : gq::fp8_bytes(d); }
+
+int64_t fp8_row_scales(int64_t d) { return d < 1 || d > gq::MX_MAX_D ? 0 : gq::fp8_scales(d); }
+
+static bool scale_ok(gq_scale s) { return s == GQ_SCALE_E8M0 || s == GQ_SCALE_F32; }
+
+static size_t scale_bytes(gq_scale s) { return s == GQ_SCALE_F32 ? 4 : 1; }
+
+static bool scale_al(const void* p, gq_scale s, bool rows) {
+    return ((uintptr_t)p & (rows || s == GQ_SCALE_F32 ? 3u : 0u)) == 0;
+}
+
+// Outputs (the first `outs` of the spans, with ws among them) overlap neither each other nor the rest.
+struct MmSpan {
+    const void* p;
+    size_t n;
+};
+static bool mm_apart(const MmSpan* s, int count, int outs) {
+    for (int i = 0; i < outs; ++i)
+        for (int j = i + 1; j < count; ++j)
+            if (mx_overlap(s[i].p, s[i].n, s[j].p, s[j].n)) return false;
+    return true;
+}
+
+// What the four conversions check: `scales` of them for `rows` rows.
+static gq_status fp8_rows_check(const void* x, gq_dtype dt, int64_t rows, int64_t d, const uint8_t* Q,
+                                const void* S, gq_scale s_dt, int64_t scales, bool weight) {
+    if (rows > 0 && (!x || !Q || !S)) return fail(GQ_EINVAL, "null values, codes or scales");
+    if (!al16(Q) || !scale_al(S, s_dt, !weight) || !mx_el_al(x, dt))
+        return fail(GQ_EINVAL, "codes must be 16-byte, the scales of rows 4-byte and all else element-aligned");
+    const size_t n = (size_t)rows;
+    const MmSpan spans[] = {{x, n * d * (dt == GQ_BF16 ? 2 : 4)}, {Q, n * gq::fp8_bytes(d)},
+                            {S, (size_t)scales * scale_bytes(s_dt)}};
+    if (!mm_apart(spans, 3, 2)) return fail(GQ_EINVAL, "values, codes and scales must not overlap");
+    return GQ_OK;
+}
+
+static gq_status fp8_row_sizes(gq_dtype dt, gq_scale s_dt, int64_t rows, int64_t d) {
+    if (!dtype_ok(dt) || !scale_ok(s_dt)) return fail(GQ_EDTYPE, "unsupported dtype %d or scale %d", (int)dt, (int)s_dt);
+    if (rows < 0 || d < 1) return fail(GQ_ESHAPE, "rows=%lld d=%lld", (long long)rows, (long long)d);
+    if (d > gq::MX_MAX_D) return fail(GQ_ENOTIMPL, "d=%lld above 2^20", (long long)d);
+    if (rows > ((int64_t)1 << 40) / d)
+        return fail(GQ_ENOTIMPL, "rows=%lld of d=%lld: more than 2^40 values", (long long)rows, (long long)d);
+    return GQ_OK;
+}
+
+gq_status fp8_quantize(const void* x, gq_dtype x_dt, int64_t rows, int64_t d, uint8_t* Q, void* S,
+                       gq_scale s_dt, void* stream) {
+    gq_status rc = fp8_row_sizes(x_dt, s_dt, rows, d);
+    if (rc == GQ_OK) rc = fp8_rows_check(x, x_dt, rows, d, Q, S, s_dt, rows * gq::fp8_scales(d), false);
+    if (rc != GQ_OK || rows == 0) return rc;
+    const hipError_t e = gq::fp8_quantize_run(x, x_dt == GQ_BF16, rows, d, Q, S, s_dt == GQ_SCALE_F32, (hipStream_t)stream);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, "fp8_quantize");
+}
+
+gq_status fp8_dequantize(const uint8_t* Q, const void* S, gq_scale s_dt, int64_t rows, int64_t d,
+                         void* y, gq_dtype y_dt, void* stream) {
+    gq_status rc = fp8_row_sizes(y_dt, s_dt, rows, d);
+    if (rc == GQ_OK) rc = fp8_rows_check(y, y_dt, rows, d, Q, S, s_dt, rows * gq::fp8_scales(d), false);
+    if (rc != GQ_OK || rows == 0) return rc;
+    const hipError_t e = gq::fp8_dequantize_run(Q, S, s_dt == GQ_SCALE_F32, rows, d, y, y_dt == GQ_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, "fp8_dequantize");
+}
+
+static gq_status fp8_weight_check(const void* W, gq_dtype dt, int32_t experts, int64_t d_out, int64_t d_in,
+                                  const uint8_t* Q, const void* S, gq_scale s_dt) {
+    if (experts < 1) return fail(GQ_EINVAL, "experts must be >= 1 (got %d)", experts);
+    if (experts > gq::MX_MAX_EXPERTS || d_out > gq::MX_MAX_D)
+        return fail(GQ_ENOTIMPL, "experts=%d d_out=%lld: at most 4096 and 2^20", experts, (long long)d_out);
+    if (d_out < 1) return fail(GQ_ESHAPE, "d_out=%lld", (long long)d_out);
+    gq_status rc = fp8_row_sizes(dt, s_dt, experts * d_out, d_in);
+    if (rc != GQ_OK) return rc;
+    return fp8_rows_check(W, dt, experts * d_out, d_in, Q, S, s_dt, experts * ((d_out + 127) / 128) * gq::fp8_blocks(d_in), true);
+}
+
+gq_status fp8_quantize_weight(const void* W, gq_dtype w_dt, int32_t experts, int64_t d_out,
+                              int64_t d_in, uint8_t* Q, void* S, gq_scale s_dt, void* stream) {
+    const gq_status rc = fp8_weight_check(W, w_dt, experts, d_out, d_in, Q, S, s_dt);
+    if (rc != GQ_OK) return rc;
+    const hipError_t e = gq::fp8_quantize_weight_run(W, w_dt == GQ_BF16, experts, d_out, d_in, Q, S, s_dt == GQ_SCALE_F32, (hipStream_t)stream);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, "fp8_quantize_weight");
+}
+
+gq_status fp8_dequantize_weight(const uint8_t* Q, const void* S, gq_scale s_dt, int32_t experts,
+                                int64_t d_out, int64_t d_in, void* y, gq_dtype y_dt, void* stream) {
+    const gq_status rc = fp8_weight_check(y, y_dt, experts, d_out, d_in, Q, S, s_dt);
+    if (rc != GQ_OK) return rc;
+    const hipError_t e = gq::fp8_dequantize_weight_run(Q, S, s_dt == GQ_SCALE_F32, experts, d_out, d_in, y, y_dt == GQ_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, "fp8_dequantize_weight");
+}
+
+static size_t mm_size(gq::MmForm form, gq::MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int32_t experts, bool packed) {
+    if (!mx_sizes_ok(n, d_in, d_out, experts) || (n == 0 && form != gq::MM_TN)) return 0;
+    return gq::mm_workspace(form, elt, n, d_in, d_out, experts, packed);
+}
+
+static gq::MmElt fp8_elt(gq_scale s) { return s == GQ_SCALE_F32 ? gq::MM_FS : gq::MM_E8; }
+
+size_t fp8_gemm_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts, gq_scale s_dt) {
+    return scale_ok(s_dt) ? mm_size(gq::MM_NT, fp8_elt(s_dt), n, d_in, d_out, experts, false) : 0;
+}
+
+size_t fp8_gemm_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts, gq_scale s_dt) {
+    return scale_ok(s_dt) ? mm_size(gq::MM_NN, fp8_elt(s_dt), n, d_in, d_out, experts, false) : 0;
+}
+
+size_t fp8_ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts, gq_scale s_dt) {
+    return scale_ok(s_dt) ? mm_size(gq::MM_GATE, fp8_elt(s_dt), n, d_in, d_ff, experts, false) : 0;
+}
+
+size_t fp8_ffn_gate_packed_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts, gq_scale s_dt) {
+    return scale_ok(s_dt) ? mm_size(gq::MM_GATE, fp8_elt(s_dt), n, d_in, d_ff, experts, true) : 0;
+}
+
+size_t ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts) {
+    return mm_size(gq::MM_GATE, gq::MM_BF16, n, d_in, d_ff, experts, false);
+}
+
+size_t ffn_gate_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts) {
+    return mm_size(gq::MM_NN, gq::MM_BF16, n, d_in, d_ff, experts, false);
+}
+
+size_t ffn_gate_dw_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts) {
+    return mm_size(gq::MM_TN, gq::MM_BF16, n, d_in, d_ff, experts, false);
+}
+
+// Checks and runs a product whose operands are in `c`: s_dt and y_dt the types of scales and output.
+static gq_status mm_product(gq::MmCall& c, gq_scale s_dt, gq_dtype y_dt, int act, void* ws, size_t ws_bytes,
+                            void* stream, const char* name) {
+    using namespace gq;
+    if (!scale_ok(s_dt)) return fail(GQ_EDTYPE, "unsupported scale type %d", (int)s_dt);
+    gq_status rc = mx_sizes_check(y_dt, y_dt, c.n, c.d_in, c.d_out, c.experts);
+    if (rc != GQ_OK) return rc;
+    if (act < ACT_SILU || act > ACT_GELU_TANH) return fail(GQ_EINVAL, "unknown activation %d", act);
+    if (c.experts > 1 && !c.offsets) return fail(GQ_EINVAL, "several experts need offsets");
+    if ((uintptr_t)c.offsets & 7u) return fail(GQ_EINVAL, "offsets must be 8-byte aligned");
+    if (c.n == 0 && c.form != MM_TN) return GQ_OK;
+    const bool fp8 = c.elt != MM_BF16, tn = c.form == MM_TN, two_a = tn || (c.form == MM_NN && !fp8);
+    const bool two_w = c.form == MM_GATE || (c.form == MM_NN && !fp8), packed = c.hs || c.hq;
+    if (tn && !c.y[0] && !c.y[1]) return fail(GQ_EINVAL, "null dG and dU: nothing to compute");
+    if (c.n > 0 && (!c.a[0] || (two_a && !c.a[1]) || !c.w[0]))
+        return fail(GQ_EINVAL, "null operand");
+    if ((two_w && !c.w[1]) || (fp8 && (!c.as || !c.ws[0] || (two_w && !c.ws[1]))))
+        return fail(GQ_EINVAL, "null operand or scales");
+    if (packed ? !c.hq || !c.hs : (!tn && !c.y[0])) return fail(GQ_EINVAL, "null output");
+    if (c.form == MM_GATE && !c.z[0] != !c.z[1]) return fail(GQ_EINVAL, "zg and zu: both or neither");
+    // lengths and alignment of the operands
+    const int64_t ak = c.form == MM_NT || c.form == MM_GATE ? c.d_in : c.d_out;
+    const int64_t m = c.form == MM_NN || tn ? c.d_in : c.d_out, wrows = tn ? c.n : c.experts * c.d_out;
+    const size_t a_len = (size_t)c.n * (fp8 ? fp8_bytes(ak) : 2 * ak);
+    const size_t w_len = (size_t)wrows * (fp8 ? fp8_bytes(c.d_in) : 2 * c.d_in);
+    const size_t as_len = fp8 ? (size_t)c.n * fp8_scales(ak) * scale_bytes(s_dt) : 0;
+    const size_t ws_len = fp8 ? (size_t)c.experts * ((c.d_out + 127) / 128) * fp8_blocks(c.d_in) * scale_bytes(s_dt) : 0;
+    const size_t y_rows = tn ? (size_t)c.experts * c.d_out : (size_t)c.n, y_len = y_rows * m * (y_dt == GQ_BF16 ? 2 : 4);
+    const uintptr_t a_al = fp8 || ak % 8 == 0 ? 15u : 1u, w_al = fp8 || c.d_in % 8 == 0 ? 15u : 1u;
+    if ((((uintptr_t)c.a[0] | (uintptr_t)c.a[1]) & a_al) || (((uintptr_t)c.w[0] | (uintptr_t)c.w[1]) & w_al))
+        return fail(GQ_EINVAL, "operands must be 16-byte aligned (element-aligned where their rows are no multiple of 8 bfloat16 values)");
+    if (!scale_al(c.as, s_dt, true) || !scale_al(c.ws[0], s_dt, false) || !scale_al(c.ws[1], s_dt, false))
+        return fail(GQ_EINVAL, "the scales of rows must be 4-byte, of weights element-aligned");
+    if (!mx_el_al(c.y[0], y_dt) || !mx_el_al(c.y[1], y_dt) || (((uintptr_t)c.z[0] | (uintptr_t)c.z[1]) & 3u) ||
+        !al16(c.hq) || ((uintptr_t)c.hs & 3u) || ((uintptr_t)ws & 255u))
+        return fail(GQ_EINVAL, "outputs must be element-aligned (packed codes 16-byte, their scales 4-byte) and ws 256-byte");
+    if (!mm_fits(c.form, c.elt, c.n, c.d_in, c.d_out, c.experts, c.offsets != nullptr, packed))
+        return fail(GQ_ENOTIMPL, "n=%lld d_in=%lld d_out=%lld experts=%d: more tiles than a launch takes",
+                    (long long)c.n, (long long)c.d_in, (long long)c.d_out, c.experts);
+    const size_t need = mm_workspace(c.form, c.elt, c.n, c.d_in, c.d_out, c.experts, packed);
+    const size_t z_len = c.z[0] ? (size_t)c.n * m * 4 : 0;
+    const MmSpan spans[] = {{c.y[0], c.y[0] ? y_len : 0}, {c.y[1], c.y[1] ? y_len : 0}, {c.z[0], z_len}, {c.z[1], z_len},
+                            {c.hq, packed ? (size_t)c.n * fp8_bytes(m) : 0},
+                            {c.hs, packed ? (size_t)c.n * fp8_scales(m) * scale_bytes(s_dt) : 0}, {ws, ws ? need : 0},
+                            {c.a[0], a_len}, {c.a[1], c.a[1] ? a_len : 0}, {c.as, as_len}, {c.w[0], w_len},
+                            {c.w[1], c.w[1] ? w_len : 0}, {c.ws[0], ws_len}, {c.ws[1], c.ws[1] ? ws_len : 0},
+                            {c.offsets, c.offsets ? (size_t)(c.experts + 1) * 8 : 0}};
+    if (!mm_apart(spans, sizeof spans / sizeof spans[0], 7))
+        return fail(GQ_EINVAL, "outputs and ws must not overlap each other or the inputs");
+    c.y_bf16 = y_dt == GQ_BF16;
+    c.act = act;
+    hipStream_t st = (hipStream_t)stream;
+    Scratch s;
+    if ((rc = s.acquire(ws, ws_bytes, need, st)) != GQ_OK) return rc;
+    const hipError_t e = mm_run(c, s.ptr, st);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, name);
+}
+
+gq_status fp8_gemm(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_in, const uint8_t* Q,
+                   const void* S, gq_scale s_dt, int64_t d_out, int32_t experts,
+                   const int64_t* offsets, void* y, gq_dtype y_dt, void* ws, size_t ws_bytes,
+                   void* stream) {
+    gq::MmCall c{gq::MM_NT, fp8_elt(s_dt), {XQ, nullptr}, XS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {y, nullptr}};
+    return mm_product(c, s_dt, y_dt, 0, ws, ws_bytes, stream, "fp8_gemm");
+}
+
+gq_status fp8_gemm_dx(const uint8_t* GQ, const void* GS, int64_t n, int64_t d_out, const uint8_t* Q,
+                      const void* S, gq_scale s_dt, int64_t d_in, int32_t experts,
+                      const int64_t* offsets, void* dx, gq_dtype dx_dt, void* ws, size_t ws_bytes,
+                      void* stream) {
+    gq::MmCall c{gq::MM_NN, fp8_elt(s_dt), {GQ, nullptr}, GS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {dx, nullptr}};
+    return mm_product(c, s_dt, dx_dt, 0, ws, ws_bytes, stream, "fp8_gemm_dx");
+}
+
+gq_status fp8_ffn_gate(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_in, const uint8_t* GQ,
+                       const void* GS, const uint8_t* UQ, const void* US, gq_scale s_dt, int64_t d_ff,
+                       gq_activation act, int32_t experts, const int64_t* offsets, void* h,
+                       gq_dtype h_dt, void* ws, size_t ws_bytes, void* stream) {
+    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets, {h, nullptr}};
+    return mm_product(c, s_dt, h_dt, act, ws, ws_bytes, stream, "fp8_ffn_gate");
+}
+
+gq_status fp8_ffn_gate_packed(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_in,
+                              const uint8_t* GQ, const void* GS, const uint8_t* UQ, const void* US,
+                              gq_scale s_dt, int64_t d_ff, gq_activation act, int32_t experts,
+                              const int64_t* offsets, uint8_t* HQ, void* HS, void* ws,
+                              size_t ws_bytes, void* stream) {
+    if (n > 0 && (!HQ || !HS)) return fail(GQ_EINVAL, "null output");
+    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets};
+    c.hq = HQ;
+    c.hs = HS;
+    return mm_product(c, s_dt, GQ_F32, act, ws, ws_bytes, stream, "fp8_ffn_gate_packed");
+}
+
+gq_status ffn_gate(const void* x, int64_t n, int64_t d_in, const void* G, const void* U, int64_t d_ff,
+                   gq_activation act, int32_t experts, const int64_t* offsets, void* h,
+                   gq_dtype h_dt, float* zg, float* zu, void* ws, size_t ws_bytes, void* stream) {
+    gq::MmCall c{gq::MM_GATE, gq::MM_BF16, {x, nullptr}, nullptr, n, d_in, d_ff, {G, U}, {nullptr, nullptr}, experts, offsets, {h, nullptr}};
+    c.z[0] = zg;
+    c.z[1] = zu;
+    return mm_product(c, GQ_SCALE_E8M0, h_dt, act, ws, ws_bytes, stream, "ffn_gate");
+}
+
+gq_status ffn_gate_dz(const void* dh, gq_dtype dh_dt, const float* zg, const float* zu, int64_t count,
+                      gq_activation act, void* dzg, void* dzu, void* stream) {
+    if (!dtype_ok(dh_dt)) return fail(GQ_EDTYPE, "unsupported dtype %d", (int)dh_dt);
+    if (count < 0) return fail(GQ_ESHAPE, "count=%lld", (long long)count);
+    if (count > (int64_t)1 << 50) return fail(GQ_ENOTIMPL, "count=%lld above 2^50", (long long)count);
+    if ((int)act < gq::ACT_SILU || (int)act > gq::ACT_GELU_TANH) return fail(GQ_EINVAL, "unknown activation %d", (int)act);
+    if (count == 0) return GQ_OK;
+    if (!dh || !zg || !zu || !dzg || !dzu) return fail(GQ_EINVAL, "null dh, zg, zu, dzg or dzu");
+    if (!mx_el_al(dh, dh_dt) || (((uintptr_t)zg | (uintptr_t)zu) & 3u) || (((uintptr_t)dzg | (uintptr_t)dzu) & 1u))
+        return fail(GQ_EINVAL, "all arrays must be element-aligned");
+    const size_t n = (size_t)count;
+    const MmSpan spans[] = {{dzg, 2 * n}, {dzu, 2 * n}, {dh, n * (dh_dt == GQ_BF16 ? 2 : 4)}, {zg, 4 * n}, {zu, 4 * n}};
+    if (!mm_apart(spans, 5, 2)) return fail(GQ_EINVAL, "dzg and dzu must not overlap each other or the inputs");
+    const hipError_t e = gq::ffn_dz_run(dh, dh_dt == GQ_BF16, zg, zu, count, act, (uint16_t*)dzg, (uint16_t*)dzu, (hipStream_t)stream);
+    return e == hipSuccess ? GQ_OK : hip_fail(e, "ffn_gate_dz");
+}
+
+gq_status ffn_gate_dx(const void* dzg, const void* dzu, int64_t n, int64_t d_ff, const void* G,
+                      const void* U, int64_t d_in, int32_t experts, const int64_t* offsets, void* dx,
+                      gq_dtype dx_dt, void* ws, size_t ws_bytes, void* stream) {
+    gq::MmCall c{gq::MM_NN, gq::MM_BF16, {dzg, dzu}, nullptr, n, d_in, d_ff, {G, U}, {nullptr, nullptr}, experts, offsets, {dx, nullptr}};
+    return mm_product(c, GQ_SCALE_E8M0, dx_dt, 0, ws, ws_bytes, stream, "ffn_gate_dx");
+}
+
+gq_status ffn_gate_dw(const void* dzg, const void* dzu, int64_t n, int64_t d_ff, const void* x,
+                      int64_t d_in, int32_t experts, const int64_t* offsets, void* dG, void* dU,
+                      gq_dtype dw_dt, void* ws, size_t ws_bytes, void* stream) {
+    gq::MmCall c{gq::MM_TN, gq::MM_BF16, {dzg, dzu}, nullptr, n, d_in, d_ff, {x, nullptr}, {nullptr, nullptr}, experts, offsets, {dG, dU}};
+    return mm_product(c, GQ_SCALE_E8M0, dw_dt, 0, ws, ws_bytes, stream, "ffn_gate_dw");
 }
 
 size_t ganq_workspace_size(int64_t d_out, int64_t d_in, int32_t groups, int32_t bits,

@@ -1,0 +1,122 @@
+"""Inputs, float64 references and bounds for the 8-bit products and the gated feed-forward block.
+
+Bounds.  Products of two codes (four significant bits each) or two bfloat16 values are exact in
+float32, so only sums round: a float32 addition is off by at most 2^-23 of its result (2^-24 where it
+rounds to nearest), every partial sum is at most A = sum |a w|, so T terms are off by at most
+(T + 8) 2^-23 A.  With float32 scales a block's sum takes one more rounding by the product of its
+scales and one as it is added (2^-24 each, of at most A): within the 8.  A bfloat16 output adds half a
+step, 2^-8 |y|, and 2^-134 below the normal range.
+
+The gate h = act(zg) zu: |act'| <= 1.13 for all three, so h moves by at most 1.13 dzg (|zu| + dzu) +
+|act(zg)| dzu for products off by dzg and dzu.  act itself is evaluated in float32 from at most six roundings
+(2^-24) and two library functions (4 ulp: 2^-21) of which the exponential's argument carries up to three
+roundings, each moving it by |arg| 2^-24 <= (1 + z^2) 2^-23: together within 32 2^-23 (1 + z^2) of act(z), and of
+max(1, ...) for the slope, whose terms can cancel.
+"""
+import numpy as np
+import torch
+
+import post_weight_quantization_gq_amd as gq
+
+BF, F32, U8, FP8 = torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn
+EPS = 2.0 ** -23
+
+
+def f64(t):
+    return t.detach().to("cpu").to(torch.float64).numpy()
+
+
+def generator(device, seed):
+    g = torch.Generator(device=device)
+    g.manual_seed(seed)
+    return g
+
+
+def normal(device, *shape, seed, dtype=F32, scale=1.0, spread=0.0):
+    """Gaussian values; `spread`: rows of very different sizes."""
+    g = generator(device, seed)
+    x = torch.randn(shape, generator=g, device=device) * scale
+    if spread:
+        x = x * torch.exp(spread * torch.randn((*shape[:-1], 1), generator=g, device=device))
+    return x.to(dtype)
+
+
+def rows(device, n, d, scales, seed, spread=1.0):
+    """Packed rows and their float64 values."""
+    XQ, XS = gq.fp8_quantize(normal(device, n, d, seed=seed, spread=spread), scales=scales)
+    return XQ, XS, gq.fp8_dequantize(XQ, XS, d, dtype=F32).double()
+
+
+def weight(device, d_out, d_in, scales, seed, experts=None):
+    """A packed weight with scales of its own (float32 ones are no powers of two), and its float64 values."""
+    shape = (d_out, d_in) if experts is None else (experts, d_out, d_in)
+    Q, S = gq.fp8_quantize_weight(normal(device, *shape, seed=seed, scale=0.05, spread=1.0), scales=scales)
+    if scales == F32:
+        S = S * (1 + torch.rand(S.shape, generator=generator(device, seed + 1), device=device))
+    s = S.double() if scales == F32 else torch.exp2(S.double() - 127)
+    s = s.repeat_interleave(128, -2)[..., :d_out, :].repeat_interleave(128, -1)
+    return Q, S, (Q.to(F32).double() * s)[..., :d_in]
+
+
+def counts(n, experts, seed):
+    """Offsets of a skewed routing: experts without rows among them, rows of none at both ends."""
+    rng = np.random.default_rng(seed)
+    first, last = n // 11, n - n // 7
+    p = rng.exponential(size=experts) * (rng.random(experts) < 0.8) + 1e-9
+    cut = np.cumsum(rng.multinomial(last - first, p / p.sum()))
+    return [first] + (first + cut).tolist()
+
+
+def spans(n, offsets):
+    """(weight, rows) pairs of a call."""
+    if offsets is None:
+        return [(None, slice(0, n))]
+    return [(e, slice(offsets[e], offsets[e + 1])) for e in range(len(offsets) - 1)]
+
+
+def of(W, e):
+    return W if e is None else W[e]
+
+
+def rounding(ref, out):
+    return 2.0 ** -8 * ref.abs() + 2.0 ** -134 if out == BF else torch.zeros_like(ref)
+
+
+def check(y, ref, limit, out, what):
+    """|y - ref| <= limit + the output's rounding, NaN nowhere."""
+    far, most = (y.double() - ref).abs(), limit + rounding(ref, out)
+    worst = float((far / most.clamp_min(1e-300)).max()) if far.numel() else 0.0
+    print(f"{what}: worst error / bound {worst:.3g}", flush=True)
+    assert bool((far <= most).all()), what
+
+
+def check_product(y, a, W, offsets, terms, out, what):
+    """y = a W^T by the rows' weights; the other rows zero."""
+    done = torch.zeros(a.shape[0], dtype=torch.bool)
+    for e, r in spans(a.shape[0], offsets):
+        w = of(W, e)
+        check(y[r], a[r] @ w.T, (terms + 8) * EPS * (a[r].abs() @ w.T.abs()), out, what)
+        done[r] = True
+    assert not y[~done].double().abs().sum().item()
+
+
+def act64(z, act):
+    """(act(z), act'(z)) in float64."""
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return z * s, s + z * s * (1 - s)
+    if act == "gelu":
+        c = torch.special.ndtr(z)
+        return z * c, c + z * torch.exp(-z * z / 2) * 0.3989422804014327
+    u = 0.7978845608028654 * (z + 0.044715 * z ** 3)
+    s = torch.sigmoid(2 * u)
+    return z * s, s + 2 * z * s * (1 - s) * 0.7978845608028654 * (1 + 0.134145 * z * z)
+
+
+def gate64(a, G, U, act, terms):
+    """(h, bound of h before its rounding, zg, zu, bounds of zg and zu)."""
+    zg, zu = a @ G.T, a @ U.T
+    bg, bu = ((terms + 8) * EPS * (a.abs() @ w.T.abs()) for w in (G, U))
+    v = act64(zg, act)[0]
+    limit = 1.13 * bg * (zu.abs() + bu) + v.abs() * bu + 33 * EPS * (1 + zg * zg) * (v * zu).abs()
+    return v * zu, limit + 2.0 ** -140, zg, zu, bg, bu

@@ -27,12 +27,10 @@
 //   8 rows, 28672 -> 8192, both MXFP4       27 to 29 us on the GPU, 4.3 to 4.6 TB/s (a large copy: 5.0)
 //   96 rows over 64 experts, 2048 -> 1408   16 us           4.4 TB/s
 #include "gq_mx.h"
-
-#include <type_traits>
+#include "gq_tile.h"
 
 namespace gq {
 
-typedef __attribute__((address_space(3))) void* mx_lds_t;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------------------
@@ -136,136 +134,6 @@ struct MxTile {
     float* part;                  // partial sums [split][n][m], or null
 };
 
-// At most N loads in flight, and this wave's LDS accesses done.  The copies into LDS are loads
-// whose arrival only this counter tells, so no access moves across the wait.
-template <int N>
-__device__ __forceinline__ void mx_wait_vmcnt() {
-    static_assert(N >= 0 && N < 64, "a 6-bit counter");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
-    asm volatile("" ::: "memory");
-}
-
-// lgkmcnt(0) alone
-__device__ __forceinline__ void mx_wait_lds() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
-    asm volatile("" ::: "memory");
-}
-
-__device__ __forceinline__ void mx_barrier() {
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// One wave copies 64 x 16 bytes into LDS from `dst` on; lane l's come from r at voff + soff
-// (zeros out of r's range).
-__device__ __forceinline__ void mx_dma(__amdgpu_buffer_rsrc_t r, u32x4* dst, uint32_t voff, uint32_t soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mx_lds_t)dst, 16, voff, soff, 0, 0);
-}
-
-// `rows` rows of `row` bytes from p on, the first `skip` bytes left out (none where `on` is
-// false: every load reads zeros).  A tile's rows come to less than 2^31 bytes (256 of 2^20
-// values in three planes), so 32 bits hold it, which the scalar unit compares and selects.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const uint8_t* p, int rows, int64_t row, bool on = true, int skip = 0) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, on ? rows * (int)row - skip : 0, 0x00020000);
-}
-
-// Rows of expert e, clamped to [0, n].
-__device__ __forceinline__ void mx_expert_rows(const int64_t* offsets, int e, int64_t n, int64_t& lo,
-                                               int64_t& hi) {
-    lo = offsets[e];
-    hi = offsets[e + 1];
-    lo = lo < 0 ? 0 : (lo > n ? n : lo);
-    hi = hi < 0 ? 0 : (hi > n ? n : hi);
-}
-
-struct MxPlace {
-    int e;
-    int64_t t0;                   // first row of the tile
-    int rows;                     // rows of it
-    int col;                      // column tile
-    bool ok;
-};
-
-// Tiles of bm rows that expert e's rows make, the first `skip` left out.
-__device__ __forceinline__ int mx_row_tiles(const MxTile& p, int bm, int e, int skip = 0) {
-    if (e >= p.experts) return 0;
-    int64_t lo, hi;
-    mx_expert_rows(p.offsets, e, p.n, lo, hi);
-    lo += (int64_t)skip * bm;
-    return hi > lo ? (int)((hi - lo + bm - 1) / bm) : 0;
-}
-
-// Row tile `row` of the experts' (without the first `skip` of each) in their order, counted from
-// the offsets by each wave for itself, 64 experts at a time; not ok past the last one.
-__device__ __forceinline__ void mx_row_tile(const MxTile& p, int bm, int row, MxPlace& r, int skip = 0) {
-    const int lane = threadIdx.x & 63;
-    r.ok = false;
-    int first = 0;
-    for (int b = 0; b < p.experts; b += 64) {
-        const int c = mx_row_tiles(p, bm, b + lane, skip);
-        if (skip && !__ballot(c > 0)) continue;
-        int s = c;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(s, o, 64);
-            if (lane >= o) s += v;
-        }
-        const unsigned long long hit = __ballot(first + s > row);
-        if (hit) {
-            const int l = __ffsll((unsigned long long)hit) - 1;
-            r.e = __builtin_amdgcn_readfirstlane(b + l);
-            const int before = __builtin_amdgcn_readfirstlane(first + __shfl(s - c, l, 64));
-            int64_t lo, hi;
-            mx_expert_rows(p.offsets, r.e, p.n, lo, hi);
-            r.t0 = lo + (int64_t)(skip + row - before) * bm;
-            r.rows = (int)(hi - r.t0 < bm ? hi - r.t0 : bm);
-            r.ok = row >= before && r.rows > 0;     // (offsets out of order could count wrongly)
-            return;
-        }
-        first += __builtin_amdgcn_readfirstlane(__shfl(s, 63, 64));
-    }
-}
-
-// Block hw -> its tile.  XCD x (= hw % 8) takes a contiguous eighth of the tiles, which run
-// row-tile fastest within groups of 8 row tiles, so the blocks that one L2 serves at a time
-// share both operands.
-__device__ __forceinline__ MxPlace mx_place(const MxTile& p, int bm, int ncol) {
-    MxPlace r;
-    r.ok = false;
-    int64_t nrow;
-    if (p.offsets) {
-        int c = 0;
-        for (int b = 0; b < p.experts; b += 64) c += mx_row_tiles(p, bm, b + (threadIdx.x & 63));
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) c += __shfl_xor(c, o, 64);
-        nrow = __builtin_amdgcn_readfirstlane(c);
-    } else {
-        nrow = (p.n + bm - 1) / bm;
-    }
-    const int64_t total = nrow * ncol, eighth = (total + 7) / 8;
-    const int64_t in = blockIdx.x >> 3, lin = (int64_t)(blockIdx.x & 7) * eighth + in;
-    if (in >= eighth || lin >= total) return r;
-    constexpr int H = 8;
-    const int64_t g = lin / (H * ncol), rest = lin - g * (H * ncol);
-    const int64_t left = nrow - g * H;
-    const int64_t h = left < H ? left : H;
-    const int64_t row = g * H + rest % h;
-    r.col = (int)(rest / h);
-    if (p.offsets) {
-        mx_row_tile(p, bm, (int)row, r);
-        return r;
-    }
-    r.e = 0;
-    r.t0 = row * bm;
-    r.rows = (int)(p.n - r.t0 < bm ? p.n - r.t0 : bm);
-    r.ok = true;
-    return r;
-}
-
 // Geometry of a stage in 16-byte LDS slots.  KS (MX_GEMM): pieces of 64 values a stage.  With
 // one, the planes of float32 activations are stages of their own (and the weight is read for
 // each); with more, a stage holds them all.
@@ -294,15 +162,6 @@ struct MxGeo {
         return KS == 4 ? (row >> 1) & 7 : (KS == 2 ? (row >> 2) & 3 : (row >> 3) & 1);
     }
 };
-
-// f(integral_constant 0) .. f(integral_constant N - 1)
-template <int N, class F>
-__device__ __forceinline__ void mx_each(F f) {
-    if constexpr (N > 0) {
-        mx_each<N - 1>(f);
-        f(std::integral_constant<int, N - 1>{});
-    }
-}
 
 // The fragments of a part of a stage, and an accumulator.
 template <int MODE, int FM, int FN> struct MxHalf;
@@ -335,7 +194,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     extern __shared__ u32x4 mx_lds[];
     u32x4* const sc_lds = mx_lds + R * G::STAGE;
 
-    MxPlace at = mx_place(p, BM, (int)((p.m + BN - 1) / BN));
+    TilePlace at = tile_place(p, BM, (int)((p.m + BN - 1) / BN));
     if (!at.ok) return;
     // (the same in every lane; said so, or the descriptors built from it are looped over lanes)
     at.e = __builtin_amdgcn_readfirstlane(at.e);
@@ -359,13 +218,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     }
 
     // ---- sources
-    const __amdgpu_buffer_rsrc_t xr = mx_rsrc(p.A + at.t0 * p.a_row, at.rows, p.a_row);
+    const __amdgpu_buffer_rsrc_t xr = tile_rsrc(p.A + at.t0 * p.a_row, at.rows, p.a_row);
     const uint8_t* const Qe = p.Q + (int64_t)at.e * p.d_out * p.qb;
     const uint8_t* const Se = p.S + (int64_t)at.e * p.d_out * p.sb;
     const int wrows = (int)(p.m - j0 < BN ? p.m - j0 : BN);
-    const __amdgpu_buffer_rsrc_t sr = mx_rsrc(Se + j0 * p.sb, wrows, p.sb);
+    const __amdgpu_buffer_rsrc_t sr = tile_rsrc(Se + j0 * p.sb, wrows, p.sb);
     const __amdgpu_buffer_rsrc_t xsr =
-        MODE == MX_GEMM_MX ? mx_rsrc(p.AS + at.t0 * p.sb, at.rows, p.sb) : sr;
+        MODE == MX_GEMM_MX ? tile_rsrc(p.AS + at.t0 * p.sb, at.rows, p.sb) : sr;
 
     constexpr int XPW = G::X / NW, WPW = G::W / NW;          // slots a wave copies
     constexpr int XI = (XPW + 63) / 64, WI = (WPW + 63) / 64;
@@ -405,22 +264,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         const int ks = s / PA;
         if constexpr (MODE == MX_GEMM_DX) {
             const int o0 = ks * 64, left = (int)p.d_out - o0 < 64 ? (int)p.d_out - o0 : 64;
-            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + o0 * p.sb + j0 / 32, left, p.sb, s < s_hi, (int)(j0 / 32));
+            const __amdgpu_buffer_rsrc_t z = tile_rsrc(Se + o0 * p.sb + j0 / 32, left, p.sb, s < s_hi, (int)(j0 / 32));
             u32x4* wb = mx_lds + (s % R) * G::STAGE + G::X;
-            if (lane < SR) mx_dma(z, wb + G::W + wave * SR, sv, 0);
+            if (lane < SR) tile_dma(z, wb + G::W + wave * SR, sv, 0);
         } else {
             // a share of the next span's
             const int span = ks / SPAN + 1, part = ks % SPAN;
             u32x4* sb = sc_lds + (span % 3) * G::SROWS;
-            const __amdgpu_buffer_rsrc_t z = mx_rsrc(Se + j0 * p.sb, wrows, p.sb, s < s_hi);
+            const __amdgpu_buffer_rsrc_t z = tile_rsrc(Se + j0 * p.sb, wrows, p.sb, s < s_hi);
             constexpr int WR = BN / SPAN / NW;
             const int row = part * (BN / SPAN) + wave * WR;
-            if (lane < WR) mx_dma(z, sb + row, (uint32_t)((row + lane) * p.sb) + 16u * span, 0);
+            if (lane < WR) tile_dma(z, sb + row, (uint32_t)((row + lane) * p.sb) + 16u * span, 0);
             if constexpr (MODE == MX_GEMM_MX) {
-                const __amdgpu_buffer_rsrc_t xz = mx_rsrc(p.AS + at.t0 * p.sb, at.rows, p.sb, s < s_hi);
+                const __amdgpu_buffer_rsrc_t xz = tile_rsrc(p.AS + at.t0 * p.sb, at.rows, p.sb, s < s_hi);
                 constexpr int XR = BM / SPAN / NW;
                 const int xrow = part * (BM / SPAN) + wave * XR;
-                if (lane < XR) mx_dma(xz, sb + BN + xrow, (uint32_t)((xrow + lane) * p.sb) + 16u * span, 0);
+                if (lane < XR) tile_dma(xz, sb + BN + xrow, (uint32_t)((xrow + lane) * p.sb) + 16u * span, 0);
             }
         }
     };
@@ -428,18 +287,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         u32x4* base = mx_lds + (s % R) * G::STAGE;
         if (i < XI) {
             const uint32_t v = s < xe[i % XE] ? xv[i] : 0xC0000000u;          // past the row: zeros
-            if (XPW % 64 == 0 || lane < XPW % 64) mx_dma(xr, base + wave * XPW + i * 64, v, (uint32_t)s * (16u * G::XSPR));
+            if (XPW % 64 == 0 || lane < XPW % 64) tile_dma(xr, base + wave * XPW + i * 64, v, (uint32_t)s * (16u * G::XSPR));
         } else {
             i -= XI;
             u32x4* wb = base + G::X + wave * WPW + i * 64;
             const int ks = s / PA;
             if constexpr (MODE == MX_GEMM_DX) {
                 const int o0 = ks * 64, left = (int)p.d_out - o0 < 64 ? (int)p.d_out - o0 : 64;
-                const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + o0 * p.qb + j0 / 2, left, p.qb, s < s_hi, (int)(j0 / 2));
-                if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(q, wb, wv[i], 0);
+                const __amdgpu_buffer_rsrc_t q = tile_rsrc(Qe + o0 * p.qb + j0 / 2, left, p.qb, s < s_hi, (int)(j0 / 2));
+                if (WPW % 64 == 0 || lane < WPW % 64) tile_dma(q, wb, wv[i], 0);
             } else {
-                const __amdgpu_buffer_rsrc_t q = mx_rsrc(Qe + j0 * p.qb, wrows, p.qb, s < s_hi);
-                if (WPW % 64 == 0 || lane < WPW % 64) mx_dma(q, wb, wv[i], (uint32_t)ks * (16u * G::WSPR));
+                const __amdgpu_buffer_rsrc_t q = tile_rsrc(Qe + j0 * p.qb, wrows, p.qb, s < s_hi);
+                if (WPW % 64 == 0 || lane < WPW % 64) tile_dma(q, wb, wv[i], (uint32_t)ks * (16u * G::WSPR));
             }
         }
     };
@@ -454,10 +313,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         const int span = s_lo / PA / SPAN;
         u32x4* sb = sc_lds + (span % 3) * G::SROWS;
         constexpr int WR = BN / NW;
-        if (lane < WR) mx_dma(sr, sb + wave * WR, (uint32_t)((wave * WR + lane) * p.sb) + 16u * span, 0);
+        if (lane < WR) tile_dma(sr, sb + wave * WR, (uint32_t)((wave * WR + lane) * p.sb) + 16u * span, 0);
         if constexpr (MODE == MX_GEMM_MX) {
             constexpr int XR = BM / NW;
-            if (lane < XR) mx_dma(xsr, sb + BN + wave * XR, (uint32_t)((wave * XR + lane) * p.sb) + 16u * span, 0);
+            if (lane < XR) tile_dma(xsr, sb + BN + wave * XR, (uint32_t)((wave * XR + lane) * p.sb) + 16u * span, 0);
         }
     }
 
@@ -588,7 +447,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     auto run = [&](const Half& cur, auto own, int s, auto part, Half& nxt, int sl, auto l0, auto l1) {
         constexpr int MM = Half::PRODUCTS, L0 = decltype(l0)::value, LN = decltype(l1)::value - L0;
         constexpr int RP = (2 * Half::STEPS + MM - 1) / MM;                   // reads beside a product
-        mx_each<MM>([&](auto index) {
+        tile_each<MM>([&](auto index) {
             constexpr int i = decltype(index)::value;
 #pragma unroll
             for (int k = RP * i; k < RP * (i + 1); ++k)
@@ -610,15 +469,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         issue_scales(s_lo + R - 1);
 #pragma unroll
         for (int i = 0; i < SOON; ++i) issue_one(s_lo + R - 1, i);
-        mx_wait_vmcnt<LOADS * (R - 2) + LOADS - LATE>();
-        mx_barrier();
+        tile_wait_vmcnt<LOADS * (R - 2) + LOADS - LATE>();
+        tile_barrier();
         // a wave whose rows all lie past the tile's own only copies
         const bool idle = wm * TM >= at.rows;
         for (int s = s_lo; idle && s < s_hi; ++s) {
 #pragma unroll
             for (int i = SOON; i < ALL; ++i) issue_one(s + R - 1, i);
-            mx_wait_vmcnt<LOADS * (R - 2)>();
-            mx_barrier();
+            tile_wait_vmcnt<LOADS * (R - 2)>();
+            tile_barrier();
             issue_scales(s + R);
 #pragma unroll
             for (int i = 0; i < SOON; ++i) issue_one(s + R, i);
@@ -631,19 +490,19 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         for (int s = s_lo; !idle && s < s_hi; ++s) {
             // the rest of the last stage's loads go out with the first part
             run(A, zero, s, std::integral_constant<int, 1>{}, B, s + R - 1, soon, all);
-            mx_each<G::PARTS / 2 - 1>([&](auto i) {
+            tile_each<G::PARTS / 2 - 1>([&](auto i) {
                 constexpr int h = 2 * decltype(i)::value;
                 run(B, std::integral_constant<int, h + 1>{}, s, std::integral_constant<int, h + 2>{}, A, 0, zero, zero);
                 run(A, std::integral_constant<int, h + 2>{}, s, std::integral_constant<int, h + 3>{}, B, 0, zero, zero);
             });
-            mx_wait_vmcnt<LOADS * (R - 2)>();    // stage s + 1 has landed
-            mx_barrier();                        // and this one's slot has been read by every wave
+            tile_wait_vmcnt<LOADS * (R - 2)>();    // stage s + 1 has landed
+            tile_barrier();                        // and this one's slot has been read by every wave
             issue_scales(s + R);
             run(B, std::integral_constant<int, G::PARTS - 1>{}, s + 1, zero, A, s + R, zero, soon);  // past the last stage: read and not used
             take_scales(s + 1);
         }
     }
-    mx_wait_vmcnt<0>();          // no load may land in the LDS later
+    tile_wait_vmcnt<0>();          // no load may land in the LDS later
     __syncthreads();
 
     // ---- store, T rows of a wave's tile at a time, by way of LDS of its own: in the
@@ -746,16 +605,16 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
     // the groups that experts have beyond those.
     const int beyond = (int)blockIdx.y - p.experts, step = (int)gridDim.y - p.experts;
     int64_t lo = 0, hi = p.n;
-    if (p.offsets && beyond < 0) mx_expert_rows(p.offsets, blockIdx.y, p.n, lo, hi);
+    if (p.offsets && beyond < 0) tile_expert_rows(p.offsets, blockIdx.y, p.n, lo, hi);
     for (int turn = 0;; ++turn) {
-        MxPlace place;
+        TilePlace place;
         if (beyond < 0) {
             place.e = blockIdx.y;
             place.t0 = lo + 16 * turn;
             place.rows = (int)(hi - place.t0 < 16 ? hi - place.t0 : 16);
             place.ok = turn < MX_FIRST && place.rows > 0;
         } else {
-            mx_row_tile(p, 16, beyond + turn * step, place, MX_FIRST);
+            tile_of_row(p, 16, beyond + turn * step, place, MX_FIRST);
         }
         if (!place.ok) return;
         if (turn > 0) __syncthreads();           // the sums of the rows before have been read
@@ -763,11 +622,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
         const int64_t t0 = place.t0, row0 = (int64_t)place.e * p.d_out + j0;
         auto copy = [&](int c) {                     // past the last piece: clears, reads nothing
             u32x4* to = ring + (c & 1) * PIECE;
-            const __amdgpu_buffer_rsrc_t wr = mx_rsrc(p.Q + row0 * p.qb, wrows, p.qb, c < c1);
-            const __amdgpu_buffer_rsrc_t sr = mx_rsrc(p.S + row0 * p.sb, wrows, p.sb, c < c1);
+            const __amdgpu_buffer_rsrc_t wr = tile_rsrc(p.Q + row0 * p.qb, wrows, p.qb, c < c1);
+            const __amdgpu_buffer_rsrc_t sr = tile_rsrc(p.S + row0 * p.sb, wrows, p.sb, c < c1);
 #pragma unroll
-            for (int i = 0; i < WS / 64; ++i) mx_dma(wr, to + 64 * i, wv[i], (uint32_t)c * (16u * SPR));
-            mx_dma(sr, to + WS, lane < 16 * MT ? (uint32_t)(lane * p.sb) : 0xC0000000u, (uint32_t)c * (4u * KU));
+            for (int i = 0; i < WS / 64; ++i) tile_dma(wr, to + 64 * i, wv[i], (uint32_t)c * (16u * SPR));
+            tile_dma(sr, to + WS, lane < 16 * MT ? (uint32_t)(lane * p.sb) : 0xC0000000u, (uint32_t)c * (4u * KU));
         };
 
         const int64_t xrow = t0 + (r < rows ? r : rows - 1);
@@ -803,7 +662,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
             }
             __builtin_amdgcn_sched_barrier(0);
             copy(c + 1);
-            mx_wait_vmcnt<LOADS>();
+            tile_wait_vmcnt<LOADS>();
             __builtin_amdgcn_sched_barrier(0);
             const uint8_t* const at = (const uint8_t*)(ring + (c & 1) * PIECE);
 #pragma unroll
@@ -831,9 +690,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_stream(MxTile p) {
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            mx_wait_lds();                       // read, before its half of the ring is copied into
+            tile_wait_lds();                       // read, before its half of the ring is copied into
         }
-        mx_wait_vmcnt<0>();                      // no copy into the ring may land later
+        tile_wait_vmcnt<0>();                      // no copy into the ring may land later
 #pragma unroll
         for (int t = 0; t < MT; ++t) *(f32x4*)(sums(wave, t) + 4 * lane) = acc[t];
         __syncthreads();
@@ -862,8 +721,8 @@ __global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part,
     int64_t lo = 0, hi = n;
     if (offsets) {
         int64_t a, b;
-        mx_expert_rows(offsets, 0, n, lo, a);
-        mx_expert_rows(offsets, experts - 1, n, b, hi);
+        tile_expert_rows(offsets, 0, n, lo, a);
+        tile_expert_rows(offsets, experts - 1, n, b, hi);
     }
     const int64_t first = lo * m, end = hi * m, all = n * m, stride = (int64_t)gridDim.x * 256;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;

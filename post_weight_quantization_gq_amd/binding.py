@@ -128,13 +128,13 @@ _SIGS = {
     "fp8_quantize_weight": (ctypes.c_int, [_vp, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _vp]),
     "fp8_dequantize": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i64, _vp, _i32, _vp]),
     "fp8_dequantize_weight": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i64, _i64, _vp, _i32, _vp]),
-    "fp8_gemm_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "fp8_gemm_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i32]),
     "fp8_gemm": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _i32,
                                 _vp, _sz, _vp]),
-    "fp8_gemm_dx_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "fp8_gemm_dx_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i32]),
     "fp8_gemm_dx": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _i32,
                                    _vp, _sz, _vp]),
-    "fp8_ffn_gate_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "fp8_ffn_gate_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i32]),
     "fp8_ffn_gate": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32,
                                     _vp, _vp, _i32, _vp, _sz, _vp]),
     "fp8_ffn_gate_packed_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
@@ -1099,8 +1099,8 @@ def _mm_scratch(x, ws, size, size_args):
     return ws, ws.data_ptr(), ws.numel()
 
 
-def _mm_product(x, first, offsets, shape, y, out_dtype, ws, size, size_args, call, stream):
-    """What products with one output share.  call(out, out dtype, ws, ws bytes, stream) makes it.
+def _mm_product(x, first, offsets, shape, y, out_dtype, ws, size, size_args, call, stream, by_type=True):
+    """What products with one output share.  by_type: the workspace's size goes by the output's type.
     An output of its own has zeros in the rows of no expert."""
     if ws is not None and ws is not False:
         _mx_tensor(ws, "ws", x.get_device(), _U8)
@@ -1108,23 +1108,27 @@ def _mm_product(x, first, offsets, shape, y, out_dtype, ws, size, size_args, cal
     with where:
         if y is None:
             y = (x.new_empty if offsets is None else x.new_zeros)(shape, dtype=out_dtype)
-        keep, wp, wn = _mm_scratch(x, ws, size, size_args)
-        status = call(*first, y.data_ptr(), _MX_DTYPES[y.dtype], wp, wn, st)
+        dt = _MX_DTYPES[y.dtype]
+        keep, wp, wn = _mm_scratch(x, ws, size, (*size_args, dt) if by_type else size_args)
+        status = call(*first, y.data_ptr(), dt, wp, wn, st)
     if status:
         _check(status)
     return y
 
 
-def fp8_gemm_workspace_size(n, d_in, d_out, experts=1, scales=torch.uint8) -> int:
-    return int(library().fp8_gemm_workspace_size(n, d_in, d_out, experts, _scale_type(scales)))
+def fp8_gemm_workspace_size(n, d_in, d_out, experts=1, scales=torch.uint8, dtype=GQ_BF16) -> int:
+    """dtype: the output's."""
+    return int(library().fp8_gemm_workspace_size(n, d_in, d_out, experts, _scale_type(scales), dtype))
 
 
-def fp8_gemm_dx_workspace_size(n, d_in, d_out, experts=1, scales=torch.uint8) -> int:
-    return int(library().fp8_gemm_dx_workspace_size(n, d_in, d_out, experts, _scale_type(scales)))
+def fp8_gemm_dx_workspace_size(n, d_in, d_out, experts=1, scales=torch.uint8, dtype=GQ_BF16) -> int:
+    """dtype: the output's."""
+    return int(library().fp8_gemm_dx_workspace_size(n, d_in, d_out, experts, _scale_type(scales), dtype))
 
 
-def fp8_ffn_gate_workspace_size(n, d_in, d_ff, experts=1, scales=torch.uint8) -> int:
-    return int(library().fp8_ffn_gate_workspace_size(n, d_in, d_ff, experts, _scale_type(scales)))
+def fp8_ffn_gate_workspace_size(n, d_in, d_ff, experts=1, scales=torch.uint8, dtype=GQ_BF16) -> int:
+    """dtype: the output's."""
+    return int(library().fp8_ffn_gate_workspace_size(n, d_in, d_ff, experts, _scale_type(scales), dtype))
 
 
 def fp8_ffn_gate_packed_workspace_size(n, d_in, d_ff, experts=1, scales=torch.uint8) -> int:
@@ -1147,7 +1151,8 @@ def fp8_gemm(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=N
              stream=None) -> torch.Tensor:
     """y [n][d_out] = x W^T for x packed by fp8_quantize (XQ, XS) and W by fp8_quantize_weight
     (Q, S), or by others: codes in rows of whole 128s and float32 scales [ceil(d_out / 128)]
-    [ceil(d_in / 128)].  Both have scales of one type.  With offsets (int64 [experts + 1] on the device)
+    [ceil(d_in / 128)].  Both have scales of one type.  A float32 output has float32 sums throughout; a
+    bfloat16 one is faster, with products of eight added to 14 bits.  With offsets (int64 [experts + 1] on the device)
     rows offsets[e] .. offsets[e + 1] - 1 are multiplied by weight e of Q [experts][d_out][..],
     and the other rows of a given y keep their values (of a new one: zeros).  out_dtype: bfloat16
     unless given.  Codes carry no gradient: fp8_gemm_dx is the product's part of it."""
@@ -1371,7 +1376,7 @@ def ffn_gate_dx(dzg, dzu, G, U, offsets=None, y=None, out_dtype=None, ws=None, s
     _mm_output(y, out_dtype, (n, d_in), index)
     first = (dzg.data_ptr(), dzu.data_ptr(), n, d_ff, G.data_ptr(), U.data_ptr(), d_in, experts, op)
     return _mm_product(dzg, first, offsets, (n, d_in), y, out_dtype, ws, lib.ffn_gate_dx_workspace_size,
-                       (n, d_in, d_ff, experts), lib.ffn_gate_dx, stream)
+                       (n, d_in, d_ff, experts), lib.ffn_gate_dx, stream, by_type=False)
 
 
 def ffn_gate_dw(dzg, dzu, x, experts=None, offsets=None, which=(True, True), dG=None, dU=None,

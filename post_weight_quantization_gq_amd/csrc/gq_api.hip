@@ -1098,22 +1098,26 @@ static size_t mm_size(gq::MmForm form, gq::MmElt elt, int64_t n, int64_t d_in, i
     return gq::mm_workspace(form, elt, n, d_in, d_out, experts, packed);
 }
 
-static gq::MmElt fp8_elt(gq_scale s) { return s == GQ_SCALE_F32 ? gq::MM_FS : gq::MM_E8; }
-
-size_t fp8_gemm_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts, gq_scale s_dt) {
-    return scale_ok(s_dt) ? mm_size(gq::MM_NT, fp8_elt(s_dt), n, d_in, d_out, experts, false) : 0;
+// float32 outputs have products whose sums are float32 throughout
+static gq::MmElt fp8_elt(gq_scale s, gq_dtype y) {
+    if (y == GQ_F32) return s == GQ_SCALE_F32 ? gq::MM_FSW : gq::MM_E8W;
+    return s == GQ_SCALE_F32 ? gq::MM_FS : gq::MM_E8;
 }
 
-size_t fp8_gemm_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts, gq_scale s_dt) {
-    return scale_ok(s_dt) ? mm_size(gq::MM_NN, fp8_elt(s_dt), n, d_in, d_out, experts, false) : 0;
+size_t fp8_gemm_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts, gq_scale s_dt, gq_dtype y_dt) {
+    return scale_ok(s_dt) && dtype_ok(y_dt) ? mm_size(gq::MM_NT, fp8_elt(s_dt, y_dt), n, d_in, d_out, experts, false) : 0;
 }
 
-size_t fp8_ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts, gq_scale s_dt) {
-    return scale_ok(s_dt) ? mm_size(gq::MM_GATE, fp8_elt(s_dt), n, d_in, d_ff, experts, false) : 0;
+size_t fp8_gemm_dx_workspace_size(int64_t n, int64_t d_in, int64_t d_out, int32_t experts, gq_scale s_dt, gq_dtype y_dt) {
+    return scale_ok(s_dt) && dtype_ok(y_dt) ? mm_size(gq::MM_NN, fp8_elt(s_dt, y_dt), n, d_in, d_out, experts, false) : 0;
+}
+
+size_t fp8_ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts, gq_scale s_dt, gq_dtype y_dt) {
+    return scale_ok(s_dt) && dtype_ok(y_dt) ? mm_size(gq::MM_GATE, fp8_elt(s_dt, y_dt), n, d_in, d_ff, experts, false) : 0;
 }
 
 size_t fp8_ffn_gate_packed_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts, gq_scale s_dt) {
-    return scale_ok(s_dt) ? mm_size(gq::MM_GATE, fp8_elt(s_dt), n, d_in, d_ff, experts, true) : 0;
+    return scale_ok(s_dt) ? mm_size(gq::MM_GATE, fp8_elt(s_dt, GQ_BF16), n, d_in, d_ff, experts, true) : 0;
 }
 
 size_t ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts) {
@@ -1190,7 +1194,7 @@ gq_status fp8_gemm(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_in, c
                    const void* S, gq_scale s_dt, int64_t d_out, int32_t experts,
                    const int64_t* offsets, void* y, gq_dtype y_dt, void* ws, size_t ws_bytes,
                    void* stream) {
-    gq::MmCall c{gq::MM_NT, fp8_elt(s_dt), {XQ, nullptr}, XS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {y, nullptr}};
+    gq::MmCall c{gq::MM_NT, fp8_elt(s_dt, y_dt), {XQ, nullptr}, XS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {y, nullptr}};
     return mm_product(c, s_dt, y_dt, 0, ws, ws_bytes, stream, "fp8_gemm");
 }
 
@@ -1198,7 +1202,7 @@ gq_status fp8_gemm_dx(const uint8_t* GQ, const void* GS, int64_t n, int64_t d_ou
                       const void* S, gq_scale s_dt, int64_t d_in, int32_t experts,
                       const int64_t* offsets, void* dx, gq_dtype dx_dt, void* ws, size_t ws_bytes,
                       void* stream) {
-    gq::MmCall c{gq::MM_NN, fp8_elt(s_dt), {GQ, nullptr}, GS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {dx, nullptr}};
+    gq::MmCall c{gq::MM_NN, fp8_elt(s_dt, dx_dt), {GQ, nullptr}, GS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {dx, nullptr}};
     return mm_product(c, s_dt, dx_dt, 0, ws, ws_bytes, stream, "fp8_gemm_dx");
 }
 
@@ -1206,7 +1210,7 @@ gq_status fp8_ffn_gate(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_i
                        const void* GS, const uint8_t* UQ, const void* US, gq_scale s_dt, int64_t d_ff,
                        gq_activation act, int32_t experts, const int64_t* offsets, void* h,
                        gq_dtype h_dt, void* ws, size_t ws_bytes, void* stream) {
-    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets, {h, nullptr}};
+    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt, h_dt), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets, {h, nullptr}};
     return mm_product(c, s_dt, h_dt, act, ws, ws_bytes, stream, "fp8_ffn_gate");
 }
 
@@ -1216,7 +1220,7 @@ gq_status fp8_ffn_gate_packed(const uint8_t* XQ, const void* XS, int64_t n, int6
                               const int64_t* offsets, uint8_t* HQ, void* HS, void* ws,
                               size_t ws_bytes, void* stream) {
     if (n > 0 && (!HQ || !HS)) return fail(GQ_EINVAL, "null output");
-    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets};
+    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt, GQ_BF16), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets};
     c.hq = HQ;
     c.hs = HS;
     return mm_product(c, s_dt, GQ_F32, act, ws, ws_bytes, stream, "fp8_ffn_gate_packed");

@@ -32,7 +32,14 @@ enum MmForm {
     MM_NN = 2,                    // y = a W, or a[0] W[0] + a[1] W[1]
     MM_TN = 3                     // y[i] = a[i]^T w, for two a
 };
-enum MmElt { MM_BF16 = 0, MM_E8 = 1, MM_FS = 2 };   // bfloat16; e4m3 with scales 2^(s - 127), or float32 ones
+// bfloat16; e4m3 with scales 2^(s - 127), or float32 ones.  The matrix cores add the products of 8 codes
+// to 14 bits of their largest (a second product 2^-13 as large counts, one of 2^-14 is lost; between eights, and with
+// the accumulator, all 24 bits count).  That is a tenth of a bfloat16 output's rounding or less, so such
+// outputs take it; the W types are for float32 outputs: codes converted to bfloat16, whose products are
+// added in float32, at half the rate.
+enum MmElt { MM_BF16 = 0, MM_E8 = 1, MM_FS = 2, MM_E8W = 3, MM_FSW = 4 };
+constexpr bool mm_bytes(int elt) { return elt == MM_E8 || elt == MM_E8W; }     // scales are bytes
+constexpr bool mm_wide(int elt) { return elt == MM_E8W || elt == MM_FSW; }
 
 struct MmCall {
     MmForm form;

@@ -5,175 +5,325 @@
 //   MM_GATE  h[t][j] = act(zg) zu, zg[t][j] = sum_i a[t][i] g[j][i], zu alike
 //   MM_NN    y[t][i] = sum_j a[t][j] w[j][i], of two pairs (a, w) added
 //   MM_TN    y[j][i] = sum_t a[t][j] x[t][i], for two a
-#include "gq_mm.h"
+//
+// This file plans a call and runs what is not a product: copies of rows whose length the
+// asynchronous loads cannot take, and the outputs of contractions that are split over blocks.
+#include "gq_mm_plan.h"
+#include "gq_tile.h"
 
 namespace gq {
 
-// ---------------------------------------------------------------------------
-// Every product in its plainest form: blocks of 64 x 64 outputs, 16 of the contraction at a time
-// through LDS as float32.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ float mm_value(MmElt elt, const void* p, int64_t row_bytes, int64_t row, int64_t i) {
-    if (elt == MM_BF16) return bf16_bits_to_f32(*(const uint16_t*)((const char*)p + row * row_bytes + 2 * i));
-    return __builtin_amdgcn_cvt_f32_fp8((int)*((const uint8_t*)p + row * row_bytes + i), 0);
-}
-
-__device__ __forceinline__ float mm_scale(MmElt elt, const void* S, int64_t i) {
-    if (elt == MM_BF16) return 1.f;
-    return elt == MM_E8 ? fp8_load_scale<false>(S, i) : fp8_load_scale<true>(S, i);
-}
-
-__global__ __launch_bounds__(256) void k_mm_plain(MmCall c, int64_t a_row, int64_t w_row) {
-    __shared__ float xs[16][65], wsh[2][16][65];
-    __shared__ int64_t place[4];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const bool tn = c.form == MM_TN, nn = c.form == MM_NN, gate = c.form == MM_GATE;
-    const int64_t m = nn || tn ? c.d_in : c.d_out, j0 = (int64_t)blockIdx.x * 64;
-    int64_t e = 0, lo = 0, hi = c.n, t0 = (int64_t)blockIdx.y * 64;
-    const int which = tn ? blockIdx.z & 1 : 0;
-    if (tn && !c.y[which]) return;
-    if (tn) {
-        e = blockIdx.z >> 1;
-        if (c.offsets) {
-            lo = c.offsets[e];
-            hi = c.offsets[e + 1];
-            lo = lo < 0 ? 0 : (lo > c.n ? c.n : lo);
-            hi = hi < lo ? lo : (hi > c.n ? c.n : hi);
-        }
-    } else if (c.offsets) {
-        if (tid == 0) {
-            int64_t left = blockIdx.y, found = -1, a = 0, b = 0;
-            for (int x = 0; x < c.experts && found < 0; ++x) {
-                a = c.offsets[x];
-                b = c.offsets[x + 1];
-                a = a < 0 ? 0 : (a > c.n ? c.n : a);
-                b = b < a ? a : (b > c.n ? c.n : b);
-                const int64_t tiles = (b - a + 63) / 64;
-                if (left < tiles) found = x;
-                else left -= tiles;
-            }
-            place[0] = found;
-            place[1] = a + 64 * left;
-            place[2] = b;
-        }
-        __syncthreads();
-        e = place[0];
-        if (e < 0) return;
-        t0 = place[1];
-        hi = place[2];
+// Rows of k bfloat16 values as rows of a multiple of 8, zeros behind.
+__global__ __launch_bounds__(256) void k_mm_pad(const void* __restrict__ x, int64_t rows, int64_t k, int64_t pieces,
+                                               u32x4* __restrict__ out) {
+    const int64_t total = rows * pieces, stride = (int64_t)gridDim.x * 256;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += stride) {
+        const int64_t r = mx_div(t, pieces), i = (t - r * pieces) * 8;
+        float v[8];
+        mx_load8<true>(x, r * k, i, k, v);
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = (__float_as_uint(v[2 * e]) >> 16) | (__float_as_uint(v[2 * e + 1]) & 0xffff0000u);
+        out[t] = w;
     }
-    const int64_t rows_end = tn ? c.d_out : hi;
-    if (t0 >= rows_end) return;
-    const int64_t k_one = tn ? hi - lo : (nn ? c.d_out : c.d_in), k_all = nn && c.a[1] ? 2 * k_one : k_one;
-    const int64_t wblocks = fp8_blocks(c.d_in), sbase = e * ((c.d_out + 127) / 128) * wblocks;
-    const int64_t aspr = fp8_scales(nn ? c.d_out : c.d_in);
-    float acc[2][4][4] = {};
-    for (int64_t k0 = 0; k0 < k_all; k0 += 16) {
-        for (int i = tid; i < 1024; i += 256) {
-            const int kk = i & 15, r = i >> 4;
-            const int64_t k = k0 + kk, src = nn && k >= k_one ? 1 : 0, kl = k - src * k_one;
-            float x = 0.f, w[2] = {0.f, 0.f};
-            if (k < k_all) {
-                if (t0 + r < rows_end) {
-                    if (tn) x = mm_value(c.elt, c.a[which], a_row, lo + kl, t0 + r);
-                    else x = mm_value(c.elt, c.a[src], a_row, t0 + r, kl) * mm_scale(c.elt, c.as, (t0 + r) * aspr + kl / 128);
-                }
-                if (j0 + r < m) {
-                    if (tn) w[0] = mm_value(c.elt, c.w[0], w_row, lo + kl, j0 + r);
-                    else if (nn) w[0] = mm_value(c.elt, c.w[src], w_row, e * c.d_out + kl, j0 + r) * mm_scale(c.elt, c.ws[src], sbase + kl / 128 * wblocks + (j0 + r) / 128);
-                    else
-                        for (int q = 0; q <= gate; ++q)
-                            w[q] = mm_value(c.elt, c.w[q], w_row, e * c.d_out + j0 + r, kl) * mm_scale(c.elt, c.ws[q], sbase + (j0 + r) / 128 * wblocks + kl / 128);
-                }
-            }
-            xs[kk][r] = x;
-            wsh[0][kk][r] = w[0];
-            wsh[1][kk][r] = w[1];
-        }
-        __syncthreads();
-        for (int kk = 0; kk < 16; ++kk)
-            for (int a = 0; a < 4; ++a)
-                for (int b = 0; b < 4; ++b) {
-                    acc[0][a][b] += xs[kk][ty + 16 * a] * wsh[0][kk][tx + 16 * b];
-                    if (gate) acc[1][a][b] += xs[kk][ty + 16 * a] * wsh[1][kk][tx + 16 * b];
-                }
-        __syncthreads();
-    }
-    void* y = tn ? (char*)c.y[which] + e * c.d_out * m * (c.y_bf16 ? 2 : 4) : c.y[0];
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) {
-            const int64_t t = t0 + ty + 16 * a, j = j0 + tx + 16 * b;
-            if (t >= rows_end || j >= m) continue;
-            float v = acc[0][a][b];
-            if (gate) {
-                if (c.z[0]) {
-                    c.z[0][t * m + j] = v;
-                    c.z[1][t * m + j] = acc[1][a][b];
-                }
-                v = act_of<false>(v, c.act, nullptr) * acc[1][a][b];
-            }
-            if (c.y_bf16) ((uint16_t*)y)[t * m + j] = (uint16_t)f32_to_bf16_bits(v);
-            else ((float*)y)[t * m + j] = v;
-        }
 }
 
-// h [n][m] of float32 into packed rows, those of an expert alone
+// The rows of the experts' (all without offsets).
+__device__ __forceinline__ void mm_rows(const int64_t* offsets, int experts, int64_t n, int64_t& lo, int64_t& hi) {
+    lo = 0;
+    hi = n;
+    if (offsets) {
+        int64_t a, b;
+        tile_expert_rows(offsets, 0, n, lo, a);
+        tile_expert_rows(offsets, experts - 1, n, b, hi);
+    }
+}
+
+// The sum of `split` parts `all` values apart, V values of it, in their order.
+template <class V>
+__device__ __forceinline__ V mm_sum(const float* part, int split, int64_t all) {
+    V s = *(const V*)part;
+    int k = 1;
+    for (; k + 4 <= split; k += 4) {               // four loads in flight, added in their order
+        V v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = *(const V*)(part + (k + i) * all);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += v[i];
+    }
+    for (; k < split; ++k) s += *(const V*)(part + k * all);
+    return s;
+}
+
+// y = the sum of a split contraction's parts, or of MM_GATE's two products h = act(zg) zu.
+template <bool GATE>
+__global__ __launch_bounds__(256) void k_mm_join(const float* __restrict__ part, int split, int64_t all, int64_t n, int64_t m,
+                                                const int64_t* __restrict__ offsets, int experts, void* __restrict__ y, int y_bf16,
+                                                int act, float* __restrict__ zg, float* __restrict__ zu) {
+    int64_t lo, hi;
+    mm_rows(offsets, experts, n, lo, hi);
+    const int64_t first = lo * m, end = hi * m, stride = (int64_t)gridDim.x * 256;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, step = GATE ? 2 * all : all;
+    auto value = [&](auto a, auto b) {
+        if constexpr (!GATE) return a;
+        else {
+            auto v = a;
+            if constexpr (sizeof(a) == 4) v = act_of<false>(a, act, nullptr) * b;
+            else
+                for (int i = 0; i < 4; ++i) v[i] = act_of<false>(a[i], act, nullptr) * b[i];
+            return v;
+        }
+    };
+    if (all % 4 == 0 && m % 4 == 0 && (((uintptr_t)y & (y_bf16 ? 7u : 15u)) | (((uintptr_t)zg | (uintptr_t)zu) & 15u)) == 0) {
+        for (int64_t t = first + 4 * id; t < end; t += 4 * stride) {
+            const f32x4 a = mm_sum<f32x4>(part + t, split, step), b = GATE ? mm_sum<f32x4>(part + all + t, split, step) : a;
+            if (GATE && zg) {
+                *(f32x4*)(zg + t) = a;
+                *(f32x4*)(zu + t) = b;
+            }
+            const f32x4 s = value(a, b);
+            if (y_bf16) *(u32x2*)((uint16_t*)y + t) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+            else *(f32x4*)((float*)y + t) = s;
+        }
+        return;
+    }
+    for (int64_t t = first + id; t < end; t += stride) {
+        const float a = mm_sum<float>(part + t, split, step), b = GATE ? mm_sum<float>(part + all + t, split, step) : a;
+        if (GATE && zg) {
+            zg[t] = a;
+            zu[t] = b;
+        }
+        const float s = value(a, b);
+        if (y_bf16) ((uint16_t*)y)[t] = (uint16_t)f32_to_bf16_bits(s);
+        else ((float*)y)[t] = s;
+    }
+}
+
+// MM_GATE's h of a split contraction, or of tiles narrower than a block, into packed rows.  A lane takes
+// 8 values, 16 lanes a block.
 template <bool F32>
-__global__ __launch_bounds__(256) void k_mm_pack(const float* __restrict__ h, int64_t n, int64_t m,
-                                                const int64_t* __restrict__ offsets, int experts, u32x2* __restrict__ Q,
-                                                void* __restrict__ S) {
-    const int64_t ppr = 16 * fp8_blocks(m), spr = fp8_scales(m), pieces = n * ppr;
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= pieces) return;
-    const int64_t r = mx_div(t, ppr), p = t - r * ppr, i = p * 8;
-    if (offsets && (r < offsets[0] || r >= offsets[experts])) return;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (i < m) mx_load8<false>(h, r * m, i, m, v);
-    uint32_t top = 0u;
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t b = __float_as_uint(v[k]) & 0x7fffffffu;
-        top = top > b ? top : b;
-    }
-    for (int o = 1; o < 16; o <<= 1) {
-        const uint32_t b = (uint32_t)__shfl_xor((int)top, o, 64);
-        top = top > b ? top : b;
-    }
-    const uint32_t s = fp8_scale_byte(top);
-    const float f = fp8_scale_inverse(s);
-    const u32x2 q{fp8_pack4(v[0] * f, v[1] * f, v[2] * f, v[3] * f), fp8_pack4(v[4] * f, v[5] * f, v[6] * f, v[7] * f)};
-    Q[t] = s == 255u ? u32x2{0u, 0u} : q;
-    if (p % 16 == 0)
-        for (int64_t b = p / 16; b < (p + 16 >= ppr ? spr : p / 16 + 1); ++b) {
-            const uint32_t byte = b == p / 16 ? s : 127u;
-            if (F32) ((float*)S)[r * spr + b] = fp8_scale_value(byte);
-            else ((uint8_t*)S)[r * spr + b] = (uint8_t)byte;
+__global__ __launch_bounds__(256) void k_mm_join_pack(const float* __restrict__ part, int split, int64_t n, int64_t m,
+                                                     const int64_t* __restrict__ offsets, int experts, int act,
+                                                     u32x2* __restrict__ Q, void* __restrict__ S) {
+    int64_t lo, hi;
+    mm_rows(offsets, experts, n, lo, hi);
+    const int64_t ppr = 16 * fp8_blocks(m), spr = fp8_scales(m), end = hi * ppr, all = n * m;
+    for (int64_t t = lo * ppr + (int64_t)blockIdx.x * 256 + threadIdx.x; t < end; t += (int64_t)gridDim.x * 256) {
+        const int64_t r = mx_div(t, ppr), p = t - r * ppr, i = p * 8;
+        float v[8];
+        if (m % 4 == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x4 a{0.f, 0.f, 0.f, 0.f}, b = a;
+                if (i + 4 * h < m) {
+                    const float* const from = part + r * m + i + 4 * h;
+                    a = mm_sum<f32x4>(from, split, 2 * all);
+                    b = mm_sum<f32x4>(from + all, split, 2 * all);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[4 * h + k] = act_of<false>(a[k], act, nullptr) * b[k];
+            }
+        } else {
+            for (int k = 0; k < 8; ++k) {
+                v[k] = 0.f;
+                if (i + k < m) {
+                    const float* const from = part + r * m + i + k;
+                    v[k] = act_of<false>(mm_sum<float>(from, split, 2 * all), act, nullptr) * mm_sum<float>(from + all, split, 2 * all);
+                }
+            }
         }
+        uint32_t top = 0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t b = __float_as_uint(v[k]) & 0x7fffffffu;
+            top = top > b ? top : b;
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+            const uint32_t b = (uint32_t)__shfl_xor((int)top, o, 64);
+            top = top > b ? top : b;
+        }
+        const uint32_t s = fp8_scale_byte(top);
+        const float f = fp8_scale_inverse(s);
+        const u32x2 q{fp8_pack4(v[0] * f, v[1] * f, v[2] * f, v[3] * f), fp8_pack4(v[4] * f, v[5] * f, v[6] * f, v[7] * f)};
+        Q[t] = s == 255u ? u32x2{0u, 0u} : q;
+        if (p % 16 == 0)                           // with the row's last block, what fills its scales up: 1
+            for (int64_t b = p / 16; b < (p + 16 >= ppr ? spr : p / 16 + 1); ++b) {
+                const uint32_t byte = b == p / 16 ? s : 127u;
+                if constexpr (F32) ((float*)S)[r * spr + b] = fp8_scale_value(byte);
+                else ((uint8_t*)S)[r * spr + b] = (uint8_t)byte;
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+static size_t mm_al256(size_t x) { return (x + 255) & ~(size_t)255; }
+static int64_t mm_al8(int64_t x) { return (x + 7) / 8 * 8; }
+
+// Bytes of the padded copies of a call's activations and weights (each of them).
+struct MmPads {
+    size_t a, w;
+    int as, ws;                   // how many
+};
+static MmPads mm_pads(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts) {
+    MmPads p{};
+    if (elt != MM_BF16) return p;
+    const int64_t ak = form == MM_GATE ? d_in : d_out;
+    p.as = form == MM_GATE ? 1 : 2;
+    p.ws = form == MM_TN ? 1 : 2;
+    if (ak % 8) p.a = mm_al256((size_t)n * mm_al8(ak) * 2);
+    if (d_in % 8) p.w = mm_al256((size_t)(form == MM_TN ? n : experts * d_out) * mm_al8(d_in) * 2);
+    return p;
+}
+
+static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed) {
+    MmPlan P{};
+    const bool tn = form == MM_TN, gate = form == MM_GATE, nn = form == MM_NN, fp8 = elt != MM_BF16;
+    const int64_t k = tn ? n : (nn ? d_out : d_in), m = tn || nn ? d_in : d_out, ke = fp8 ? 128 : 64;
+    const int64_t one = (k + ke - 1) / ke, per = (n + experts - 1) / experts;
+    const int64_t live = experts > 1 ? (experts < n ? experts : n) : 1;           // experts with rows, at most
+    const MmPads pads = mm_pads(form, elt, n, d_in, d_out, experts);
+    P.pad_bytes = pads.a * pads.as + pads.w * pads.ws;
+    P.stages = (int)(nn && !fp8 ? 2 * one : one);
+    P.unit = fp8 ? 4 : 1;
+    P.split = 1;
+    int64_t blocks, units;
+    const int64_t wcols = gate ? 2 * m : m;                                       // rows of weights that outputs need
+    P.stream = (form == MM_NT || gate) && per <= 16 && per * k * (fp8 ? 1 : 2) <= 1 << 18 && live * ((wcols + 127) / 128) < 192;
+    if (P.stream) {
+        P.bm = 16;
+        P.bn = gate || live * ((m + 31) / 32) >= 256 ? 32 : 16;
+        const int64_t pieces = (one + 1) / 2;
+        P.waves = pieces >= 8 ? 8 : 4;
+        blocks = live * ((wcols + P.bn - 1) / P.bn);
+        units = pieces / P.waves;
+    } else if (tn) {
+        P.bm = 256;
+        for (;; P.bm /= 2) {
+            P.bn = P.bm;
+            P.waves = P.bm == 256 ? 8 : 4;
+            blocks = 2 * (int64_t)experts * ((d_out + P.bm - 1) / P.bm) * ((m + P.bn - 1) / P.bn);
+            if (P.bm == 128 || blocks >= 192) break;
+        }
+        units = experts > 1 ? 1 : P.stages;
+    } else {
+        P.bm = per > 128 && !mm_wide(elt) ? 256 : (per > 64 ? 128 : (per > 32 || nn ? 64 : 32));
+        for (;; P.bm /= 2) {
+            P.bn = P.bm == 256 || nn ? 256 : 128;
+            const int64_t rows = experts > 1 ? n / P.bm + live : (n + P.bm - 1) / P.bm;
+            blocks = rows * ((wcols + P.bn - 1) / P.bn);
+            if (P.bm <= 64 || blocks >= (nn ? 48 : 192)) break;
+        }
+        P.waves = P.bm == 256 || (nn && P.bm == 128) ? 8 : 4;
+        units = (P.stages + P.unit - 1) / P.unit;
+    }
+    if (units < 1) units = 1;
+    if (blocks < 256) {
+        int64_t s = (P.stream ? 512 : 256) / (blocks > 0 ? blocks : 1);
+        s = s < units ? s : units;
+        s = s < 1 ? 1 : (s > 16 ? 16 : s);
+        const int64_t each = (units + s - 1) / s;                                 // no part without work
+        P.split = (int)((units + each - 1) / each);
+    }
+    P.join = P.split > 1 || (packed && P.bm != 256);
+    const int64_t outputs = tn ? 2 * (int64_t)experts * d_out * m : (gate ? 2 : 1) * n * m;
+    P.part_bytes = P.join ? mm_al256((size_t)P.split * outputs * 4) : 0;
+    return P;
 }
 
 size_t mm_workspace(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed) {
-    return packed ? ((size_t)n * d_out * 4 + 255) / 256 * 256 : 0;
+    const MmPlan P = mm_plan(form, elt, n, d_in, d_out, experts, packed);
+    return P.pad_bytes + P.part_bytes;
 }
 
 bool mm_fits(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets, bool packed) {
-    const int64_t rows = form == MM_TN ? d_out : n + 64 * (offsets ? experts : 0);
-    return rows <= 65535 * 64 && ((form == MM_NN || form == MM_TN ? d_in : d_out) + 63) / 64 <= 1 << 23;
+    const MmPlan P = mm_plan(form, elt, n, d_in, d_out, experts, packed);
+    const int64_t m = form == MM_TN || form == MM_NN ? d_in : d_out;
+    return P.stream || mm_blocks(form, n, m, d_out, experts, offsets, 2, P) * 64 * P.waves <= MM_MAX_LANES;
 }
 
-hipError_t mm_run(const MmCall& call, void* ws, hipStream_t st) {
-    MmCall c = call;
+hipError_t mm_run(const MmCall& c, void* ws, hipStream_t st) {
     StageTimer tm(c.form == MM_GATE ? ST_FFN_GATE : (c.elt == MM_BF16 ? ST_FFN_BACK : ST_FP8_GEMM), st);
-    if (c.hq) c.y[0] = ws;
-    const bool fp8 = c.elt != MM_BF16;
-    const int64_t ak = c.form == MM_NT || c.form == MM_GATE ? c.d_in : c.d_out;
-    const int64_t m = c.form == MM_NN || c.form == MM_TN ? c.d_in : c.d_out;
-    const int64_t rows = c.form == MM_TN ? (c.d_out + 63) / 64 : (c.n + 63) / 64 + (c.offsets ? c.experts : 0);
-    const dim3 grid((unsigned)((m + 63) / 64), (unsigned)rows, c.form == MM_TN ? 2 * c.experts : 1);
-    hipLaunchKernelGGL(k_mm_plain, grid, dim3(256), 0, st, c, fp8 ? fp8_bytes(ak) : 2 * ak, fp8 ? fp8_bytes(c.d_in) : 2 * c.d_in);
-    GQ_LAUNCH_CHECK();
-    if (c.hq) {
-        const int64_t pieces = c.n * 16 * fp8_blocks(m);
-        const auto k = c.elt == MM_FS ? k_mm_pack<true> : k_mm_pack<false>;
-        hipLaunchKernelGGL(k, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, st, (const float*)ws, c.n, m, c.offsets, c.experts, (u32x2*)c.hq, c.hs);
+    const bool packed = c.hq != nullptr, fp8 = c.elt != MM_BF16, tn = c.form == MM_TN, nn = c.form == MM_NN;
+    const MmPlan P = mm_plan(c.form, c.elt, c.n, c.d_in, c.d_out, c.experts, packed);
+    const MmPads pads = mm_pads(c.form, c.elt, c.n, c.d_in, c.d_out, c.experts);
+    const int64_t ak = nn || tn ? c.d_out : c.d_in, m = nn || tn ? c.d_in : c.d_out;
+    char* at = (char*)ws;
+    // rows of k values, copied to a multiple of 8 where they are none
+    auto padded = [&](const void* x, int64_t rows, int64_t k, size_t bytes, const uint8_t*& out) -> hipError_t {
+        out = (const uint8_t*)x;
+        if (!bytes || !x) return hipSuccess;
+        const int64_t pieces = mm_al8(k) / 8, blocks = (rows * pieces + 255) / 256;
+        out = (const uint8_t*)at;
+        if (blocks > 0) {
+            hipLaunchKernelGGL(k_mm_pad, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, x, rows, k, pieces, (u32x4*)at);
+            GQ_LAUNCH_CHECK();
+        }
+        at += bytes;
+        return hipSuccess;
+    };
+    MmTile t{};
+    hipError_t e;
+    for (int i = 0; i < 2; ++i) {
+        if ((e = padded(c.a[i], c.n, ak, pads.a, t.A[i])) != hipSuccess) return e;
+        if ((e = padded(c.w[i], tn ? c.n : c.experts * c.d_out, c.d_in, pads.w, t.W[i])) != hipSuccess) return e;
+        t.WS[i] = c.ws[i];
+        t.y[i] = c.y[i];
+        t.z[i] = c.z[i];
+    }
+    t.a_row = t.a_bytes = fp8 ? fp8_bytes(ak) : 2 * mm_al8(ak);
+    t.w_row = t.w_bytes = fp8 ? fp8_bytes(c.d_in) : 2 * mm_al8(c.d_in);
+    t.AS = c.as;
+    t.as_row = fp8_scales(ak) * (mm_bytes(c.elt) ? 1 : 4);
+    t.ws_row = fp8_blocks(c.d_in);
+    t.ws_rows = fp8_blocks(c.d_out);
+    t.offsets = c.offsets;
+    t.experts = c.experts;
+    t.n = c.n;
+    t.m = m;
+    t.d_out = c.d_out;
+    t.stages = P.stages;
+    t.stages_one = nn && !fp8 ? P.stages / 2 : P.stages;
+    t.unit = P.unit;
+    t.y_bf16 = c.y_bf16;
+    t.outs = 1;
+    if (tn) {                                      // the outputs that are wanted, in front
+        t.outs = (c.y[0] != nullptr) + (c.y[1] != nullptr);
+        if (!c.y[0]) {
+            t.y[0] = t.y[1];
+            t.A[0] = t.A[1];
+        }
+    }
+    t.hq = c.hq;
+    t.hs = c.hs;
+    t.hq_row = fp8_bytes(m);
+    t.hs_row = fp8_scales(m);
+    t.act = c.act;
+    t.part = P.join ? (float*)((char*)ws + P.pad_bytes) : nullptr;
+    switch (c.elt) {
+        case MM_BF16: e = mm_launch_bf16(c.form, t, P, st); break;
+        case MM_E8: e = mm_launch_e8(c.form, t, P, st); break;
+        case MM_FS: e = mm_launch_fs(c.form, t, P, st); break;
+        case MM_E8W: e = mm_launch_e8w(c.form, t, P, st); break;
+        default: e = mm_launch_fsw(c.form, t, P, st); break;
+    }
+    if (e != hipSuccess || !P.join) return e;
+    if (packed) {
+        const int64_t blocks = (c.n * 16 * fp8_blocks(m) + 255) / 256;
+        const auto k = c.elt == MM_FS ? k_mm_join_pack<true> : k_mm_join_pack<false>;
+        hipLaunchKernelGGL(k, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, t.part, P.split, c.n, m, c.offsets, c.experts, c.act,
+                           (u32x2*)c.hq, c.hs);
+        GQ_LAUNCH_CHECK();
+        return hipSuccess;
+    }
+    const int64_t rows = tn ? c.experts * c.d_out : c.n, each = rows * m;
+    const int64_t blocks = (each + 255) / 256 / (m % 4 == 0 ? 4 : 1) + 1;                    // four outputs a lane, or one
+    const auto k = c.form == MM_GATE ? k_mm_join<true> : k_mm_join<false>;
+    for (int i = 0; i < t.outs; ++i) {
+        hipLaunchKernelGGL(k, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, t.part + i * each, P.split, t.outs * each, rows, m,
+                           tn ? nullptr : c.offsets, c.experts, t.y[i], (int)c.y_bf16, c.act, t.z[0], t.z[1]);
         GQ_LAUNCH_CHECK();
     }
     return hipSuccess;

@@ -1,0 +1,878 @@
+// Tiled products of one element type on gfx950: the kernels that gq_mm.hip plans and launches, included
+// by the one file of each type (gq_mm_bf16.hip, gq_mm_e8.hip, gq_mm_fs.hip).
+#pragma once
+#include "gq_mm.h"
+#include "gq_mm_plan.h"
+#include "gq_tile.h"
+
+namespace gq {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// A stage's line of 128 bytes is 8 chunks of 16.  Operands whose contraction runs along their rows lie
+// in LDS as lines of a row, chunk c of row r in place c ^ mm_swz(r), so that the 16 rows of a fragment's read
+// spread over the banks.  Operands whose contraction runs over their rows ("turned": the weights of
+// MM_NN, both operands of MM_TN) lie as rows of the contraction, and are turned by the reads:
+// ds_read_b64_tr_b16 and _b8 hand 16 lanes a block of 4 x 16 or 8 x 16 values, lane i the i-th column.
+// mm_tswz spreads the rows of such a block, and those of a half-wave's other one, over the banks.
+__device__ __forceinline__ int mm_swz(int row) { return (row >> 1) & 7; }
+template <int ES>
+__device__ __forceinline__ int mm_tswz(int row) {
+    return ES == 2 ? (4 * (row & 1)) ^ (10 * ((row >> 1) & 1)) ^ (2 * ((row >> 3) & 1))
+                   : (2 * (row & 3)) ^ (9 * ((row >> 2) & 1)) ^ ((row >> 4) & 1);
+}
+
+template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
+struct MmGeo {
+    static constexpr int ES = ELT == MM_BF16 ? 2 : 1, KE = 128 / ES;    // bytes of a value, values of a stage
+    static constexpr bool XT = FORM == MM_TN, WT = FORM == MM_NN || FORM == MM_TN;
+    static constexpr int WN = NW / WM, TM = BM / WM, TN = BN / WN;      // waves, and a wave's tile
+    static constexpr int FM = TM / T, FN = TN / T, V = T * T / 64;      // its fragments, an accumulator
+    static constexpr int CH = T / 8, NP = 64 / T;                       // chunks a lane has of a line, lanes a row
+    static constexpr int X = BM * 8, W = BN * 8, STAGE = X + W;         // 16-byte slots
+    static constexpr bool SC = ELT != MM_BF16;
+    static constexpr int SB = mm_bytes(ELT) ? 4 : 16;                   // bytes of four stages' scales of a row
+    static constexpr int SCB = SC ? BM * SB : 0;                        // one of three buffers of them
+    static constexpr size_t IN = (size_t)R * STAGE * 16 + 3 * SCB;
+    static constexpr int HC = FORM == MM_GATE ? TN / 2 : TN;            // output columns of a wave
+    static constexpr size_t OUT = (size_t)NW * T * (HC * 4 + 16) + (FORM == MM_GATE ? 8 * BM : 0);
+    static constexpr size_t BYTES = IN > OUT ? IN : OUT;
+    static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
+    static_assert(FN % 2 == 0 && TM % T == 0 && TN % T == 0, "fragments go in pairs");
+};
+
+// Which tile a block of MM_TN has: weight gradient z / E of expert z % E.
+struct MmTurned {
+    int e, which;
+    int64_t t0, lo, hi;           // first row of the output, rows of the contraction
+    int col;
+    bool ok;
+};
+__device__ __forceinline__ MmTurned mm_place_turned(const MmTile& p, int bm, int ncol) {
+    MmTurned r;
+    const int64_t nrow = (p.d_out + bm - 1) / bm, each = nrow * ncol, total = each * p.experts * p.outs;
+    const int64_t eighth = (total + 7) / 8, in = blockIdx.x >> 3, lin = (int64_t)(blockIdx.x & 7) * eighth + in;
+    r.ok = in < eighth && lin < total;
+    const int64_t z = lin / each, rest = lin - z * each;
+    r.e = (int)(z / p.outs);
+    r.which = (int)(z - (int64_t)r.e * p.outs);
+    constexpr int H = 8;
+    const int64_t g = rest / (H * ncol), q = rest - g * (H * ncol), left = nrow - g * H, h = left < H ? left : H;
+    r.t0 = (g * H + q % h) * bm;
+    r.col = (int)(q / h);
+    r.lo = 0;
+    r.hi = p.n;
+    if (p.offsets && r.ok) tile_expert_rows(p.offsets, r.e, p.n, r.lo, r.hi);
+    if (r.hi < r.lo) r.hi = r.lo;
+    return r;
+}
+
+// 16 codes as bfloat16, 8 and 8: exact
+__device__ __forceinline__ void mm_widen(u32x4 q, u32x4& lo, u32x4& hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], 1.f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], 1.f, true);
+        u32x4& to = i < 2 ? lo : hi;
+        to[2 * (i % 2)] = __builtin_bit_cast(uint32_t, a);
+        to[2 * (i % 2) + 1] = __builtin_bit_cast(uint32_t, b);
+    }
+}
+
+template <int ELT, int T>
+struct MmAcc;
+template <int ELT> struct MmAcc<ELT, 32> { typedef f32x16 Type; };
+template <int ELT> struct MmAcc<ELT, 16> { typedef f32x4 Type; };
+
+__device__ __forceinline__ i32x8 mm_pair(u32x4 a, u32x4 b) {
+    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+// ---------------------------------------------------------------------------
+// A wave holds its rows' fragments of a stage (x) and takes its columns' one after another (w): while
+// the products of one column fragment run, the next is read, and the loads of a later stage go out one
+// beside each product or two.  One barrier a stage, before its last part: by then every wave has read
+// all of the stage, so its slot is refilled from there on, and the last part's products run while the
+// next stage's rows and first columns are read.
+// ---------------------------------------------------------------------------
+template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
+__global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
+    typedef MmGeo<ELT, FORM, BM, BN, WM, NW, T, R> G;
+    constexpr int ES = G::ES, KE = G::KE, FM = G::FM, FN = G::FN, V = G::V, CH = G::CH, NP = G::NP, TM = G::TM, TN = G::TN;
+    constexpr bool XT = G::XT, WT = G::WT, SC = G::SC, GATE = FORM == MM_GATE;
+    constexpr int BC = GATE ? BN / 2 : BN;                       // output columns of a tile
+    extern __shared__ u32x4 mm_lds[];
+    uint8_t* const lds = (uint8_t*)mm_lds;
+
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & (T - 1), g = lane / T;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave % WM, wn = wave / WM;
+    const int ncol = (int)((p.m + BC - 1) / BC);
+    int e, rows, col, which = 0, stages = p.stages;
+    int64_t t0, k_lo = 0, k_rows = 0;
+    if constexpr (FORM == MM_TN) {
+        const MmTurned at = mm_place_turned(p, BM, ncol);
+        if (!at.ok) return;
+        e = __builtin_amdgcn_readfirstlane(at.e);
+        which = __builtin_amdgcn_readfirstlane(at.which);
+        col = __builtin_amdgcn_readfirstlane(at.col);
+        t0 = (int64_t)__builtin_amdgcn_readfirstlane((int)at.t0);
+        rows = (int)(p.d_out - t0 < BM ? p.d_out - t0 : BM);
+        k_lo = (int64_t)__builtin_amdgcn_readfirstlane((int)at.lo);
+        k_rows = (int64_t)__builtin_amdgcn_readfirstlane((int)at.hi) - k_lo;
+        stages = (int)((k_rows + KE - 1) / KE);
+    } else {
+        TilePlace at = tile_place(p, BM, ncol);
+        if (!at.ok) return;
+        // (the same in every lane; said so, or the descriptors built from it are looped over lanes)
+        e = __builtin_amdgcn_readfirstlane(at.e);
+        col = __builtin_amdgcn_readfirstlane(at.col);
+        rows = __builtin_amdgcn_readfirstlane(at.rows);
+        t0 = (int64_t)__builtin_amdgcn_readfirstlane((int)at.t0);              // below 2^31
+    }
+    const int64_t j0 = (int64_t)col * BC;
+
+    // this split's stages
+    int s_lo = 0, s_hi = stages;
+    if (gridDim.y > 1) {
+        const int units = (stages + p.unit - 1) / p.unit;
+        const int per = (units + (int)gridDim.y - 1) / (int)gridDim.y;
+        s_lo = (int)blockIdx.y * per * p.unit;
+        s_hi = s_lo + per * p.unit;
+        s_lo = s_lo < stages ? s_lo : stages;
+        s_hi = s_hi < stages ? s_hi : stages;
+    }
+
+    // ---- what is copied into LDS: a wave's slots of both operands
+    constexpr int XPW = G::X / NW, WPW = G::W / NW, XI = XPW / 64, WI = WPW / 64, LOADS = XI + WI + (SC ? 1 : 0);
+    static_assert(XPW % 64 == 0 && WPW % 64 == 0, "whole copies");
+    const int wcols = (int)(p.m - j0 < BC ? p.m - j0 : BC);
+    uint32_t xv[XI], wv[WI];
+    // bfloat16 rows end within a stage: the first of this lane's stages past the row
+    constexpr bool EDGE = ELT == MM_BF16;
+    int xe[EDGE && !XT ? XI : 1], we[EDGE && !WT ? WI : 1];
+    auto first_past = [&](int64_t bytes, int chunk) {
+        const int64_t n = (bytes - 16 * chunk + 127) / 128;
+        return (int)(n < 0 ? 0 : (n < 0x7fffffff ? n : 0x7fffffff));
+    };
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+        const int slot = wave * XPW + i * 64 + lane;
+        if constexpr (XT) {
+            constexpr int PR = BM * ES / 16;                     // slots of a row of the contraction
+            const int row = slot / PR, c = slot % PR;
+            xv[i] = (uint32_t)(row * p.a_row) + 16u * (c ^ mm_tswz<ES>(row));
+        } else {
+            const int row = slot / 8, c = (slot % 8) ^ mm_swz(row);
+            xv[i] = (uint32_t)(row * p.a_row) + 16u * c;
+            if constexpr (EDGE) xe[i] = first_past(p.a_bytes, c);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < WI; ++i) {
+        const int slot = wave * WPW + i * 64 + lane;
+        if constexpr (WT) {
+            constexpr int PR = BN * ES / 16;
+            const int row = slot / PR, c = slot % PR;
+            wv[i] = (uint32_t)(row * p.w_row) + 16u * (c ^ mm_tswz<ES>(row));
+        } else {
+            const int row = slot / 8, c = (slot % 8) ^ mm_swz(row);
+            // MM_GATE: 16 rows of one weight, then the same 16 of the other
+            const int from = GATE ? row / 32 * 16 + row % 16 : row;
+            wv[i] = (uint32_t)(from * p.w_row) + 16u * c;
+            if constexpr (EDGE) we[i] = first_past(p.w_bytes, c);
+        }
+    }
+    const int64_t e_rows = (int64_t)e * p.d_out;
+    // load i of stage s (XI + WI of them).  Past the split's last stage they read nothing and clear a
+    // slot that is not read, so that the counts of loads in flight stay what they are.
+    auto issue_one = [&](int s, int i) {
+        u32x4* const base = mm_lds + (s % R) * G::STAGE;
+        const bool on = s < s_hi;
+        // MM_NN with two pairs: the stages of the first, then those of the second
+        const int src = FORM == MM_NN && s >= p.stages_one ? 1 : 0, sl = FORM == MM_NN ? s - src * p.stages_one : s;
+        if (i < XI) {
+            u32x4* const to = base + wave * XPW + i * 64;
+            if constexpr (XT) {
+                const int64_t k0 = (int64_t)s * KE, left = k_rows - k0 < KE ? k_rows - k0 : KE;
+                tile_dma(tile_rsrc(p.A[which] + (k_lo + k0) * p.a_row + t0 * ES, (int)left, p.a_row, on, (int)(t0 * ES)), to, xv[i], 0);
+            } else {
+                const __amdgpu_buffer_rsrc_t xr = tile_rsrc(p.A[src] + t0 * p.a_row, rows, p.a_row, on);
+                uint32_t v = xv[i];
+                if constexpr (EDGE) v = sl < xe[i] ? v : 0xC0000000u;                 // past the row: zeros
+                tile_dma(xr, to, v, (uint32_t)sl * 128u);
+            }
+        } else {
+            i -= XI;
+            u32x4* const to = base + G::X + wave * WPW + i * 64;
+            if constexpr (WT) {
+                const int64_t k0 = (int64_t)sl * KE, all = FORM == MM_TN ? k_rows : p.d_out, left = all - k0 < KE ? all - k0 : KE;
+                const uint8_t* const from = p.W[src] + ((FORM == MM_TN ? k_lo : e_rows) + k0) * p.w_row + j0 * ES;
+                tile_dma(tile_rsrc(from, (int)left, p.w_row, on, (int)(j0 * ES)), to, wv[i], 0);
+            } else {
+                const int half = GATE ? ((wave * WPW + i * 64) / 128) & 1 : 0;       // 8 rows a copy
+                const __amdgpu_buffer_rsrc_t q = tile_rsrc(p.W[half] + (e_rows + j0) * p.w_row, wcols, p.w_row, on);
+                uint32_t v = wv[i];
+                if constexpr (EDGE) v = s < we[i] ? v : 0xC0000000u;
+                tile_dma(q, to, v, (uint32_t)s * 128u);
+            }
+        }
+    };
+    // The rows' scales: four stages' of a row at a time, a quarter of the next four's rows with each stage.
+    uint8_t* const sc_lds = lds + R * G::STAGE * 16;
+    constexpr int SW = SC ? (BM / 4 / NW > 0 ? BM / 4 / NW : 1) : 1;              // rows of a wave's copy
+    static_assert(!SC || SW * NW * 4 == BM, "every wave copies scales");
+    auto scale_copy = [&](int span, int row, int count, bool on) {
+        if constexpr (SC) {
+            const __amdgpu_buffer_rsrc_t z = tile_rsrc((const uint8_t*)p.AS + t0 * p.as_row, rows, p.as_row, on);
+            uint8_t* const to = sc_lds + (span % 3) * G::SCB + row * G::SB;
+            const uint32_t v = (uint32_t)((row + lane) * p.as_row) + (uint32_t)(G::SB * span);
+            if constexpr (mm_bytes(ELT)) {
+                if (lane < count) __builtin_amdgcn_raw_ptr_buffer_load_lds(z, (tile_lds_t)to, 4, v, 0, 0, 0);
+            } else {
+                if (lane < count) tile_dma(z, (u32x4*)to, v, 0);
+            }
+        }
+    };
+    auto issue_scales = [&](int s) { scale_copy(s / 4 + 1, (s % 4) * (BM / 4) + wave * SW, SW, s < s_hi); };
+    auto issue = [&](int s) {
+        issue_scales(s);
+#pragma unroll
+        for (int i = 0; i < XI + WI; ++i) issue_one(s, i);
+    };
+    if constexpr (SC) {                           // the first four stages' whole
+#pragma unroll
+        for (int q = 0; q < 4; ++q) scale_copy(s_lo / 4, q * (BM / 4) + wave * SW, SW, true);
+    }
+
+    // ---- the weight's scales: one for a wave's columns and a stage, 64 stages in a register
+    float wsc[2] = {1.f, 1.f};                     // (MM_E8, MM_E8W: the byte)
+    const int64_t wblocks = p.ws_row, sbase = (int64_t)e * ((p.d_out + 127) / 128) * wblocks;
+    auto load_weight_scales = [&](int s) {
+        if constexpr (SC) {
+            const int k = s + lane < stages ? s + lane : stages - 1;
+            const int64_t jb = GATE ? j0 / 128 : (j0 + wn * TN) / 128;
+            // (columns past the last block: any scale, they are not stored)
+            const int64_t at = FORM == MM_NN ? (int64_t)k * wblocks + (jb < wblocks ? jb : wblocks - 1)
+                                             : (jb < p.ws_rows ? jb : p.ws_rows - 1) * wblocks + k;
+#pragma unroll
+            for (int h = 0; h < (GATE ? 2 : 1); ++h) {
+                if constexpr (mm_bytes(ELT)) wsc[h] = __uint_as_float(((const uint8_t*)p.WS[h])[sbase + at]);
+                else wsc[h] = ((const float*)p.WS[h])[sbase + at];
+                asm volatile("" : "+v"(wsc[h]));   // it has arrived
+            }
+        }
+    };
+    // ---- fragments.  Chunk j of a lane is chunk NP j + g of the line.
+    typedef typename MmAcc<ELT, T>::Type Acc;
+    Acc acc[FN][FM];
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int q = 0; q < FM; ++q)
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[f][q][v] = 0.f;
+    constexpr int RPC = KE / 8;                    // values of the contraction in a chunk
+    constexpr int RPR = RPC / 2;                   // and in a turned read
+    constexpr int LPR = 16 / RPR;                  // lanes that read one row of it
+    // where a turned operand's column fragment starts: row g of chunks, row and part of a block
+    auto turned = [&](int column, int pitch) {
+        const int l = lane & 15, row = g * RPC + l / LPR, byte = (l % LPR) * 8;
+        const int c = (column + (T == 32 ? 16 * (r >> 4) : 0)) * ES / 16 + byte / 16;
+        return row * pitch + 16 * (c ^ mm_tswz<ES>(row)) + byte % 16;
+    };
+    int lx[XT ? FM : CH], lw[WT ? FN : CH];
+    if constexpr (XT) {
+#pragma unroll
+        for (int q = 0; q < FM; ++q) lx[q] = turned(wm * TM + T * q, BM * ES);
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) lx[j] = (wm * TM + r) * 128 + 16 * ((NP * j + g) ^ mm_swz(r));
+    }
+    if constexpr (WT) {
+#pragma unroll
+        for (int f = 0; f < FN; ++f) lw[f] = turned(wn * TN + T * f, BN * ES);
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) lw[j] = (wn * TN + r) * 128 + 16 * ((NP * j + g) ^ mm_swz(r));
+    }
+    // chunk `chunk` of a lane's: two blocks of RPR rows
+    auto turned_read = [&](int at, int pitch) {
+        u32x4 v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x2 d;
+            if constexpr (ES == 2) {
+                typedef short s16x4 __attribute__((ext_vector_type(4)));
+                typedef __attribute__((address_space(3))) s16x4* ptr;
+                d = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(lds + at + h * RPR * pitch)));
+            } else {
+                typedef int i32x2 __attribute__((ext_vector_type(2)));
+                typedef __attribute__((address_space(3))) i32x2* ptr;
+                d = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((ptr)(lds + at + h * RPR * pitch)));
+            }
+            v[2 * h] = d[0];
+            v[2 * h + 1] = d[1];
+        }
+        return v;
+    };
+    u32x4 x[FM][CH], w[2][CH];
+    float sx[FM];                                  // scales of the rows (MM_E8, MM_E8W: the byte)
+    auto read_x = [&](int s, int q, int j) {
+        const int base = (s % R) * G::STAGE * 16;
+        if constexpr (XT) x[q][j] = turned_read(base + lx[q] + j * NP * RPC * BM * ES, BM * ES);
+        else x[q][j] = *(const u32x4*)(lds + base + lx[j] + q * T * 128);
+    };
+    auto read_sx = [&](int s, int q) {
+        if constexpr (SC) {
+            const int at = R * G::STAGE * 16 + ((s / 4) % 3) * G::SCB + (wm * TM + T * q + r) * G::SB + (s % 4) * (G::SB / 4);
+            if constexpr (mm_bytes(ELT)) sx[q] = __uint_as_float((uint32_t)lds[at]);
+            else sx[q] = *(const float*)(lds + at);
+        }
+    };
+    auto read_w = [&](int s, int f, u32x4 (&to)[CH], int j) {
+        const int base = (s % R) * G::STAGE * 16 + G::X * 16;
+        if constexpr (WT) to[j] = turned_read(base + lw[f] + j * NP * RPC * BN * ES, BN * ES);
+        else to[j] = *(const u32x4*)(lds + base + lw[j] + f * T * 128);
+    };
+
+    // ---- products.  All 8-bit types but MM_E8: a line's sum, of its 16 x 16 products alone, times its scales is
+    // added LAG products later, so that the matrix cores' result has arrived and their next products run beside.
+    constexpr int LAG = 3, RING = LAG + 1, ALL = FN * FM;
+    constexpr bool WIDE = mm_wide(ELT), FS = ELT == MM_FS || WIDE;
+    static_assert(!FS || (T == 16 && ALL % RING == 0), "sums of a line need a place that is known");
+    f32x4 sum[FS ? RING : 1];
+    float fac[2][FS ? FM : 1], old[2][FS ? FM : 1];
+    if constexpr (FS) {
+#pragma unroll
+        for (int k = 0; k < RING; ++k) sum[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < FM; ++q) fac[0][q] = fac[1][q] = 0.f;
+    }
+    uint32_t wbyte = 0u;                           // MM_E8: this lane's scale of the weight
+    u32x4 xb[WIDE ? FM : 1][2 * CH], wb[2 * CH];   // WIDE: fragments in bfloat16
+    auto take_scales = [&](int s) {                // of stage s, before its products
+        if constexpr (ELT == MM_E8) {
+            const int at = (s - s_lo) & 63;
+            wbyte = (uint32_t)__builtin_amdgcn_readlane(__float_as_int(wsc[0]), at);
+            // (32 x 32 fragments have 16 rows of each weight; 16 x 16 ones take turns)
+            if constexpr (GATE) {
+                const uint32_t up = (uint32_t)__builtin_amdgcn_readlane(__float_as_int(wsc[1]), at);
+                if constexpr (T == 32) wbyte = r < 16 ? wbyte : up;
+                else wbyte |= up << 8;
+            }
+        } else if constexpr (FS) {
+            const int at = (s - s_lo) & 63;
+#pragma unroll
+            for (int h = 0; h < (GATE ? 2 : 1); ++h) {
+                const int bits = __builtin_amdgcn_readlane(__float_as_int(wsc[h]), at);
+                const float v = mm_bytes(ELT) ? fp8_scale_value(bits) : __int_as_float(bits);
+#pragma unroll
+                for (int q = 0; q < FM; ++q) {
+                    old[h][q] = fac[h][q];
+                    fac[h][q] = v * (mm_bytes(ELT) ? fp8_scale_value(__float_as_uint(sx[q])) : sx[q]);
+                }
+            }
+        }
+    };
+    // adds the sum of product k of this stage, or (k < 0) of the last one
+    auto add_sum = [&](auto index) {
+        if constexpr (FS) {
+            constexpr int k = decltype(index)::value, i = (k + ALL) % ALL, f = i / FM, q = i % FM, h = GATE ? f & 1 : 0;
+            const float by = k < 0 ? old[h][q] : fac[h][q];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[f][q][v] = __builtin_fmaf(sum[i % RING][v], by, acc[f][q][v]);
+        }
+    };
+    constexpr int KS = ELT == MM_BF16 ? CH : CH / 2;             // products of two fragments (WIDE: four, one after the other)
+    auto product = [&](auto fragment, const u32x4 (&wf)[CH], auto index) {
+        constexpr int f = decltype(fragment)::value, i = decltype(index)::value, q = i / KS, j = i % KS;
+        if constexpr (ELT == MM_BF16) {
+            if constexpr (T == 32) acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(wf[j]), as_bf16x8(x[q][j]), acc[f][q], 0, 0, 0);
+            else acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wf[j]), as_bf16x8(x[q][j]), acc[f][q], 0, 0, 0);
+        } else {
+            const i32x8 a = mm_pair(wf[2 * j], wf[2 * j + 1]), b = mm_pair(x[q][2 * j], x[q][2 * j + 1]);
+            (void)a, (void)b;
+            if constexpr (ELT == MM_E8) {
+                const int sw = (int)wbyte, sr = __float_as_int(sx[q]);
+                if constexpr (T == 32) acc[f][q] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[f][q], 0, 0, 0, sw, 0, sr);
+                else acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[f][q], 0, 0, GATE ? f & 1 : 0, sw, 0, sr);
+            } else if constexpr (WIDE) {
+                constexpr int k = f * FM + q;
+                f32x4 d{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2 * CH; ++h) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wb[h]), as_bf16x8(xb[q][h]), d, 0, 0, 0);
+                sum[k % RING] = d;
+                add_sum(std::integral_constant<int, k - LAG>{});
+            } else {
+                constexpr int k = f * FM + q;
+                sum[k % RING] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+                add_sum(std::integral_constant<int, k - LAG>{});
+            }
+        }
+    };
+
+    constexpr int LOADS_ALL = XI + WI, LATE = LOADS_ALL / 2, SOON = LOADS_ALL - LATE, PR = FM * KS;
+    // Column fragment f of stage s, beside its products: the next fragment's reads, of the loads l0 .. l1 - 1 of stage sl
+    // one after every so many products, and with the last fragment the next stage's rows as each is done with.
+    auto part = [&](auto fragment, int s, int sl, auto l0, auto l1) {
+        constexpr int f = decltype(fragment)::value, L0 = decltype(l0)::value, LN = decltype(l1)::value - L0;
+        constexpr bool last = f == FN - 1;
+        constexpr int RP = (2 * CH + PR - 1) / PR;               // reads beside a product
+        if constexpr (WIDE) {
+            if constexpr (f == 0) {
+#pragma unroll
+                for (int q = 0; q < FM; ++q)
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) mm_widen(x[q][j], xb[q][2 * j], xb[q][2 * j + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < CH; ++j) mm_widen(w[f % 2][j], wb[2 * j], wb[2 * j + 1]);
+        }
+        tile_each<PR>([&](auto index) {
+            constexpr int i = decltype(index)::value;
+#pragma unroll
+            for (int k = RP * i; k < RP * (i + 1); ++k)
+                if (k < CH) read_w(last ? s + 1 : s, last ? 0 : f + 1, w[(f + 1) % 2], k);
+            product(fragment, w[f % 2], index);
+            if constexpr (last && i % KS == KS - 1) {
+#pragma unroll
+                for (int j = 0; j < CH; ++j) read_x(s + 1, i / KS, j);
+            }
+#pragma unroll
+            for (int l = i * LN / PR; l < (i + 1) * LN / PR; ++l) issue_one(sl, L0 + l);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+
+    const std::integral_constant<int, 0> zero{};
+    const std::integral_constant<int, SOON> soon{};
+    const std::integral_constant<int, LOADS_ALL> all{};
+    if (s_lo < s_hi) {
+#pragma unroll
+        for (int i = 0; i < R - 1; ++i) issue(s_lo + i);
+        issue_scales(s_lo + R - 1);
+#pragma unroll
+        for (int i = 0; i < SOON; ++i) issue_one(s_lo + R - 1, i);
+        tile_wait_vmcnt<LOADS * (R - 2) + LOADS - LATE>();
+        tile_barrier();
+        // a wave whose rows all lie past the tile's own only copies
+        const bool idle = wm * TM >= rows;
+        for (int s = s_lo; idle && s < s_hi; ++s) {
+#pragma unroll
+            for (int i = SOON; i < LOADS_ALL; ++i) issue_one(s + R - 1, i);
+            tile_wait_vmcnt<LOADS * (R - 2)>();
+            tile_barrier();
+            issue_scales(s + R);
+#pragma unroll
+            for (int i = 0; i < SOON; ++i) issue_one(s + R, i);
+        }
+        if (!idle) {
+#pragma unroll
+            for (int q = 0; q < FM; ++q) {
+#pragma unroll
+                for (int j = 0; j < CH; ++j) read_x(s_lo, q, j);
+                read_sx(s_lo, q);
+            }
+#pragma unroll
+            for (int j = 0; j < CH; ++j) read_w(s_lo, 0, w[0], j);
+        }
+        for (int s = s_lo; !idle && s < s_hi; ++s) {
+            if (SC && ((s - s_lo) & 63) == 0) load_weight_scales(s);
+            take_scales(s);
+            // the rest of the last stage's loads go out with the first part
+            part(zero, s, s + R - 1, soon, all);
+            tile_each<FN - 2>([&](auto i) { part(std::integral_constant<int, decltype(i)::value + 1>{}, s, 0, zero, zero); });
+            tile_wait_vmcnt<LOADS * (R - 2)>();    // stage s + 1 has landed
+            tile_barrier();                        // and this one's slot has been read by every wave
+            issue_scales(s + R);
+            part(std::integral_constant<int, FN - 1>{}, s, s + R, zero, soon);  // past the last stage: read and not used
+#pragma unroll
+            for (int q = 0; q < FM; ++q) read_sx(s + 1, q);
+        }
+        if constexpr (FS) {                        // the sums that are still on their way
+            if (!idle) {
+#pragma unroll
+                for (int q = 0; q < FM; ++q) old[0][q] = fac[0][q], old[1][q] = fac[1][q];
+                tile_each<LAG>([&](auto i) { add_sum(std::integral_constant<int, decltype(i)::value - LAG>{}); });
+            }
+        }
+    }
+    tile_wait_vmcnt<0>();          // no load may land in the LDS later
+    __syncthreads();
+
+    // ---- outputs, T rows of a wave's tile at a time, by way of LDS of its own: in the accumulators a
+    // lane's neighbours are other rows, in memory they are a row's columns.  Lane (r, g) holds row r and columns
+    // 4 g + v of a 16 x 16 product, 8 (v / 4) + 4 g + v % 4 of a 32 x 32 one.
+    constexpr int HC = G::HC, HF = HC / 16;                      // output columns of a wave, in sixteens
+    uint8_t* const own = lds + wave * (T * (HC * 4 + 16));
+    const int64_t jw = j0 + wn * HC;
+    const int cols = (int)(p.m - jw < HC ? p.m - jw : HC);       // can be negative
+    // four columns of sixteen c, those from 4 k on of them: of y, or of product `up` of MM_GATE
+    auto four = [&](int c, int k, int q, int up) {
+        if constexpr (T == 16) {
+            const f32x4 v = GATE ? acc[2 * c + up][q] : acc[c][q];
+            return v;
+        } else {
+            const int f = GATE ? c : c / 2, v0 = GATE ? 8 * up + 4 * k : 8 * (c % 2) + 4 * k;
+            return f32x4{acc[f][q][v0], acc[f][q][v0 + 1], acc[f][q][v0 + 2], acc[f][q][v0 + 3]};
+        }
+    };
+    constexpr int K4 = T == 32 ? 2 : 1;                          // fours of a sixteen in a lane
+    auto column = [&](int c, int k) { return 16 * c + (T == 32 ? 8 * k : 0) + 4 * g; };
+    // value(c, k, q) of every column into rows of `wide` bytes a value, `out` being row t0, column jw
+    auto plane = [&](uint8_t* out, int wide, auto value) {
+        const int pitch = HC * wide + 16;
+#pragma unroll
+        for (int q = 0; q < FM; ++q) {
+#pragma unroll
+            for (int c = 0; c < HF; ++c)
+#pragma unroll
+                for (int k = 0; k < K4; ++k) {
+                    const f32x4 v = value(c, k, q);
+                    uint8_t* const to = own + r * pitch + column(c, k) * wide;
+                    if (wide == 4) *(f32x4*)to = v;
+                    else *(u32x2*)to = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                }
+            const int row0 = wm * TM + T * q, left = rows - row0;
+            const int lanes = HC * wide / 16;                    // of a row: a power of two
+            auto store = [&](auto ends) {                        // ends: rows may end inside 16 bytes
+                for (int i = lane; i < T * lanes; i += 64) {
+                    const int row = i / lanes, at16 = 16 * (i - row * lanes), some = cols * wide - at16;
+                    const u32x4 v = *(const u32x4*)(own + row * pitch + at16);
+                    if (row >= left || some <= 0) continue;
+                    uint8_t* const to = out + (int64_t)(row0 + row) * p.m * wide + at16;
+                    if (!decltype(ends)::value || some >= 16) {
+                        *(u32x4_any*)to = v;
+                    } else {
+                        for (int b = 0; b < some; b += wide) {
+                            if (wide == 4) *(uint32_t*)(to + b) = v[b / 4];
+                            else *(uint16_t*)(to + b) = (uint16_t)(v[b / 4] >> (8 * (b & 2)));
+                        }
+                    }
+                }
+            };
+            if (cols * wide % 16 == 0) store(std::false_type{});
+            else store(std::true_type{});
+        }
+    };
+    const int64_t at = t0 * p.m + jw;
+    if constexpr (GATE) {
+        const int64_t all_rows = p.n * p.m;
+        float* const z0 = p.part ? p.part + 2 * blockIdx.y * all_rows : p.z[0];
+        float* const z1 = p.part ? z0 + all_rows : p.z[1];
+        if (z0) {
+            plane((uint8_t*)(z0 + at), 4, [&](int c, int k, int q) { return four(c, k, q, 0); });
+            plane((uint8_t*)(z1 + at), 4, [&](int c, int k, int q) { return four(c, k, q, 1); });
+        }
+        if (p.part) return;
+        auto h = [&](int c, int k, int q) {
+            const f32x4 a = four(c, k, q, 0), b = four(c, k, q, 1);
+            f32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = act_of<false>(a[i], p.act, nullptr) * b[i];
+            return v;
+        };
+        if constexpr (BN == 256 && SC && !mm_wide(ELT)) {
+            if (p.hq) {
+                // a row's largest magnitude over its block of 128: this wave's 64 columns, then both waves'
+                f32x4 v[HF * K4][FM];
+                float* const tops = (float*)(lds + NW * T * (HC * 4 + 16));
+#pragma unroll
+                for (int q = 0; q < FM; ++q) {
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int c = 0; c < HF; ++c)
+#pragma unroll
+                        for (int k = 0; k < K4; ++k) {
+                            v[c * K4 + k][q] = h(c, k, q);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t b = __float_as_uint(v[c * K4 + k][q][i]) & 0x7fffffffu;
+                                top = top > b ? top : b;
+                            }
+                        }
+#pragma unroll
+                    for (int o = T; o < 64; o <<= 1) {
+                        const uint32_t b = (uint32_t)__shfl_xor((int)top, o, 64);
+                        top = top > b ? top : b;
+                    }
+                    if (g == 0) tops[wn * BM + wm * TM + T * q + r] = __uint_as_float(top);
+                }
+                __syncthreads();
+                constexpr int pitch = HC + 16;
+#pragma unroll
+                for (int q = 0; q < FM; ++q) {
+                    const int row0 = wm * TM + T * q, left = rows - row0;
+                    const uint32_t a = __float_as_uint(tops[row0 + r]), b = __float_as_uint(tops[BM + row0 + r]);
+                    const uint32_t s = fp8_scale_byte(a > b ? a : b);
+                    const float f = fp8_scale_inverse(s);
+#pragma unroll
+                    for (int c = 0; c < HF; ++c)
+#pragma unroll
+                        for (int k = 0; k < K4; ++k) {
+                            const f32x4 u = v[c * K4 + k][q];
+                            *(uint32_t*)(own + r * pitch + column(c, k)) = s == 255u ? 0u : fp8_pack4(u[0] * f, u[1] * f, u[2] * f, u[3] * f);
+                        }
+                    for (int i = lane; i < T * (HC / 16); i += 64) {
+                        const int row = i / (HC / 16), at16 = 16 * (i % (HC / 16));
+                        if (row < left) *(u32x4*)(p.hq + (t0 + row0 + row) * p.hq_row + jw + at16) = *(const u32x4*)(own + row * pitch + at16);
+                    }
+                    if (wn == 0 && g == 0 && r < left) {
+                        // with the last block, what fills the row's scales up: 1
+                        const int64_t from = (t0 + row0 + r) * p.hs_row + col, to = col == ncol - 1 ? p.hs_row - col : 1;
+                        for (int64_t i = 0; i < to; ++i) {
+                            const uint32_t byte = i == 0 ? s : 127u;
+                            if constexpr (ELT == MM_E8) ((uint8_t*)p.hs)[from + i] = (uint8_t)byte;
+                            else ((float*)p.hs)[from + i] = fp8_scale_value(byte);
+                        }
+                    }
+                }
+                return;
+            }
+        }
+        if (p.y_bf16) plane((uint8_t*)p.y[0] + 2 * at, 2, h);
+        else plane((uint8_t*)p.y[0] + 4 * at, 4, h);
+    } else {
+        int64_t from = at;
+        if constexpr (FORM == MM_TN) from += ((p.part ? (int64_t)which * p.experts : 0) + e) * p.d_out * p.m;
+        const int64_t planes = FORM == MM_TN ? (int64_t)p.outs * p.experts * p.d_out * p.m : p.n * p.m;
+        auto value = [&](int c, int k, int q) { return four(c, k, q, 0); };
+        if (p.part) plane((uint8_t*)(p.part + blockIdx.y * planes + from), 4, value);
+        else if (p.y_bf16) plane((uint8_t*)p.y[which] + 2 * from, 2, value);
+        else plane((uint8_t*)p.y[which] + 4 * from, 4, value);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the weight is streamed once, each wave on its own, without a barrier before the end.  A block
+// takes 16 MT rows of the weight (MM_GATE: 16 of each) and 16 rows of activations at a time; its
+// waves share out the contraction and their sums are added in the waves' order.  A wave copies pieces of
+// two lines of its weight rows into LDS of its own, one piece ahead.  Lane (r, b) holds chunks
+// b and 4 + b of a line of weight row r, and the same of row r of the activations.
+//
+// An expert's block takes its first MM_FIRST groups of 16 rows, and what experts have beyond those is spread over
+// blocks of its own that find their groups from the offsets: the plan knows the mean of the experts' rows alone.
+// ---------------------------------------------------------------------------
+template <int ELT, bool GATE, int MT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_mm_stream(MmTile p) {
+    constexpr int PIECE = 16 * MT * 16, LOADS = PIECE / 64;     // slots of a piece, copies
+    constexpr bool SC = ELT != MM_BF16;
+    static_assert(!GATE || MT == 2, "16 rows of each weight");
+    extern __shared__ u32x4 mm_lds[];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, b = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    u32x4* const ring = mm_lds + wave * 2 * PIECE;
+    auto sums = [&](int w, int t) { return (float*)(mm_lds + w * 2 * PIECE) + 256 * t; };    // over the rings at the end
+    constexpr int BC = GATE ? 16 : 16 * MT;
+    const int64_t j0 = (int64_t)blockIdx.x * BC;
+    const int lines = (int)((p.w_bytes + 127) / 128), pieces = (lines + 1) / 2;
+    const int shares = WAVES * (int)gridDim.z, per = (pieces + shares - 1) / shares;
+    const int c0 = ((int)blockIdx.z * WAVES + wave) * per;
+    const int c1 = c0 + per < pieces ? c0 + per : pieces;
+
+    const int wrows = (int)(p.m - j0 < BC ? p.m - j0 : BC);
+    uint32_t wv[LOADS];
+    int wc[LOADS];                                 // the chunk's byte within a piece
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int slot = i * 64 + lane, row = slot / 16;
+        wc[i] = 16 * ((slot % 16) ^ (row & 15));
+        wv[i] = (uint32_t)((GATE ? row % 16 : row) * p.w_row) + wc[i];
+    }
+    const int beyond = (int)blockIdx.y - p.experts, step = (int)gridDim.y - p.experts;
+    int64_t lo = 0, hi = p.n;
+    if (p.offsets && beyond < 0) tile_expert_rows(p.offsets, blockIdx.y, p.n, lo, hi);
+    for (int turn = 0;; ++turn) {
+        TilePlace place;
+        if (beyond < 0) {
+            place.e = blockIdx.y;
+            place.t0 = lo + 16 * turn;
+            place.rows = (int)(hi - place.t0 < 16 ? hi - place.t0 : 16);
+            place.ok = turn < MM_FIRST && place.rows > 0;
+        } else {
+            tile_of_row(p, 16, beyond + turn * step, place, MM_FIRST);
+        }
+        if (!place.ok) return;
+        if (turn > 0) __syncthreads();             // the sums of the rows before have been read
+        const int rows = place.rows;
+        const int64_t t0 = place.t0, row0 = (int64_t)place.e * p.d_out + j0;
+        auto copy = [&](int c) {                   // past the last piece: clears, reads nothing
+            u32x4* const to = ring + (c & 1) * PIECE;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const __amdgpu_buffer_rsrc_t wr = tile_rsrc(p.W[GATE ? i / (LOADS / 2) : 0] + row0 * p.w_row, wrows, p.w_row, c < c1);
+                const int64_t byte = (int64_t)c * 256 + wc[i];
+                tile_dma(wr, to + 64 * i, byte < p.w_bytes ? wv[i] : 0xC0000000u, (uint32_t)c * 256u);
+            }
+        };
+        const int64_t xrow = t0 + (r < rows ? r : rows - 1);
+        const uint8_t* const xp = p.A[0] + xrow * p.a_row;
+        const int64_t sbase = ((int64_t)place.e * p.ws_rows + j0 / 128) * p.ws_row;
+        f32x4 acc[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (c0 < c1) copy(c0);
+        for (int c = c0; c < c1; ++c) {
+            // this piece's activations and scales, then the next piece's copies: once those alone are in
+            // flight, both this piece's copies and its activations have arrived
+            u32x4 x[2][2];
+            uint32_t xs[2], ws[2][GATE ? 2 : 1];
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                const int line = 2 * c + l, kept = line < lines ? line : lines - 1;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t byte = 128 * (int64_t)line + 64 * j + 16 * b;
+                    const u32x4 v = *(const u32x4*)(xp + (byte < p.a_bytes ? byte : 0));
+                    x[l][j] = byte < p.a_bytes ? v : u32x4{0u, 0u, 0u, 0u};
+                }
+                if constexpr (SC) {
+                    const uint8_t* const s = (const uint8_t*)p.AS + xrow * p.as_row;
+                    xs[l] = mm_bytes(ELT) ? (uint32_t)s[kept] : ((const uint32_t*)s)[kept];
+#pragma unroll
+                    for (int h = 0; h < (GATE ? 2 : 1); ++h)
+                        ws[l][h] = mm_bytes(ELT) ? (uint32_t)((const uint8_t*)p.WS[h])[sbase + kept] : ((const uint32_t*)p.WS[h])[sbase + kept];
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            copy(c + 1);
+            tile_wait_vmcnt<LOADS>();
+            __builtin_amdgcn_sched_barrier(0);
+            const uint8_t* const at = (const uint8_t*)(ring + (c & 1) * PIECE);
+#pragma unroll
+            for (int l = 0; l < 2; ++l)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    u32x4 w[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) w[j] = *(const u32x4*)(at + 16 * ((16 * t + r) * 16 + ((8 * l + 4 * j + b) ^ r)));
+                    if constexpr (ELT == MM_BF16) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w[j]), as_bf16x8(x[l][j]), acc[t], 0, 0, 0);
+                    } else if constexpr (ELT == MM_E8) {
+                        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm_pair(w[0], w[1]), mm_pair(x[l][0], x[l][1]), acc[t], 0, 0, 0, (int)ws[l][GATE ? t : 0], 0, (int)xs[l]);
+                    } else {
+                        f32x4 d{0.f, 0.f, 0.f, 0.f};
+                        if constexpr (mm_wide(ELT)) {
+                            u32x4 a[4], v[4];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                mm_widen(w[j], a[2 * j], a[2 * j + 1]);
+                                mm_widen(x[l][j], v[2 * j], v[2 * j + 1]);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), as_bf16x8(v[j]), d, 0, 0, 0);
+                        } else {
+                            d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm_pair(w[0], w[1]), mm_pair(x[l][0], x[l][1]), d, 0, 0, 0, 127, 0, 127);
+                        }
+                        const uint32_t wk = ws[l][GATE ? t : 0];
+                        const float by = mm_bytes(ELT) ? fp8_scale_value(wk) * fp8_scale_value(xs[l]) : __uint_as_float(wk) * __uint_as_float(xs[l]);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(d[v], by, acc[t][v]);
+                    }
+                }
+            __builtin_amdgcn_sched_barrier(0);
+            tile_wait_lds();                       // read, before its half of the ring is copied into
+        }
+        tile_wait_vmcnt<0>();                      // no copy into the ring may land later
+#pragma unroll
+        for (int t = 0; t < MT; ++t) *(f32x4*)(sums(wave, t) + 4 * lane) = acc[t];
+        __syncthreads();
+        // output (row i / BC, column i % BC) is in lane 16 (column / 4) + row, element column % 4
+        for (int i = tid; i < 16 * BC; i += 64 * WAVES) {
+            const int row = i / BC, c = i - row * BC, t = c >> 4, from = 4 * (16 * ((c & 15) >> 2) + row) + (c & 3);
+            if (row >= rows || j0 + c >= p.m) continue;
+            float v[GATE ? 2 : 1];
+#pragma unroll
+            for (int h = 0; h < (GATE ? 2 : 1); ++h) {
+                v[h] = sums(0, GATE ? h : t)[from];
+#pragma unroll
+                for (int w = 1; w < WAVES; ++w) v[h] += sums(w, GATE ? h : t)[from];
+            }
+            const int64_t all = p.n * p.m, at = (t0 + row) * p.m + j0 + c;
+            float y = v[0];
+            if constexpr (GATE) {
+                if (p.part) {
+                    p.part[2 * (int64_t)blockIdx.z * all + at] = v[0];
+                    p.part[(2 * (int64_t)blockIdx.z + 1) * all + at] = v[1];
+                    continue;
+                }
+                if (p.z[0]) {
+                    p.z[0][at] = v[0];
+                    p.z[1][at] = v[1];
+                }
+                y = act_of<false>(v[0], p.act, nullptr) * v[1];
+            } else if (p.part) {
+                p.part[(int64_t)blockIdx.z * all + at] = y;
+                continue;
+            }
+            if (p.y_bf16) ((uint16_t*)p.y[0])[at] = (uint16_t)f32_to_bf16_bits(y);
+            else ((float*)p.y[0])[at] = y;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
+static hipError_t mm_launch_tile(const MmTile& t, const MmPlan& P, hipStream_t st) {
+    const auto k = k_mm_tile<ELT, FORM, BM, BN, WM, NW, T, R>;
+    constexpr size_t lds = MmGeo<ELT, FORM, BM, BN, WM, NW, T, R>::BYTES;
+    if (P.bm != BM || P.bn != BN || P.waves != NW) return hipErrorInvalidValue;      // (the plan's are these)
+    const hipError_t e = ensure_dynamic_lds((const void*)k, lds);
+    if (e != hipSuccess) return e;
+    const int64_t grid = mm_blocks((MmForm)FORM, t.n, t.m, t.d_out, t.experts, t.offsets != nullptr, t.outs, P);
+    if (grid * (64 * NW) > MM_MAX_LANES) return hipErrorInvalidValue;                // (refused before)
+    hipLaunchKernelGGL(k, dim3((unsigned)grid, (unsigned)P.split), dim3(64 * NW), lds, st, t);
+    GQ_LAUNCH_CHECK();
+    return hipSuccess;
+}
+
+template <int ELT, bool GATE, int MT, int WAVES>
+static hipError_t mm_launch_stream(const MmTile& t, const MmPlan& P, hipStream_t st) {
+    const auto k = k_mm_stream<ELT, GATE, MT, WAVES>;
+    const size_t lds = (size_t)WAVES * 2 * 16 * MT * 16 * 16;
+    const hipError_t e = ensure_dynamic_lds((const void*)k, lds);
+    if (e != hipSuccess) return e;
+    // a block for each expert, and for the groups beyond its own those of a compute unit each
+    const int64_t bc = GATE ? 16 : 16 * MT, cols = (t.m + bc - 1) / bc, far = (t.n + 15) / 16 - MM_FIRST, room = 256 / (cols * P.split);
+    const int64_t more = !t.offsets || far < 1 ? 0 : (room < 1 ? 1 : (room < far ? room : far));
+    hipLaunchKernelGGL(k, dim3((unsigned)cols, (unsigned)(t.experts + more), (unsigned)P.split), dim3(64 * WAVES), lds, st, t);
+    GQ_LAUNCH_CHECK();
+    return hipSuccess;
+}
+
+// NT and GATE
+template <int ELT, int FORM>
+static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t st) {
+    constexpr bool GATE = FORM == MM_GATE;
+    constexpr int T = ELT == MM_BF16 || ELT == MM_E8 ? 32 : 16;
+    if (P.stream) {
+        if constexpr (GATE) return P.waves == 8 ? mm_launch_stream<ELT, true, 2, 8>(t, P, st) : mm_launch_stream<ELT, true, 2, 4>(t, P, st);
+        else if (P.bn == 32) return P.waves == 8 ? mm_launch_stream<ELT, false, 2, 8>(t, P, st) : mm_launch_stream<ELT, false, 2, 4>(t, P, st);
+        else return P.waves == 8 ? mm_launch_stream<ELT, false, 1, 8>(t, P, st) : mm_launch_stream<ELT, false, 1, 4>(t, P, st);
+    }
+    switch (P.bm) {
+        case 256:
+            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, FORM, 256, 256, 4, 8, T, 2>(t, P, st);
+            else return hipErrorInvalidValue;                                        // (the plan takes none)
+        case 128: return mm_launch_tile<ELT, FORM, 128, 128, 2, 4, T, 2>(t, P, st);
+        case 64: return mm_launch_tile<ELT, FORM, 64, 128, 2, 4, 16, 3>(t, P, st);
+        default: return mm_launch_tile<ELT, FORM, 32, 128, 1, 4, 16, 3>(t, P, st);
+    }
+}
+
+template <int ELT>
+static hipError_t mm_launch_back(const MmTile& t, const MmPlan& P, hipStream_t st) {
+    constexpr int T = ELT == MM_BF16 || ELT == MM_E8 ? 32 : 16;
+    switch (P.bm) {
+        case 256:
+            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, MM_NN, 256, 256, 4, 8, T, 2>(t, P, st);
+            else return hipErrorInvalidValue;
+        case 128: return mm_launch_tile<ELT, MM_NN, 128, 256, 2, 8, T, 2>(t, P, st);
+        default: return mm_launch_tile<ELT, MM_NN, 64, 256, 2, 4, T, 3>(t, P, st);
+    }
+}
+
+}  // namespace gq

@@ -22,20 +22,43 @@ __device__ __forceinline__ int mm_tswz(int row) {
                    : (2 * (row & 3)) ^ (9 * ((row >> 2) & 1)) ^ ((row >> 4) & 1);
 }
 
+// tile_dma of SIZE bytes a lane.  Kernels with turned reads take it as inline assembly: the compiler
+// does not see then that it writes LDS, and would otherwise have every such read wait for all copies in flight (plain
+// reads it leaves alone; 4096 rows, gradient of 11008 -> 4096 in bfloat16: 869 us, 618 so).  It has no
+// outputs, and the kernels count its arrival themselves as they do the builtin's.  Five wait states lie between a
+// scalar written by the vector unit and its use.
+template <bool TURNED, int SIZE>
+__device__ __forceinline__ void mm_dma(__amdgpu_buffer_rsrc_t r, void* dst, uint32_t voff, uint32_t soff) {
+    if constexpr (TURNED) {
+        const uint32_t at = (uint32_t)(uintptr_t)(tile_lds_t)dst;
+        if constexpr (SIZE == 16)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                         :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voff), "s"(r), "s"(soff) : "m0", "memory");
+        else
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                         :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voff), "s"(r), "s"(soff) : "m0", "memory");
+    } else if constexpr (SIZE == 16) {
+        tile_dma(r, (u32x4*)dst, voff, soff);
+    } else {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (tile_lds_t)dst, 4, voff, soff, 0, 0);
+    }
+}
+
 template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
 struct MmGeo {
     static constexpr int ES = ELT == MM_BF16 ? 2 : 1, KE = 128 / ES;    // bytes of a value, values of a stage
     static constexpr bool XT = FORM == MM_TN, WT = FORM == MM_NN || FORM == MM_TN;
     static constexpr int WN = NW / WM, TM = BM / WM, TN = BN / WN;      // waves, and a wave's tile
     static constexpr int FM = TM / T, FN = TN / T, V = T * T / 64;      // its fragments, an accumulator
-    static constexpr int CH = T / 8, NP = 64 / T;                       // chunks a lane has of a line, lanes a row
+    static constexpr int NP = 64 / T, CH = 8 / NP;                      // lanes a row, chunks a lane has of its line
     static constexpr int X = BM * 8, W = BN * 8, STAGE = X + W;         // 16-byte slots
     static constexpr bool SC = ELT != MM_BF16;
     static constexpr int SB = mm_bytes(ELT) ? 4 : 16;                   // bytes of four stages' scales of a row
     static constexpr int SCB = SC ? BM * SB : 0;                        // one of three buffers of them
     static constexpr size_t IN = (size_t)R * STAGE * 16 + 3 * SCB;
     static constexpr int HC = FORM == MM_GATE ? TN / 2 : TN;            // output columns of a wave
-    static constexpr size_t OUT = (size_t)NW * T * (HC * 4 + 16) + (FORM == MM_GATE ? 8 * BM : 0);
+    static constexpr int PITCH = (FORM == MM_GATE ? 2 : 1) * HC * 4 + 16;  // bytes of a row on its way out
+    static constexpr size_t OUT = (size_t)NW * T * PITCH + (FORM == MM_GATE ? 8 * BM : 0);
     static constexpr size_t BYTES = IN > OUT ? IN : OUT;
     static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
     static_assert(FN % 2 == 0 && TM % T == 0 && TN % T == 0, "fragments go in pairs");
@@ -96,7 +119,7 @@ __device__ __forceinline__ i32x8 mm_pair(u32x4 a, u32x4 b) {
 // next stage's rows and first columns are read.
 // ---------------------------------------------------------------------------
 template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
-__global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM == 256 && NW == 4 ? 1 : 8))) void k_mm_tile(MmTile p) {
     typedef MmGeo<ELT, FORM, BM, BN, WM, NW, T, R> G;
     constexpr int ES = G::ES, KE = G::KE, FM = G::FM, FN = G::FN, V = G::V, CH = G::CH, NP = G::NP, TM = G::TM, TN = G::TN;
     constexpr bool XT = G::XT, WT = G::WT, SC = G::SC, GATE = FORM == MM_GATE;
@@ -194,12 +217,12 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             u32x4* const to = base + wave * XPW + i * 64;
             if constexpr (XT) {
                 const int64_t k0 = (int64_t)s * KE, left = k_rows - k0 < KE ? k_rows - k0 : KE;
-                tile_dma(tile_rsrc(p.A[which] + (k_lo + k0) * p.a_row + t0 * ES, (int)left, p.a_row, on, (int)(t0 * ES)), to, xv[i], 0);
+                mm_dma<WT, 16>(tile_rsrc(p.A[which] + (k_lo + k0) * p.a_row + t0 * ES, (int)left, p.a_row, on, (int)(t0 * ES)), to, xv[i], 0);
             } else {
                 const __amdgpu_buffer_rsrc_t xr = tile_rsrc(p.A[src] + t0 * p.a_row, rows, p.a_row, on);
                 uint32_t v = xv[i];
                 if constexpr (EDGE) v = sl < xe[i] ? v : 0xC0000000u;                 // past the row: zeros
-                tile_dma(xr, to, v, (uint32_t)sl * 128u);
+                mm_dma<WT, 16>(xr, to, v, (uint32_t)sl * 128u);
             }
         } else {
             i -= XI;
@@ -207,19 +230,19 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             if constexpr (WT) {
                 const int64_t k0 = (int64_t)sl * KE, all = FORM == MM_TN ? k_rows : p.d_out, left = all - k0 < KE ? all - k0 : KE;
                 const uint8_t* const from = p.W[src] + ((FORM == MM_TN ? k_lo : e_rows) + k0) * p.w_row + j0 * ES;
-                tile_dma(tile_rsrc(from, (int)left, p.w_row, on, (int)(j0 * ES)), to, wv[i], 0);
+                mm_dma<WT, 16>(tile_rsrc(from, (int)left, p.w_row, on, (int)(j0 * ES)), to, wv[i], 0);
             } else {
                 const int half = GATE ? ((wave * WPW + i * 64) / 128) & 1 : 0;       // 8 rows a copy
                 const __amdgpu_buffer_rsrc_t q = tile_rsrc(p.W[half] + (e_rows + j0) * p.w_row, wcols, p.w_row, on);
                 uint32_t v = wv[i];
                 if constexpr (EDGE) v = s < we[i] ? v : 0xC0000000u;
-                tile_dma(q, to, v, (uint32_t)s * 128u);
+                mm_dma<WT, 16>(q, to, v, (uint32_t)s * 128u);
             }
         }
     };
     // The rows' scales: four stages' of a row at a time, a quarter of the next four's rows with each stage.
     uint8_t* const sc_lds = lds + R * G::STAGE * 16;
-    constexpr int SW = SC ? (BM / 4 / NW > 0 ? BM / 4 / NW : 1) : 1;              // rows of a wave's copy
+        constexpr int SW = SC ? (BM / 4 / NW > 0 ? BM / 4 / NW : 1) : 1;        // rows of a wave's copy
     static_assert(!SC || SW * NW * 4 == BM, "every wave copies scales");
     auto scale_copy = [&](int span, int row, int count, bool on) {
         if constexpr (SC) {
@@ -227,9 +250,9 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             uint8_t* const to = sc_lds + (span % 3) * G::SCB + row * G::SB;
             const uint32_t v = (uint32_t)((row + lane) * p.as_row) + (uint32_t)(G::SB * span);
             if constexpr (mm_bytes(ELT)) {
-                if (lane < count) __builtin_amdgcn_raw_ptr_buffer_load_lds(z, (tile_lds_t)to, 4, v, 0, 0, 0);
+                if (lane < count) mm_dma<WT, 4>(z, to, v, 0);
             } else {
-                if (lane < count) tile_dma(z, (u32x4*)to, v, 0);
+                if (lane < count) mm_dma<WT, 16>(z, to, v, 0);
             }
         }
     };
@@ -249,7 +272,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
     const int64_t wblocks = p.ws_row, sbase = (int64_t)e * ((p.d_out + 127) / 128) * wblocks;
     auto load_weight_scales = [&](int s) {
         if constexpr (SC) {
-            const int k = s + lane < stages ? s + lane : stages - 1;
+            const int k = s + lane < p.ws_k ? s + lane : (int)p.ws_k - 1;
             const int64_t jb = GATE ? j0 / 128 : (j0 + wn * TN) / 128;
             // (columns past the last block: any scale, they are not stored)
             const int64_t at = FORM == MM_NN ? (int64_t)k * wblocks + (jb < wblocks ? jb : wblocks - 1)
@@ -271,7 +294,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
         for (int q = 0; q < FM; ++q)
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[f][q][v] = 0.f;
-    constexpr int RPC = KE / 8;                    // values of the contraction in a chunk
+    constexpr int RPC = 16 / ES;                   // values of the contraction in a chunk
     constexpr int RPR = RPC / 2;                   // and in a turned read
     constexpr int LPR = 16 / RPR;                  // lanes that read one row of it
     // where a turned operand's column fragment starts: row g of chunks, row and part of a block
@@ -411,7 +434,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
         }
     };
 
-    constexpr int LOADS_ALL = XI + WI, LATE = LOADS_ALL / 2, SOON = LOADS_ALL - LATE, PR = FM * KS;
+    constexpr int LOADS_ALL = XI + WI, LATE = ELT == MM_FS ? 0 : LOADS_ALL / 2, SOON = LOADS_ALL - LATE, PR = FM * KS;
     // Column fragment f of stage s, beside its products: the next fragment's reads, of the loads l0 .. l1 - 1 of stage sl
     // one after every so many products, and with the last fragment the next stage's rows as each is done with.
     auto part = [&](auto fragment, int s, int sl, auto l0, auto l1) {
@@ -504,7 +527,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
     // lane's neighbours are other rows, in memory they are a row's columns.  Lane (r, g) holds row r and columns
     // 4 g + v of a 16 x 16 product, 8 (v / 4) + 4 g + v % 4 of a 32 x 32 one.
     constexpr int HC = G::HC, HF = HC / 16;                      // output columns of a wave, in sixteens
-    uint8_t* const own = lds + wave * (T * (HC * 4 + 16));
+    uint8_t* const own = lds + wave * (T * G::PITCH);
     const int64_t jw = j0 + wn * HC;
     const int cols = (int)(p.m - jw < HC ? p.m - jw : HC);       // can be negative
     // four columns of sixteen c, those from 4 k on of them: of y, or of product `up` of MM_GATE
@@ -519,20 +542,149 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
     };
     constexpr int K4 = T == 32 ? 2 : 1;                          // fours of a sixteen in a lane
     auto column = [&](int c, int k) { return 16 * c + (T == 32 ? 8 * k : 0) + 4 * g; };
-    // value(c, k, q) of every column into rows of `wide` bytes a value, `out` being row t0, column jw
-    auto plane = [&](uint8_t* out, int wide, auto value) {
-        const int pitch = HC * wide + 16;
-#pragma unroll
+    const int64_t at = t0 * p.m + jw;
+    if constexpr (GATE) {
+        const int64_t all_rows = p.n * p.m;
+        float* const z0 = p.part ? p.part + 2 * blockIdx.y * all_rows : p.z[0];
+        float* const z1 = p.part ? z0 + all_rows : p.z[1];
+        constexpr bool PACKS = BN == 256 && SC && !mm_wide(ELT);
+        const bool packs = PACKS && p.hq && !p.part;
+        float* const tops = (float*)(lds + NW * T * G::PITCH);   // [WN][BM]
+        constexpr int LANES = HC / 8;                            // a lane takes 8 columns of a row
+        // (one copy of what follows for all q: with the activations in it, one for each would not fit the
+        // instruction cache; 8-bit gate of 4096 rows, 8192 -> 2048: 139 us, 114 so)
+#pragma unroll 1
         for (int q = 0; q < FM; ++q) {
+            tile_each<FM>([&](auto index) {
+                constexpr int Q = decltype(index)::value;
+                if (q == Q) {
 #pragma unroll
-            for (int c = 0; c < HF; ++c)
+                    for (int c = 0; c < HF; ++c)
 #pragma unroll
-                for (int k = 0; k < K4; ++k) {
-                    const f32x4 v = value(c, k, q);
-                    uint8_t* const to = own + r * pitch + column(c, k) * wide;
-                    if (wide == 4) *(f32x4*)to = v;
-                    else *(u32x2*)to = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                        for (int k = 0; k < K4; ++k) {
+                            uint8_t* const to = own + r * G::PITCH + column(c, k) * 4;
+                            *(f32x4*)to = four(c, k, Q, 0);
+                            *(f32x4*)(to + HC * 4) = four(c, k, Q, 1);
+                        }
                 }
+            });
+            const int row0 = wm * TM + T * q, left = rows - row0;
+#pragma unroll 1
+            for (int i = lane; i < T * LANES; i += 64) {         // products out, h out or back in their place
+                const int row = i / LANES, c8 = 8 * (i % LANES), some = cols - c8;
+                uint8_t* const from = own + row * G::PITCH + c8 * 4;
+                f32x4 a[2], b[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    a[k] = *(const f32x4*)(from + 16 * k);
+                    b[k] = *(const f32x4*)(from + HC * 4 + 16 * k);
+                }
+                const bool stored = row < left && some > 0;
+                const int64_t to = at + (int64_t)(row0 + row) * p.m + c8;
+                auto values = [&](float* y, const f32x4 (&x)[2]) {
+                    if (some >= 8) {
+                        *(f32x4_any*)(y + to) = x[0];
+                        *(f32x4_any*)(y + to + 4) = x[1];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < some) y[to + k] = x[k / 4][k % 4];
+                    }
+                };
+                if (z0 && stored) {
+                    values(z0, a);
+                    values(z1, b);
+                }
+                if (p.part) continue;
+                f32x4 h[2];
+                if (p.act == ACT_SILU) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) h[k / 4][k % 4] = act_of<false>(a[k / 4][k % 4], ACT_SILU, nullptr) * b[k / 4][k % 4];
+                } else if (p.act == ACT_GELU) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) h[k / 4][k % 4] = act_of<false>(a[k / 4][k % 4], ACT_GELU, nullptr) * b[k / 4][k % 4];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) h[k / 4][k % 4] = act_of<false>(a[k / 4][k % 4], ACT_GELU_TANH, nullptr) * b[k / 4][k % 4];
+                }
+                if (packs) {
+                    // a row's largest magnitude over this wave's 64 columns
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t v = __float_as_uint(h[k / 4][k % 4]) & 0x7fffffffu;
+                        top = top > v ? top : v;
+                    }
+#pragma unroll
+                    for (int o = 1; o < LANES; o <<= 1) {
+                        const uint32_t v = (uint32_t)__shfl_xor((int)top, o, 64);
+                        top = top > v ? top : v;
+                    }
+                    if (i % LANES == 0) tops[wn * BM + row0 + row] = __uint_as_float(top);
+                    *(f32x4*)from = h[0];
+                    *(f32x4*)(from + 16) = h[1];
+                    continue;
+                }
+                if (!stored) continue;
+                if (!p.y_bf16) {
+                    values((float*)p.y[0], h);
+                } else if (some >= 8) {
+                    *(u32x4_any*)((uint16_t*)p.y[0] + to) = u32x4{pack_bf16x2(h[0][0], h[0][1]), pack_bf16x2(h[0][2], h[0][3]),
+                                                                  pack_bf16x2(h[1][0], h[1][1]), pack_bf16x2(h[1][2], h[1][3])};
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < some) ((uint16_t*)p.y[0])[to + k] = (uint16_t)f32_to_bf16_bits(h[k / 4][k % 4]);
+                }
+            }
+            if constexpr (PACKS) {
+                if (!packs) continue;
+                __syncthreads();                                 // both waves of a block of 128 columns
+#pragma unroll 1
+                for (int i = lane; i < T * LANES; i += 64) {
+                    const int row = i / LANES, c8 = 8 * (i % LANES);
+                    const uint32_t a = __float_as_uint(tops[row0 + row]), b = __float_as_uint(tops[BM + row0 + row]);
+                    const uint32_t s = fp8_scale_byte(a > b ? a : b);
+                    const float f = fp8_scale_inverse(s);
+                    const uint8_t* const from = own + row * G::PITCH + c8 * 4;
+                    const f32x4 u = *(const f32x4*)from, v = *(const f32x4*)(from + 16);
+                    const u32x2 codes{fp8_pack4(u[0] * f, u[1] * f, u[2] * f, u[3] * f), fp8_pack4(v[0] * f, v[1] * f, v[2] * f, v[3] * f)};
+                    if (row >= left) continue;
+                    *(u32x2*)(p.hq + (t0 + row0 + row) * p.hq_row + jw + c8) = s == 255u ? u32x2{0u, 0u} : codes;
+                    if (wn == 0 && c8 == 0) {
+                        // with the last block, what fills the row's scales up: 1
+                        const int64_t at0 = (t0 + row0 + row) * p.hs_row + col, n = col == ncol - 1 ? p.hs_row - col : 1;
+                        for (int64_t k = 0; k < n; ++k) {
+                            const uint32_t byte = k == 0 ? s : 127u;
+                            if constexpr (mm_bytes(ELT)) ((uint8_t*)p.hs)[at0 + k] = (uint8_t)byte;
+                            else ((float*)p.hs)[at0 + k] = fp8_scale_value(byte);
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        int64_t from = at;
+        if constexpr (FORM == MM_TN) from += ((p.part ? (int64_t)which * p.experts : 0) + e) * p.d_out * p.m;
+        const int64_t planes = FORM == MM_TN ? (int64_t)p.outs * p.experts * p.d_out * p.m : p.n * p.m;
+        const int wide = p.part || !p.y_bf16 ? 4 : 2, pitch = HC * wide + 16;
+        uint8_t* const out = p.part ? (uint8_t*)(p.part + blockIdx.y * planes + from) : (uint8_t*)p.y[which] + from * wide;
+#pragma unroll 1
+        for (int q = 0; q < FM; ++q) {
+            tile_each<FM>([&](auto index) {
+                constexpr int Q = decltype(index)::value;
+                if (q == Q) {
+#pragma unroll
+                    for (int c = 0; c < HF; ++c)
+#pragma unroll
+                        for (int k = 0; k < K4; ++k) {
+                            const f32x4 v = four(c, k, Q, 0);
+                            uint8_t* const to = own + r * pitch + column(c, k) * wide;
+                            if (wide == 4) *(f32x4*)to = v;
+                            else *(u32x2*)to = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                        }
+                }
+            });
             const int row0 = wm * TM + T * q, left = rows - row0;
             const int lanes = HC * wide / 16;                    // of a row: a power of two
             auto store = [&](auto ends) {                        // ends: rows may end inside 16 bytes
@@ -554,92 +706,6 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             if (cols * wide % 16 == 0) store(std::false_type{});
             else store(std::true_type{});
         }
-    };
-    const int64_t at = t0 * p.m + jw;
-    if constexpr (GATE) {
-        const int64_t all_rows = p.n * p.m;
-        float* const z0 = p.part ? p.part + 2 * blockIdx.y * all_rows : p.z[0];
-        float* const z1 = p.part ? z0 + all_rows : p.z[1];
-        if (z0) {
-            plane((uint8_t*)(z0 + at), 4, [&](int c, int k, int q) { return four(c, k, q, 0); });
-            plane((uint8_t*)(z1 + at), 4, [&](int c, int k, int q) { return four(c, k, q, 1); });
-        }
-        if (p.part) return;
-        auto h = [&](int c, int k, int q) {
-            const f32x4 a = four(c, k, q, 0), b = four(c, k, q, 1);
-            f32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = act_of<false>(a[i], p.act, nullptr) * b[i];
-            return v;
-        };
-        if constexpr (BN == 256 && SC && !mm_wide(ELT)) {
-            if (p.hq) {
-                // a row's largest magnitude over its block of 128: this wave's 64 columns, then both waves'
-                f32x4 v[HF * K4][FM];
-                float* const tops = (float*)(lds + NW * T * (HC * 4 + 16));
-#pragma unroll
-                for (int q = 0; q < FM; ++q) {
-                    uint32_t top = 0u;
-#pragma unroll
-                    for (int c = 0; c < HF; ++c)
-#pragma unroll
-                        for (int k = 0; k < K4; ++k) {
-                            v[c * K4 + k][q] = h(c, k, q);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t b = __float_as_uint(v[c * K4 + k][q][i]) & 0x7fffffffu;
-                                top = top > b ? top : b;
-                            }
-                        }
-#pragma unroll
-                    for (int o = T; o < 64; o <<= 1) {
-                        const uint32_t b = (uint32_t)__shfl_xor((int)top, o, 64);
-                        top = top > b ? top : b;
-                    }
-                    if (g == 0) tops[wn * BM + wm * TM + T * q + r] = __uint_as_float(top);
-                }
-                __syncthreads();
-                constexpr int pitch = HC + 16;
-#pragma unroll
-                for (int q = 0; q < FM; ++q) {
-                    const int row0 = wm * TM + T * q, left = rows - row0;
-                    const uint32_t a = __float_as_uint(tops[row0 + r]), b = __float_as_uint(tops[BM + row0 + r]);
-                    const uint32_t s = fp8_scale_byte(a > b ? a : b);
-                    const float f = fp8_scale_inverse(s);
-#pragma unroll
-                    for (int c = 0; c < HF; ++c)
-#pragma unroll
-                        for (int k = 0; k < K4; ++k) {
-                            const f32x4 u = v[c * K4 + k][q];
-                            *(uint32_t*)(own + r * pitch + column(c, k)) = s == 255u ? 0u : fp8_pack4(u[0] * f, u[1] * f, u[2] * f, u[3] * f);
-                        }
-                    for (int i = lane; i < T * (HC / 16); i += 64) {
-                        const int row = i / (HC / 16), at16 = 16 * (i % (HC / 16));
-                        if (row < left) *(u32x4*)(p.hq + (t0 + row0 + row) * p.hq_row + jw + at16) = *(const u32x4*)(own + row * pitch + at16);
-                    }
-                    if (wn == 0 && g == 0 && r < left) {
-                        // with the last block, what fills the row's scales up: 1
-                        const int64_t from = (t0 + row0 + r) * p.hs_row + col, to = col == ncol - 1 ? p.hs_row - col : 1;
-                        for (int64_t i = 0; i < to; ++i) {
-                            const uint32_t byte = i == 0 ? s : 127u;
-                            if constexpr (ELT == MM_E8) ((uint8_t*)p.hs)[from + i] = (uint8_t)byte;
-                            else ((float*)p.hs)[from + i] = fp8_scale_value(byte);
-                        }
-                    }
-                }
-                return;
-            }
-        }
-        if (p.y_bf16) plane((uint8_t*)p.y[0] + 2 * at, 2, h);
-        else plane((uint8_t*)p.y[0] + 4 * at, 4, h);
-    } else {
-        int64_t from = at;
-        if constexpr (FORM == MM_TN) from += ((p.part ? (int64_t)which * p.experts : 0) + e) * p.d_out * p.m;
-        const int64_t planes = FORM == MM_TN ? (int64_t)p.outs * p.experts * p.d_out * p.m : p.n * p.m;
-        auto value = [&](int c, int k, int q) { return four(c, k, q, 0); };
-        if (p.part) plane((uint8_t*)(p.part + blockIdx.y * planes + from), 4, value);
-        else if (p.y_bf16) plane((uint8_t*)p.y[which] + 2 * from, 2, value);
-        else plane((uint8_t*)p.y[which] + 4 * from, 4, value);
     }
 }
 
@@ -848,6 +914,7 @@ template <int ELT, int FORM>
 static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t st) {
     constexpr bool GATE = FORM == MM_GATE;
     constexpr int T = ELT == MM_BF16 || ELT == MM_E8 ? 32 : 16;
+    constexpr bool W8 = mm_big_waves(ELT) == 8;
     if (P.stream) {
         if constexpr (GATE) return P.waves == 8 ? mm_launch_stream<ELT, true, 2, 8>(t, P, st) : mm_launch_stream<ELT, true, 2, 4>(t, P, st);
         else if (P.bn == 32) return P.waves == 8 ? mm_launch_stream<ELT, false, 2, 8>(t, P, st) : mm_launch_stream<ELT, false, 2, 4>(t, P, st);
@@ -855,7 +922,7 @@ static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t s
     }
     switch (P.bm) {
         case 256:
-            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, FORM, 256, 256, 4, 8, T, 2>(t, P, st);
+            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, FORM, 256, 256, W8 ? 4 : 2, W8 ? 8 : 4, T, 2>(t, P, st);
             else return hipErrorInvalidValue;                                        // (the plan takes none)
         case 128: return mm_launch_tile<ELT, FORM, 128, 128, 2, 4, T, 2>(t, P, st);
         case 64: return mm_launch_tile<ELT, FORM, 64, 128, 2, 4, 16, 3>(t, P, st);
@@ -866,9 +933,10 @@ static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t s
 template <int ELT>
 static hipError_t mm_launch_back(const MmTile& t, const MmPlan& P, hipStream_t st) {
     constexpr int T = ELT == MM_BF16 || ELT == MM_E8 ? 32 : 16;
+    constexpr bool W8 = mm_big_waves(ELT) == 8;
     switch (P.bm) {
         case 256:
-            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, MM_NN, 256, 256, 4, 8, T, 2>(t, P, st);
+            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, MM_NN, 256, 256, W8 ? 4 : 2, W8 ? 8 : 4, T, 2>(t, P, st);
             else return hipErrorInvalidValue;
         case 128: return mm_launch_tile<ELT, MM_NN, 128, 256, 2, 8, T, 2>(t, P, st);
         default: return mm_launch_tile<ELT, MM_NN, 64, 256, 2, 4, T, 3>(t, P, st);

@@ -69,6 +69,14 @@ hipError_t ffn_dz_run(const void* dh, bool dh_bf16, const float* zg, const float
 // ---- activations (gq_activation of gq.h)
 enum Act { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 
+// 1 / (1 + e^-z) by the exponential and reciprocal instructions (an ulp each; the exponential's argument, rounded
+// once more, adds |z| 2^-24): a gate's epilogue evaluates one for two products of the whole contraction, and the
+// library's exponential and division took four times the instructions (8-bit gate of 4096 rows, 8192 -> 2048 packed:
+// 118 us, 114 so).
+__device__ __forceinline__ float logistic(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
+
 // act(z); *slope = act'(z).  Written so that neither tail cancels: 1 + tanh(u) = 2 / (1 + e^-2u), and
 // the normal distribution's lower tail by erfc.
 template <bool SLOPE>
@@ -80,11 +88,11 @@ __device__ __forceinline__ float act_of(float z, int act, float* slope) {
     }
     if (act == ACT_GELU_TANH) {
         const float k = 0.79788456080286536f, z2 = z * z;
-        const float s = 1.f / (1.f + expf(-2.f * k * z * (1.f + 0.044715f * z2)));
+        const float s = logistic(2.f * k * z * (1.f + 0.044715f * z2));
         if (SLOPE) *slope = s + 2.f * z * s * (1.f - s) * (k * (1.f + 0.134145f * z2));
         return z * s;
     }
-    const float s = 1.f / (1.f + expf(-z));
+    const float s = logistic(z);
     if (SLOPE) *slope = s * (1.f + z * (1.f - s));
     return z * s;
 }

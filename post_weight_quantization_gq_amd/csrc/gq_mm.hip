@@ -203,7 +203,7 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
         P.bm = 256;
         for (;; P.bm /= 2) {
             P.bn = P.bm;
-            P.waves = P.bm == 256 ? mm_big_waves(elt) : 4;
+            P.waves = P.bm == 256 ? 8 : 4;
             blocks = 2 * (int64_t)experts * ((d_out + P.bm - 1) / P.bm) * ((m + P.bn - 1) / P.bn);
             if (P.bm == 128 || blocks >= 192) break;
         }
@@ -216,7 +216,7 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
             blocks = rows * ((wcols + P.bn - 1) / P.bn);
             if (P.bm <= 64 || blocks >= (nn ? 48 : 192)) break;
         }
-        P.waves = P.bm == 256 ? mm_big_waves(elt) : (nn && P.bm == 128 ? 8 : 4);
+        P.waves = P.bm == 256 ? 8 : (nn && P.bm == 128 ? 8 : 4);
         units = (P.stages + P.unit - 1) / P.unit;
     }
     if (units < 1) units = 1;

@@ -38,12 +38,6 @@ struct MmTile {
                                   // [split][outs][experts][d_out][m]), or null
 };
 
-// Waves of a tile of 256 x 256.  Four of 128 x 128 read each value from LDS two thirds as often as eight of
-// 64 x 128 and suit the 8-bit products; the bfloat16 ones wait less with two waves to a SIMD.  4096 rows, 8192 (bfloat16:
-// 4096) -> 4096, us by eight and by four: powers of two 125 and 121, their gradient 131 and 109, float32
-// scales 196 and 170, bfloat16 gate 108 and 114, its dx 109 and 116, its dw 109 and 114.
-constexpr int mm_big_waves(int elt) { return elt == MM_BF16 ? 8 : 4; }
-
 constexpr int MM_FIRST = 2;       // groups of 16 rows that an expert's own streaming blocks take
 
 // A launch has fewer than 2^32 lanes.

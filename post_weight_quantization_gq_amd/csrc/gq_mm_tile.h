@@ -22,26 +22,36 @@ __device__ __forceinline__ int mm_tswz(int row) {
                    : (2 * (row & 3)) ^ (9 * ((row >> 2) & 1)) ^ ((row >> 4) & 1);
 }
 
-// tile_dma of SIZE bytes a lane.  Kernels with turned reads take it as inline assembly: the compiler
+// tile_dma.  Kernels with turned reads take it as inline assembly: the compiler
 // does not see then that it writes LDS, and would otherwise have every such read wait for all copies in flight (plain
 // reads it leaves alone; 4096 rows, gradient of 11008 -> 4096 in bfloat16: 869 us, 618 so).  It has no
 // outputs, and the kernels count its arrival themselves as they do the builtin's.  Five wait states lie between a
 // scalar written by the vector unit and its use.
-template <bool TURNED, int SIZE>
+template <bool TURNED>
 __device__ __forceinline__ void mm_dma(__amdgpu_buffer_rsrc_t r, void* dst, uint32_t voff, uint32_t soff) {
     if constexpr (TURNED) {
-        const uint32_t at = (uint32_t)(uintptr_t)(tile_lds_t)dst;
-        if constexpr (SIZE == 16)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                         :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voff), "s"(r), "s"(soff) : "m0", "memory");
-        else
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                         :: "s"(__builtin_amdgcn_readfirstlane(at)), "v"(voff), "s"(r), "s"(soff) : "m0", "memory");
-    } else if constexpr (SIZE == 16) {
-        tile_dma(r, (u32x4*)dst, voff, soff);
+        const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(tile_lds_t)dst);
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :: "s"(at), "v"(voff), "s"(r), "s"(soff) : "m0", "memory");
     } else {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (tile_lds_t)dst, 4, voff, soff, 0, 0);
+        tile_dma(r, (u32x4*)dst, voff, soff);
     }
+}
+
+// The first LANES lanes' copies of SIZE bytes each, the others idle: by the execution mask, in place of a branch that
+// would cut the loop in two (the compiler then moves products from one side to the other).  All lanes are
+// active before and after.
+template <int LANES, int SIZE>
+__device__ __forceinline__ void mm_dma_first(__amdgpu_buffer_rsrc_t r, void* dst, uint32_t voff) {
+    static_assert(LANES < 64 && (SIZE == 4 || SIZE == 16), "a part of a wave, words or four of them");
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(tile_lds_t)dst);
+    uint64_t all;
+    if constexpr (SIZE == 16)
+        asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, exec\n\ts_mov_b64 exec, %2\n\ts_nop 1\n\tbuffer_load_dwordx4 %3, %4, 0 offen lds\n\ts_mov_b64 exec, %0"
+                     : "=&s"(all) : "s"(at), "s"((uint64_t(1) << LANES) - 1), "v"(voff), "s"(r) : "m0", "memory");
+    else
+        asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, exec\n\ts_mov_b64 exec, %2\n\ts_nop 1\n\tbuffer_load_dword %3, %4, 0 offen lds\n\ts_mov_b64 exec, %0"
+                     : "=&s"(all) : "s"(at), "s"((uint64_t(1) << LANES) - 1), "v"(voff), "s"(r) : "m0", "memory");
 }
 
 template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
@@ -116,10 +126,15 @@ __device__ __forceinline__ i32x8 mm_pair(u32x4 a, u32x4 b) {
 // the products of one column fragment run, the next is read, and the loads of a later stage go out one
 // beside each product or two.  One barrier a stage, before its last part: by then every wave has read
 // all of the stage, so its slot is refilled from there on, and the last part's products run while the
-// next stage's rows and first columns are read.
+// next stage's rows and first columns are read.  Half of those loads go out with the last part, half with the next
+// stage's first one: all at once they hold the waves up (bfloat16 gate of 4096 x 4096 -> 2048: 112 us, 108 so).
+//
+// Tiles of 256 x 256 have eight waves of 64 x 128, two to a SIMD.  Four of 128 x 128 read each value from LDS two
+// thirds as often, but have nothing beside their waits and epilogues: 4096 rows, 8192 -> 4096 124 us, 121 by eight;
+// 2048 -> 4096 packed gate 47 and 39; with float32 scales, whose sums go through the vector unit, 153 and 118.
 // ---------------------------------------------------------------------------
 template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM == 256 && NW == 4 ? 1 : 8))) void k_mm_tile(MmTile p) {
+__global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
     typedef MmGeo<ELT, FORM, BM, BN, WM, NW, T, R> G;
     constexpr int ES = G::ES, KE = G::KE, FM = G::FM, FN = G::FN, V = G::V, CH = G::CH, NP = G::NP, TM = G::TM, TN = G::TN;
     constexpr bool XT = G::XT, WT = G::WT, SC = G::SC, GATE = FORM == MM_GATE;
@@ -217,12 +232,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             u32x4* const to = base + wave * XPW + i * 64;
             if constexpr (XT) {
                 const int64_t k0 = (int64_t)s * KE, left = k_rows - k0 < KE ? k_rows - k0 : KE;
-                mm_dma<WT, 16>(tile_rsrc(p.A[which] + (k_lo + k0) * p.a_row + t0 * ES, (int)left, p.a_row, on, (int)(t0 * ES)), to, xv[i], 0);
+                mm_dma<WT>(tile_rsrc(p.A[which] + (k_lo + k0) * p.a_row + t0 * ES, (int)left, p.a_row, on, (int)(t0 * ES)), to, xv[i], 0);
             } else {
                 const __amdgpu_buffer_rsrc_t xr = tile_rsrc(p.A[src] + t0 * p.a_row, rows, p.a_row, on);
                 uint32_t v = xv[i];
                 if constexpr (EDGE) v = sl < xe[i] ? v : 0xC0000000u;                 // past the row: zeros
-                mm_dma<WT, 16>(xr, to, v, (uint32_t)sl * 128u);
+                mm_dma<WT>(xr, to, v, (uint32_t)sl * 128u);
             }
         } else {
             i -= XI;
@@ -230,13 +245,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             if constexpr (WT) {
                 const int64_t k0 = (int64_t)sl * KE, all = FORM == MM_TN ? k_rows : p.d_out, left = all - k0 < KE ? all - k0 : KE;
                 const uint8_t* const from = p.W[src] + ((FORM == MM_TN ? k_lo : e_rows) + k0) * p.w_row + j0 * ES;
-                mm_dma<WT, 16>(tile_rsrc(from, (int)left, p.w_row, on, (int)(j0 * ES)), to, wv[i], 0);
+                mm_dma<WT>(tile_rsrc(from, (int)left, p.w_row, on, (int)(j0 * ES)), to, wv[i], 0);
             } else {
                 const int half = GATE ? ((wave * WPW + i * 64) / 128) & 1 : 0;       // 8 rows a copy
                 const __amdgpu_buffer_rsrc_t q = tile_rsrc(p.W[half] + (e_rows + j0) * p.w_row, wcols, p.w_row, on);
                 uint32_t v = wv[i];
                 if constexpr (EDGE) v = s < we[i] ? v : 0xC0000000u;
-                mm_dma<WT, 16>(q, to, v, (uint32_t)s * 128u);
+                mm_dma<WT>(q, to, v, (uint32_t)s * 128u);
             }
         }
     };
@@ -244,19 +259,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     uint8_t* const sc_lds = lds + R * G::STAGE * 16;
         constexpr int SW = SC ? (BM / 4 / NW > 0 ? BM / 4 / NW : 1) : 1;        // rows of a wave's copy
     static_assert(!SC || SW * NW * 4 == BM, "every wave copies scales");
-    auto scale_copy = [&](int span, int row, int count, bool on) {
+    auto scale_copy = [&](int span, int row, bool on) {
         if constexpr (SC) {
             const __amdgpu_buffer_rsrc_t z = tile_rsrc((const uint8_t*)p.AS + t0 * p.as_row, rows, p.as_row, on);
             uint8_t* const to = sc_lds + (span % 3) * G::SCB + row * G::SB;
             const uint32_t v = (uint32_t)((row + lane) * p.as_row) + (uint32_t)(G::SB * span);
-            if constexpr (mm_bytes(ELT)) {
-                if (lane < count) mm_dma<WT, 4>(z, to, v, 0);
-            } else {
-                if (lane < count) mm_dma<WT, 16>(z, to, v, 0);
-            }
+            mm_dma_first<SW, G::SB>(z, to, v);
         }
     };
-    auto issue_scales = [&](int s) { scale_copy(s / 4 + 1, (s % 4) * (BM / 4) + wave * SW, SW, s < s_hi); };
+    auto issue_scales = [&](int s) { scale_copy(s / 4 + 1, (s % 4) * (BM / 4) + wave * SW, s < s_hi); };
     auto issue = [&](int s) {
         issue_scales(s);
 #pragma unroll
@@ -264,7 +275,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     };
     if constexpr (SC) {                           // the first four stages' whole
 #pragma unroll
-        for (int q = 0; q < 4; ++q) scale_copy(s_lo / 4, q * (BM / 4) + wave * SW, SW, true);
+        for (int q = 0; q < 4; ++q) scale_copy(s_lo / 4, q * (BM / 4) + wave * SW, true);
     }
 
     // ---- the weight's scales: one for a wave's columns and a stage, 64 stages in a register
@@ -364,13 +375,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
     constexpr bool WIDE = mm_wide(ELT), FS = ELT == MM_FS || WIDE;
     static_assert(!FS || (T == 16 && ALL % RING == 0), "sums of a line need a place that is known");
     f32x4 sum[FS ? RING : 1];
-    float fac[2][FS ? FM : 1], old[2][FS ? FM : 1];
-    if constexpr (FS) {
-#pragma unroll
-        for (int k = 0; k < RING; ++k) sum[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < FM; ++q) fac[0][q] = fac[1][q] = 0.f;
-    }
+    float fac[2][FS ? FM : 1];
     uint32_t wbyte = 0u;                           // MM_E8: this lane's scale of the weight
     u32x4 xb[WIDE ? FM : 1][2 * CH], wb[2 * CH];   // WIDE: fragments in bfloat16
     auto take_scales = [&](int s) {                // of stage s, before its products
@@ -391,19 +396,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
                 const float v = mm_bytes(ELT) ? fp8_scale_value(bits) : __int_as_float(bits);
 #pragma unroll
                 for (int q = 0; q < FM; ++q) {
-                    old[h][q] = fac[h][q];
                     fac[h][q] = v * (mm_bytes(ELT) ? fp8_scale_value(__float_as_uint(sx[q])) : sx[q]);
                 }
             }
         }
     };
-    // adds the sum of product k of this stage, or (k < 0) of the last one
+    // adds the sum of product k (none for k < 0)
     auto add_sum = [&](auto index) {
-        if constexpr (FS) {
-            constexpr int k = decltype(index)::value, i = (k + ALL) % ALL, f = i / FM, q = i % FM, h = GATE ? f & 1 : 0;
-            const float by = k < 0 ? old[h][q] : fac[h][q];
+        constexpr int k = decltype(index)::value;
+        if constexpr (FS && k >= 0) {
+            constexpr int f = k / FM, q = k % FM, h = GATE ? f & 1 : 0;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[f][q][v] = __builtin_fmaf(sum[i % RING][v], by, acc[f][q][v]);
+            for (int v = 0; v < 4; ++v) acc[f][q][v] = __builtin_fmaf(sum[k % RING][v], fac[h][q], acc[f][q][v]);
         }
     };
     constexpr int KS = ELT == MM_BF16 ? CH : CH / 2;             // products of two fragments (WIDE: four, one after the other)
@@ -434,7 +438,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
         }
     };
 
-    constexpr int LOADS_ALL = XI + WI, LATE = ELT == MM_FS ? 0 : LOADS_ALL / 2, SOON = LOADS_ALL - LATE, PR = FM * KS;
+    constexpr int LOADS_ALL = XI + WI, LATE = LOADS_ALL / 2, SOON = LOADS_ALL - LATE, PR = FM * KS;
     // Column fragment f of stage s, beside its products: the next fragment's reads, of the loads l0 .. l1 - 1 of stage sl
     // one after every so many products, and with the last fragment the next stage's rows as each is done with.
     auto part = [&](auto fragment, int s, int sl, auto l0, auto l1) {
@@ -509,15 +513,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, BM =
             tile_barrier();                        // and this one's slot has been read by every wave
             issue_scales(s + R);
             part(std::integral_constant<int, FN - 1>{}, s, s + R, zero, soon);  // past the last stage: read and not used
+            // the stage's last sums, while the next one's rows are read
+            tile_each<LAG>([&](auto i) { add_sum(std::integral_constant<int, ALL - LAG + decltype(i)::value>{}); });
 #pragma unroll
             for (int q = 0; q < FM; ++q) read_sx(s + 1, q);
-        }
-        if constexpr (FS) {                        // the sums that are still on their way
-            if (!idle) {
-#pragma unroll
-                for (int q = 0; q < FM; ++q) old[0][q] = fac[0][q], old[1][q] = fac[1][q];
-                tile_each<LAG>([&](auto i) { add_sum(std::integral_constant<int, decltype(i)::value - LAG>{}); });
-            }
         }
     }
     tile_wait_vmcnt<0>();          // no load may land in the LDS later
@@ -914,7 +913,6 @@ template <int ELT, int FORM>
 static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t st) {
     constexpr bool GATE = FORM == MM_GATE;
     constexpr int T = ELT == MM_BF16 || ELT == MM_E8 ? 32 : 16;
-    constexpr bool W8 = mm_big_waves(ELT) == 8;
     if (P.stream) {
         if constexpr (GATE) return P.waves == 8 ? mm_launch_stream<ELT, true, 2, 8>(t, P, st) : mm_launch_stream<ELT, true, 2, 4>(t, P, st);
         else if (P.bn == 32) return P.waves == 8 ? mm_launch_stream<ELT, false, 2, 8>(t, P, st) : mm_launch_stream<ELT, false, 2, 4>(t, P, st);
@@ -922,7 +920,7 @@ static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t s
     }
     switch (P.bm) {
         case 256:
-            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, FORM, 256, 256, W8 ? 4 : 2, W8 ? 8 : 4, T, 2>(t, P, st);
+            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, FORM, 256, 256, 4, 8, T, 2>(t, P, st);
             else return hipErrorInvalidValue;                                        // (the plan takes none)
         case 128: return mm_launch_tile<ELT, FORM, 128, 128, 2, 4, T, 2>(t, P, st);
         case 64: return mm_launch_tile<ELT, FORM, 64, 128, 2, 4, 16, 3>(t, P, st);
@@ -933,10 +931,9 @@ static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t s
 template <int ELT>
 static hipError_t mm_launch_back(const MmTile& t, const MmPlan& P, hipStream_t st) {
     constexpr int T = ELT == MM_BF16 || ELT == MM_E8 ? 32 : 16;
-    constexpr bool W8 = mm_big_waves(ELT) == 8;
     switch (P.bm) {
         case 256:
-            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, MM_NN, 256, 256, W8 ? 4 : 2, W8 ? 8 : 4, T, 2>(t, P, st);
+            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, MM_NN, 256, 256, 4, 8, T, 2>(t, P, st);
             else return hipErrorInvalidValue;
         case 128: return mm_launch_tile<ELT, MM_NN, 128, 256, 2, 8, T, 2>(t, P, st);
         default: return mm_launch_tile<ELT, MM_NN, 64, 256, 2, 4, T, 3>(t, P, st);

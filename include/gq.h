@@ -537,7 +537,7 @@ gq_status fp8_gemm_dx(const uint8_t* GQ, const void* GS, int64_t n, int64_t d_ou
  * (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
  *
  * fp8_ffn_gate: x, G and U packed; h (h_dt) rounded once from float32, sums as fp8_gemm's by h_dt (packed: as
- * for bfloat16).  fp8_ffn_gate_packed: h in
+ * for float32, since a code on the other side of a border is off by a sixteenth of its value).  fp8_ffn_gate_packed: h in
  * packed rows HQ, HS (scales of type s_dt, as fp8_quantize makes them from h in float32), which
  * fp8_gemm takes with the down projection's weight.
  */

@@ -1098,7 +1098,7 @@ static size_t mm_size(gq::MmForm form, gq::MmElt elt, int64_t n, int64_t d_in, i
     return gq::mm_workspace(form, elt, n, d_in, d_out, experts, packed);
 }
 
-// float32 outputs have products whose sums are float32 throughout
+// float32 outputs, and packed ones, have products whose sums are float32 throughout
 static gq::MmElt fp8_elt(gq_scale s, gq_dtype y) {
     if (y == GQ_F32) return s == GQ_SCALE_F32 ? gq::MM_FSW : gq::MM_E8W;
     return s == GQ_SCALE_F32 ? gq::MM_FS : gq::MM_E8;
@@ -1117,7 +1117,7 @@ size_t fp8_ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_
 }
 
 size_t fp8_ffn_gate_packed_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts, gq_scale s_dt) {
-    return scale_ok(s_dt) ? mm_size(gq::MM_GATE, fp8_elt(s_dt, GQ_BF16), n, d_in, d_ff, experts, true) : 0;
+    return scale_ok(s_dt) ? mm_size(gq::MM_GATE, fp8_elt(s_dt, GQ_F32), n, d_in, d_ff, experts, true) : 0;
 }
 
 size_t ffn_gate_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts) {
@@ -1220,7 +1220,7 @@ gq_status fp8_ffn_gate_packed(const uint8_t* XQ, const void* XS, int64_t n, int6
                               const int64_t* offsets, uint8_t* HQ, void* HS, void* ws,
                               size_t ws_bytes, void* stream) {
     if (n > 0 && (!HQ || !HS)) return fail(GQ_EINVAL, "null output");
-    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt, GQ_BF16), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets};
+    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt, GQ_F32), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets};
     c.hq = HQ;
     c.hs = HS;
     return mm_product(c, s_dt, GQ_F32, act, ws, ws_bytes, stream, "fp8_ffn_gate_packed");

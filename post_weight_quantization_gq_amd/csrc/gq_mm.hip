@@ -211,12 +211,12 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
     } else {
         P.bm = per > 128 && !mm_wide(elt) ? 256 : (per > 64 ? 128 : (per > 32 || nn ? 64 : 32));
         for (;; P.bm /= 2) {
-            P.bn = P.bm == 256 || nn ? 256 : 128;
+            P.bn = P.bm == 256 || nn || (P.bm == 128 && mm_wide(elt)) ? 256 : 128;
             const int64_t rows = experts > 1 ? n / P.bm + live : (n + P.bm - 1) / P.bm;
             blocks = rows * ((wcols + P.bn - 1) / P.bn);
             if (P.bm <= 64 || blocks >= (nn ? 48 : 192)) break;
         }
-        P.waves = P.bm == 256 ? 8 : (nn && P.bm == 128 ? 8 : 4);
+        P.waves = P.bm >= 128 && P.bn == 256 ? 8 : (P.bm == 32 && mm_wide(elt) ? 2 : 4);
         units = (P.stages + P.unit - 1) / P.unit;
     }
     if (units < 1) units = 1;
@@ -227,7 +227,7 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
         const int64_t each = (units + s - 1) / s;                                 // no part without work
         P.split = (int)((units + each - 1) / each);
     }
-    P.join = P.split > 1 || (packed && P.bm != 256);
+    P.join = P.split > 1 || (packed && P.bn != 256);
     const int64_t outputs = tn ? 2 * (int64_t)experts * d_out * m : (gate ? 2 : 1) * n * m;
     P.part_bytes = P.join ? mm_al256((size_t)P.split * outputs * 4) : 0;
     return P;
@@ -313,7 +313,7 @@ hipError_t mm_run(const MmCall& c, void* ws, hipStream_t st) {
     if (e != hipSuccess || !P.join) return e;
     if (packed) {
         const int64_t blocks = (c.n * 16 * fp8_blocks(m) + 255) / 256;
-        const auto k = c.elt == MM_FS ? k_mm_join_pack<true> : k_mm_join_pack<false>;
+        const auto k = mm_bytes(c.elt) ? k_mm_join_pack<false> : k_mm_join_pack<true>;
         hipLaunchKernelGGL(k, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, t.part, P.split, c.n, m, c.offsets, c.experts, c.act,
                            (u32x2*)c.hq, c.hs);
         GQ_LAUNCH_CHECK();

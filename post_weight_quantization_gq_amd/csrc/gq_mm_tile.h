@@ -68,7 +68,7 @@ struct MmGeo {
     static constexpr size_t IN = (size_t)R * STAGE * 16 + 3 * SCB;
     static constexpr int HC = FORM == MM_GATE ? TN / 2 : TN;            // output columns of a wave
     static constexpr int PITCH = (FORM == MM_GATE ? 2 : 1) * HC * 4 + 16;  // bytes of a row on its way out
-    static constexpr size_t OUT = (size_t)NW * T * PITCH + (FORM == MM_GATE ? 8 * BM : 0);
+    static constexpr size_t OUT = (size_t)NW * T * PITCH + (FORM == MM_GATE ? 4 * WN * BM : 0);
     static constexpr size_t BYTES = IN > OUT ? IN : OUT;
     static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
     static_assert(FN % 2 == 0 && TM % T == 0 && TN % T == 0, "fragments go in pairs");
@@ -100,16 +100,24 @@ __device__ __forceinline__ MmTurned mm_place_turned(const MmTile& p, int bm, int
     return r;
 }
 
+// 8 codes (words i and i + 1 of q) times the power of two that the exponent of `scale` is, as bfloat16: exact (but
+// below bfloat16's smallest number, 2^-133, and over its largest)
+__device__ __forceinline__ u32x4 mm_widen8(u32x4 q, int i, float scale) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    u32x4 to;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i + k], scale, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i + k], scale, true);
+        to[2 * k] = __builtin_bit_cast(uint32_t, a);
+        to[2 * k + 1] = __builtin_bit_cast(uint32_t, b);
+    }
+    return to;
+}
+
 // 16 codes as bfloat16, 8 and 8: exact
 __device__ __forceinline__ void mm_widen(u32x4 q, u32x4& lo, u32x4& hi) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], 1.f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], 1.f, true);
-        u32x4& to = i < 2 ? lo : hi;
-        to[2 * (i % 2)] = __builtin_bit_cast(uint32_t, a);
-        to[2 * (i % 2) + 1] = __builtin_bit_cast(uint32_t, b);
-    }
+    lo = mm_widen8(q, 0, 1.f);
+    hi = mm_widen8(q, 2, 1.f);
 }
 
 template <int ELT, int T>
@@ -369,17 +377,18 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
         else to[j] = *(const u32x4*)(lds + base + lw[j] + f * T * 128);
     };
 
-    // ---- products.  All 8-bit types but MM_E8: a line's sum, of its 16 x 16 products alone, times its scales is
+    // ---- products.  MM_FS, MM_FSW: a line's sum, of its 16 x 16 products alone, times its scales is
     // added LAG products later, so that the matrix cores' result has arrived and their next products run beside.
     constexpr int LAG = 3, RING = LAG + 1, ALL = FN * FM;
-    constexpr bool WIDE = mm_wide(ELT), FS = ELT == MM_FS || WIDE;
+    constexpr bool E8W = ELT == MM_E8W, WIDE = mm_wide(ELT), FS = ELT == MM_FS || ELT == MM_FSW;
     static_assert(!FS || (T == 16 && ALL % RING == 0), "sums of a line need a place that is known");
     f32x4 sum[FS ? RING : 1];
     float fac[2][FS ? FM : 1];
-    uint32_t wbyte = 0u;                           // MM_E8: this lane's scale of the weight
-    u32x4 xb[WIDE ? FM : 1][2 * CH], wb[2 * CH];   // WIDE: fragments in bfloat16
+    uint32_t wbyte = 0u;                           // MM_E8, MM_E8W: this lane's scale of the weight
+    u32x4 xb[WIDE ? FM : 1][2 * CH], wb[E8W ? 2 : 2 * CH];       // WIDE: fragments in bfloat16
+    static_assert(!E8W || T == 32, "scales of a lane's own rows and columns");
     auto take_scales = [&](int s) {                // of stage s, before its products
-        if constexpr (ELT == MM_E8) {
+        if constexpr (mm_bytes(ELT)) {
             const int at = (s - s_lo) & 63;
             wbyte = (uint32_t)__builtin_amdgcn_readlane(__float_as_int(wsc[0]), at);
             // (32 x 32 fragments have 16 rows of each weight; 16 x 16 ones take turns)
@@ -392,11 +401,10 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             const int at = (s - s_lo) & 63;
 #pragma unroll
             for (int h = 0; h < (GATE ? 2 : 1); ++h) {
-                const int bits = __builtin_amdgcn_readlane(__float_as_int(wsc[h]), at);
-                const float v = mm_bytes(ELT) ? fp8_scale_value(bits) : __int_as_float(bits);
+                const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wsc[h]), at));
 #pragma unroll
                 for (int q = 0; q < FM; ++q) {
-                    fac[h][q] = v * (mm_bytes(ELT) ? fp8_scale_value(__float_as_uint(sx[q])) : sx[q]);
+                    fac[h][q] = v * sx[q];
                 }
             }
         }
@@ -410,10 +418,24 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             for (int v = 0; v < 4; ++v) acc[f][q][v] = __builtin_fmaf(sum[k % RING][v], fac[h][q], acc[f][q][v]);
         }
     };
-    constexpr int KS = ELT == MM_BF16 ? CH : CH / 2;             // products of two fragments (WIDE: four, one after the other)
+    // products of two fragments (MM_FSW: four, one after the other); MM_E8W goes through the columns' eights first and
+    // converts each once, the others through the rows
+    constexpr int KS = E8W ? 2 * CH : (ELT == MM_BF16 ? CH : CH / 2);
+    // MM_E8W: eight j of the columns, and with the first fragment of the rows, as the products before it run
+    auto widen = [&](auto fragment, const u32x4 (&wf)[CH], auto eight) {
+        constexpr int j = decltype(eight)::value;
+        wb[j % 2] = mm_widen8(wf[j / 2], 2 * (j % 2), mx_scale(wbyte));
+        if constexpr (decltype(fragment)::value == 0) {
+#pragma unroll
+            for (int q = 0; q < FM; ++q) xb[q][j] = mm_widen8(x[q][j / 2], 2 * (j % 2), mx_scale(__float_as_uint(sx[q])));
+        }
+    };
     auto product = [&](auto fragment, const u32x4 (&wf)[CH], auto index) {
-        constexpr int f = decltype(fragment)::value, i = decltype(index)::value, q = i / KS, j = i % KS;
-        if constexpr (ELT == MM_BF16) {
+        constexpr int f = decltype(fragment)::value, i = decltype(index)::value, q = E8W ? i % FM : i / KS, j = E8W ? i / FM : i % KS;
+        if constexpr (E8W) {
+            acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(wb[j % 2]), as_bf16x8(xb[q][j]), acc[f][q], 0, 0, 0);
+            if constexpr (q == 0 && j + 1 < 2 * CH) widen(fragment, wf, std::integral_constant<int, j + 1>{});
+        } else if constexpr (ELT == MM_BF16) {
             if constexpr (T == 32) acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(wf[j]), as_bf16x8(x[q][j]), acc[f][q], 0, 0, 0);
             else acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wf[j]), as_bf16x8(x[q][j]), acc[f][q], 0, 0, 0);
         } else {
@@ -445,7 +467,9 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
         constexpr int f = decltype(fragment)::value, L0 = decltype(l0)::value, LN = decltype(l1)::value - L0;
         constexpr bool last = f == FN - 1;
         constexpr int RP = (2 * CH + PR - 1) / PR;               // reads beside a product
-        if constexpr (WIDE) {
+        if constexpr (E8W) {
+            widen(fragment, w[f % 2], std::integral_constant<int, 0>{});
+        } else if constexpr (WIDE) {
             if constexpr (f == 0) {
 #pragma unroll
                 for (int q = 0; q < FM; ++q)
@@ -461,7 +485,10 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             for (int k = RP * i; k < RP * (i + 1); ++k)
                 if (k < CH) read_w(last ? s + 1 : s, last ? 0 : f + 1, w[(f + 1) % 2], k);
             product(fragment, w[f % 2], index);
-            if constexpr (last && i % KS == KS - 1) {
+            if constexpr (last && E8W) {               // (its rows have been converted)
+#pragma unroll
+                for (int k = i * FM * CH / PR; k < (i + 1) * FM * CH / PR; ++k) read_x(s + 1, k / CH, k % CH);
+            } else if constexpr (last && i % KS == KS - 1) {
 #pragma unroll
                 for (int j = 0; j < CH; ++j) read_x(s + 1, i / KS, j);
             }
@@ -546,7 +573,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
         const int64_t all_rows = p.n * p.m;
         float* const z0 = p.part ? p.part + 2 * blockIdx.y * all_rows : p.z[0];
         float* const z1 = p.part ? z0 + all_rows : p.z[1];
-        constexpr bool PACKS = BN == 256 && SC && !mm_wide(ELT);
+        constexpr bool PACKS = BN == 256 && mm_wide(ELT);        // (a block of 128 columns)
         const bool packs = PACKS && p.hq && !p.part;
         float* const tops = (float*)(lds + NW * T * G::PITCH);   // [WN][BM]
         constexpr int LANES = HC / 8;                            // a lane takes 8 columns of a row
@@ -607,7 +634,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                     for (int k = 0; k < 8; ++k) h[k / 4][k % 4] = act_of<false>(a[k / 4][k % 4], ACT_GELU_TANH, nullptr) * b[k / 4][k % 4];
                 }
                 if (packs) {
-                    // a row's largest magnitude over this wave's 64 columns
+                    // a row's largest magnitude over this wave's columns
                     uint32_t top = 0u;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -638,12 +665,17 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             }
             if constexpr (PACKS) {
                 if (!packs) continue;
-                __syncthreads();                                 // both waves of a block of 128 columns
+                __syncthreads();                                 // all waves of a row
 #pragma unroll 1
                 for (int i = lane; i < T * LANES; i += 64) {
                     const int row = i / LANES, c8 = 8 * (i % LANES);
-                    const uint32_t a = __float_as_uint(tops[row0 + row]), b = __float_as_uint(tops[BM + row0 + row]);
-                    const uint32_t s = fp8_scale_byte(a > b ? a : b);
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int n = 0; n < G::WN; ++n) {
+                        const uint32_t a = __float_as_uint(tops[n * BM + row0 + row]);
+                        top = top > a ? top : a;
+                    }
+                    const uint32_t s = fp8_scale_byte(top);
                     const float f = fp8_scale_inverse(s);
                     const uint8_t* const from = own + row * G::PITCH + c8 * 4;
                     const f32x4 u = *(const f32x4*)from, v = *(const f32x4*)(from + 16);
@@ -911,33 +943,31 @@ static hipError_t mm_launch_stream(const MmTile& t, const MmPlan& P, hipStream_t
 // NT and GATE
 template <int ELT, int FORM>
 static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t st) {
-    constexpr bool GATE = FORM == MM_GATE;
-    constexpr int T = ELT == MM_BF16 || ELT == MM_E8 ? 32 : 16;
+    constexpr bool GATE = FORM == MM_GATE, WIDE = mm_wide(ELT);
+    constexpr int T = mm_side(ELT), TS = ELT == MM_E8W ? 32 : 16;
     if (P.stream) {
         if constexpr (GATE) return P.waves == 8 ? mm_launch_stream<ELT, true, 2, 8>(t, P, st) : mm_launch_stream<ELT, true, 2, 4>(t, P, st);
         else if (P.bn == 32) return P.waves == 8 ? mm_launch_stream<ELT, false, 2, 8>(t, P, st) : mm_launch_stream<ELT, false, 2, 4>(t, P, st);
         else return P.waves == 8 ? mm_launch_stream<ELT, false, 1, 8>(t, P, st) : mm_launch_stream<ELT, false, 1, 4>(t, P, st);
     }
-    switch (P.bm) {
-        case 256:
-            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, FORM, 256, 256, 4, 8, T, 2>(t, P, st);
-            else return hipErrorInvalidValue;                                        // (the plan takes none)
-        case 128: return mm_launch_tile<ELT, FORM, 128, 128, 2, 4, T, 2>(t, P, st);
-        case 64: return mm_launch_tile<ELT, FORM, 64, 128, 2, 4, 16, 3>(t, P, st);
-        default: return mm_launch_tile<ELT, FORM, 32, 128, 1, 4, 16, 3>(t, P, st);
+    if constexpr (WIDE) {
+        if (P.bm == 128) return mm_launch_tile<ELT, FORM, 128, 256, 2, 8, T, 3>(t, P, st);
+    } else {
+        if (P.bm == 256) return mm_launch_tile<ELT, FORM, 256, 256, 4, 8, T, 2>(t, P, st);
+        if (P.bm == 128) return mm_launch_tile<ELT, FORM, 128, 128, 2, 4, T, 2>(t, P, st);
     }
+    if (P.bm == 64) return mm_launch_tile<ELT, FORM, 64, 128, 2, 4, TS, 3>(t, P, st);
+    return mm_launch_tile<ELT, FORM, 32, 128, 1, WIDE ? 2 : 4, TS, 3>(t, P, st);
 }
 
 template <int ELT>
 static hipError_t mm_launch_back(const MmTile& t, const MmPlan& P, hipStream_t st) {
-    constexpr int T = ELT == MM_BF16 || ELT == MM_E8 ? 32 : 16;
-    switch (P.bm) {
-        case 256:
-            if constexpr (!mm_wide(ELT)) return mm_launch_tile<ELT, MM_NN, 256, 256, 4, 8, T, 2>(t, P, st);
-            else return hipErrorInvalidValue;
-        case 128: return mm_launch_tile<ELT, MM_NN, 128, 256, 2, 8, T, 2>(t, P, st);
-        default: return mm_launch_tile<ELT, MM_NN, 64, 256, 2, 4, T, 3>(t, P, st);
+    constexpr int T = mm_side(ELT);
+    if constexpr (!mm_wide(ELT)) {
+        if (P.bm == 256) return mm_launch_tile<ELT, MM_NN, 256, 256, 4, 8, T, 2>(t, P, st);
     }
+    if (P.bm == 128) return mm_launch_tile<ELT, MM_NN, 128, 256, 2, 8, T, mm_wide(ELT) ? 3 : 2>(t, P, st);
+    return mm_launch_tile<ELT, MM_NN, 64, 256, 2, 4, T, 3>(t, P, st);
 }
 
 }  // namespace gq

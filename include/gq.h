@@ -585,6 +585,18 @@ gq_status ffn_gate_dw(const void* dzg, const void* dzu, int64_t n, int64_t d_ff,
                       gq_dtype dw_dt, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * The last three in one call, with dzg and dzu in ws: dx, dG and dU from dh and what ffn_gate saved (the same
+ * bits; any of the three can be NULL and is left out, with it what it alone needs of x, G and U).  Rows of no expert
+ * of dh, zg and zu are not used.
+ */
+size_t ffn_gate_backward_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts);
+gq_status ffn_gate_backward(const void* dh, gq_dtype dh_dt, const void* x, int64_t n, int64_t d_in,
+                            const void* G, const void* U, int64_t d_ff, gq_activation act,
+                            int32_t experts, const int64_t* offsets, const float* zg, const float* zu,
+                            void* dx, gq_dtype dx_dt, void* dG, void* dU, gq_dtype dw_dt, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
  * GANQ-style alternation.  The GANQ summary page ("Approach") solves each row by
  * alternating a closed-form least-squares codebook update with an assignment of
  * the indices by Cholesky / back-substitution.  Here: F'_g = L L^T (float64

@@ -45,7 +45,7 @@ EXPORTS = (
     "fp8_gemm_dx", "fp8_ffn_gate_workspace_size", "fp8_ffn_gate",
     "fp8_ffn_gate_packed_workspace_size", "fp8_ffn_gate_packed", "ffn_gate_workspace_size", "ffn_gate",
     "ffn_gate_dz", "ffn_gate_dx_workspace_size", "ffn_gate_dx", "ffn_gate_dw_workspace_size",
-    "ffn_gate_dw",
+    "ffn_gate_dw", "ffn_gate_backward_workspace_size", "ffn_gate_backward",
     "gq_timing_enable", "gq_timing_read", "gq_timing_read_mxfp4", "gq_timing_read_product",
     "gq_stage_name",
 )
@@ -150,6 +150,9 @@ _SIGS = {
     "ffn_gate_dw_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
     "ffn_gate_dw": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _vp,
                                    _sz, _vp]),
+    "ffn_gate_backward_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
+    "ffn_gate_backward": (ctypes.c_int, [_vp, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i32, _vp, _vp,
+                                         _vp, _vp, _i32, _vp, _vp, _i32, _vp, _sz, _vp]),
     "gq_timing_enable": (None, [ctypes.c_int]),
     "gq_timing_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gq_timing_read_mxfp4": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
@@ -1147,6 +1150,10 @@ def ffn_gate_dw_workspace_size(n, d_in, d_ff, experts=1) -> int:
     return int(library().ffn_gate_dw_workspace_size(n, d_in, d_ff, experts))
 
 
+def ffn_gate_backward_workspace_size(n, d_in, d_ff, experts=1) -> int:
+    return int(library().ffn_gate_backward_workspace_size(n, d_in, d_ff, experts))
+
+
 def fp8_gemm(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,
              stream=None) -> torch.Tensor:
     """y [n][d_out] = x W^T for x packed by fp8_quantize (XQ, XS) and W by fp8_quantize_weight
@@ -1248,7 +1255,8 @@ def _ffn_weights(G, U, offsets, index):
     return (1, *G.shape) if offsets is None else tuple(G.shape)
 
 
-def _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream):
+def _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream, fill=True):
+    """fill: saved products have zeros in the rows of no expert."""
     lib = _lib or library()
     act = _act_id(act)
     if x.dim() != 2:
@@ -1268,7 +1276,10 @@ def _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream):
         new = x.new_empty if offsets is None else x.new_zeros
         if y is None:
             y = new((n, d_ff), dtype=out_dtype)
-        zg, zu = (new((n, d_ff), dtype=torch.float32) for _ in range(2)) if save else (None, None)
+        zg = zu = None
+        if save:
+            keep = new if fill else x.new_empty
+            zg, zu = keep((n, d_ff), dtype=torch.float32), keep((n, d_ff), dtype=torch.float32)
         keep, wp, wn = _mm_scratch(x, ws, lib.ffn_gate_workspace_size, (n, d_in, d_ff, experts))
         status = lib.ffn_gate(x.data_ptr(), n, d_in, G.data_ptr(), U.data_ptr(), d_ff, act, experts, op,
                               y.data_ptr(), _MX_DTYPES[y.dtype], zg.data_ptr() if save else None,
@@ -1283,7 +1294,7 @@ class _FfnGate(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, G, U, act, offsets, out_dtype, ws):
-        h, zg, zu = _ffn_forward(x, G, U, act, offsets, None, out_dtype, True, ws, None)
+        h, zg, zu = _ffn_forward(x, G, U, act, offsets, None, out_dtype, True, ws, None, fill=False)
         ctx.save_for_backward(x, G, U, zg, zu, offsets)
         ctx.act = act
         return h
@@ -1292,14 +1303,9 @@ class _FfnGate(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh):
         x, G, U, zg, zu, offsets = ctx.saved_tensors
-        dzg, dzu = ffn_gate_dz(dh.contiguous(), zg, zu, act=ctx.act)
-        need = ctx.needs_input_grad
-        dx = ffn_gate_dx(dzg, dzu, G, U, offsets=offsets) if need[0] else None
-        dG = dU = None
-        if need[1] or need[2]:
-            dG, dU = ffn_gate_dw(dzg, dzu, x, experts=None if offsets is None else G.shape[0],
-                                 offsets=offsets, which=(need[1], need[2]))
-        return dx, dG, dU, None, None, None, None
+        grads = ffn_gate_backward(dh.contiguous(), x, G, U, zg, zu, act=ctx.act, offsets=offsets,
+                                  which=ctx.needs_input_grad[:3])
+        return (*grads, None, None, None, None)
 
 
 def ffn_gate(x, G, U, act: str = "silu", offsets=None, y=None, out_dtype=None, save: bool = False,
@@ -1310,8 +1316,8 @@ def ffn_gate(x, G, U, act: str = "silu", offsets=None, y=None, out_dtype=None, s
     offsets[e + 1] - 1 take weights e of G and U [experts][d_ff][d_in], and the other rows of a given y keep their
     values (of a new one: zeros).  out_dtype: float32 or bfloat16, x's unless given.
     With save: (h, zg, zu), zg = x G^T and zu = x U^T in float32, as ffn_gate_dz takes them.
-    Where x, G or U requires a gradient, autograd gets it by ffn_gate_dz, ffn_gate_dx and ffn_gate_dw (and
-    neither y nor save can be given)."""
+    Where x, G or U requires a gradient, autograd gets it by ffn_gate_backward (and neither y nor save can be
+    given)."""
     if torch.is_grad_enabled() and (x.requires_grad or G.requires_grad or U.requires_grad):
         if y is not None or save:
             raise GQError(GQ_EINVAL, "x, G or U requires a gradient, which a given y or saved products would "
@@ -1419,6 +1425,58 @@ def ffn_gate_dw(dzg, dzu, x, experts=None, offsets=None, which=(True, True), dG=
         status = lib.ffn_gate_dw(dzg.data_ptr(), dzu.data_ptr(), n, d_ff, x.data_ptr(), d_in, experts or 1, op,
                                  out[0].data_ptr() if which[0] else None,
                                  out[1].data_ptr() if which[1] else None, _MX_DTYPES[dt], wp, wn, st)
+    if status:
+        _check(status)
+    return tuple(out)
+
+
+def ffn_gate_backward(dh, x, G, U, zg, zu, act: str = "silu", offsets=None, which=(True, True, True), dx=None,
+                      dG=None, dU=None, ws=None, stream=None):
+    """(dx, dG, dU), the gradients of ffn_gate's x, G and U from that of h (float32 or bfloat16) and
+    the products that ffn_gate saved: ffn_gate_dz, ffn_gate_dx and ffn_gate_dw in one call.  which: the
+    ones wanted (None for the others).  New outputs are bfloat16; given ones can be float32, dG and dU of one
+    type.  Rows of no expert: zeros in a new dx, a given one's values in it."""
+    lib = _lib or library()
+    act = _act_id(act)
+    if x.dim() != 2:
+        raise GQError(GQ_ESHAPE, "x must be [n][d_in]")
+    n, index = x.shape[0], x.get_device()
+    experts, d_ff, d_in = _ffn_weights(G, U, offsets, index)
+    _mx_shape(x, (n, d_in), "x")
+    _mx_shape(dh, (n, d_ff), "dh")
+    _mx_tensor(x, "x", index, _BF16)
+    _mx_tensor(dh, "dh", index)
+    for t, name in ((zg, "zg"), (zu, "zu")):
+        _mx_shape(t, (n, d_ff), name)
+        _mx_tensor(t, name, index, _F32)
+    op = _mm_offsets(offsets, experts, index)
+    out, shapes = [dx, dG, dU], ((n, d_in), G.shape, G.shape)
+    for i, name in enumerate(("dx", "dG", "dU")):
+        if out[i] is not None:
+            if not which[i]:
+                raise GQError(GQ_EINVAL, f"{name} is given, but not asked for")
+            _mx_shape(out[i], shapes[i], name)
+            _mx_tensor(out[i], name, index)
+    if not any(which):
+        return None, None, None
+    dw = torch.bfloat16 if dG is None and dU is None else (dG if dG is not None else dU).dtype
+    if dG is not None and dU is not None and dG.dtype != dU.dtype:
+        raise GQError(GQ_EDTYPE, f"dG is {dG.dtype}, dU {dU.dtype}")
+    if ws is not None and ws is not False:
+        _mx_tensor(ws, "ws", index, _U8)
+    where, st = _place(x, stream)
+    with where:
+        if which[0] and dx is None:
+            out[0] = (x.new_empty if offsets is None else x.new_zeros)((n, d_in))
+        for i in (1, 2):
+            if which[i] and out[i] is None:
+                out[i] = x.new_empty(G.shape, dtype=dw)
+        keep, wp, wn = _mm_scratch(x, ws, lib.ffn_gate_backward_workspace_size, (n, d_in, d_ff, experts))
+        at = [None if t is None else t.data_ptr() for t in out]
+        status = lib.ffn_gate_backward(dh.data_ptr(), _MX_DTYPES[dh.dtype], x.data_ptr(), n, d_in, G.data_ptr(),
+                                       U.data_ptr(), d_ff, act, experts, op, zg.data_ptr(), zu.data_ptr(), at[0],
+                                       _MX_DTYPES[out[0].dtype] if which[0] else GQ_BF16, at[1], at[2],
+                                       _MX_DTYPES[dw], wp, wn, st)
     if status:
         _check(status)
     return tuple(out)

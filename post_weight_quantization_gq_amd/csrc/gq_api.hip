@@ -1194,7 +1194,7 @@ gq_status fp8_gemm(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_in, c
                    const void* S, gq_scale s_dt, int64_t d_out, int32_t experts,
                    const int64_t* offsets, void* y, gq_dtype y_dt, void* ws, size_t ws_bytes,
                    void* stream) {
-    gq::MmCall c{gq::MM_NT, fp8_elt(s_dt, y_dt), {XQ, nullptr}, XS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {y, nullptr}};
+    gq::MmCall c{gq::MM_NT, fp8_elt(s_dt, y_dt), {XQ, nullptr}, false, XS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {y, nullptr}};
     return mm_product(c, s_dt, y_dt, 0, ws, ws_bytes, stream, "fp8_gemm");
 }
 
@@ -1202,7 +1202,7 @@ gq_status fp8_gemm_dx(const uint8_t* GQ, const void* GS, int64_t n, int64_t d_ou
                       const void* S, gq_scale s_dt, int64_t d_in, int32_t experts,
                       const int64_t* offsets, void* dx, gq_dtype dx_dt, void* ws, size_t ws_bytes,
                       void* stream) {
-    gq::MmCall c{gq::MM_NN, fp8_elt(s_dt, dx_dt), {GQ, nullptr}, GS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {dx, nullptr}};
+    gq::MmCall c{gq::MM_NN, fp8_elt(s_dt, dx_dt), {GQ, nullptr}, false, GS, n, d_in, d_out, {Q, nullptr}, {S, nullptr}, experts, offsets, {dx, nullptr}};
     return mm_product(c, s_dt, dx_dt, 0, ws, ws_bytes, stream, "fp8_gemm_dx");
 }
 
@@ -1210,7 +1210,7 @@ gq_status fp8_ffn_gate(const uint8_t* XQ, const void* XS, int64_t n, int64_t d_i
                        const void* GS, const uint8_t* UQ, const void* US, gq_scale s_dt, int64_t d_ff,
                        gq_activation act, int32_t experts, const int64_t* offsets, void* h,
                        gq_dtype h_dt, void* ws, size_t ws_bytes, void* stream) {
-    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt, h_dt), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets, {h, nullptr}};
+    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt, h_dt), {XQ, nullptr}, false, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets, {h, nullptr}};
     return mm_product(c, s_dt, h_dt, act, ws, ws_bytes, stream, "fp8_ffn_gate");
 }
 
@@ -1220,7 +1220,7 @@ gq_status fp8_ffn_gate_packed(const uint8_t* XQ, const void* XS, int64_t n, int6
                               const int64_t* offsets, uint8_t* HQ, void* HS, void* ws,
                               size_t ws_bytes, void* stream) {
     if (n > 0 && (!HQ || !HS)) return fail(GQ_EINVAL, "null output");
-    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt, GQ_F32), {XQ, nullptr}, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets};
+    gq::MmCall c{gq::MM_GATE, fp8_elt(s_dt, GQ_F32), {XQ, nullptr}, false, XS, n, d_in, d_ff, {GQ, UQ}, {GS, US}, experts, offsets};
     c.hq = HQ;
     c.hs = HS;
     return mm_product(c, s_dt, GQ_F32, act, ws, ws_bytes, stream, "fp8_ffn_gate_packed");
@@ -1229,7 +1229,7 @@ gq_status fp8_ffn_gate_packed(const uint8_t* XQ, const void* XS, int64_t n, int6
 gq_status ffn_gate(const void* x, int64_t n, int64_t d_in, const void* G, const void* U, int64_t d_ff,
                    gq_activation act, int32_t experts, const int64_t* offsets, void* h,
                    gq_dtype h_dt, float* zg, float* zu, void* ws, size_t ws_bytes, void* stream) {
-    gq::MmCall c{gq::MM_GATE, gq::MM_BF16, {x, nullptr}, nullptr, n, d_in, d_ff, {G, U}, {nullptr, nullptr}, experts, offsets, {h, nullptr}};
+    gq::MmCall c{gq::MM_GATE, gq::MM_BF16, {x, nullptr}, false, nullptr, n, d_in, d_ff, {G, U}, {nullptr, nullptr}, experts, offsets, {h, nullptr}};
     c.z[0] = zg;
     c.z[1] = zu;
     return mm_product(c, GQ_SCALE_E8M0, h_dt, act, ws, ws_bytes, stream, "ffn_gate");
@@ -1248,22 +1248,88 @@ gq_status ffn_gate_dz(const void* dh, gq_dtype dh_dt, const float* zg, const flo
     const size_t n = (size_t)count;
     const MmSpan spans[] = {{dzg, 2 * n}, {dzu, 2 * n}, {dh, n * (dh_dt == GQ_BF16 ? 2 : 4)}, {zg, 4 * n}, {zu, 4 * n}};
     if (!mm_apart(spans, 5, 2)) return fail(GQ_EINVAL, "dzg and dzu must not overlap each other or the inputs");
-    const hipError_t e = gq::ffn_dz_run(dh, dh_dt == GQ_BF16, zg, zu, count, act, (uint16_t*)dzg, (uint16_t*)dzu, (hipStream_t)stream);
+    const hipError_t e = gq::ffn_dz_run(dh, dh_dt == GQ_BF16, zg, zu, 1, count, count, act, (uint16_t*)dzg, (uint16_t*)dzu, (hipStream_t)stream);
     return e == hipSuccess ? GQ_OK : hip_fail(e, "ffn_gate_dz");
 }
 
 gq_status ffn_gate_dx(const void* dzg, const void* dzu, int64_t n, int64_t d_ff, const void* G,
                       const void* U, int64_t d_in, int32_t experts, const int64_t* offsets, void* dx,
                       gq_dtype dx_dt, void* ws, size_t ws_bytes, void* stream) {
-    gq::MmCall c{gq::MM_NN, gq::MM_BF16, {dzg, dzu}, nullptr, n, d_in, d_ff, {G, U}, {nullptr, nullptr}, experts, offsets, {dx, nullptr}};
+    gq::MmCall c{gq::MM_NN, gq::MM_BF16, {dzg, dzu}, false, nullptr, n, d_in, d_ff, {G, U}, {nullptr, nullptr}, experts, offsets, {dx, nullptr}};
     return mm_product(c, GQ_SCALE_E8M0, dx_dt, 0, ws, ws_bytes, stream, "ffn_gate_dx");
 }
 
 gq_status ffn_gate_dw(const void* dzg, const void* dzu, int64_t n, int64_t d_ff, const void* x,
                       int64_t d_in, int32_t experts, const int64_t* offsets, void* dG, void* dU,
                       gq_dtype dw_dt, void* ws, size_t ws_bytes, void* stream) {
-    gq::MmCall c{gq::MM_TN, gq::MM_BF16, {dzg, dzu}, nullptr, n, d_in, d_ff, {x, nullptr}, {nullptr, nullptr}, experts, offsets, {dG, dU}};
+    gq::MmCall c{gq::MM_TN, gq::MM_BF16, {dzg, dzu}, false, nullptr, n, d_in, d_ff, {x, nullptr}, {nullptr, nullptr}, experts, offsets, {dG, dU}};
     return mm_product(c, GQ_SCALE_E8M0, dw_dt, 0, ws, ws_bytes, stream, "ffn_gate_dw");
+}
+
+// The two gradients of zg and zu with their rows at multiples of 8 values, then the larger scratch of the products.
+static size_t ffn_dz_bytes(int64_t n, int64_t d_ff) { return al256((size_t)n * ((d_ff + 7) / 8 * 8) * 2); }
+
+static size_t ffn_backward_need(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts) {
+    const size_t a = gq::mm_workspace(gq::MM_NN, gq::MM_BF16, n, d_in, d_ff, experts, false, true);
+    const size_t b = gq::mm_workspace(gq::MM_TN, gq::MM_BF16, n, d_in, d_ff, experts, false, true);
+    return 2 * ffn_dz_bytes(n, d_ff) + (a > b ? a : b);
+}
+
+size_t ffn_gate_backward_workspace_size(int64_t n, int64_t d_in, int64_t d_ff, int32_t experts) {
+    return mx_sizes_ok(n, d_in, d_ff, experts) ? ffn_backward_need(n, d_in, d_ff, experts) : 0;
+}
+
+gq_status ffn_gate_backward(const void* dh, gq_dtype dh_dt, const void* x, int64_t n, int64_t d_in, const void* G,
+                            const void* U, int64_t d_ff, gq_activation act, int32_t experts, const int64_t* offsets,
+                            const float* zg, const float* zu, void* dx, gq_dtype dx_dt, void* dG, void* dU,
+                            gq_dtype dw_dt, void* ws, size_t ws_bytes, void* stream) {
+    gq_status rc = mx_sizes_check(dh_dt, dx_dt, n, d_in, d_ff, experts);
+    if (rc != GQ_OK) return rc;
+    if (!dtype_ok(dw_dt)) return fail(GQ_EDTYPE, "unsupported dtype");
+    if ((int)act < gq::ACT_SILU || (int)act > gq::ACT_GELU_TANH) return fail(GQ_EINVAL, "unknown activation %d", (int)act);
+    if (experts > 1 && !offsets) return fail(GQ_EINVAL, "several experts need offsets");
+    if ((uintptr_t)offsets & 7u) return fail(GQ_EINVAL, "offsets must be 8-byte aligned");
+    if (!dx && !dG && !dU) return fail(GQ_EINVAL, "null dx, dG and dU: nothing to compute");
+    const bool dw = dG || dU;
+    if (n == 0 && !dw) return GQ_OK;
+    if (n > 0 && (!dh || !zg || !zu || (dw && !x))) return fail(GQ_EINVAL, "null dh, x, zg or zu");
+    if (dx && n > 0 && (!G || !U)) return fail(GQ_EINVAL, "null G or U");
+    const uintptr_t al = d_in % 8 == 0 ? 15u : 1u;
+    if (!mx_el_al(dh, dh_dt) || (((uintptr_t)zg | (uintptr_t)zu) & 3u) || (((uintptr_t)x | (uintptr_t)G | (uintptr_t)U) & al) ||
+        !mx_el_al(dx, dx_dt) || !mx_el_al(dG, dw_dt) || !mx_el_al(dU, dw_dt) || ((uintptr_t)ws & 255u))
+        return fail(GQ_EINVAL, "x, G and U must be 16-byte aligned (element-aligned where d_in is no multiple of 8), all else "
+                    "element-aligned and ws 256-byte");
+    if (!gq::mm_fits(gq::MM_NN, gq::MM_BF16, n, d_in, d_ff, experts, offsets != nullptr, false) ||
+        !gq::mm_fits(gq::MM_TN, gq::MM_BF16, n, d_in, d_ff, experts, offsets != nullptr, false))
+        return fail(GQ_ENOTIMPL, "n=%lld d_in=%lld d_ff=%lld experts=%d: more tiles than a launch takes", (long long)n,
+                    (long long)d_in, (long long)d_ff, experts);
+    const size_t need = ffn_backward_need(n, d_in, d_ff, experts), rows = (size_t)n, w_len = (size_t)experts * d_ff * d_in;
+    const size_t f4 = rows * d_ff * 4, de = dw_dt == GQ_BF16 ? 2 : 4;
+    const MmSpan spans[] = {{dx, dx ? rows * d_in * (dx_dt == GQ_BF16 ? 2 : 4) : 0}, {dG, dG ? w_len * de : 0}, {dU, dU ? w_len * de : 0},
+                            {ws, ws ? need : 0}, {dh, rows * d_ff * (dh_dt == GQ_BF16 ? 2 : 4)}, {zg, f4}, {zu, f4},
+                            {x, x ? rows * d_in * 2 : 0}, {G, G ? w_len * 2 : 0}, {U, U ? w_len * 2 : 0},
+                            {offsets, offsets ? (size_t)(experts + 1) * 8 : 0}};
+    if (!mm_apart(spans, sizeof spans / sizeof spans[0], 4))
+        return fail(GQ_EINVAL, "outputs and ws must not overlap each other or the inputs");
+    hipStream_t st = (hipStream_t)stream;
+    Scratch s;
+    if ((rc = s.acquire(ws, ws_bytes, need, st)) != GQ_OK) return rc;
+    uint16_t* const dzg = (uint16_t*)s.ptr;
+    uint16_t* const dzu = (uint16_t*)((char*)s.ptr + ffn_dz_bytes(n, d_ff));
+    void* const rest = (char*)s.ptr + 2 * ffn_dz_bytes(n, d_ff);
+    hipError_t e = hipSuccess;
+    if (n > 0) e = gq::ffn_dz_run(dh, dh_dt == GQ_BF16, zg, zu, n, d_ff, (d_ff + 7) / 8 * 8, act, dzg, dzu, st);
+    if (e == hipSuccess && dx && n > 0) {
+        gq::MmCall c{gq::MM_NN, gq::MM_BF16, {dzg, dzu}, true, nullptr, n, d_in, d_ff, {G, U}, {nullptr, nullptr}, experts, offsets, {dx, nullptr}};
+        c.y_bf16 = dx_dt == GQ_BF16;
+        e = gq::mm_run(c, rest, st);
+    }
+    if (e == hipSuccess && dw) {
+        gq::MmCall c{gq::MM_TN, gq::MM_BF16, {dzg, dzu}, true, nullptr, n, d_in, d_ff, {x, nullptr}, {nullptr, nullptr}, experts, offsets, {dG, dU}};
+        c.y_bf16 = dw_dt == GQ_BF16;
+        e = gq::mm_run(c, rest, st);
+    }
+    return e == hipSuccess ? GQ_OK : hip_fail(e, "ffn_gate_backward");
 }
 
 size_t ganq_workspace_size(int64_t d_out, int64_t d_in, int32_t groups, int32_t bits,

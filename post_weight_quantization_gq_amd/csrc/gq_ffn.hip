@@ -10,16 +10,18 @@
 
 namespace gq {
 
+// A lane takes 8 values of a row.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_ffn_dz(const void* __restrict__ dh, const float* __restrict__ zg,
-                                               const float* __restrict__ zu, int64_t count, int act,
+                                               const float* __restrict__ zu, int64_t rows, int64_t f, int64_t pitch, int act,
                                                uint16_t* __restrict__ dzg, uint16_t* __restrict__ dzu) {
-    const int64_t stride = (int64_t)gridDim.x * 256 * 8;
-    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < count; i += stride) {
+    const int64_t ppr = (f + 7) / 8, pieces = rows * ppr, stride = (int64_t)gridDim.x * 256;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < pieces; t += stride) {
+        const int64_t r = mx_div(t, ppr), i = (t - r * ppr) * 8, at = r * pitch + i;
         float d[8], g[8], u[8];
-        mx_load8<BF16>(dh, 0, i, count, d);
-        mx_load8<false>(zg, 0, i, count, g);
-        mx_load8<false>(zu, 0, i, count, u);
+        mx_load8<BF16>(dh, r * f, i, f, d);
+        mx_load8<false>(zg, r * f, i, f, g);
+        mx_load8<false>(zu, r * f, i, f, u);
         uint32_t a[4], b[4];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
@@ -28,27 +30,27 @@ __global__ __launch_bounds__(256) void k_ffn_dz(const void* __restrict__ dh, con
             a[k / 2] = pack_bf16x2(d[k] * u[k] * s0, d[k + 1] * u[k + 1] * s1);
             b[k / 2] = pack_bf16x2(d[k] * v0, d[k + 1] * v1);
         }
-        if (i + 8 <= count) {
-            *(u32x4_any*)(dzg + i) = u32x4{a[0], a[1], a[2], a[3]};
-            *(u32x4_any*)(dzu + i) = u32x4{b[0], b[1], b[2], b[3]};
+        if (i + 8 <= pitch) {
+            *(u32x4_any*)(dzg + at) = u32x4{a[0], a[1], a[2], a[3]};
+            *(u32x4_any*)(dzu + at) = u32x4{b[0], b[1], b[2], b[3]};
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (i + k < count) {
-                    dzg[i + k] = (uint16_t)(a[k / 2] >> (16 * (k & 1)));
-                    dzu[i + k] = (uint16_t)(b[k / 2] >> (16 * (k & 1)));
+                if (i + k < f) {
+                    dzg[at + k] = (uint16_t)(a[k / 2] >> (16 * (k & 1)));
+                    dzu[at + k] = (uint16_t)(b[k / 2] >> (16 * (k & 1)));
                 }
         }
     }
 }
 
-hipError_t ffn_dz_run(const void* dh, bool dh_bf16, const float* zg, const float* zu, int64_t count, int act,
-                      uint16_t* dzg, uint16_t* dzu, hipStream_t st) {
+hipError_t ffn_dz_run(const void* dh, bool dh_bf16, const float* zg, const float* zu, int64_t rows, int64_t f, int64_t pitch,
+                      int act, uint16_t* dzg, uint16_t* dzu, hipStream_t st) {
     StageTimer tm(ST_FFN_BACK, st);
-    const int64_t blocks = (count + 2047) / 2048;
+    const int64_t blocks = (rows * ((f + 7) / 8) + 255) / 256;
     const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
-    if (dh_bf16) hipLaunchKernelGGL(k_ffn_dz<true>, grid, dim3(256), 0, st, dh, zg, zu, count, act, dzg, dzu);
-    else hipLaunchKernelGGL(k_ffn_dz<false>, grid, dim3(256), 0, st, dh, zg, zu, count, act, dzg, dzu);
+    if (dh_bf16) hipLaunchKernelGGL(k_ffn_dz<true>, grid, dim3(256), 0, st, dh, zg, zu, rows, f, pitch, act, dzg, dzu);
+    else hipLaunchKernelGGL(k_ffn_dz<false>, grid, dim3(256), 0, st, dh, zg, zu, rows, f, pitch, act, dzg, dzu);
     GQ_LAUNCH_CHECK();
     return hipSuccess;
 }

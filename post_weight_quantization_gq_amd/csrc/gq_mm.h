@@ -48,6 +48,7 @@ struct MmCall {
     MmForm form;
     MmElt elt;
     const void* a[2];             // rows of activations, n of them (MM_GATE: one; MM_NN: as many as weights)
+    bool a_padded;                // bfloat16 rows that start at multiples of 8 values, zeros between
     const void* as;               // their scales
     int64_t n, d_in, d_out;
     const void* w[2];             // weights [experts][d_out][d_in] (MM_TN: x [n][d_in])
@@ -61,13 +62,14 @@ struct MmCall {
     void* hs;
     int act;
 };
-size_t mm_workspace(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed);
+size_t mm_workspace(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed, bool a_padded = false);
 bool mm_fits(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets, bool packed);
 hipError_t mm_run(const MmCall& c, void* ws, hipStream_t st);
 
-// dzg = dh zu act'(zg), dzu = dh act(zg), `count` values each
-hipError_t ffn_dz_run(const void* dh, bool dh_bf16, const float* zg, const float* zu, int64_t count, int act,
-                      uint16_t* dzg, uint16_t* dzu, hipStream_t st);
+// dzg = dh zu act'(zg), dzu = dh act(zg), `rows` rows of f values; those of dzg and dzu start `pitch` values
+// (f, or f rounded up to a multiple of 8: zeros between) apart
+hipError_t ffn_dz_run(const void* dh, bool dh_bf16, const float* zg, const float* zu, int64_t rows, int64_t f, int64_t pitch,
+                      int act, uint16_t* dzg, uint16_t* dzu, hipStream_t st);
 
 // ---- activations (gq_activation of gq.h)
 enum Act { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };

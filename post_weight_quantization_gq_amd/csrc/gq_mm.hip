@@ -167,24 +167,24 @@ struct MmPads {
     size_t a, w;
     int as, ws;                   // how many
 };
-static MmPads mm_pads(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts) {
+static MmPads mm_pads(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool a_padded) {
     MmPads p{};
     if (elt != MM_BF16) return p;
     const int64_t ak = form == MM_GATE ? d_in : d_out;
     p.as = form == MM_GATE ? 1 : 2;
     p.ws = form == MM_TN ? 1 : 2;
-    if (ak % 8) p.a = mm_al256((size_t)n * mm_al8(ak) * 2);
+    if (ak % 8 && !a_padded) p.a = mm_al256((size_t)n * mm_al8(ak) * 2);
     if (d_in % 8) p.w = mm_al256((size_t)(form == MM_TN ? n : experts * d_out) * mm_al8(d_in) * 2);
     return p;
 }
 
-static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed) {
+static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed, bool a_padded = false) {
     MmPlan P{};
     const bool tn = form == MM_TN, gate = form == MM_GATE, nn = form == MM_NN, fp8 = elt != MM_BF16;
     const int64_t k = tn ? n : (nn ? d_out : d_in), m = tn || nn ? d_in : d_out, ke = fp8 ? 128 : 64;
     const int64_t one = (k + ke - 1) / ke, per = (n + experts - 1) / experts;
     const int64_t live = experts > 1 ? (experts < n ? experts : n) : 1;           // experts with rows, at most
-    const MmPads pads = mm_pads(form, elt, n, d_in, d_out, experts);
+    const MmPads pads = mm_pads(form, elt, n, d_in, d_out, experts, a_padded);
     P.pad_bytes = pads.a * pads.as + pads.w * pads.ws;
     P.stages = (int)(nn && !fp8 ? 2 * one : one);
     P.unit = fp8 ? 4 : 1;
@@ -196,7 +196,9 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
         P.bm = 16;
         P.bn = gate || live * ((m + 31) / 32) >= 256 ? 32 : 16;
         const int64_t pieces = (one + 1) / 2;
-        P.waves = pieces >= 8 ? 8 : 4;
+        // eight waves of two fragments fill a compute unit's LDS: worth it from four pieces a wave on (16 rows,
+        // 8-bit gate 4096 -> 11008: 29.2 us, 25.8 by four waves; 1 row in bfloat16 38.9 and 42.4)
+        P.waves = pieces >= (P.bn == 32 ? 32 : 8) ? 8 : 4;
         blocks = live * ((wcols + P.bn - 1) / P.bn);
         units = pieces / P.waves;
     } else if (tn) {
@@ -233,8 +235,8 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
     return P;
 }
 
-size_t mm_workspace(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed) {
-    const MmPlan P = mm_plan(form, elt, n, d_in, d_out, experts, packed);
+size_t mm_workspace(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed, bool a_padded) {
+    const MmPlan P = mm_plan(form, elt, n, d_in, d_out, experts, packed, a_padded);
     return P.pad_bytes + P.part_bytes;
 }
 
@@ -247,8 +249,8 @@ bool mm_fits(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int
 hipError_t mm_run(const MmCall& c, void* ws, hipStream_t st) {
     StageTimer tm(c.form == MM_GATE ? ST_FFN_GATE : (c.elt == MM_BF16 ? ST_FFN_BACK : ST_FP8_GEMM), st);
     const bool packed = c.hq != nullptr, fp8 = c.elt != MM_BF16, tn = c.form == MM_TN, nn = c.form == MM_NN;
-    const MmPlan P = mm_plan(c.form, c.elt, c.n, c.d_in, c.d_out, c.experts, packed);
-    const MmPads pads = mm_pads(c.form, c.elt, c.n, c.d_in, c.d_out, c.experts);
+    const MmPlan P = mm_plan(c.form, c.elt, c.n, c.d_in, c.d_out, c.experts, packed, c.a_padded);
+    const MmPads pads = mm_pads(c.form, c.elt, c.n, c.d_in, c.d_out, c.experts, c.a_padded);
     const int64_t ak = nn || tn ? c.d_out : c.d_in, m = nn || tn ? c.d_in : c.d_out;
     char* at = (char*)ws;
     // rows of k values, copied to a multiple of 8 where they are none

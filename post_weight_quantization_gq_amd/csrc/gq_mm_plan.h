@@ -38,10 +38,6 @@ struct MmTile {
                                   // [split][outs][experts][d_out][m]), or null
 };
 
-// Rows and columns of a large tile's products: with float32 scales each line's sum is taken out of the matrix
-// cores, and a 16 x 16 one takes a quarter of the registers.
-constexpr int mm_side(int elt) { return elt == MM_FS || elt == MM_FSW ? 16 : 32; }
-
 constexpr int MM_FIRST = 2;       // groups of 16 rows that an expert's own streaming blocks take
 
 // A launch has fewer than 2^32 lanes.

@@ -54,13 +54,12 @@ __device__ __forceinline__ void mm_dma_first(__amdgpu_buffer_rsrc_t r, void* dst
                      : "=&s"(all) : "s"(at), "s"((uint64_t(1) << LANES) - 1), "v"(voff), "s"(r) : "m0", "memory");
 }
 
-template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
+template <int ELT, int FORM, int BM, int BN, int WM, int NW, int R>
 struct MmGeo {
     static constexpr int ES = ELT == MM_BF16 ? 2 : 1, KE = 128 / ES;    // bytes of a value, values of a stage
     static constexpr bool XT = FORM == MM_TN, WT = FORM == MM_NN || FORM == MM_TN;
     static constexpr int WN = NW / WM, TM = BM / WM, TN = BN / WN;      // waves, and a wave's tile
-    static constexpr int FM = TM / T, FN = TN / T, V = T * T / 64;      // its fragments, an accumulator
-    static constexpr int NP = 64 / T, CH = 8 / NP;                      // lanes a row, chunks a lane has of its line
+    static constexpr int FM = TM / 16, FN = TN / 16;                    // its fragments
     static constexpr int X = BM * 8, W = BN * 8, STAGE = X + W;         // 16-byte slots
     static constexpr bool SC = ELT != MM_BF16;
     static constexpr int SB = mm_bytes(ELT) ? 4 : 16;                   // bytes of four stages' scales of a row
@@ -68,10 +67,10 @@ struct MmGeo {
     static constexpr size_t IN = (size_t)R * STAGE * 16 + 3 * SCB;
     static constexpr int HC = FORM == MM_GATE ? TN / 2 : TN;            // output columns of a wave
     static constexpr int PITCH = (FORM == MM_GATE ? 2 : 1) * HC * 4 + 16;  // bytes of a row on its way out
-    static constexpr size_t OUT = (size_t)NW * T * PITCH + (FORM == MM_GATE ? 4 * WN * BM : 0);
+    static constexpr size_t OUT = (size_t)NW * 16 * PITCH + (FORM == MM_GATE ? 4 * WN * BM : 0);
     static constexpr size_t BYTES = IN > OUT ? IN : OUT;
     static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
-    static_assert(FN % 2 == 0 && TM % T == 0 && TN % T == 0, "fragments go in pairs");
+    static_assert(FN % 2 == 0 && TM % 16 == 0 && TN % 32 == 0, "fragments go in pairs");
 };
 
 // Which tile a block of MM_TN has: weight gradient z / E of expert z % E.
@@ -120,11 +119,6 @@ __device__ __forceinline__ void mm_widen(u32x4 q, u32x4& lo, u32x4& hi) {
     hi = mm_widen8(q, 2, 1.f);
 }
 
-template <int ELT, int T>
-struct MmAcc;
-template <int ELT> struct MmAcc<ELT, 32> { typedef f32x16 Type; };
-template <int ELT> struct MmAcc<ELT, 16> { typedef f32x4 Type; };
-
 __device__ __forceinline__ i32x8 mm_pair(u32x4 a, u32x4 b) {
     return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
@@ -137,20 +131,24 @@ __device__ __forceinline__ i32x8 mm_pair(u32x4 a, u32x4 b) {
 // next stage's rows and first columns are read.  Half of those loads go out with the last part, half with the next
 // stage's first one: all at once they hold the waves up (bfloat16 gate of 4096 x 4096 -> 2048: 112 us, 108 so).
 //
+// The products are the 16 x 16 ones.  On random data power holds the clock down, and for the same work they take less of
+// it than the 32 x 32 ones: loops of either alone reach 2.08 and 1.80 PFLOP/s in bfloat16, 4.2 and 3.8 in 8 bits
+// (gate of 4096 rows, 4096 -> 2048: 104 us, 111 by 32 x 32; dx 106 and 115).
+//
 // Tiles of 256 x 256 have eight waves of 64 x 128, two to a SIMD.  Four of 128 x 128 read each value from LDS two
 // thirds as often, but have nothing beside their waits and epilogues: 4096 rows, 8192 -> 4096 124 us, 121 by eight;
 // 2048 -> 4096 packed gate 47 and 39; with float32 scales, whose sums go through the vector unit, 153 and 118.
 // ---------------------------------------------------------------------------
-template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
+template <int ELT, int FORM, int BM, int BN, int WM, int NW, int R>
 __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
-    typedef MmGeo<ELT, FORM, BM, BN, WM, NW, T, R> G;
-    constexpr int ES = G::ES, KE = G::KE, FM = G::FM, FN = G::FN, V = G::V, CH = G::CH, NP = G::NP, TM = G::TM, TN = G::TN;
+    typedef MmGeo<ELT, FORM, BM, BN, WM, NW, R> G;
+    constexpr int ES = G::ES, KE = G::KE, FM = G::FM, FN = G::FN, TM = G::TM, TN = G::TN;
     constexpr bool XT = G::XT, WT = G::WT, SC = G::SC, GATE = FORM == MM_GATE;
     constexpr int BC = GATE ? BN / 2 : BN;                       // output columns of a tile
     extern __shared__ u32x4 mm_lds[];
     uint8_t* const lds = (uint8_t*)mm_lds;
 
-    const int tid = threadIdx.x, lane = tid & 63, r = lane & (T - 1), g = lane / T;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave % WM, wn = wave / WM;
     const int ncol = (int)((p.m + BC - 1) / BC);
     int e, rows, col, which = 0, stages = p.stages;
@@ -304,38 +302,35 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             }
         }
     };
-    // ---- fragments.  Chunk j of a lane is chunk NP j + g of the line.
-    typedef typename MmAcc<ELT, T>::Type Acc;
-    Acc acc[FN][FM];
+    // ---- fragments.  A lane has two chunks of its line, 4 j + g.
+    constexpr int CH = 2;
+    f32x4 acc[FN][FM];
 #pragma unroll
     for (int f = 0; f < FN; ++f)
 #pragma unroll
-        for (int q = 0; q < FM; ++q)
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[f][q][v] = 0.f;
+        for (int q = 0; q < FM; ++q) acc[f][q] = f32x4{0.f, 0.f, 0.f, 0.f};
     constexpr int RPC = 16 / ES;                   // values of the contraction in a chunk
     constexpr int RPR = RPC / 2;                   // and in a turned read
     constexpr int LPR = 16 / RPR;                  // lanes that read one row of it
     // where a turned operand's column fragment starts: row g of chunks, row and part of a block
     auto turned = [&](int column, int pitch) {
-        const int l = lane & 15, row = g * RPC + l / LPR, byte = (l % LPR) * 8;
-        const int c = (column + (T == 32 ? 16 * (r >> 4) : 0)) * ES / 16 + byte / 16;
+        const int row = g * RPC + r / LPR, byte = (r % LPR) * 8, c = column * ES / 16 + byte / 16;
         return row * pitch + 16 * (c ^ mm_tswz<ES>(row)) + byte % 16;
     };
     int lx[XT ? FM : CH], lw[WT ? FN : CH];
     if constexpr (XT) {
 #pragma unroll
-        for (int q = 0; q < FM; ++q) lx[q] = turned(wm * TM + T * q, BM * ES);
+        for (int q = 0; q < FM; ++q) lx[q] = turned(wm * TM + 16 * q, BM * ES);
     } else {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) lx[j] = (wm * TM + r) * 128 + 16 * ((NP * j + g) ^ mm_swz(r));
+        for (int j = 0; j < CH; ++j) lx[j] = (wm * TM + r) * 128 + 16 * ((4 * j + g) ^ mm_swz(r));
     }
     if constexpr (WT) {
 #pragma unroll
-        for (int f = 0; f < FN; ++f) lw[f] = turned(wn * TN + T * f, BN * ES);
+        for (int f = 0; f < FN; ++f) lw[f] = turned(wn * TN + 16 * f, BN * ES);
     } else {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) lw[j] = (wn * TN + r) * 128 + 16 * ((NP * j + g) ^ mm_swz(r));
+        for (int j = 0; j < CH; ++j) lw[j] = (wn * TN + r) * 128 + 16 * ((4 * j + g) ^ mm_swz(r));
     }
     // chunk `chunk` of a lane's: two blocks of RPR rows
     auto turned_read = [&](int at, int pitch) {
@@ -361,42 +356,36 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
     float sx[FM];                                  // scales of the rows (MM_E8, MM_E8W: the byte)
     auto read_x = [&](int s, int q, int j) {
         const int base = (s % R) * G::STAGE * 16;
-        if constexpr (XT) x[q][j] = turned_read(base + lx[q] + j * NP * RPC * BM * ES, BM * ES);
-        else x[q][j] = *(const u32x4*)(lds + base + lx[j] + q * T * 128);
+        if constexpr (XT) x[q][j] = turned_read(base + lx[q] + j * 4 * RPC * BM * ES, BM * ES);
+        else x[q][j] = *(const u32x4*)(lds + base + lx[j] + q * 16 * 128);
     };
     auto read_sx = [&](int s, int q) {
         if constexpr (SC) {
-            const int at = R * G::STAGE * 16 + ((s / 4) % 3) * G::SCB + (wm * TM + T * q + r) * G::SB + (s % 4) * (G::SB / 4);
+            const int at = R * G::STAGE * 16 + ((s / 4) % 3) * G::SCB + (wm * TM + 16 * q + r) * G::SB + (s % 4) * (G::SB / 4);
             if constexpr (mm_bytes(ELT)) sx[q] = __uint_as_float((uint32_t)lds[at]);
             else sx[q] = *(const float*)(lds + at);
         }
     };
     auto read_w = [&](int s, int f, u32x4 (&to)[CH], int j) {
         const int base = (s % R) * G::STAGE * 16 + G::X * 16;
-        if constexpr (WT) to[j] = turned_read(base + lw[f] + j * NP * RPC * BN * ES, BN * ES);
-        else to[j] = *(const u32x4*)(lds + base + lw[j] + f * T * 128);
+        if constexpr (WT) to[j] = turned_read(base + lw[f] + j * 4 * RPC * BN * ES, BN * ES);
+        else to[j] = *(const u32x4*)(lds + base + lw[j] + f * 16 * 128);
     };
 
     // ---- products.  MM_FS, MM_FSW: a line's sum, of its 16 x 16 products alone, times its scales is
     // added LAG products later, so that the matrix cores' result has arrived and their next products run beside.
     constexpr int LAG = 3, RING = LAG + 1, ALL = FN * FM;
     constexpr bool E8W = ELT == MM_E8W, WIDE = mm_wide(ELT), FS = ELT == MM_FS || ELT == MM_FSW;
-    static_assert(!FS || (T == 16 && ALL % RING == 0), "sums of a line need a place that is known");
+    static_assert(!FS || ALL % RING == 0, "sums of a line need a place that is known");
     f32x4 sum[FS ? RING : 1];
     float fac[2][FS ? FM : 1];
-    uint32_t wbyte = 0u;                           // MM_E8, MM_E8W: this lane's scale of the weight
+    uint32_t wbyte = 0u;                           // MM_E8, MM_E8W: the weight's scale (MM_GATE: both, whose fragments take turns)
     u32x4 xb[WIDE ? FM : 1][2 * CH], wb[E8W ? 2 : 2 * CH];       // WIDE: fragments in bfloat16
-    static_assert(!E8W || T == 32, "scales of a lane's own rows and columns");
     auto take_scales = [&](int s) {                // of stage s, before its products
         if constexpr (mm_bytes(ELT)) {
             const int at = (s - s_lo) & 63;
             wbyte = (uint32_t)__builtin_amdgcn_readlane(__float_as_int(wsc[0]), at);
-            // (32 x 32 fragments have 16 rows of each weight; 16 x 16 ones take turns)
-            if constexpr (GATE) {
-                const uint32_t up = (uint32_t)__builtin_amdgcn_readlane(__float_as_int(wsc[1]), at);
-                if constexpr (T == 32) wbyte = r < 16 ? wbyte : up;
-                else wbyte |= up << 8;
-            }
+            if constexpr (GATE) wbyte |= (uint32_t)__builtin_amdgcn_readlane(__float_as_int(wsc[1]), at) << 8;
         } else if constexpr (FS) {
             const int at = (s - s_lo) & 63;
 #pragma unroll
@@ -424,27 +413,26 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
     // MM_E8W: eight j of the columns, and with the first fragment of the rows, as the products before it run
     auto widen = [&](auto fragment, const u32x4 (&wf)[CH], auto eight) {
         constexpr int j = decltype(eight)::value;
-        wb[j % 2] = mm_widen8(wf[j / 2], 2 * (j % 2), mx_scale(wbyte));
+        constexpr int up = GATE ? 8 * (decltype(fragment)::value & 1) : 0;
+        wb[j % 2] = mm_widen8(wf[j / 2], 2 * (j % 2), mx_scale((wbyte >> up) & 255u));
         if constexpr (decltype(fragment)::value == 0) {
 #pragma unroll
             for (int q = 0; q < FM; ++q) xb[q][j] = mm_widen8(x[q][j / 2], 2 * (j % 2), mx_scale(__float_as_uint(sx[q])));
         }
     };
     auto product = [&](auto fragment, const u32x4 (&wf)[CH], auto index) {
-        constexpr int f = decltype(fragment)::value, i = decltype(index)::value, q = E8W ? i % FM : i / KS, j = E8W ? i / FM : i % KS;
+        constexpr int f = decltype(fragment)::value, i = decltype(index)::value, q = i % FM, j = i / FM;
         if constexpr (E8W) {
-            acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(wb[j % 2]), as_bf16x8(xb[q][j]), acc[f][q], 0, 0, 0);
+            acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wb[j % 2]), as_bf16x8(xb[q][j]), acc[f][q], 0, 0, 0);
             if constexpr (q == 0 && j + 1 < 2 * CH) widen(fragment, wf, std::integral_constant<int, j + 1>{});
         } else if constexpr (ELT == MM_BF16) {
-            if constexpr (T == 32) acc[f][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(wf[j]), as_bf16x8(x[q][j]), acc[f][q], 0, 0, 0);
-            else acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wf[j]), as_bf16x8(x[q][j]), acc[f][q], 0, 0, 0);
+            acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wf[j]), as_bf16x8(x[q][j]), acc[f][q], 0, 0, 0);
         } else {
             const i32x8 a = mm_pair(wf[2 * j], wf[2 * j + 1]), b = mm_pair(x[q][2 * j], x[q][2 * j + 1]);
             (void)a, (void)b;
             if constexpr (ELT == MM_E8) {
                 const int sw = (int)wbyte, sr = __float_as_int(sx[q]);
-                if constexpr (T == 32) acc[f][q] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[f][q], 0, 0, 0, sw, 0, sr);
-                else acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[f][q], 0, 0, GATE ? f & 1 : 0, sw, 0, sr);
+                acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[f][q], 0, 0, GATE ? f & 1 : 0, sw, 0, sr);
             } else if constexpr (WIDE) {
                 constexpr int k = f * FM + q;
                 f32x4 d{0.f, 0.f, 0.f, 0.f};
@@ -488,9 +476,10 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
             if constexpr (last && E8W) {               // (its rows have been converted)
 #pragma unroll
                 for (int k = i * FM * CH / PR; k < (i + 1) * FM * CH / PR; ++k) read_x(s + 1, k / CH, k % CH);
-            } else if constexpr (last && i % KS == KS - 1) {
+            } else if constexpr (last) {               // each where its last product has been
+                constexpr int q = i % FM, j = i / FM;
 #pragma unroll
-                for (int j = 0; j < CH; ++j) read_x(s + 1, i / KS, j);
+                for (int k = j * CH / KS; k < (j + 1) * CH / KS; ++k) read_x(s + 1, q, k);
             }
 #pragma unroll
             for (int l = i * LN / PR; l < (i + 1) * LN / PR; ++l) issue_one(sl, L0 + l);
@@ -549,25 +538,13 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
     tile_wait_vmcnt<0>();          // no load may land in the LDS later
     __syncthreads();
 
-    // ---- outputs, T rows of a wave's tile at a time, by way of LDS of its own: in the accumulators a
+    // ---- outputs, 16 rows of a wave's tile at a time, by way of LDS of its own: in the accumulators a
     // lane's neighbours are other rows, in memory they are a row's columns.  Lane (r, g) holds row r and columns
-    // 4 g + v of a 16 x 16 product, 8 (v / 4) + 4 g + v % 4 of a 32 x 32 one.
+    // 4 g .. of each fragment.
     constexpr int HC = G::HC, HF = HC / 16;                      // output columns of a wave, in sixteens
-    uint8_t* const own = lds + wave * (T * G::PITCH);
+    uint8_t* const own = lds + wave * (16 * G::PITCH);
     const int64_t jw = j0 + wn * HC;
     const int cols = (int)(p.m - jw < HC ? p.m - jw : HC);       // can be negative
-    // four columns of sixteen c, those from 4 k on of them: of y, or of product `up` of MM_GATE
-    auto four = [&](int c, int k, int q, int up) {
-        if constexpr (T == 16) {
-            const f32x4 v = GATE ? acc[2 * c + up][q] : acc[c][q];
-            return v;
-        } else {
-            const int f = GATE ? c : c / 2, v0 = GATE ? 8 * up + 4 * k : 8 * (c % 2) + 4 * k;
-            return f32x4{acc[f][q][v0], acc[f][q][v0 + 1], acc[f][q][v0 + 2], acc[f][q][v0 + 3]};
-        }
-    };
-    constexpr int K4 = T == 32 ? 2 : 1;                          // fours of a sixteen in a lane
-    auto column = [&](int c, int k) { return 16 * c + (T == 32 ? 8 * k : 0) + 4 * g; };
     const int64_t at = t0 * p.m + jw;
     if constexpr (GATE) {
         const int64_t all_rows = p.n * p.m;
@@ -575,7 +552,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
         float* const z1 = p.part ? z0 + all_rows : p.z[1];
         constexpr bool PACKS = BN == 256 && mm_wide(ELT);        // (a block of 128 columns)
         const bool packs = PACKS && p.hq && !p.part;
-        float* const tops = (float*)(lds + NW * T * G::PITCH);   // [WN][BM]
+        float* const tops = (float*)(lds + NW * 16 * G::PITCH);   // [WN][BM]
         constexpr int LANES = HC / 8;                            // a lane takes 8 columns of a row
         // (one copy of what follows for all q: with the activations in it, one for each would not fit the
         // instruction cache; 8-bit gate of 4096 rows, 8192 -> 2048: 139 us, 114 so)
@@ -585,18 +562,16 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                 constexpr int Q = decltype(index)::value;
                 if (q == Q) {
 #pragma unroll
-                    for (int c = 0; c < HF; ++c)
-#pragma unroll
-                        for (int k = 0; k < K4; ++k) {
-                            uint8_t* const to = own + r * G::PITCH + column(c, k) * 4;
-                            *(f32x4*)to = four(c, k, Q, 0);
-                            *(f32x4*)(to + HC * 4) = four(c, k, Q, 1);
-                        }
+                    for (int c = 0; c < HF; ++c) {
+                        uint8_t* const to = own + r * G::PITCH + (16 * c + 4 * g) * 4;
+                        *(f32x4*)to = acc[2 * c][Q];
+                        *(f32x4*)(to + HC * 4) = acc[2 * c + 1][Q];
+                    }
                 }
             });
-            const int row0 = wm * TM + T * q, left = rows - row0;
+            const int row0 = wm * TM + 16 * q, left = rows - row0;
 #pragma unroll 1
-            for (int i = lane; i < T * LANES; i += 64) {         // products out, h out or back in their place
+            for (int i = lane; i < 16 * LANES; i += 64) {         // products out, h out or back in their place
                 const int row = i / LANES, c8 = 8 * (i % LANES), some = cols - c8;
                 uint8_t* const from = own + row * G::PITCH + c8 * 4;
                 f32x4 a[2], b[2];
@@ -667,7 +642,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                 if (!packs) continue;
                 __syncthreads();                                 // all waves of a row
 #pragma unroll 1
-                for (int i = lane; i < T * LANES; i += 64) {
+                for (int i = lane; i < 16 * LANES; i += 64) {
                     const int row = i / LANES, c8 = 8 * (i % LANES);
                     uint32_t top = 0u;
 #pragma unroll
@@ -706,20 +681,18 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                 constexpr int Q = decltype(index)::value;
                 if (q == Q) {
 #pragma unroll
-                    for (int c = 0; c < HF; ++c)
-#pragma unroll
-                        for (int k = 0; k < K4; ++k) {
-                            const f32x4 v = four(c, k, Q, 0);
-                            uint8_t* const to = own + r * pitch + column(c, k) * wide;
-                            if (wide == 4) *(f32x4*)to = v;
-                            else *(u32x2*)to = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                        }
+                    for (int c = 0; c < HF; ++c) {
+                        const f32x4 v = acc[c][Q];
+                        uint8_t* const to = own + r * pitch + (16 * c + 4 * g) * wide;
+                        if (wide == 4) *(f32x4*)to = v;
+                        else *(u32x2*)to = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    }
                 }
             });
-            const int row0 = wm * TM + T * q, left = rows - row0;
+            const int row0 = wm * TM + 16 * q, left = rows - row0;
             const int lanes = HC * wide / 16;                    // of a row: a power of two
             auto store = [&](auto ends) {                        // ends: rows may end inside 16 bytes
-                for (int i = lane; i < T * lanes; i += 64) {
+                for (int i = lane; i < 16 * lanes; i += 64) {
                     const int row = i / lanes, at16 = 16 * (i - row * lanes), some = cols * wide - at16;
                     const u32x4 v = *(const u32x4*)(own + row * pitch + at16);
                     if (row >= left || some <= 0) continue;
@@ -912,10 +885,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_mm_stream(MmTile p) {
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-template <int ELT, int FORM, int BM, int BN, int WM, int NW, int T, int R>
+template <int ELT, int FORM, int BM, int BN, int WM, int NW, int R>
 static hipError_t mm_launch_tile(const MmTile& t, const MmPlan& P, hipStream_t st) {
-    const auto k = k_mm_tile<ELT, FORM, BM, BN, WM, NW, T, R>;
-    constexpr size_t lds = MmGeo<ELT, FORM, BM, BN, WM, NW, T, R>::BYTES;
+    const auto k = k_mm_tile<ELT, FORM, BM, BN, WM, NW, R>;
+    constexpr size_t lds = MmGeo<ELT, FORM, BM, BN, WM, NW, R>::BYTES;
     if (P.bm != BM || P.bn != BN || P.waves != NW) return hipErrorInvalidValue;      // (the plan's are these)
     const hipError_t e = ensure_dynamic_lds((const void*)k, lds);
     if (e != hipSuccess) return e;
@@ -944,30 +917,28 @@ static hipError_t mm_launch_stream(const MmTile& t, const MmPlan& P, hipStream_t
 template <int ELT, int FORM>
 static hipError_t mm_launch_rows(const MmTile& t, const MmPlan& P, hipStream_t st) {
     constexpr bool GATE = FORM == MM_GATE, WIDE = mm_wide(ELT);
-    constexpr int T = mm_side(ELT), TS = ELT == MM_E8W ? 32 : 16;
     if (P.stream) {
         if constexpr (GATE) return P.waves == 8 ? mm_launch_stream<ELT, true, 2, 8>(t, P, st) : mm_launch_stream<ELT, true, 2, 4>(t, P, st);
         else if (P.bn == 32) return P.waves == 8 ? mm_launch_stream<ELT, false, 2, 8>(t, P, st) : mm_launch_stream<ELT, false, 2, 4>(t, P, st);
         else return P.waves == 8 ? mm_launch_stream<ELT, false, 1, 8>(t, P, st) : mm_launch_stream<ELT, false, 1, 4>(t, P, st);
     }
     if constexpr (WIDE) {
-        if (P.bm == 128) return mm_launch_tile<ELT, FORM, 128, 256, 2, 8, T, 3>(t, P, st);
+        if (P.bm == 128) return mm_launch_tile<ELT, FORM, 128, 256, 2, 8, 3>(t, P, st);
     } else {
-        if (P.bm == 256) return mm_launch_tile<ELT, FORM, 256, 256, 4, 8, T, 2>(t, P, st);
-        if (P.bm == 128) return mm_launch_tile<ELT, FORM, 128, 128, 2, 4, T, 2>(t, P, st);
+        if (P.bm == 256) return mm_launch_tile<ELT, FORM, 256, 256, 4, 8, 2>(t, P, st);
+        if (P.bm == 128) return mm_launch_tile<ELT, FORM, 128, 128, 2, 4, 2>(t, P, st);
     }
-    if (P.bm == 64) return mm_launch_tile<ELT, FORM, 64, 128, 2, 4, TS, 3>(t, P, st);
-    return mm_launch_tile<ELT, FORM, 32, 128, 1, WIDE ? 2 : 4, TS, 3>(t, P, st);
+    if (P.bm == 64) return mm_launch_tile<ELT, FORM, 64, 128, 2, 4, 3>(t, P, st);
+    return mm_launch_tile<ELT, FORM, 32, 128, 1, WIDE ? 2 : 4, 3>(t, P, st);
 }
 
 template <int ELT>
 static hipError_t mm_launch_back(const MmTile& t, const MmPlan& P, hipStream_t st) {
-    constexpr int T = mm_side(ELT);
     if constexpr (!mm_wide(ELT)) {
-        if (P.bm == 256) return mm_launch_tile<ELT, MM_NN, 256, 256, 4, 8, T, 2>(t, P, st);
+        if (P.bm == 256) return mm_launch_tile<ELT, MM_NN, 256, 256, 4, 8, 2>(t, P, st);
     }
-    if (P.bm == 128) return mm_launch_tile<ELT, MM_NN, 128, 256, 2, 8, T, mm_wide(ELT) ? 3 : 2>(t, P, st);
-    return mm_launch_tile<ELT, MM_NN, 64, 256, 2, 4, T, 3>(t, P, st);
+    if (P.bm == 128) return mm_launch_tile<ELT, MM_NN, 128, 256, 2, 8, mm_wide(ELT) ? 3 : 2>(t, P, st);
+    return mm_launch_tile<ELT, MM_NN, 64, 256, 2, 4, 3>(t, P, st);
 }
 
 }  // namespace gq

@@ -10,6 +10,7 @@
 // asynchronous loads cannot take, and the outputs of contractions that are split over blocks.
 #include "gq_mm_plan.h"
 #include "gq_tile.h"
+#include <math.h>
 
 namespace gq {
 
@@ -178,20 +179,45 @@ static MmPads mm_pads(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
     return p;
 }
 
+// What a launch of tiles takes, in microseconds, as the tile and the split are chosen by: with L tiles on the fullest
+// compute unit and S stages each, fixed L^0.5 + stage S L^0.85, and of a split contraction the joining launch
+// with its float32 sums (thousands of them a microsecond, written and read).  Fitted to launches of 16 to 4096 rows,
+// contractions of 1024 to 11008 and as many columns, every tile by splits of 1 to 16: of 200 such products
+// the chosen pair takes 2 percent longer than the best one on average and 18 at most.  A rule of "the
+// largest tile that leaves 192 blocks, split to 256" took 9 percent longer, and 115 at most (200 rows, 1024 x 1024:
+// 13.3 us, 7.4 by tiles of 32 rows with no split; 400 rows, gradient of 1024 -> 4096: 22.3 and 13.3).
+struct MmCost {
+    float fixed[4], stage[4];     // by tiles of 32, 64, 128 and 256 rows; 0: no such tile
+    float join, sums;
+};
+static const MmCost& mm_cost(MmForm form, MmElt elt) {
+    static const MmCost rows8{{4.5f, 5.4f, 6.1f, 11.f}, {.38f, .42f, .63f, 1.23f}, 3.1f, 890.f};
+    static const MmCost rowsw{{5.7f, 6.4f, 9.6f, 0.f}, {.66f, .63f, 1.49f, 0.f}, 2.6f, 830.f};
+    static const MmCost gate{{3.6f, 5.3f, 6.1f, 8.9f}, {.35f, .4f, .63f, 1.37f}, 3.8f, 850.f};
+    static const MmCost back8{{0.f, 6.8f, 6.6f, 9.4f}, {0.f, .79f, 1.13f, 1.25f}, 3.5f, 700.f};
+    static const MmCost backw{{0.f, 8.3f, 9.1f, 0.f}, {0.f, 1.35f, 1.59f, 0.f}, 1.7f, 580.f};
+    static const MmCost back{{0.f, 9.6f, 9.1f, 11.3f}, {0.f, .72f, .98f, 1.24f}, 1.f, 650.f};
+    static const MmCost turned{{0.f, 0.f, 8.6f, 14.5f}, {0.f, 0.f, .57f, 1.45f}, 1.7f, 800.f};
+    if (form == MM_TN) return turned;
+    if (form == MM_NN) return elt == MM_BF16 ? back : (mm_wide(elt) ? backw : back8);
+    return elt == MM_BF16 ? gate : (mm_wide(elt) ? rowsw : rows8);
+}
+
 static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed, bool a_padded = false) {
     MmPlan P{};
-    const bool tn = form == MM_TN, gate = form == MM_GATE, nn = form == MM_NN, fp8 = elt != MM_BF16;
+    const bool tn = form == MM_TN, gate = form == MM_GATE, nn = form == MM_NN, fp8 = elt != MM_BF16, wide = mm_wide(elt);
     const int64_t k = tn ? n : (nn ? d_out : d_in), m = tn || nn ? d_in : d_out, ke = fp8 ? 128 : 64;
     const int64_t one = (k + ke - 1) / ke, per = (n + experts - 1) / experts;
     const int64_t live = experts > 1 ? (experts < n ? experts : n) : 1;           // experts with rows, at most
+    const int64_t outputs = tn ? 2 * (int64_t)experts * d_out * m : (gate ? 2 : 1) * n * m;
     const MmPads pads = mm_pads(form, elt, n, d_in, d_out, experts, a_padded);
     P.pad_bytes = pads.a * pads.as + pads.w * pads.ws;
     P.stages = (int)(nn && !fp8 ? 2 * one : one);
     P.unit = fp8 ? 4 : 1;
     P.split = 1;
-    int64_t blocks, units;
     const int64_t wcols = gate ? 2 * m : m;                                       // rows of weights that outputs need
-    P.stream = (form == MM_NT || gate) && per <= 16 && per * k * (fp8 ? 1 : 2) <= 1 << 18 && live * ((wcols + 127) / 128) < 192;
+    P.stream = (form == MM_NT || gate) && per <= 16 && per * k * (fp8 ? 1 : 2) <= 1 << 18 && k * (fp8 ? 1 : 2) <= 1 << 15 &&
+               live * ((wcols + 127) / 128) < 192;
     if (P.stream) {
         P.bm = 16;
         P.bn = gate || live * ((m + 31) / 32) >= 256 ? 32 : 16;
@@ -199,38 +225,51 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
         // eight waves of two fragments fill a compute unit's LDS: worth it from four pieces a wave on (16 rows,
         // 8-bit gate 4096 -> 11008: 29.2 us, 25.8 by four waves; 1 row in bfloat16 38.9 and 42.4)
         P.waves = pieces >= (P.bn == 32 ? 32 : 8) ? 8 : 4;
-        blocks = live * ((wcols + P.bn - 1) / P.bn);
-        units = pieces / P.waves;
-    } else if (tn) {
-        P.bm = 256;
-        for (;; P.bm /= 2) {
-            P.bn = P.bm;
-            P.waves = P.bm == 256 ? 8 : 4;
-            blocks = 2 * (int64_t)experts * ((d_out + P.bm - 1) / P.bm) * ((m + P.bn - 1) / P.bn);
-            if (P.bm == 128 || blocks >= 192) break;
-        }
-        units = experts > 1 ? 1 : P.stages;
-    } else {
-        P.bm = per > 128 && !mm_wide(elt) ? 256 : (per > 64 ? 128 : (per > 32 || nn ? 64 : 32));
-        for (;; P.bm /= 2) {
-            P.bn = P.bm == 256 || nn || (P.bm == 128 && mm_wide(elt)) ? 256 : 128;
-            const int64_t rows = experts > 1 ? n / P.bm + live : (n + P.bm - 1) / P.bm;
-            blocks = rows * ((wcols + P.bn - 1) / P.bn);
-            if (P.bm <= 64 || blocks >= (nn ? 48 : 192)) break;
-        }
-        P.waves = P.bm >= 128 && P.bn == 256 ? 8 : (P.bm == 32 && mm_wide(elt) ? 2 : 4);
-        units = (P.stages + P.unit - 1) / P.unit;
-    }
-    if (units < 1) units = 1;
-    if (blocks < 256) {
-        int64_t s = (P.stream ? 512 : 256) / (blocks > 0 ? blocks : 1);
+        const int64_t blocks = live * ((wcols + P.bn - 1) / P.bn), units = pieces / P.waves;
+        // a block to each compute unit (bfloat16 gate of 4 rows, 8192 -> 1024: 11.0 us whole, 9.5 split by 4, 12.1 by 8),
+        // but for few pieces (16 rows, 4096 -> 1024: 6.7 us whole, 7.1 split by 2)
+        int64_t s = units < 4 || blocks >= 256 ? 1 : 256 / blocks;
         s = s < units ? s : units;
         s = s < 1 ? 1 : (s > 16 ? 16 : s);
-        const int64_t each = (units + s - 1) / s;                                 // no part without work
-        P.split = (int)((units + each - 1) / each);
+        if (s > 1) {
+            const int64_t each = (units + s - 1) / s;                             // no part without work
+            P.split = (int)((units + each - 1) / each);
+        }
+        P.join = P.split > 1 || packed;
+    } else {
+        const MmCost& cost = mm_cost(form, elt);
+        const int64_t stages = tn ? (per + ke - 1) / ke : P.stages, units = tn && experts > 1 ? 1 : (stages + P.unit - 1) / P.unit;
+        float best = 0.f;
+        for (int i = 0; i < 4; ++i) {
+            if (cost.stage[i] == 0.f) continue;
+            const int bm = 32 << i, bn = tn ? bm : (bm == 256 || nn || (bm == 128 && wide) ? 256 : 128);
+            // (an expert's last tile is half empty)
+            const int64_t rows = tn ? 2 * experts * ((d_out + bm - 1) / bm) : (experts > 1 ? n / bm + (live + 1) / 2 : (n + bm - 1) / bm);
+            const int64_t blocks = rows * ((wcols + bn - 1) / bn);
+            int last = 0;
+            for (int want = 1; want <= 16; want *= 2) {
+                const int64_t each = units > 0 ? (units + want - 1) / want : 1;
+                const int split = units > 0 ? (int)((units + each - 1) / each) : 1;
+                if (split == last) continue;
+                last = split;
+                const int64_t some = stages < each * P.unit ? stages : each * P.unit;
+                float load = (float)(blocks * split) / 256.f;
+                load = load < 1.f ? 1.f : (load < 8.f ? ceilf(load) : load);
+                const bool join = split > 1 || (packed && bn != 256);
+                const float t = cost.fixed[i] * sqrtf(load) + cost.stage[i] * (float)(split > 1 ? some : stages) * powf(load, .85f) +
+                                (join ? cost.join + (float)split * (float)outputs / (1000.f * cost.sums) : 0.f);
+                if (best == 0.f || t < best) {
+                    best = t;
+                    P.bm = bm;
+                    P.bn = bn;
+                    P.split = split;
+                    P.join = join;
+                }
+                if (blocks >= 512) break;          // the card is full: parts would only cost
+            }
+        }
+        P.waves = P.bm >= 128 && P.bn == 256 ? 8 : (P.bm == 32 && wide ? 2 : 4);
     }
-    P.join = P.split > 1 || (packed && P.bn != 256);
-    const int64_t outputs = tn ? 2 * (int64_t)experts * d_out * m : (gate ? 2 : 1) * n * m;
     P.part_bytes = P.join ? mm_al256((size_t)P.split * outputs * 4) : 0;
     return P;
 }

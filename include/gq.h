@@ -715,6 +715,27 @@ gq_status gq_timing_read_product(double* ms, int64_t* launches);
 gq_status mxfp4_plan(int32_t op, gq_dtype a_dt, int64_t n, int64_t d_in, int64_t d_out,
                      int32_t experts, int32_t grouped, int32_t plan[6], int64_t* first_rows);
 
+/*
+ * Likewise how an 8-bit product or one of the gated feed-forward block is done.  s_dt and y_dt, the
+ * types of its scales and its output (a packed output has none, the bfloat16 block no scales: not
+ * used); d_out: d_ff of the block's.  plan: 1 where sums are float32 throughout (0: sums of eight 8-bit
+ * products as the matrix cores take them), then as above: streamed, rows, columns, waves, parts.  Columns
+ * count both weights' of a gate.  n >= 1; else statuses as the products'.
+ */
+typedef enum {
+    GQ_PRODUCT_FP8_GEMM = 0,
+    GQ_PRODUCT_FP8_GEMM_DX,
+    GQ_PRODUCT_FP8_FFN_GATE,
+    GQ_PRODUCT_FP8_FFN_GATE_PACKED,
+    GQ_PRODUCT_FFN_GATE,
+    GQ_PRODUCT_FFN_GATE_DX,
+    GQ_PRODUCT_FFN_GATE_DW,
+    GQ_PRODUCT_COUNT
+} gq_product;
+
+gq_status gq_product_plan(gq_product op, gq_scale s_dt, gq_dtype y_dt, int64_t n, int64_t d_in,
+                          int64_t d_out, int32_t experts, int32_t plan[6]);
+
 #ifdef __cplusplus
 }
 #endif

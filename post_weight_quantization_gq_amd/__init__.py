@@ -12,7 +12,7 @@ from .binding import (  # noqa: F401
     mxfp4_dequantize, mxfp4_gemm, mxfp4_gemm_mx, mxfp4_gemm_dx, mxfp4_gemm_workspace_size,
     mxfp4_gemm_mx_workspace_size, mxfp4_gemm_dx_workspace_size, mxfp4_plan,
     fp8_row_bytes, fp8_row_scales, fp8_quantize, fp8_quantize_weight, fp8_dequantize,
-    fp8_dequantize_weight, fp8_gemm, fp8_gemm_dx, fp8_ffn_gate, ffn_gate, ffn_gate_dz, ffn_gate_dx,
+    fp8_dequantize_weight, product_plan, fp8_gemm, fp8_gemm_dx, fp8_ffn_gate, ffn_gate, ffn_gate_dz, ffn_gate_dx,
     ffn_gate_dw, ffn_gate_backward, ffn_gate_backward_workspace_size, fp8_gemm_workspace_size, fp8_gemm_dx_workspace_size, fp8_ffn_gate_workspace_size,
     fp8_ffn_gate_packed_workspace_size, ffn_gate_workspace_size, ffn_gate_dx_workspace_size,
     ffn_gate_dw_workspace_size, gq_fisher_accumulate_host, fisher_stream_workspace_size,

@@ -47,6 +47,7 @@ EXPORTS = (
     "ffn_gate_dz", "ffn_gate_dx_workspace_size", "ffn_gate_dx", "ffn_gate_dw_workspace_size",
     "ffn_gate_dw", "ffn_gate_backward_workspace_size", "ffn_gate_backward",
     "gq_timing_enable", "gq_timing_read", "gq_timing_read_mxfp4", "gq_timing_read_product",
+    "gq_product_plan",
     "gq_stage_name",
 )
 STAGE_COUNT, MXFP4_STAGE_COUNT, PRODUCT_STAGE_COUNT = 18, 2, 4
@@ -156,6 +157,7 @@ _SIGS = {
     "gq_timing_enable": (None, [ctypes.c_int]),
     "gq_timing_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gq_timing_read_mxfp4": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
+    "gq_product_plan": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i32, ctypes.POINTER(_i32)]),
     "gq_timing_read_product": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
     "gq_stage_name": (ctypes.c_char_p, [ctypes.c_int]),
 }
@@ -1152,6 +1154,19 @@ def ffn_gate_dw_workspace_size(n, d_in, d_ff, experts=1) -> int:
 
 def ffn_gate_backward_workspace_size(n, d_in, d_ff, experts=1) -> int:
     return int(library().ffn_gate_backward_workspace_size(n, d_in, d_ff, experts))
+
+
+PRODUCTS = ("fp8_gemm", "fp8_gemm_dx", "fp8_ffn_gate", "fp8_ffn_gate_packed", "ffn_gate", "ffn_gate_dx",
+            "ffn_gate_dw")
+
+
+def product_plan(op: str, n, d_in, d_out, experts=1, scales=torch.uint8, dtype=GQ_BF16) -> dict:
+    """How a product (one of PRODUCTS; d_out: the block's d_ff) of these sizes is done: wide (its sums
+    are float32 throughout), streamed, rows and cols of a tile, waves of a block, split.  dtype: the
+    output's."""
+    plan = (_i32 * 6)()
+    _check(library().gq_product_plan(PRODUCTS.index(op), _scale_type(scales), dtype, n, d_in, d_out, experts, plan))
+    return dict(zip(("wide", "streamed", "rows", "cols", "waves", "split"), plan))
 
 
 def fp8_gemm(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=None,

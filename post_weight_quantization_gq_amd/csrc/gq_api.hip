@@ -1266,6 +1266,25 @@ gq_status ffn_gate_dw(const void* dzg, const void* dzu, int64_t n, int64_t d_ff,
     return mm_product(c, GQ_SCALE_E8M0, dw_dt, 0, ws, ws_bytes, stream, "ffn_gate_dw");
 }
 
+gq_status gq_product_plan(gq_product op, gq_scale s_dt, gq_dtype y_dt, int64_t n, int64_t d_in,
+                          int64_t d_out, int32_t experts, int32_t plan[6]) {
+    if ((int)op < 0 || op >= GQ_PRODUCT_COUNT) return fail(GQ_EINVAL, "op=%d outside [0, %d]", (int)op, GQ_PRODUCT_COUNT - 1);
+    if (!plan) return fail(GQ_EINVAL, "null plan");
+    const bool fp8 = op < GQ_PRODUCT_FFN_GATE, packed = op == GQ_PRODUCT_FP8_FFN_GATE_PACKED;
+    if (fp8 && !scale_ok(s_dt)) return fail(GQ_EDTYPE, "unsupported scale type %d", (int)s_dt);
+    if (packed) y_dt = GQ_F32;
+    const gq_status rc = mx_sizes_check(y_dt, y_dt, n, d_in, d_out, experts);
+    if (rc != GQ_OK) return rc;
+    if (n < 1) return fail(GQ_ESHAPE, "n=%lld: no rows, no plan", (long long)n);
+    const gq::MmForm forms[] = {gq::MM_NT, gq::MM_NN, gq::MM_GATE, gq::MM_GATE, gq::MM_GATE, gq::MM_NN, gq::MM_TN};
+    const gq::MmElt elt = fp8 ? fp8_elt(s_dt, y_dt) : gq::MM_BF16;
+    if (!gq::mm_fits(forms[op], elt, n, d_in, d_out, experts, experts > 1, packed))
+        return fail(GQ_ENOTIMPL, "n=%lld d_in=%lld d_out=%lld experts=%d: more tiles than a launch takes",
+                    (long long)n, (long long)d_in, (long long)d_out, experts);
+    gq::mm_describe(forms[op], elt, n, d_in, d_out, experts, packed, plan);
+    return GQ_OK;
+}
+
 // The two gradients of zg and zu with their rows at multiples of 8 values, then the larger scratch of the products.
 static size_t ffn_dz_bytes(int64_t n, int64_t d_ff) { return al256((size_t)n * ((d_ff + 7) / 8 * 8) * 2); }
 

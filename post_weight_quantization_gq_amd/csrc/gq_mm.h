@@ -64,6 +64,8 @@ struct MmCall {
 };
 size_t mm_workspace(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed, bool a_padded = false);
 bool mm_fits(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool offsets, bool packed);
+// plan: wide, streamed, rows, columns, waves, parts
+void mm_describe(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed, int32_t plan[6]);
 hipError_t mm_run(const MmCall& c, void* ws, hipStream_t st);
 
 // dzg = dh zu act'(zg), dzu = dh act(zg), `rows` rows of f values; those of dzg and dzu start `pitch` values
@@ -77,7 +79,7 @@ enum Act { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 // 1 / (1 + e^-z) by the exponential and reciprocal instructions (an ulp each; the exponential's argument, rounded
 // once more, adds |z| 2^-24): a gate's epilogue evaluates one for two products of the whole contraction, and the
 // library's exponential and division took four times the instructions (8-bit gate of 4096 rows, 8192 -> 2048 packed:
-// 118 us, 114 so).
+// 118 us, 114 so).  The reciprocal's results below 2^-126 are zero.
 __device__ __forceinline__ float logistic(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
@@ -94,7 +96,8 @@ __device__ __forceinline__ float act_of(float z, int act, float* slope) {
     if (act == ACT_GELU_TANH) {
         const float k = 0.79788456080286536f, z2 = z * z;
         const float s = logistic(2.f * k * z * (1.f + 0.044715f * z2));
-        if (SLOPE) *slope = s + 2.f * z * s * (1.f - s) * (k * (1.f + 0.134145f * z2));
+        // (where z z is over the largest number, s (1 - s) is zero)
+        if (SLOPE) *slope = s + 2.f * z * s * (1.f - s) * (k * (1.f + 0.134145f * fminf(z2, 1e30f)));
         return z * s;
     }
     const float s = logistic(z);

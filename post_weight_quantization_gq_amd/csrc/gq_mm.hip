@@ -182,9 +182,9 @@ static MmPads mm_pads(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
 // What a launch of tiles takes, in microseconds, as the tile and the split are chosen by: with L tiles on the fullest
 // compute unit and S stages each, fixed L^0.5 + stage S L^0.85, and of a split contraction the joining launch
 // with its float32 sums (thousands of them a microsecond, written and read).  Fitted to launches of 16 to 4096 rows,
-// contractions of 1024 to 11008 and as many columns, every tile by splits of 1 to 16: of 200 such products
-// the chosen pair takes 2 percent longer than the best one on average and 18 at most.  A rule of "the
-// largest tile that leaves 192 blocks, split to 256" took 9 percent longer, and 115 at most (200 rows, 1024 x 1024:
+// contractions of 1024 to 11008 and as many columns, every tile by splits of 1 to 16: in 257 such products
+// the chosen pair takes 4 percent longer than the best one (geometric mean, on another card).  A rule of "the largest
+// tile that leaves 192 blocks, split to 256" took 7 percent longer, and up to twice as long (200 rows, 1024 x 1024:
 // 13.3 us, 7.4 by tiles of 32 rows with no split; 400 rows, gradient of 1024 -> 4096: 22.3 and 13.3).
 struct MmCost {
     float fixed[4], stage[4];     // by tiles of 32, 64, 128 and 256 rows; 0: no such tile
@@ -283,6 +283,12 @@ bool mm_fits(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int
     const MmPlan P = mm_plan(form, elt, n, d_in, d_out, experts, packed);
     const int64_t m = form == MM_TN || form == MM_NN ? d_in : d_out;
     return P.stream || mm_blocks(form, n, m, d_out, experts, offsets, 2, P) * 64 * P.waves <= MM_MAX_LANES;
+}
+
+void mm_describe(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d_out, int experts, bool packed, int32_t plan[6]) {
+    const MmPlan P = mm_plan(form, elt, n, d_in, d_out, experts, packed);
+    const int32_t v[6] = {elt == MM_BF16 || mm_wide(elt), P.stream, P.bm, P.bn, P.waves, P.split};
+    for (int i = 0; i < 6; ++i) plan[i] = v[i];
 }
 
 hipError_t mm_run(const MmCall& c, void* ws, hipStream_t st) {

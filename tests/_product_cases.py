@@ -14,7 +14,8 @@ The gate h = act(zg) zu: |act'| <= 1.13 for all three, so h moves by at most 1.1
 |act(zg)| dzu for products off by dzg and dzu.  act itself is evaluated in float32 from at most six roundings
 (2^-24) and two library functions (4 ulp: 2^-21) of which the exponential's argument carries up to three
 roundings, each moving it by |arg| 2^-24 <= (1 + z^2) 2^-23: together within 32 2^-23 (1 + z^2) of act(z), and of
-max(1, ...) for the slope, whose terms can cancel.
+max(1, ...) for the slope, whose terms can cancel.  A logistic function below 2^-126 is zero: |z| 2^-126 of
+act(z), |z zu| 2^-126 of h.
 """
 import numpy as np
 import torch
@@ -120,7 +121,7 @@ def act64(z, act):
         s = torch.sigmoid(z)
         return z * s, s + z * s * (1 - s)
     if act == "gelu":
-        c = torch.special.ndtr(z)
+        c = 0.5 * torch.special.erfc(-0.7071067811865476 * z)          # (1 + erf) / 2 cancels in the tail
         return z * c, c + z * torch.exp(-z * z / 2) * 0.3989422804014327
     u = 0.7978845608028654 * (z + 0.044715 * z ** 3)
     s = torch.sigmoid(2 * u)
@@ -133,4 +134,4 @@ def gate64(a, G, U, act, terms, eight=False):
     bg, bu = ((terms + 8) * EPS * (a.abs() @ w.T.abs()) + (cut(a, w) if eight else 0.0) for w in (G, U))
     v = act64(zg, act)[0]
     limit = 1.13 * bg * (zu.abs() + bu) + v.abs() * bu + 33 * EPS * (1 + zg * zg) * (v * zu).abs()
-    return v * zu, limit + 2.0 ** -140, zg, zu, bg, bu
+    return v * zu, limit + (zg * zu).abs() * 2.0 ** -126 + 2.0 ** -140, zg, zu, bg, bu

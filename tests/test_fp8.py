@@ -10,6 +10,7 @@ import torch
 import oracle as O
 import post_weight_quantization_gq_amd as gq
 from post_weight_quantization_gq_amd import binding as B
+from _product_kernels import CASES, U8, kernel, types
 
 FP8 = torch.float8_e4m3fn
 FAR = [ctypes.c_void_p(i << 52) for i in range(1, 17)]      # apart, aligned, never dereferenced
@@ -226,6 +227,47 @@ def test_dz_argument_errors():
     assert call(count=0, dh=None, zg=None, zu=None, a=None, b=None) == B.GQ_OK
 
 
+def test_backward_argument_errors():
+    lib = gq.library()
+    names = "dh x G U zg zu dx dG dU".split()
+
+    def call(dt=1, n=8, k=256, m=128, act=0, experts=1, offsets=None, dxt=1, dwt=1, ws=None, wsb=0, **p):
+        p = {name: p.get(name, FAR[i]) for i, name in enumerate(names)}
+        return lib.ffn_gate_backward(p["dh"], dt, p["x"], n, k, p["G"], p["U"], m, act, experts, offsets, p["zg"], p["zu"],
+                                     p["dx"], dxt, p["dG"], p["dU"], dwt, ws, wsb, None)
+
+    for p in names[:6]:
+        assert call(**{p: None}) == B.GQ_EINVAL and "null" in err(), p
+    none = dict(dx=None, dG=None, dU=None)
+    assert call(**none) == B.GQ_EINVAL and "nothing" in err()
+    assert call(**none, n=0) == B.GQ_EINVAL
+    # what an output does not need can be left out: these get as far as the overlap of what is there
+    assert call(dx=None, G=None, U=None, dU=FAR[0]) == B.GQ_EINVAL and "overlap" in err()
+    assert call(dG=None, dU=None, x=None, dx=FAR[0]) == B.GQ_EINVAL and "overlap" in err()
+    assert call(dt=2) == B.GQ_EDTYPE and call(dxt=2) == B.GQ_EDTYPE and call(dwt=-1) == B.GQ_EDTYPE
+    assert call(act=3) == B.GQ_EINVAL and call(act=-1) == B.GQ_EINVAL
+    assert call(n=-1) == B.GQ_ESHAPE and call(k=0) == B.GQ_ESHAPE and call(m=0) == B.GQ_ESHAPE
+    assert call(n=1 << 31) == B.GQ_ENOTIMPL and call(k=(1 << 20) + 1) == B.GQ_ENOTIMPL and call(m=(1 << 20) + 1) == B.GQ_ENOTIMPL
+    assert call(experts=0) == B.GQ_EINVAL and call(experts=2) == B.GQ_EINVAL and "offsets" in err()
+    assert call(experts=4097, offsets=FAR[10]) == B.GQ_ENOTIMPL
+    assert call(offsets=off(FAR[10], 4)) == B.GQ_EINVAL
+    assert call(dh=off(FAR[0], 1)) == B.GQ_EINVAL and call(dh=off(FAR[0], 2), dt=0) == B.GQ_EINVAL
+    for p in ("x", "G", "U"):
+        assert call(**{p: off(FAR[12], 8)}) == B.GQ_EINVAL and "aligned" in err()
+        assert call(**{p: off(FAR[12], 8)}, k=257, dx=FAR[0]) == B.GQ_EINVAL and "overlap" in err()
+    assert call(zg=off(FAR[4], 2)) == B.GQ_EINVAL and call(dx=off(FAR[6], 1)) == B.GQ_EINVAL
+    assert call(dU=off(FAR[8], 2), dwt=0) == B.GQ_EINVAL and call(ws=off(FAR[10], 8), wsb=1 << 30) == B.GQ_EINVAL
+    for a in ("dx", "dG", "dU"):
+        for b in names:
+            if a != b:
+                assert call(**{a: FAR[names.index(b)]}) == B.GQ_EINVAL and "overlap" in err(), (a, b)
+    assert call(n=0, dG=None, dU=None) == B.GQ_OK
+    need = gq.ffn_gate_backward_workspace_size(8, 256, 128)
+    assert need >= 2 * 8 * 128 * 2 and gq.ffn_gate_backward_workspace_size(8, 256, 129) >= 2 * 8 * 136 * 2
+    assert call(ws=FAR[10], wsb=need - 1) == B.GQ_EINVAL and "workspace" in err()
+    assert gq.ffn_gate_backward_workspace_size(0, 256, 128) >= 0 and gq.ffn_gate_backward_workspace_size(8, 0, 128) == 0
+
+
 # ---- refusals of the binding --------------------------------------------------------------
 
 def status(fn, *a, **k):
@@ -292,3 +334,78 @@ def test_stages_of_the_library_and_the_binding():
     ms, n = (ctypes.c_double * 4)(*[5.0] * 4), (ctypes.c_int64 * 4)(*[7] * 4)
     assert lib.gq_timing_read_product(ms, n) == B.GQ_OK and list(ms) == [0.0] * 4 and list(n) == [0] * 4
     assert math.isclose(sum(ms), 0.0)
+
+
+# ---- how products are done --------------------------------------------------------------
+
+def test_the_kernels_cases_reach_every_kernel():
+    """Whatever a sweep over rows, widths, experts and types can choose is run by a case of the kernels' tests."""
+    rows = (1, 2, 8, 16, 17, 32, 33, 64, 100, 129, 200, 257, 333, 512, 700, 1024, 1500, 2048, 4096, 8192, 20000)
+    widths = (32, 64, 200, 512, 640, 1000, 1100, 2048, 4096, 5000, 8192, 11008, 28672, 100000)
+    missing = {}
+    for op in B.PRODUCTS:
+        for t in types(op):
+            covered = {kernel(op, *c, *t) for c in CASES[op]}
+            for n in rows:
+                for d_in in widths:
+                    for d_out in widths:
+                        for experts in (None, 2, 8, 64, 300):
+                            if (experts or 1) * d_in * d_out > 1 << 37:          # weights past a card's memory
+                                continue
+                            k = kernel(op, n, d_in, d_out, experts, *t)
+                            if k not in covered:
+                                missing.setdefault(k, (n, d_in, d_out, experts))
+    assert not missing
+
+
+@pytest.mark.parametrize("op", B.PRODUCTS)
+def test_parts_and_workspaces_stay_small(op):
+    """A split contraction's float32 parts: no more than a few hundred tiles' of 256 x 256."""
+    size = getattr(gq, op + "_workspace_size")
+    for n in (1, 16, 100, 1000, 4096, 65536):
+        for d_in in (128, 4096, 28672):
+            for d_out in (128, 4096, 28672):
+                for experts in (1, 8, 256):
+                    extra = () if op.startswith("ffn") else (U8,) if op.endswith("packed") else (U8, gq.GQ_F32)
+                    p = gq.product_plan(op, n, d_in, d_out, experts, dtype=gq.GQ_F32)
+                    assert 1 <= p["split"] <= 16
+                    outputs = n * d_out * (1 + ("gate" in op)) * 4
+                    if p["split"] > 1:
+                        assert size(n, d_in, d_out, experts, *extra) <= 16 * 512 * 256 * 256 * 4
+                    elif not op.endswith("packed"):
+                        assert size(n, d_in, d_out, experts, *extra) == 0, (n, d_in, d_out, experts)
+                    else:
+                        assert size(n, d_in, d_out, experts, *extra) <= outputs + 256
+
+
+@pytest.mark.parametrize("op,n,d_in,d_out,experts", [
+    ("fp8_gemm", (1 << 31) - 1, 8, 1, 1), ("fp8_gemm", 4096, 128, 1 << 19, 4096), ("fp8_gemm_dx", (1 << 31) - 1, 1, 8, 1),
+    ("fp8_ffn_gate", 4096, 128, 1 << 19, 4096), ("ffn_gate", 1 << 30, 8, 1 << 10, 1), ("ffn_gate_dx", 1 << 30, 1 << 10, 8, 1),
+    ("ffn_gate_dw", 1, 1 << 19, 1 << 19, 64)])
+def test_more_tiles_than_a_launch_takes(op, n, d_in, d_out, experts):
+    """Refused by the sizes, and the largest sizes that are not have a plan."""
+    with pytest.raises(gq.GQError) as e:
+        gq.product_plan(op, n, d_in, d_out, experts)
+        gq.product_plan(op, (1 << 31) - (1 << 21) - 1, d_in, d_out, experts)
+    assert e.value.status == B.GQ_ENOTIMPL
+
+
+def test_plan_refusals():
+    lib = gq.library()
+    plan = (ctypes.c_int32 * 6)()
+
+    def status(op=0, s=0, dt=1, n=8, d_in=128, d_out=128, experts=1, plan=plan):
+        return lib.gq_product_plan(op, s, dt, n, d_in, d_out, experts, plan)
+
+    assert status() == B.GQ_OK and list(plan) == [0, 1, 16, 16, 4, 1]
+    assert status(dt=0) == B.GQ_OK and list(plan)[:2] == [1, 1]
+    assert status(op=-1) == B.GQ_EINVAL and status(op=7) == B.GQ_EINVAL and status(plan=None) == B.GQ_EINVAL
+    assert status(s=2) == B.GQ_EDTYPE and status(op=4, s=2) == B.GQ_OK
+    assert status(dt=2) == B.GQ_EDTYPE and status(op=3, dt=2) == B.GQ_OK
+    assert status(n=0) == B.GQ_ESHAPE and status(d_in=0) == B.GQ_ESHAPE and status(d_out=-1) == B.GQ_ESHAPE
+    assert status(n=1 << 31) == B.GQ_ENOTIMPL and status(d_in=(1 << 20) + 1) == B.GQ_ENOTIMPL
+    assert status(experts=0) == B.GQ_EINVAL and status(experts=4097) == B.GQ_ENOTIMPL
+    with pytest.raises(ValueError):
+        gq.product_plan("gemv", 8, 128, 128)
+    with pytest.raises(gq.GQError):
+        gq.product_plan("fp8_gemm", 8, 0, 128)

@@ -221,13 +221,14 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
     if (P.stream) {
         P.bm = 16;
         P.bn = gate || live * ((m + 31) / 32) >= 256 ? 32 : 16;
-        const int64_t pieces = (one + 1) / 2;
-        // eight waves of two fragments fill a compute unit's LDS: worth it from four pieces a wave on (16 rows,
-        // 8-bit gate 4096 -> 11008: 29.2 us, 25.8 by four waves; 1 row in bfloat16 38.9 and 42.4)
-        P.waves = pieces >= (P.bn == 32 ? 32 : 8) ? 8 : 4;
-        const int64_t blocks = live * ((wcols + P.bn - 1) / P.bn), units = pieces / P.waves;
-        // a block to each compute unit (bfloat16 gate of 4 rows, 8192 -> 1024: 11.0 us whole, 9.5 split by 4, 12.1 by 8),
-        // but for few pieces (16 rows, 4096 -> 1024: 6.7 us whole, 7.1 split by 2)
+        const int64_t blocks = live * ((wcols + P.bn - 1) / P.bn);
+        // eight waves, of at least two lines each, where all blocks fit the card at once: of 32 columns two a compute unit
+        // (16 rows, float32 scales, 4096 -> 8192: 10.3 us by four waves, 8.7 by eight; 8-bit gate 4096 -> 11008, 688 blocks:
+        // 21.7 and 23.4)
+        P.waves = one >= 16 && (P.bn == 16 || blocks <= 512) ? 8 : 4;
+        const int64_t units = one / (2 * P.waves);
+        // a block to each compute unit (16 rows, 8192 -> 1024: 9.6 us whole, 7.7 split by 4, 8.4 by 8), but for
+        // fewer than eight lines a wave (4096 -> 1024: 6.6 us whole, 7.1 split by 2)
         int64_t s = units < 4 || blocks >= 256 ? 1 : 256 / blocks;
         s = s < units ? s : units;
         s = s < 1 ? 1 : (s > 16 ? 16 : s);

@@ -716,37 +716,38 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
 // ---------------------------------------------------------------------------
 // Few rows: the weight is streamed once, each wave on its own, without a barrier before the end.  A block
 // takes 16 MT rows of the weight (MM_GATE: 16 of each) and 16 rows of activations at a time; its
-// waves share out the contraction and their sums are added in the waves' order.  A wave copies pieces of
-// two lines of its weight rows into LDS of its own, one piece ahead.  Lane (r, b) holds chunks
-// b and 4 + b of a line of weight row r, and the same of row r of the activations.
+// waves share out the contraction and their sums are added in the waves' order.  A wave copies a line of each of
+// its weight rows into LDS of its own, one line ahead.  Lane (r, b) holds chunks b and 4 + b of a line of
+// weight row r, and the same of row r of the activations.  (8-bit gate of 16 rows, 4096 -> 11008: 21.7 us at 4.2 TB/s;
+// 25.7 by two lines at a time, of which fewer waves fit a compute unit; 24.0 and 25.4 with two and three lines ahead.)
 //
 // An expert's block takes its first MM_FIRST groups of 16 rows, and what experts have beyond those is spread over
 // blocks of its own that find their groups from the offsets: the plan knows the mean of the experts' rows alone.
 // ---------------------------------------------------------------------------
 template <int ELT, bool GATE, int MT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mm_stream(MmTile p) {
-    constexpr int PIECE = 16 * MT * 16, LOADS = PIECE / 64;     // slots of a piece, copies
+    constexpr int LINE = 16 * MT * 8, LOADS = LINE / 64;        // slots of a line of each row, copies
     constexpr bool SC = ELT != MM_BF16;
     static_assert(!GATE || MT == 2, "16 rows of each weight");
     extern __shared__ u32x4 mm_lds[];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, b = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    u32x4* const ring = mm_lds + wave * 2 * PIECE;
-    auto sums = [&](int w, int t) { return (float*)(mm_lds + w * 2 * PIECE) + 256 * t; };    // over the rings at the end
+    u32x4* const ring = mm_lds + wave * 2 * LINE;
+    auto sums = [&](int w, int t) { return (float*)(mm_lds + w * 2 * LINE) + 256 * t; };    // over the rings at the end
     constexpr int BC = GATE ? 16 : 16 * MT;
     const int64_t j0 = (int64_t)blockIdx.x * BC;
-    const int lines = (int)((p.w_bytes + 127) / 128), pieces = (lines + 1) / 2;
-    const int shares = WAVES * (int)gridDim.z, per = (pieces + shares - 1) / shares;
+    const int lines = (int)((p.w_bytes + 127) / 128);
+    const int shares = WAVES * (int)gridDim.z, per = (lines + shares - 1) / shares;
     const int c0 = ((int)blockIdx.z * WAVES + wave) * per;
-    const int c1 = c0 + per < pieces ? c0 + per : pieces;
+    const int c1 = c0 + per < lines ? c0 + per : lines;
 
     const int wrows = (int)(p.m - j0 < BC ? p.m - j0 : BC);
     uint32_t wv[LOADS];
-    int wc[LOADS];                                 // the chunk's byte within a piece
+    int wc[LOADS];                                 // the chunk's byte within a line
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-        const int slot = i * 64 + lane, row = slot / 16;
-        wc[i] = 16 * ((slot % 16) ^ (row & 15));
+        const int slot = i * 64 + lane, row = slot / 8;
+        wc[i] = 16 * ((slot % 8) ^ mm_swz(row));
         wv[i] = (uint32_t)((GATE ? row % 16 : row) * p.w_row) + wc[i];
     }
     const int beyond = (int)blockIdx.y - p.experts, step = (int)gridDim.y - p.experts;
@@ -766,13 +767,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_mm_stream(MmTile p) {
         if (turn > 0) __syncthreads();             // the sums of the rows before have been read
         const int rows = place.rows;
         const int64_t t0 = place.t0, row0 = (int64_t)place.e * p.d_out + j0;
-        auto copy = [&](int c) {                   // past the last piece: clears, reads nothing
-            u32x4* const to = ring + (c & 1) * PIECE;
+        auto copy = [&](int c) {                   // past the last line: clears, reads nothing
+            u32x4* const to = ring + (c & 1) * LINE;
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
                 const __amdgpu_buffer_rsrc_t wr = tile_rsrc(p.W[GATE ? i / (LOADS / 2) : 0] + row0 * p.w_row, wrows, p.w_row, c < c1);
-                const int64_t byte = (int64_t)c * 256 + wc[i];
-                tile_dma(wr, to + 64 * i, byte < p.w_bytes ? wv[i] : 0xC0000000u, (uint32_t)c * 256u);
+                const int64_t byte = (int64_t)c * 128 + wc[i];
+                tile_dma(wr, to + 64 * i, byte < p.w_bytes ? wv[i] : 0xC0000000u, (uint32_t)c * 128u);
             }
         };
         const int64_t xrow = t0 + (r < rows ? r : rows - 1);
@@ -783,64 +784,58 @@ __global__ __launch_bounds__(64 * WAVES) void k_mm_stream(MmTile p) {
         for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (c0 < c1) copy(c0);
         for (int c = c0; c < c1; ++c) {
-            // this piece's activations and scales, then the next piece's copies: once those alone are in
-            // flight, both this piece's copies and its activations have arrived
-            u32x4 x[2][2];
-            uint32_t xs[2], ws[2][GATE ? 2 : 1];
+            // this line's activations and scales, then the next line's copies: once those alone are in
+            // flight, both this line's copies and its activations have arrived
+            u32x4 x[2];
+            uint32_t xs, ws[GATE ? 2 : 1];
 #pragma unroll
-            for (int l = 0; l < 2; ++l) {
-                const int line = 2 * c + l, kept = line < lines ? line : lines - 1;
+            for (int j = 0; j < 2; ++j) {
+                const int64_t byte = 128 * (int64_t)c + 64 * j + 16 * b;
+                const u32x4 v = *(const u32x4*)(xp + (byte < p.a_bytes ? byte : 0));
+                x[j] = byte < p.a_bytes ? v : u32x4{0u, 0u, 0u, 0u};
+            }
+            if constexpr (SC) {
+                const uint8_t* const s = (const uint8_t*)p.AS + xrow * p.as_row;
+                xs = mm_bytes(ELT) ? (uint32_t)s[c] : ((const uint32_t*)s)[c];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int64_t byte = 128 * (int64_t)line + 64 * j + 16 * b;
-                    const u32x4 v = *(const u32x4*)(xp + (byte < p.a_bytes ? byte : 0));
-                    x[l][j] = byte < p.a_bytes ? v : u32x4{0u, 0u, 0u, 0u};
-                }
-                if constexpr (SC) {
-                    const uint8_t* const s = (const uint8_t*)p.AS + xrow * p.as_row;
-                    xs[l] = mm_bytes(ELT) ? (uint32_t)s[kept] : ((const uint32_t*)s)[kept];
-#pragma unroll
-                    for (int h = 0; h < (GATE ? 2 : 1); ++h)
-                        ws[l][h] = mm_bytes(ELT) ? (uint32_t)((const uint8_t*)p.WS[h])[sbase + kept] : ((const uint32_t*)p.WS[h])[sbase + kept];
-                }
+                for (int h = 0; h < (GATE ? 2 : 1); ++h)
+                    ws[h] = mm_bytes(ELT) ? (uint32_t)((const uint8_t*)p.WS[h])[sbase + c] : ((const uint32_t*)p.WS[h])[sbase + c];
             }
             __builtin_amdgcn_sched_barrier(0);
             copy(c + 1);
             tile_wait_vmcnt<LOADS>();
             __builtin_amdgcn_sched_barrier(0);
-            const uint8_t* const at = (const uint8_t*)(ring + (c & 1) * PIECE);
+            const uint8_t* const at = (const uint8_t*)(ring + (c & 1) * LINE);
 #pragma unroll
-            for (int l = 0; l < 2; ++l)
+            for (int t = 0; t < MT; ++t) {
+                u32x4 w[2];
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    u32x4 w[2];
+                for (int j = 0; j < 2; ++j) w[j] = *(const u32x4*)(at + 16 * ((16 * t + r) * 8 + ((4 * j + b) ^ mm_swz(r))));
+                if constexpr (ELT == MM_BF16) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) w[j] = *(const u32x4*)(at + 16 * ((16 * t + r) * 16 + ((8 * l + 4 * j + b) ^ r)));
-                    if constexpr (ELT == MM_BF16) {
+                    for (int j = 0; j < 2; ++j) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w[j]), as_bf16x8(x[j]), acc[t], 0, 0, 0);
+                } else if constexpr (ELT == MM_E8) {
+                    acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm_pair(w[0], w[1]), mm_pair(x[0], x[1]), acc[t], 0, 0, 0, (int)ws[GATE ? t : 0], 0, (int)xs);
+                } else {
+                    f32x4 d{0.f, 0.f, 0.f, 0.f};
+                    if constexpr (mm_wide(ELT)) {
+                        u32x4 a[4], v[4];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w[j]), as_bf16x8(x[l][j]), acc[t], 0, 0, 0);
-                    } else if constexpr (ELT == MM_E8) {
-                        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm_pair(w[0], w[1]), mm_pair(x[l][0], x[l][1]), acc[t], 0, 0, 0, (int)ws[l][GATE ? t : 0], 0, (int)xs[l]);
-                    } else {
-                        f32x4 d{0.f, 0.f, 0.f, 0.f};
-                        if constexpr (mm_wide(ELT)) {
-                            u32x4 a[4], v[4];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                mm_widen(w[j], a[2 * j], a[2 * j + 1]);
-                                mm_widen(x[l][j], v[2 * j], v[2 * j + 1]);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), as_bf16x8(v[j]), d, 0, 0, 0);
-                        } else {
-                            d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm_pair(w[0], w[1]), mm_pair(x[l][0], x[l][1]), d, 0, 0, 0, 127, 0, 127);
+                        for (int j = 0; j < 2; ++j) {
+                            mm_widen(w[j], a[2 * j], a[2 * j + 1]);
+                            mm_widen(x[j], v[2 * j], v[2 * j + 1]);
                         }
-                        const uint32_t wk = ws[l][GATE ? t : 0];
-                        const float by = mm_bytes(ELT) ? fp8_scale_value(wk) * fp8_scale_value(xs[l]) : __uint_as_float(wk) * __uint_as_float(xs[l]);
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(d[v], by, acc[t][v]);
+                        for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[j]), as_bf16x8(v[j]), d, 0, 0, 0);
+                    } else {
+                        d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm_pair(w[0], w[1]), mm_pair(x[0], x[1]), d, 0, 0, 0, 127, 0, 127);
                     }
+                    const uint32_t wk = ws[GATE ? t : 0];
+                    const float by = mm_bytes(ELT) ? fp8_scale_value(wk) * fp8_scale_value(xs) : __uint_as_float(wk) * __uint_as_float(xs);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(d[v], by, acc[t][v]);
                 }
+            }
             __builtin_amdgcn_sched_barrier(0);
             tile_wait_lds();                       // read, before its half of the ring is copied into
         }
@@ -902,7 +897,7 @@ static hipError_t mm_launch_tile(const MmTile& t, const MmPlan& P, hipStream_t s
 template <int ELT, bool GATE, int MT, int WAVES>
 static hipError_t mm_launch_stream(const MmTile& t, const MmPlan& P, hipStream_t st) {
     const auto k = k_mm_stream<ELT, GATE, MT, WAVES>;
-    const size_t lds = (size_t)WAVES * 2 * 16 * MT * 16 * 16;
+    const size_t lds = (size_t)WAVES * 2 * 16 * MT * 8 * 16;
     const hipError_t e = ensure_dynamic_lds((const void*)k, lds);
     if (e != hipSuccess) return e;
     // a block for each expert, and for the groups beyond its own those of a compute unit each

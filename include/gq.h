@@ -510,7 +510,8 @@ gq_status fp8_dequantize_weight(const uint8_t* Q, const void* S, gq_scale s_dt, 
  *
  * Precision: products of codes are exact.  Each block's sum is multiplied by the product of its two scales, a
  * float32 rounding each (none with GQ_SCALE_E8M0, within float32's range), and added in float32.  For a float32
- * output all sums are float32.  For a bfloat16 one the matrix cores add the products of eight
+ * output all sums are float32 (with GQ_SCALE_E8M0 a code times its scale that is below 2^-133 is rounded to a multiple of
+ * that there, one from 2^128 on an infinity).  For a bfloat16 one the matrix cores add the products of eight
  * consecutive values to 14 bits: each is cut off at 2^-13 of the largest of the eight, which leaves about 4e-5 of the
  * result, a fortieth of its rounding, for twice the rate; between eights sums are float32.  y is rounded once to
  * y_dt.  A NaN stays within its row of x (and, from a weight's block, its columns of y).

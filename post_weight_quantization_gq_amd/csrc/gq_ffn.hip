@@ -5,7 +5,7 @@
 // zg and zu are the forward pass's float32 products: rounded to bfloat16 they would add its half step to
 // every gradient a second time, and their bytes are a twentieth of a training step's time.  dzg and dzu are
 // rounded once, to the bfloat16 that the products after them multiply (and that the Fisher takes).
-// One pass, bound by HBM: 14 bytes a value with a bfloat16 dh.
+// One pass, bound by HBM: 14 bytes a value with a bfloat16 dh (4096 x 11008: 125 us, 5.0 TB/s).
 #include "gq_mm.h"
 
 namespace gq {

@@ -8,6 +8,9 @@
 //
 // A lane takes 8 consecutive values: 16 lanes are a row's block, its maximum four exchanges.  A weight's
 // block is 256 lanes that keep their 64 values in registers between the maximum and the rounding.
+//
+// 8192 x 28672 bfloat16 values: rows packed in 122 to 125 us (5.7 TB/s), a weight in 145 to 160 (4.4 to 4.9), read back in
+// 118 to 128 (5.5 to 6.0); one row of 4096 in 1.8 us.
 #include "gq_mm.h"
 
 namespace gq {

@@ -1270,8 +1270,9 @@ def _ffn_weights(G, U, offsets, index):
     return (1, *G.shape) if offsets is None else tuple(G.shape)
 
 
-def _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream, fill=True):
-    """fill: saved products have zeros in the rows of no expert."""
+def _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream):
+    """(h, zg, zu, sizes); for autograd (save = "joint") both products are one tensor [2][n][d_ff], whose rows of
+    no expert are not filled."""
     lib = _lib or library()
     act = _act_id(act)
     if x.dim() != 2:
@@ -1291,17 +1292,34 @@ def _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream, fill=Tru
         new = x.new_empty if offsets is None else x.new_zeros
         if y is None:
             y = new((n, d_ff), dtype=out_dtype)
-        zg = zu = None
-        if save:
-            keep = new if fill else x.new_empty
-            zg, zu = keep((n, d_ff), dtype=torch.float32), keep((n, d_ff), dtype=torch.float32)
+        zg = zu = zgp = zup = None
+        if save == "joint":
+            zg = x.new_empty((2, n, d_ff), dtype=torch.float32)
+            zgp = zg.data_ptr()
+            zup = zgp + 4 * n * d_ff
+        elif save:
+            zg, zu = new((n, d_ff), dtype=torch.float32), new((n, d_ff), dtype=torch.float32)
+            zgp, zup = zg.data_ptr(), zu.data_ptr()
         keep, wp, wn = _mm_scratch(x, ws, lib.ffn_gate_workspace_size, (n, d_in, d_ff, experts))
         status = lib.ffn_gate(x.data_ptr(), n, d_in, G.data_ptr(), U.data_ptr(), d_ff, act, experts, op,
-                              y.data_ptr(), _MX_DTYPES[y.dtype], zg.data_ptr() if save else None,
-                              zu.data_ptr() if save else None, wp, wn, st)
+                              y.data_ptr(), _MX_DTYPES[y.dtype], zgp, zup, wp, wn, st)
     if status:
         _check(status)
-    return (y, zg, zu) if save else y
+    return y, zg, zu, (n, d_in, d_ff, experts, act)
+
+
+def _ffn_gradients(ctx, dh):
+    """What _FfnGate.backward gives; the forward pass has checked all but dh."""
+    x, G, U, z, offsets = ctx.saved_tensors
+    n, _, d_ff, _, _ = ctx.sizes
+    dh = dh.contiguous()
+    _mx_tensor(dh, "dh", x.get_device())
+    zg = z.data_ptr()
+    return (*_ffn_backward(dh, x, G, U, zg, zg + 4 * n * d_ff, offsets, ctx.sizes, ctx.needs_input_grad,
+                           [None, None, None], torch.bfloat16, None, None), None, None, None, None)
+
+
+_ffn_gradients_once = torch.autograd.function.once_differentiable(_ffn_gradients)
 
 
 class _FfnGate(torch.autograd.Function):
@@ -1309,18 +1327,14 @@ class _FfnGate(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, G, U, act, offsets, out_dtype, ws):
-        h, zg, zu = _ffn_forward(x, G, U, act, offsets, None, out_dtype, True, ws, None, fill=False)
-        ctx.save_for_backward(x, G, U, zg, zu, offsets)
-        ctx.act = act
+        h, z, _, ctx.sizes = _ffn_forward(x, G, U, act, offsets, None, out_dtype, "joint", ws, None)
+        ctx.save_for_backward(x, G, U, z, offsets)
         return h
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dh):
-        x, G, U, zg, zu, offsets = ctx.saved_tensors
-        grads = ffn_gate_backward(dh.contiguous(), x, G, U, zg, zu, act=ctx.act, offsets=offsets,
-                                  which=ctx.needs_input_grad[:3])
-        return (*grads, None, None, None, None)
+        # (a graph of the gradients is asked for: they are marked as without one)
+        return (_ffn_gradients_once if torch.is_grad_enabled() else _ffn_gradients)(ctx, dh)
 
 
 def ffn_gate(x, G, U, act: str = "silu", offsets=None, y=None, out_dtype=None, save: bool = False,
@@ -1341,7 +1355,8 @@ def ffn_gate(x, G, U, act: str = "silu", offsets=None, y=None, out_dtype=None, s
         where, _ = _place(x, stream)
         with where:
             return _FfnGate.apply(x, G, U, act, offsets, out_dtype, ws)
-    return _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream)
+    h, zg, zu, _ = _ffn_forward(x, G, U, act, offsets, y, out_dtype, bool(save), ws, stream)
+    return (h, zg, zu) if save else h
 
 
 def ffn_gate_dz(dh, zg, zu, act: str = "silu", dzg=None, dzu=None, stream=None):
@@ -1445,6 +1460,28 @@ def ffn_gate_dw(dzg, dzu, x, experts=None, offsets=None, which=(True, True), dG=
     return tuple(out)
 
 
+def _ffn_backward(dh, x, G, U, zg, zu, offsets, sizes, which, out, dw, ws, stream):
+    """The call of ffn_gate_backward: zg and zu by their addresses, `out` the outputs that are given."""
+    lib = _lib or library()
+    n, d_in, d_ff, experts, act = sizes
+    where, st = _place(x, stream)
+    with where:
+        if which[0] and out[0] is None:
+            out[0] = (x.new_empty if offsets is None else x.new_zeros)((n, d_in))
+        for i in (1, 2):
+            if which[i] and out[i] is None:
+                out[i] = x.new_empty(G.shape, dtype=dw)
+        keep, wp, wn = _mm_scratch(x, ws, lib.ffn_gate_backward_workspace_size, sizes[:4])
+        at = [None if t is None else t.data_ptr() for t in out]
+        status = lib.ffn_gate_backward(dh.data_ptr(), _MX_DTYPES[dh.dtype], x.data_ptr(), n, d_in, G.data_ptr(),
+                                       U.data_ptr(), d_ff, act, experts, None if offsets is None else offsets.data_ptr(),
+                                       zg, zu, at[0], GQ_BF16 if out[0] is None else _MX_DTYPES[out[0].dtype], at[1], at[2],
+                                       _MX_DTYPES[dw], wp, wn, st)
+    if status:
+        _check(status)
+    return tuple(out)
+
+
 def ffn_gate_backward(dh, x, G, U, zg, zu, act: str = "silu", offsets=None, which=(True, True, True), dx=None,
                       dG=None, dU=None, ws=None, stream=None):
     """(dx, dG, dU), the gradients of ffn_gate's x, G and U from that of h (float32 or bfloat16) and
@@ -1464,7 +1501,7 @@ def ffn_gate_backward(dh, x, G, U, zg, zu, act: str = "silu", offsets=None, whic
     for t, name in ((zg, "zg"), (zu, "zu")):
         _mx_shape(t, (n, d_ff), name)
         _mx_tensor(t, name, index, _F32)
-    op = _mm_offsets(offsets, experts, index)
+    _mm_offsets(offsets, experts, index)
     out, shapes = [dx, dG, dU], ((n, d_in), G.shape, G.shape)
     for i, name in enumerate(("dx", "dG", "dU")):
         if out[i] is not None:
@@ -1479,22 +1516,8 @@ def ffn_gate_backward(dh, x, G, U, zg, zu, act: str = "silu", offsets=None, whic
         raise GQError(GQ_EDTYPE, f"dG is {dG.dtype}, dU {dU.dtype}")
     if ws is not None and ws is not False:
         _mx_tensor(ws, "ws", index, _U8)
-    where, st = _place(x, stream)
-    with where:
-        if which[0] and dx is None:
-            out[0] = (x.new_empty if offsets is None else x.new_zeros)((n, d_in))
-        for i in (1, 2):
-            if which[i] and out[i] is None:
-                out[i] = x.new_empty(G.shape, dtype=dw)
-        keep, wp, wn = _mm_scratch(x, ws, lib.ffn_gate_backward_workspace_size, (n, d_in, d_ff, experts))
-        at = [None if t is None else t.data_ptr() for t in out]
-        status = lib.ffn_gate_backward(dh.data_ptr(), _MX_DTYPES[dh.dtype], x.data_ptr(), n, d_in, G.data_ptr(),
-                                       U.data_ptr(), d_ff, act, experts, op, zg.data_ptr(), zu.data_ptr(), at[0],
-                                       _MX_DTYPES[out[0].dtype] if which[0] else GQ_BF16, at[1], at[2],
-                                       _MX_DTYPES[dw], wp, wn, st)
-    if status:
-        _check(status)
-    return tuple(out)
+    return _ffn_backward(dh, x, G, U, zg.data_ptr(), zu.data_ptr(), offsets, (n, d_in, d_ff, experts, act), which, out, dw, ws,
+                         stream)
 
 
 STAGES = ("group_scale", "fisher_mfma", "fisher_finalize", "fisher_plain", "lnq_prepare",

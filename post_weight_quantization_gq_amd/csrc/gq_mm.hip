@@ -216,8 +216,13 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
     P.unit = fp8 ? 4 : 1;
     P.split = 1;
     const int64_t wcols = gate ? 2 * m : m;                                       // rows of weights that outputs need
-    P.stream = (form == MM_NT || gate) && per <= 16 && per * k * (fp8 ? 1 : 2) <= 1 << 18 && k * (fp8 ? 1 : 2) <= 1 << 15 &&
-               live * ((wcols + 127) / 128) < 192;
+    // Streamed: up to 16 rows of one weight, 8 an expert on average.  Its activations come from the L2 again for
+    // each block, so not for the longest rows (16 rows with float32 scales, 28672 -> 8192: 47.0 us streamed, 40.6 by
+    // tiles; 1 row 36.4 and 40.3), and 8-bit sums of one weight so wide that tiles fill the card go by tiles (1 row,
+    // 8192 -> 28672: 39.7 and 36.2; in bfloat16 sums 38.7 and 49.9).  16 rows, 128 experts of 4096 -> 1536: 20.2 us streamed,
+    // 23.9 by tiles, their packed gate 40.7 and 64.6; 512 rows, 64 experts of 2048 -> 1408 35.3 and 34.5, 700 rows 41.3 and 34.9.
+    P.stream = (form == MM_NT || gate) && per <= (experts > 1 ? 8 : 16) && per * k <= 1 << 18 &&
+               (experts > 1 || !fp8 || wide || (wcols + 127) / 128 < 192);
     if (P.stream) {
         P.bm = 16;
         P.bn = gate || live * ((m + 31) / 32) >= 256 ? 32 : 16;

@@ -152,11 +152,11 @@ def test_one_tensor_for_both_weights_and_an_expanded_gradient(device):
     assert torch.equal(gq.fp8_ffn_gate(*rows, Q, S, Q, S, d_in), a)
 
 
-@pytest.mark.parametrize("n,experts,full", [(2000, 200, 7), (2000, 200, 199), (640, 40, 0)])
+@pytest.mark.parametrize("n,experts,full", [(1600, 200, 7), (1600, 200, 199), (280, 40, 0), (2000, 40, 39)])
 @pytest.mark.parametrize("op", ["gemm", "gate8", "gate", "packed"])
 def test_one_expert_has_nearly_all_rows(device, op, n, experts, full):
-    """Ten and sixteen rows an expert on average, so that weights are streamed: and one has them all but
-    a few."""
+    """Eight rows an expert or fewer on average, so that weights are streamed, and one expert has them all but
+    a few; and more rows, by tiles."""
     d_in, d_out = 264, 130
     some = [0 if e % 3 else 1 for e in range(experts)]
     some[full] = n - 5 - (sum(some) - some[full])

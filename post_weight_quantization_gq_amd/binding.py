@@ -954,14 +954,18 @@ def _act_id(act):
 def _pack(fn, x, codes, scale_shape, sizes, Q, S, scales, stream):
     """What both quantisations share: x's checks, the outputs and the call."""
     index = x.get_device()
-    if S is not None and scales is not None and S.dtype != scales:
-        raise GQError(GQ_EDTYPE, f"S is {S.dtype}, scales {scales}")
-    dt = torch.uint8 if S is None and scales is None else (scales if S is None else S.dtype)
+    if S is None:
+        dt = torch.uint8 if scales is None else scales
+    else:
+        dt = S.dtype
+        if scales is not None and dt != scales:
+            raise GQError(GQ_EDTYPE, f"S is {S.dtype}, scales {scales}")
+        _mx_shape(S, scale_shape, "S")
+        _mx_tensor(S, "S", index, _SCALES)
     st_dt = _scale_type(dt)
-    for t, shape, name, kinds in ((Q, codes, "Q", _FP8), (S, scale_shape, "S", _SCALES)):
-        if t is not None:
-            _mx_shape(t, shape, name)
-            _mx_tensor(t, name, index, kinds)
+    if Q is not None:
+        _mx_shape(Q, codes, "Q")
+        _mx_tensor(Q, "Q", index, _FP8)
     _mx_tensor(x, "x", index)
     where, st = _place(x, stream)
     with where:
@@ -982,7 +986,7 @@ def fp8_quantize(x, Q=None, S=None, scales=None, stream=None):
     lib = _lib or library()
     if x.dim() < 1:
         raise GQError(GQ_ESHAPE, "x needs a last dimension to quantise along")
-    lead, d = x.shape[:-1], x.shape[-1]
+    *lead, d = x.shape
     rb, rs = _fp8_width(d)
     return _pack(lib.fp8_quantize, x, (*lead, rb), (*lead, rs), (x.numel() // d, d), Q, S, scales, stream)
 
@@ -1052,6 +1056,11 @@ def _fp8_weight_shape(Q, S, d_in, offsets):
 
 def _fp8_weight(Q, S, d_in, offsets, index, scales):
     """(experts, d_out) of a packed weight whose scales are of the type of the rows' scales."""
+    shape, blocks = Q.shape, (d_in + 127) // 128
+    if (offsets is None and len(shape) == 2 and shape[1] == 128 * blocks and
+            S.shape == ((shape[0] + 127) // 128, blocks) and Q.get_device() == S.get_device() == index and
+            Q.dtype in _FP8 and S.dtype == scales and Q.is_contiguous() and S.is_contiguous()):
+        return 1, shape[0]
     found = _fp8_weight_shape(Q, S, d_in, offsets)
     _mx_tensor(Q, "Q", index, _FP8)
     _mx_tensor(S, "S", index, _SCALES)
@@ -1061,8 +1070,12 @@ def _fp8_weight(Q, S, d_in, offsets, index, scales):
 
 
 def _fp8_rows(Q, S, d, names):
-    """Rows of a packed operand."""
+    """(rows, device) of a packed operand."""
     rb, rs = _fp8_width(d)
+    shape, index = Q.shape, Q.get_device()
+    if (len(shape) == 2 and shape[1] == rb and S.shape == (shape[0], rs) and S.get_device() == index >= 0 and
+            Q.dtype in _FP8 and S.dtype in _SCALES and Q.is_contiguous() and S.is_contiguous()):
+        return shape[0], index
     if Q.dim() != 2:
         raise GQError(GQ_ESHAPE, f"{names[0]} must be [n][row bytes]")
     n, index = Q.shape[0], Q.get_device()

@@ -262,7 +262,8 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
                 float load = (float)(blocks * split) / 256.f;
                 load = load < 1.f ? 1.f : (load < 8.f ? ceilf(load) : load);
                 const bool join = split > 1 || (packed && bn != 256);
-                const float t = cost.fixed[i] * sqrtf(load) + cost.stage[i] * (float)(split > 1 ? some : stages) * powf(load, .85f) +
+                const float each_tile = load > 1.f ? powf(load, .85f) : 1.f;
+                const float t = cost.fixed[i] * sqrtf(load) + cost.stage[i] * (float)(split > 1 ? some : stages) * each_tile +
                                 (join ? cost.join + (float)split * (float)outputs / (1000.f * cost.sums) : 0.f);
                 if (best == 0.f || t < best) {
                     best = t;

@@ -14,18 +14,35 @@
 
 namespace gq {
 
-// Rows of k bfloat16 values as rows of a multiple of 8, zeros behind.
-__global__ __launch_bounds__(256) void k_mm_pad(const void* __restrict__ x, int64_t rows, int64_t k, int64_t pieces,
-                                               u32x4* __restrict__ out) {
-    const int64_t total = rows * pieces, stride = (int64_t)gridDim.x * 256;
+// Rows of k bfloat16 values as rows of a multiple of 8, zeros behind: up to four arrays of them, `ends` the
+// pieces of 8 up to each one's end.  One launch: a call of few rows is mostly launches (196 rows, gate of 1967 -> 585: 24.2 us by
+// three launches, 20.3 so).
+struct MmPadded {
+    const void* x[4];
+    int64_t k[4], ends[4];
+    u32x4* out[4];
+};
+__global__ __launch_bounds__(256) void k_mm_pad(MmPadded a, int arrays) {
+    const int64_t total = a.ends[arrays - 1], stride = (int64_t)gridDim.x * 256;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += stride) {
-        const int64_t r = mx_div(t, pieces), i = (t - r * pieces) * 8;
+        const void* x = a.x[0];
+        int64_t k = a.k[0], at = t;
+        u32x4* out = a.out[0];
+#pragma unroll
+        for (int n = 1; n < 4; ++n)
+            if (n < arrays && t >= a.ends[n - 1]) {
+                x = a.x[n];
+                k = a.k[n];
+                at = t - a.ends[n - 1];
+                out = a.out[n];
+            }
+        const int64_t pieces = (k + 7) / 8, r = mx_div(at, pieces), i = (at - r * pieces) * 8;
         float v[8];
         mx_load8<true>(x, r * k, i, k, v);
         u32x4 w;
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = (__float_as_uint(v[2 * e]) >> 16) | (__float_as_uint(v[2 * e + 1]) & 0xffff0000u);
-        out[t] = w;
+        out[at] = w;
     }
 }
 
@@ -306,26 +323,34 @@ hipError_t mm_run(const MmCall& c, void* ws, hipStream_t st) {
     const int64_t ak = nn || tn ? c.d_out : c.d_in, m = nn || tn ? c.d_in : c.d_out;
     char* at = (char*)ws;
     // rows of k values, copied to a multiple of 8 where they are none
-    auto padded = [&](const void* x, int64_t rows, int64_t k, size_t bytes, const uint8_t*& out) -> hipError_t {
-        out = (const uint8_t*)x;
-        if (!bytes || !x) return hipSuccess;
-        const int64_t pieces = mm_al8(k) / 8, blocks = (rows * pieces + 255) / 256;
-        out = (const uint8_t*)at;
-        if (blocks > 0) {
-            hipLaunchKernelGGL(k_mm_pad, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, x, rows, k, pieces, (u32x4*)at);
-            GQ_LAUNCH_CHECK();
+    MmPadded copies{};
+    int arrays = 0;
+    auto padded = [&](const void* x, int64_t rows, int64_t k, size_t bytes) -> const uint8_t* {
+        if (!bytes || !x) return (const uint8_t*)x;
+        const uint8_t* const out = (const uint8_t*)at;
+        const int64_t pieces = rows * (mm_al8(k) / 8);
+        if (pieces > 0) {
+            copies.x[arrays] = x;
+            copies.k[arrays] = k;
+            copies.ends[arrays] = pieces + (arrays ? copies.ends[arrays - 1] : 0);
+            copies.out[arrays++] = (u32x4*)at;
         }
         at += bytes;
-        return hipSuccess;
+        return out;
     };
     MmTile t{};
     hipError_t e;
     for (int i = 0; i < 2; ++i) {
-        if ((e = padded(c.a[i], c.n, ak, pads.a, t.A[i])) != hipSuccess) return e;
-        if ((e = padded(c.w[i], tn ? c.n : c.experts * c.d_out, c.d_in, pads.w, t.W[i])) != hipSuccess) return e;
+        t.A[i] = padded(c.a[i], c.n, ak, pads.a);
+        t.W[i] = padded(c.w[i], tn ? c.n : c.experts * c.d_out, c.d_in, pads.w);
         t.WS[i] = c.ws[i];
         t.y[i] = c.y[i];
         t.z[i] = c.z[i];
+    }
+    if (arrays) {
+        const int64_t blocks = (copies.ends[arrays - 1] + 255) / 256;
+        hipLaunchKernelGGL(k_mm_pad, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, copies, arrays);
+        GQ_LAUNCH_CHECK();
     }
     t.a_row = t.a_bytes = fp8 ? fp8_bytes(ak) : 2 * mm_al8(ak);
     t.w_row = t.w_bytes = fp8 ? fp8_bytes(c.d_in) : 2 * mm_al8(c.d_in);

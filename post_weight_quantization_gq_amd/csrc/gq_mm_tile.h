@@ -1,5 +1,5 @@
 // Tiled products of one element type on gfx950: the kernels that gq_mm.hip plans and launches, included
-// by the one file of each type (gq_mm_bf16.hip, gq_mm_e8.hip, gq_mm_fs.hip).
+// by the one file of each type (gq_mm_bf16.hip, gq_mm_e8.hip, gq_mm_fs.hip, gq_mm_e8w.hip, gq_mm_fsw.hip).
 #pragma once
 #include "gq_mm.h"
 #include "gq_mm_plan.h"
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
     };
     // The rows' scales: four stages' of a row at a time, a quarter of the next four's rows with each stage.
     uint8_t* const sc_lds = lds + R * G::STAGE * 16;
-        constexpr int SW = SC ? (BM / 4 / NW > 0 ? BM / 4 / NW : 1) : 1;        // rows of a wave's copy
+    constexpr int SW = SC ? (BM / 4 / NW > 0 ? BM / 4 / NW : 1) : 1;            // rows of a wave's copy
     static_assert(!SC || SW * NW * 4 == BM, "every wave copies scales");
     auto scale_copy = [&](int span, int row, bool on) {
         if constexpr (SC) {

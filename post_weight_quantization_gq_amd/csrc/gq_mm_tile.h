@@ -575,8 +575,34 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                 }
             });
             const int row0 = wm * TM + 16 * q, left = rows - row0;
+            // products out, whole lines at a time, and h past the caches' order, which leaves them the operands (4 rounds of
+            // 25 stages in bfloat16: 184 us for h alone, 178 so; with both products 227 and 214.  The products too: 209, but
+            // the backward pass that reads them next is slower by as much)
+            if (z0) {
+                constexpr int FOURS = HC / 4;
 #pragma unroll 1
-            for (int i = lane; i < 16 * LANES; i += 64) {         // products out, h out or back in their place
+                for (int i = lane; i < 16 * FOURS; i += 64) {
+                    const int row = i / FOURS, c4 = 4 * (i % FOURS), some = cols - c4;
+                    if (row >= left || some <= 0) continue;
+                    const uint8_t* const from = own + row * G::PITCH + c4 * 4;
+                    const f32x4 a = *(const f32x4*)from, b = *(const f32x4*)(from + HC * 4);
+                    const int64_t to = at + (int64_t)(row0 + row) * p.m + c4;
+                    if (some >= 4) {
+                        *(f32x4_any*)(z0 + to) = a;
+                        *(f32x4_any*)(z1 + to) = b;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+                            if (k < some) {
+                                z0[to + k] = a[k];
+                                z1[to + k] = b[k];
+                            }
+                    }
+                }
+                if (p.part) continue;
+            }
+#pragma unroll 1
+            for (int i = lane; i < 16 * LANES; i += 64) {         // h out or back in its place
                 const int row = i / LANES, c8 = 8 * (i % LANES), some = cols - c8;
                 uint8_t* const from = own + row * G::PITCH + c8 * 4;
                 f32x4 a[2], b[2];
@@ -597,11 +623,6 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                             if (k < some) y[to + k] = x[k / 4][k % 4];
                     }
                 };
-                if (z0 && stored) {
-                    values(z0, a);
-                    values(z1, b);
-                }
-                if (p.part) continue;
                 f32x4 h[2];
                 if (p.act == ACT_SILU) {
 #pragma unroll
@@ -635,8 +656,9 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                 if (!p.y_bf16) {
                     values((float*)p.y[0], h);
                 } else if (some >= 8) {
-                    *(u32x4_any*)((uint16_t*)p.y[0] + to) = u32x4{pack_bf16x2(h[0][0], h[0][1]), pack_bf16x2(h[0][2], h[0][3]),
-                                                                  pack_bf16x2(h[1][0], h[1][1]), pack_bf16x2(h[1][2], h[1][3])};
+                    __builtin_nontemporal_store((u32x4_any)u32x4{pack_bf16x2(h[0][0], h[0][1]), pack_bf16x2(h[0][2], h[0][3]),
+                                                                 pack_bf16x2(h[1][0], h[1][1]), pack_bf16x2(h[1][2], h[1][3])},
+                                                (u32x4_any*)((uint16_t*)p.y[0] + to));
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)

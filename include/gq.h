@@ -563,7 +563,7 @@ gq_status fp8_ffn_gate_packed(const uint8_t* XQ, const void* XS, int64_t n, int6
  *   ffn_gate     h (h_dt), and where zg and zu are not NULL (both or neither) the two products
  *                zg = x G^T and zu = x U^T [n][d_ff] in float32, which the backward pass takes;
  *   ffn_gate_dz  dzg = dh zu act'(zg), dzu = dh act(zg), in bfloat16: the gradients of both projections'
- *                outputs, which gq_fisher_accumulate takes with x; `count` values each;
+ *                outputs, which gq_fisher_accumulate takes with x; `count` values each, at most 2^34;
  *   ffn_gate_dx  dx [n][d_in] = dzg G + dzu U;
  *   ffn_gate_dw  dG [d_ff][d_in] = dzg^T x, dU = dzu^T x (dw_dt), each expert's over its own rows
  *                (zeros where it has none); with NULL for dG or dU that one is left out.

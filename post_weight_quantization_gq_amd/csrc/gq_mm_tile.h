@@ -725,7 +725,10 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                     if (row >= left || some <= 0) continue;
                     uint8_t* const to = out + (int64_t)(row0 + row) * p.m * wide + at16;
                     if (!decltype(ends)::value || some >= 16) {
-                        *(u32x4_any*)to = v;
+                        // (weights' gradients past the caches' order: forward and back of 4096 tokens, 4096 -> 11008 1957
+                        // us, 1945 so; the other forms' outputs, which are read next, gain nothing)
+                        if constexpr (FORM == MM_TN) __builtin_nontemporal_store((u32x4_any)v, (u32x4_any*)to);
+                        else *(u32x4_any*)to = v;
                     } else {
                         for (int b = 0; b < some; b += wide) {
                             if (wide == 4) *(uint32_t*)(to + b) = v[b / 4];

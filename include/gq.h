@@ -509,7 +509,9 @@ gq_status fp8_dequantize_weight(const uint8_t* Q, const void* S, gq_scale s_dt, 
  * range; the rows that they concern hold unspecified values.
  *
  * Precision: products of codes are exact.  Each block's sum is multiplied by the product of its two scales, a
- * float32 rounding each (none with GQ_SCALE_E8M0, within float32's range), and added in float32.  For a float32
+ * float32 rounding each (none with GQ_SCALE_E8M0, within float32's range), and added in float32.  With GQ_SCALE_F32 the
+ * product of the two scales is a float32 number of its own: one from 2^128 on makes the block's sum infinite (NaN a sum of
+ * zero), one below 2^-149 zero.  For a float32
  * output all sums are float32 (with GQ_SCALE_E8M0 a code times its scale that is below 2^-133 is rounded to a multiple of
  * that there, one from 2^128 on an infinity).  For a bfloat16 one the matrix cores add the products of eight
  * consecutive values to 14 bits: each is cut off at 2^-13 of the largest of the eight, which leaves about 4e-5 of the

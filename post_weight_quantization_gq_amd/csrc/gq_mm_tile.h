@@ -861,9 +861,18 @@ __global__ __launch_bounds__(64 * WAVES) void k_mm_stream(MmTile p) {
                         d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm_pair(w[0], w[1]), mm_pair(x[0], x[1]), d, 0, 0, 0, 127, 0, 127);
                     }
                     const uint32_t wk = ws[GATE ? t : 0];
-                    const float by = mm_bytes(ELT) ? fp8_scale_value(wk) * fp8_scale_value(xs) : __uint_as_float(wk) * __uint_as_float(xs);
+                    if constexpr (mm_bytes(ELT)) {
+                        // by the sum of the exponents: their powers' product need not be a float32 number where
+                        // the result is one (2^100 by 2^100 would make NaN of a zero sum)
+                        const int by = (int)(wk + xs) - 254;
+                        const bool nan = wk == 255u || xs == 255u;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(d[v], by, acc[t][v]);
+                        for (int v = 0; v < 4; ++v) acc[t][v] += nan ? __uint_as_float(0x7fc00000u) : __builtin_amdgcn_ldexpf(d[v], by);
+                    } else {
+                        const float by = __uint_as_float(wk) * __uint_as_float(xs);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(d[v], by, acc[t][v]);
+                    }
                 }
             }
             __builtin_amdgcn_sched_barrier(0);

@@ -255,8 +255,11 @@ static MmPlan mm_plan(MmForm form, MmElt elt, int64_t n, int64_t d_in, int64_t d
         s = s < units ? s : units;
         s = s < 1 ? 1 : (s > 16 ? 16 : s);
         if (s > 1) {
-            const int64_t each = (units + s - 1) / s;                             // no part without work
-            P.split = (int)((units + each - 1) / each);
+            const int64_t some = (units + s - 1) / s, parts = (units + some - 1) / some;
+            // no part without a line, as the kernel shares them among all parts' waves (1 row, gate of 11008 -> 130: 172
+            // lines, three a wave: 8 parts, of 10 two would write and add zeros)
+            const int64_t each = (one + P.waves * parts - 1) / (P.waves * parts);
+            P.split = (int)((one + each * P.waves - 1) / (each * P.waves));
         }
         P.join = P.split > 1 || packed;
     } else {

@@ -783,15 +783,15 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
     P.stream = op != MX_GEMM_DX && per <= 16 && per * k <= room && live * ((m + 127) / 128) < 192;
     P.split = 1;
     P.stages = P.unit = 0;
-    int64_t blocks, units;
+    int64_t blocks, units, pieces = 0;
     if (P.stream) {
         P.bm = 16;
         P.bn = live * ((m + 31) / 32) >= 256 ? 32 : 16;
         const int ku = P.planes == 3 ? 2 : 4;
-        units = (mx_groups(k) + ku - 1) / ku;
-        P.waves = units >= 8 ? 8 : 4;
+        pieces = (mx_groups(k) + ku - 1) / ku;
+        P.waves = pieces >= 8 ? 8 : 4;
         blocks = live * ((m + P.bn - 1) / P.bn);
-        units /= P.waves;
+        units = pieces / P.waves;
     } else {
         // The largest tile that the rows of a weight fill and that gives most compute units
         // one, else the smallest: 1024 rows 4096 -> 4096 take 40 us by 128 x 128 and 54 by
@@ -837,6 +837,10 @@ static MxPlan mx_plan(MxOp op, bool a_bf16, int64_t n, int64_t d_in, int64_t d_o
         while (!P.stream && s > 1 && s * s * n * m * 20 > P.stages * (s - 1) * t * 1000000) --s;
         const int64_t each = (units + s - 1) / s;        // no part without work
         P.split = (int)((units + each - 1) / each);
+        if (P.stream) {                                  // (nor one without a piece, as the kernel shares them out)
+            const int64_t some = (pieces + P.waves * P.split - 1) / (P.waves * P.split);
+            P.split = (int)((pieces + some * P.waves - 1) / (some * P.waves));
+        }
     }
     P.part_bytes = P.split > 1 ? mx_al256((size_t)P.split * n * m * 4) : 0;
     return P;

@@ -668,6 +668,15 @@ def _mx_tensor(t, name, index, dtypes=_MX_DTYPES):
     raise GQError(GQ_EINVAL, f"{name} is on {t.device}, the call's first tensor is not")
 
 
+def _no_tangents(**tensors):
+    """Inside a forward-mode level: the calls give no tangents, and would drop those of their tensors."""
+    for name, t in tensors.items():
+        if torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+            raise GQError(GQ_EINVAL, f"{name} has a forward-mode tangent, which the call would not carry on: "
+                                     "there are gradients by backward() alone")
+
+
+_fw = torch.autograd.forward_ad
 _U8, _I64 = (torch.uint8,), (torch.int64,)
 _MX_MAX_D = 1 << 20
 
@@ -854,6 +863,8 @@ def mxfp4_gemm(x, Q, S, offsets=None, y=None, out_dtype=None, ws=None, stream=No
     lib = _lib or library()
     if x.dim() != 2:
         raise GQError(GQ_ESHAPE, "x must be [n][d_in]")
+    if _fw._current_level >= 0:
+        _no_tangents(x=x)
     n, d_in = x.shape
     if x.requires_grad and torch.is_grad_enabled():
         return _mx_recorded(x, "x", Q, S, d_in, offsets, y, out_dtype, ws, stream, False)
@@ -900,6 +911,8 @@ def mxfp4_gemm_dx(g, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=N
     lib = _lib or library()
     if g.dim() != 2:
         raise GQError(GQ_ESHAPE, "g must be [n][d_out]")
+    if _fw._current_level >= 0:
+        _no_tangents(g=g)
     if g.requires_grad and torch.is_grad_enabled():
         return _mx_recorded(g, "g", Q, S, d_in, offsets, y, out_dtype, ws, stream, True)
     n = g.shape[0]
@@ -1359,7 +1372,9 @@ def ffn_gate(x, G, U, act: str = "silu", offsets=None, y=None, out_dtype=None, s
     values (of a new one: zeros).  out_dtype: float32 or bfloat16, x's unless given.
     With save: (h, zg, zu), zg = x G^T and zu = x U^T in float32, as ffn_gate_dz takes them.
     Where x, G or U requires a gradient, autograd gets it by ffn_gate_backward (and neither y nor save can be
-    given)."""
+    given).  Forward-mode tangents are refused."""
+    if _fw._current_level >= 0:
+        _no_tangents(x=x, G=G, U=U)
     if torch.is_grad_enabled() and (x.requires_grad or G.requires_grad or U.requires_grad):
         if y is not None or save:
             raise GQError(GQ_EINVAL, "x, G or U requires a gradient, which a given y or saved products would "
@@ -1376,6 +1391,8 @@ def ffn_gate_dz(dh, zg, zu, act: str = "silu", dzg=None, dzu=None, stream=None):
     """(dzg, dzu) bfloat16, the gradients of zg and zu (float32, as ffn_gate saves them) from
     that of h = act(zg) zu (float32 or bfloat16); all of one shape.  gq_fisher_accumulate takes
     them with x as the gradients of the two projections' outputs."""
+    if _fw._current_level >= 0:
+        _no_tangents(dh=dh, zg=zg, zu=zu)
     lib = _lib or library()
     act = _act_id(act)
     index = dh.get_device()
@@ -1414,6 +1431,8 @@ def _ffn_dz_pair(dzg, dzu):
 def ffn_gate_dx(dzg, dzu, G, U, offsets=None, y=None, out_dtype=None, ws=None, stream=None) -> torch.Tensor:
     """dx [n][d_in] = dzg G + dzu U, the gradient of ffn_gate's x (bfloat16 operands; out_dtype
     bfloat16 unless given).  Grouped by offsets like ffn_gate."""
+    if _fw._current_level >= 0:
+        _no_tangents(dzg=dzg, dzu=dzu, G=G, U=U)
     lib = _lib or library()
     n, d_ff, index = _ffn_dz_pair(dzg, dzu)
     experts, f, d_in = _ffn_weights(G, U, offsets, index)
@@ -1433,6 +1452,8 @@ def ffn_gate_dw(dzg, dzu, x, experts=None, offsets=None, which=(True, True), dG=
     """(dG, dU), the gradients of ffn_gate's weights: dzg^T x and dzu^T x [d_ff][d_in] or, with
     `experts` and offsets, [experts][d_ff][d_in], each over its expert's rows (zeros where it has
     none).  which: the ones wanted (None for the other).  out_dtype: bfloat16 unless given."""
+    if _fw._current_level >= 0:
+        _no_tangents(dzg=dzg, dzu=dzu, x=x)
     lib = _lib or library()
     n, d_ff, index = _ffn_dz_pair(dzg, dzu)
     if x.dim() != 2:
@@ -1501,6 +1522,8 @@ def ffn_gate_backward(dh, x, G, U, zg, zu, act: str = "silu", offsets=None, whic
     the products that ffn_gate saved: ffn_gate_dz, ffn_gate_dx and ffn_gate_dw in one call.  which: the
     ones wanted (None for the others).  New outputs are bfloat16; given ones can be float32, dG and dU of one
     type.  Rows of no expert: zeros in a new dx, a given one's values in it."""
+    if _fw._current_level >= 0:
+        _no_tangents(dh=dh, x=x, G=G, U=U, zg=zg, zu=zu)
     lib = _lib or library()
     act = _act_id(act)
     if x.dim() != 2:

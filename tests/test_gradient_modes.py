@@ -1,0 +1,58 @@
+"""What the products do where torch follows a call by other means than a backward pass: nothing is lost without a word.
+
+Refusals come before any launch, so host tensors show them.
+"""
+import pytest
+import torch
+import torch.autograd.forward_ad as fw
+
+import post_weight_quantization_gq_amd as gq
+from post_weight_quantization_gq_amd import binding as B
+
+BF, F32, U8, FP8 = torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn
+
+
+def refused(fn, *a, **k):
+    with pytest.raises(B.GQError) as e:
+        fn(*a, **k)
+    return e.value
+
+
+# ---- forward mode -----------------------------------------------------------------------
+
+def _forward_mode_calls(x, G, z, dz):
+    at = dict(x=x, G=G, U=G)
+    yield "ffn_gate", gq.ffn_gate, at, "xGU"
+    yield "ffn_gate_dz", gq.ffn_gate_dz, dict(dh=z, zg=z, zu=z), ("dh", "zg", "zu")
+    yield "ffn_gate_dx", gq.ffn_gate_dx, dict(dzg=dz, dzu=dz, G=G, U=G), ("dzg", "dzu", "G", "U")
+    yield "ffn_gate_dw", gq.ffn_gate_dw, dict(dzg=dz, dzu=dz, x=x), ("dzg", "dzu", "x")
+    yield "ffn_gate_backward", gq.ffn_gate_backward, dict(dh=z, x=x, G=G, U=G, zg=z, zu=z), ("dh", "x", "G", "U", "zg", "zu")
+    Q, S = torch.zeros(64, 128, dtype=U8), torch.zeros(64, 8, dtype=U8)
+    yield "mxfp4_gemm", gq.mxfp4_gemm, dict(x=x, Q=Q, S=S), "x"
+    yield "mxfp4_gemm_dx", gq.mxfp4_gemm_dx, dict(g=dz, Q=Q, S=S, d_in=200), "g"
+
+
+def test_tangents_are_refused():
+    x, G = torch.zeros(5, 200, dtype=BF), torch.zeros(64, 200, dtype=BF)
+    z, dz = torch.zeros(5, 64), torch.zeros(5, 64, dtype=BF)
+    with fw.dual_level():
+        for name, fn, given, follows in _forward_mode_calls(x, G, z, dz):
+            assert "GPU tensor" in refused(fn, **given).message, name            # a level alone changes nothing
+            for p in follows:
+                dual = fw.make_dual(given[p], torch.ones_like(given[p]))
+                for mode in (torch.enable_grad, torch.no_grad):
+                    with mode():
+                        e = refused(fn, **{**given, p: dual})
+                        assert e.status == B.GQ_EINVAL and "tangent" in e.message and e.message.startswith(p), (name, p)
+
+
+@pytest.mark.gpu
+def test_tangents_are_refused_on_the_gpu(device):
+    """and a level without them gives the same values."""
+    x, G = torch.randn(9, 200, device=device).to(BF), torch.randn(64, 200, device=device).to(BF)
+    want = gq.ffn_gate(x, G, G)
+    with fw.dual_level():
+        assert torch.equal(gq.ffn_gate(x, G, G), want)
+        with pytest.raises(B.GQError, match="tangent"):
+            gq.ffn_gate(fw.make_dual(x, torch.ones_like(x)), G, G)
+    assert torch.equal(gq.ffn_gate(x, G, G), want)

@@ -958,6 +958,16 @@ def _scale_type(scales):
     return _SCALES[scales]
 
 
+def _scales(S, name, index):
+    """A tensor of scales on GPU `index`.  float32 ones can be learnt, but no call here gives their gradient."""
+    _mx_tensor(S, name, index, _SCALES)
+    if S.requires_grad and torch.is_grad_enabled():
+        raise GQError(GQ_EINVAL, f"{name} requires a gradient, which the call does not give: detach it, or call under "
+                                 "torch.no_grad()")
+    if _fw._current_level >= 0:
+        _no_tangents(**{name: S})
+
+
 def _act_id(act):
     if act not in _ACTS:
         raise GQError(GQ_EINVAL, f"unknown activation {act!r}: {', '.join(_ACTS)}")
@@ -1027,7 +1037,7 @@ def _unpack(fn, Q, S, sizes, shape, dtype, y, stream):
         _mx_shape(y, shape, "y")
         _mx_tensor(y, "y", index, (dtype,))
     _mx_tensor(Q, "Q", index, _FP8)
-    _mx_tensor(S, "S", index, _SCALES)
+    _scales(S, "S", index)
     where, st = _place(Q, stream)
     with where:
         if y is None:
@@ -1072,11 +1082,12 @@ def _fp8_weight(Q, S, d_in, offsets, index, scales):
     shape, blocks = Q.shape, (d_in + 127) // 128
     if (offsets is None and len(shape) == 2 and shape[1] == 128 * blocks and
             S.shape == ((shape[0] + 127) // 128, blocks) and Q.get_device() == S.get_device() == index and
-            Q.dtype in _FP8 and S.dtype == scales and Q.is_contiguous() and S.is_contiguous()):
+            Q.dtype in _FP8 and S.dtype == scales and Q.is_contiguous() and S.is_contiguous() and not S.requires_grad and
+            _fw._current_level < 0):
         return 1, shape[0]
     found = _fp8_weight_shape(Q, S, d_in, offsets)
     _mx_tensor(Q, "Q", index, _FP8)
-    _mx_tensor(S, "S", index, _SCALES)
+    _scales(S, "S", index)
     if S.dtype != scales:
         raise GQError(GQ_EDTYPE, f"the weight's scales are {S.dtype}, the rows' {scales}")
     return found
@@ -1087,7 +1098,8 @@ def _fp8_rows(Q, S, d, names):
     rb, rs = _fp8_width(d)
     shape, index = Q.shape, Q.get_device()
     if (len(shape) == 2 and shape[1] == rb and S.shape == (shape[0], rs) and S.get_device() == index >= 0 and
-            Q.dtype in _FP8 and S.dtype in _SCALES and Q.is_contiguous() and S.is_contiguous()):
+            Q.dtype in _FP8 and S.dtype in _SCALES and Q.is_contiguous() and S.is_contiguous() and not S.requires_grad and
+            _fw._current_level < 0):
         return shape[0], index
     if Q.dim() != 2:
         raise GQError(GQ_ESHAPE, f"{names[0]} must be [n][row bytes]")
@@ -1095,7 +1107,7 @@ def _fp8_rows(Q, S, d, names):
     _mx_shape(Q, (n, rb), names[0])
     _mx_shape(S, (n, rs), names[1])
     _mx_tensor(Q, names[0], index, _FP8)
-    _mx_tensor(S, names[1], index, _SCALES)
+    _scales(S, names[1], index)
     return n, index
 
 
@@ -1203,7 +1215,8 @@ def fp8_gemm(XQ, XS, Q, S, d_in: int, offsets=None, y=None, out_dtype=None, ws=N
     bfloat16 one is faster, with products of eight added to 14 bits.  With offsets (int64 [experts + 1] on the device)
     rows offsets[e] .. offsets[e + 1] - 1 are multiplied by weight e of Q [experts][d_out][..],
     and the other rows of a given y keep their values (of a new one: zeros).  out_dtype: bfloat16
-    unless given.  Codes carry no gradient: fp8_gemm_dx is the product's part of it."""
+    unless given.  Codes carry no gradient: fp8_gemm_dx is the product's part of it.  Nor do scales: float32 ones that
+    require a gradient are refused while gradients are recorded."""
     lib = _lib or library()
     n, index = _fp8_rows(XQ, XS, d_in, ("XQ", "XS"))
     experts, d_out = _fp8_weight(Q, S, d_in, offsets, index, XS.dtype)

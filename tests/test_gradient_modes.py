@@ -56,3 +56,44 @@ def test_tangents_are_refused_on_the_gpu(device):
         with pytest.raises(B.GQError, match="tangent"):
             gq.ffn_gate(fw.make_dual(x, torch.ones_like(x)), G, G)
     assert torch.equal(gq.ffn_gate(x, G, G), want)
+
+
+# ---- float32 scales ---------------------------------------------------------------------
+
+def _scaled_calls(device, lead):
+    """(name, call, its float32 scales) of everything that reads scales."""
+    n, d_in, d_out = 5, 200, 130
+    codes = lambda *shape: torch.zeros(shape, dtype=U8, device=device).view(FP8)
+    ones = lambda *shape: torch.ones(shape, device=device)
+    X, G = (codes(n, 256), ones(n, 4)), (codes(n, 256), ones(n, 4))
+    W = (codes(*lead, d_out, 256), ones(*lead, 2, 2))
+    off = dict(offsets=torch.tensor([0, 2, 5], device=device)) if lead else {}
+    yield "dequantize", lambda xs: gq.fp8_dequantize(X[0], xs, d_in), [X[1]]
+    yield "dequantize_weight", lambda s: gq.fp8_dequantize_weight(W[0], s, d_in), [W[1]]
+    yield "gemm", lambda xs, s: gq.fp8_gemm(X[0], xs, W[0], s, d_in, **off), [X[1], W[1]]
+    yield "gemm_dx", lambda gs, s: gq.fp8_gemm_dx(G[0], gs, W[0], s, d_in, **off), [G[1], W[1]]
+    for packed in (False, True):
+        yield "gate", lambda xs, g, u: gq.fp8_ffn_gate(X[0], xs, W[0], g, W[0], u, d_in, packed=packed, **off), [X[1], W[1], W[1]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lead", [(), (2,)])
+def test_scales_that_require_a_gradient(device, lead):
+    """are refused while gradients are recorded, and tangents of them too; else the values are the same."""
+    for name, fn, scales in _scaled_calls(device, lead):
+        value = lambda t: t[0].view(U8) if isinstance(t, tuple) else t
+        want = value(fn(*scales))
+        for i in range(len(scales)):
+            some = [s.clone().requires_grad_(i == k) for k, s in enumerate(scales)]
+            with pytest.raises(B.GQError, match="requires a gradient") as e:
+                fn(*some)
+            assert e.value.status == B.GQ_EINVAL
+            with torch.no_grad():
+                assert torch.equal(value(fn(*some)), want)
+            some[i] = some[i].detach()
+            assert torch.equal(value(fn(*some)), want)
+            with fw.dual_level():
+                assert torch.equal(value(fn(*some)), want)
+                some[i] = fw.make_dual(some[i], torch.ones_like(some[i]))
+                with pytest.raises(B.GQError, match="tangent"):
+                    fn(*some)

@@ -632,10 +632,19 @@ def _other_place(device, stream):
         yield
 
 
+def _untraced():
+    """A trace would record the outputs' allocation, and not the kernels that fill them."""
+    if torch._C._is_tracing() or torch._C._get_dispatch_mode(torch._C._TorchDispatchModeKey.PROXY) is not None:
+        raise GQError(GQ_EINVAL, "the call cannot be traced (make_fx, torch.jit.trace): its outputs would be memory that "
+                                 "nothing fills")
+
+
 def _place(t, stream):
     """(context, stream pointer) of a call on t's device: inside the context that device is
     current, and what the call allocates belongs to the stream it runs on (its memory is reused
     in that stream's order).  Without a device or stream to change to, the context does nothing."""
+    if torch._C._is_tracing() or torch._C._len_torch_dispatch_stack():
+        _untraced()
     index = t.get_device()
     if stream is None:
         if index == torch._C._cuda_getDevice():

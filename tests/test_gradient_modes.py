@@ -97,3 +97,46 @@ def test_scales_that_require_a_gradient(device, lead):
                 some[i] = fw.make_dual(some[i], torch.ones_like(some[i]))
                 with pytest.raises(B.GQError, match="tangent"):
                     fn(*some)
+
+
+# ---- traces -----------------------------------------------------------------------------
+
+class _Counts(torch.utils._python_dispatch.TorchDispatchMode):
+    """A mode that only looks on, as counters of operations do."""
+    seen = 0
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        _Counts.seen += 1
+        return func(*args, **(kwargs or {}))
+
+
+@pytest.mark.gpu
+def test_traces_are_refused(device):
+    """A traced call would give memory that nothing has filled; modes that only look on are not meant."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    x, w = torch.randn(5, 256, device=device).to(BF), torch.randn(130, 256, device=device).to(BF)
+    XQ, XS = gq.fp8_quantize(x)
+    Q, S = gq.fp8_quantize_weight(w)
+    M = gq.mxfp4_quantize(w)
+    GQ, GS = gq.fp8_quantize(torch.randn(5, 130, device=device))
+    h, zg, zu = gq.ffn_gate(x, w, w, save=True)
+    y = [torch.empty_like(h)]
+    leaf = x.clone().requires_grad_()
+    calls = [
+        (gq.fp8_quantize, (x,)), (gq.fp8_quantize_weight, (w,)), (lambda q, s: gq.fp8_dequantize(q, s, 256), (XQ, XS)),
+        (lambda q, s: gq.fp8_dequantize_weight(q, s, 256), (Q, S)), (lambda *t: gq.fp8_gemm(*t, 256), (XQ, XS, Q, S)),
+        (lambda *t: gq.fp8_gemm(*t, 256, y=y[0], ws=False), (XQ, XS, Q, S)),
+        (lambda *t: gq.fp8_gemm_dx(*t, 256), (GQ, GS, Q, S)), (lambda *t: gq.fp8_ffn_gate(*t, Q, S, 256), (XQ, XS, Q, S)),
+        (lambda *t: gq.fp8_ffn_gate(*t, Q, S, 256, packed=True), (XQ, XS, Q, S)), (gq.ffn_gate, (x, w, w)), (gq.ffn_gate, (leaf, w, w)),
+        (gq.ffn_gate_dz, (h, zg, zu)), (gq.ffn_gate_dx, (h, h, w, w)), (gq.ffn_gate_dw, (h, h, x)),
+        (gq.ffn_gate_backward, (h, x, w, w, zg, zu)), (gq.mxfp4_quantize, (w,)), (lambda *t: gq.mxfp4_gemm(x, *t), M)]
+    for fn, args in calls:
+        print("traced:", fn, flush=True)
+        alone = lambda *t: fn(*t)                                              # (no arguments by name)
+        with pytest.raises(B.GQError, match="traced"):
+            make_fx(alone)(*args)
+        with pytest.raises(B.GQError, match="traced"):
+            torch.jit.trace(alone, args, check_trace=False)
+    with _Counts():
+        assert torch.equal(gq.ffn_gate(x, w, w), h)
+    assert _Counts.seen > 0

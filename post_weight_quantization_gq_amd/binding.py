@@ -1367,7 +1367,17 @@ def _ffn_gradients(ctx, dh):
                            [None, None, None], torch.bfloat16, None, None), None, None, None, None)
 
 
-_ffn_gradients_once = torch.autograd.function.once_differentiable(_ffn_gradients)
+class _FfnGradients(torch.autograd.Function):
+    """_ffn_gradients where a graph of the gradients is asked for: of all that they depend on, so that who follows it is
+    refused (and does not get the rest of a sum without them)."""
+
+    @staticmethod
+    def forward(ctx, gate, dh, *leaves):
+        return _ffn_gradients(gate, dh)[:3]
+
+    @staticmethod
+    def backward(ctx, *d):
+        raise GQError(GQ_ENOTIMPL, "ffn_gate's gradients are not differentiable themselves")
 
 
 class _FfnGate(torch.autograd.Function):
@@ -1381,8 +1391,9 @@ class _FfnGate(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dh):
-        # (a graph of the gradients is asked for: they are marked as without one)
-        return (_ffn_gradients_once if torch.is_grad_enabled() else _ffn_gradients)(ctx, dh)
+        if torch.is_grad_enabled():
+            return (*_FfnGradients.apply(ctx, dh, *ctx.saved_tensors[:3]), None, None, None, None)
+        return _ffn_gradients(ctx, dh)
 
 
 def ffn_gate(x, G, U, act: str = "silu", offsets=None, y=None, out_dtype=None, save: bool = False,
@@ -1394,7 +1405,7 @@ def ffn_gate(x, G, U, act: str = "silu", offsets=None, y=None, out_dtype=None, s
     values (of a new one: zeros).  out_dtype: float32 or bfloat16, x's unless given.
     With save: (h, zg, zu), zg = x G^T and zu = x U^T in float32, as ffn_gate_dz takes them.
     Where x, G or U requires a gradient, autograd gets it by ffn_gate_backward (and neither y nor save can be
-    given).  Forward-mode tangents are refused."""
+    given), which is not differentiable itself.  Forward-mode tangents are refused."""
     if _fw._current_level >= 0:
         _no_tangents(x=x, G=G, U=U)
     if torch.is_grad_enabled() and (x.requires_grad or G.requires_grad or U.requires_grad):

@@ -140,3 +140,30 @@ def test_traces_are_refused(device):
     with _Counts():
         assert torch.equal(gq.ffn_gate(x, w, w), h)
     assert _Counts.seen > 0
+
+
+# ---- gradients of gradients -------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mask", [(1, 1, 1), (1, 0, 0), (0, 1, 0), (0, 0, 1)])
+@pytest.mark.parametrize("given", [False, True])
+def test_a_gradient_that_depends_on_the_gates_is_refused(device, mask, given):
+    """Also where the gradient of h requires none, and beside a term that has a gradient."""
+    x, G, U = (torch.randn(s, device=device).to(BF) for s in ((9, 200), (64, 200), (64, 200)))
+    leaves = [t.requires_grad_(bool(m)) for t, m in zip((x, G, U), mask)]
+    needed = [t for t in leaves if t.requires_grad]
+    dh = torch.randn(9, 64, device=device).to(BF).requires_grad_(given)
+    want = torch.autograd.grad(gq.ffn_gate(*leaves), needed, dh.detach())
+    h = gq.ffn_gate(*leaves)
+    got = torch.autograd.grad(h, needed, dh, create_graph=True)
+    assert all(torch.equal(a, b) and a.requires_grad for a, b in zip(got, want))
+    # a penalty beside the loss: its part of the gradient cannot be left out
+    with pytest.raises(B.GQError, match="not differentiable"):
+        (h.float().sum() + got[0].float().square().sum()).backward()
+    # the loss alone has its gradient, with a graph or without
+    for t in needed:
+        t.grad = None
+    gq.ffn_gate(*leaves).backward(dh.detach(), create_graph=given)
+    assert all(torch.equal(t.grad, w) for t, w in zip(needed, want))
+    for t in needed:
+        t.grad = None

@@ -1357,11 +1357,20 @@ def _ffn_forward(x, G, U, act, offsets, y, out_dtype, save, ws, stream):
 
 
 def _ffn_gradients(ctx, dh):
-    """What _FfnGate.backward gives; the forward pass has checked all but dh."""
+    """What _FfnGate.backward gives.  The forward pass has checked its tensors, but hooks of saved tensors can give others
+    back."""
     x, G, U, z, offsets = ctx.saved_tensors
-    n, _, d_ff, _, _ = ctx.sizes
+    n, d_in, d_ff, experts, _ = ctx.sizes
     dh = dh.contiguous()
-    _mx_tensor(dh, "dh", x.get_device())
+    index = x.get_device()
+    _mx_tensor(dh, "dh", index)
+    _mx_shape(x, (n, d_in), "x")
+    _mx_tensor(x, "x", index, _BF16)
+    if _ffn_weights(G, U, offsets, index) != (experts, d_ff, d_in):
+        raise GQError(GQ_ESHAPE, f"G was [..][{d_ff}][{d_in}], saved as {tuple(G.shape)}")
+    _mx_shape(z, (2, n, d_ff), "the saved products")
+    _mx_tensor(z, "the saved products", index, _F32)
+    _mm_offsets(offsets, experts, index)
     zg = z.data_ptr()
     return (*_ffn_backward(dh, x, G, U, zg, zg + 4 * n * d_ff, offsets, ctx.sizes, ctx.needs_input_grad,
                            [None, None, None], torch.bfloat16, None, None), None, None, None, None)

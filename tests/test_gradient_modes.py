@@ -167,3 +167,42 @@ def test_a_gradient_that_depends_on_the_gates_is_refused(device, mask, given):
     assert all(torch.equal(t.grad, w) for t, w in zip(needed, want))
     for t in needed:
         t.grad = None
+
+
+# ---- hooks of saved tensors -------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts", [None, 3])
+def test_saved_tensors_that_hooks_change(device, experts):
+    """Kept on the host and brought back: the same gradients.  Given back as anything but what was saved: refused, before
+    a kernel reads it."""
+    lead = (experts,) if experts else ()
+    x, G, U = (torch.randn(s, device=device).to(BF).requires_grad_() for s in ((9, 200), (*lead, 64, 200), (*lead, 64, 200)))
+    offsets = torch.tensor([0, 3, 3, 8], device=device) if experts else None
+    dh = torch.randn(9, 64, device=device).to(BF)
+    step = lambda: torch.autograd.grad(gq.ffn_gate(x, G, U, offsets=offsets), (x, G, U), dh)
+    want = step()
+    with torch.autograd.graph.save_on_cpu():
+        assert all(torch.equal(a, b) for a, b in zip(step(), want))
+    changes = dict(host=lambda t: t.cpu(), type=lambda t: t.to(torch.float16), part=lambda t: t[..., :-1].contiguous(),
+                   flat=lambda t: t.flatten(), strides=lambda t: t.transpose(-1, -2).contiguous().transpose(-1, -2) if t.dim() > 1 else t[::2])
+    count = 5 if experts else 4
+    for name, change in changes.items():
+        for which in range(count):
+            place = []
+
+            def pack(t):
+                place.append(t)
+                return len(place) - 1
+
+            def unpack(i):
+                return change(place[i]) if i == which else place[i]
+
+            if name == "flat" and which == 4:              # (offsets are flat)
+                continue
+            print(name, which, flush=True)
+            with torch.autograd.graph.saved_tensors_hooks(pack, unpack):
+                h = gq.ffn_gate(x, G, U, offsets=offsets)
+            assert len(place) == count
+            with pytest.raises(B.GQError):
+                torch.autograd.grad(h, (x, G, U), dh)

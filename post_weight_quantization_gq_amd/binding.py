@@ -632,9 +632,12 @@ def _other_place(device, stream):
         yield
 
 
+_tracing, _modes = torch._C._is_tracing, torch._C._len_torch_dispatch_stack
+
+
 def _untraced():
     """A trace would record the outputs' allocation, and not the kernels that fill them."""
-    if torch._C._is_tracing() or torch._C._get_dispatch_mode(torch._C._TorchDispatchModeKey.PROXY) is not None:
+    if _tracing() or torch._C._get_dispatch_mode(torch._C._TorchDispatchModeKey.PROXY) is not None:
         raise GQError(GQ_EINVAL, "the call cannot be traced (make_fx, torch.jit.trace): its outputs would be memory that "
                                  "nothing fills")
 
@@ -643,7 +646,7 @@ def _place(t, stream):
     """(context, stream pointer) of a call on t's device: inside the context that device is
     current, and what the call allocates belongs to the stream it runs on (its memory is reused
     in that stream's order).  Without a device or stream to change to, the context does nothing."""
-    if torch._C._is_tracing() or torch._C._len_torch_dispatch_stack():
+    if _tracing() or _modes():
         _untraced()
     index = t.get_device()
     if stream is None:

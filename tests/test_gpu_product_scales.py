@@ -1,5 +1,5 @@
 """GPU tests of the scales of 8-bit products: exponents whose sum passes what float32 holds, NaN at streamed row
-counts.
+counts, any place in memory.
 
 A scale byte s stands for 2^(s - 127), so a block's sum takes the exponent of both its bytes.  Sums here are of
 few small integers, exact in float32, and so is their product with a power of two where the result is a number of the
@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import post_weight_quantization_gq_amd as gq
-from _product_cases import BF, F32, FP8, U8
+from _product_cases import BF, F32, FP8, U8, counts
+from _product_kernels import CASES
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +115,45 @@ def test_a_scale_of_nan_makes_its_row_or_columns_nan(device, n, streamed, op, ou
     bad = torch.isnan(call(op, x.to(FP8), XS, w.to(FP8), S, d, out))
     cols = slice(0, 128) if op == "dx" else slice(128, 256)
     assert bool(bad[:, cols].all()) and int(bad.sum()) == n * 128
+
+
+def place(t, at):
+    """t's values, starting `at` elements past a 256-byte border."""
+    some = torch.zeros(t.numel() + at, dtype=t.dtype, device=t.device)
+    assert some.data_ptr() % 256 == 0
+    some[at:] = t.flatten()
+    return some[at:].view(t.shape)
+
+
+@pytest.mark.parametrize("scales", [U8, F32])
+@pytest.mark.parametrize("op", [op for op in CASES if op.startswith("fp8")])
+def test_scales_at_any_place_that_the_header_allows(device, op, scales):
+    """Rows' scales off the 16-byte border that the tiles' copies of float32 ones would like, weights' off their own: the
+    same bits, in every kernel."""
+    name = op.replace("fp8_", "").replace("ffn_", "")
+    for n, d_in, d_out, experts in CASES[op]:
+        print(op, n, d_in, d_out, experts, flush=True)
+        back = op == "fp8_gemm_dx"
+        at = counts(n, experts, seed=n) if experts else None
+        offsets = torch.tensor(at, device=device) if experts else None
+        E = (experts,) if experts else ()
+        XQ, XS = gq.fp8_quantize(torch.randn(n, d_out if back else d_in, device=device), scales=scales)
+        Q, S = gq.fp8_quantize_weight(torch.randn(*E, d_out, d_in, device=device), scales=scales)
+        for out in (BF, F32) if not name.endswith("packed") else (None,):
+            def run(xs, s, u):
+                k = dict(offsets=offsets)
+                if back:
+                    return gq.fp8_gemm_dx(XQ, xs, Q, s, d_in, out_dtype=out, **k)
+                if name == "gemm":
+                    return gq.fp8_gemm(XQ, xs, Q, s, d_in, out_dtype=out, **k)
+                if out is not None:
+                    return gq.fp8_ffn_gate(XQ, xs, Q, s, Q, u, d_in, out_dtype=out, **k)
+                HS = place(torch.zeros(n, gq.fp8_row_scales(d_out), dtype=scales, device=device), 4 if scales == U8 else 3)
+                HQ, HS = gq.fp8_ffn_gate(XQ, xs, Q, s, Q, u, d_in, packed=True, HS=HS, **k)
+                return torch.cat([HQ.view(U8).flatten(), HS.contiguous().view(U8).flatten()])
+
+            want = run(XS, S, S)
+            for a, b in ((1, 1), (2, 3), (3, 2)):
+                xs = place(XS, 4 * a if scales == U8 else a)
+                assert xs.data_ptr() % 16 == 4 * a
+                assert torch.equal(run(xs, place(S, b), place(S, a)), want), (n, d_in, d_out, experts, out, a, b)

@@ -385,6 +385,15 @@ hipError_t mm_run(const MmCall& c, void* ws, hipStream_t st) {
     t.hs_row = fp8_scales(m);
     t.act = c.act;
     t.part = P.join ? (float*)((char*)ws + P.pad_bytes) : nullptr;
+    // Large outputs that the caches would not hold until they are read, or only in place of the operands, are stored past
+    // the caches' order; others, and parts that the join reads at once, as usual.  With the product that reads h in bfloat16 (gate and
+    // down projection, us as usual and past): 1024 rows, 2048 -> 5632 (12 MB) 81 and 86; 2048 rows 142 and 143 (23 MB), 4096 rows 228 and
+    // 232 (46 MB), 8192 rows 423 and 427 (92 MB), 16384 rows 854 and 820 (185 MB); 4096 -> 11008: 512 rows 169 and 169, 3000
+    // rows 656 and 655 (66 MB), 4096 rows 829 and 826 (90 MB; the gate alone 581 and 553), 6000 rows 1280 and 1246.  With an update that
+    // reads both weights' gradients: 512 rows, 2048 -> 4096 (34 MB) 51 and 52, 4096 -> 4096 (67 MB) 93 and 99, 4096 -> 8192 (134 MB) 219
+    // and 211; 4096 rows, 8192 -> 8192 1062 and 1035.  Parts: 16384 rows, 1024 -> 1024 in 8 81 and 85.
+    if (c.form == MM_GATE) t.past = c.y_bf16 && (size_t)c.n * m * 2 >= (size_t)64 << 20;
+    if (tn) t.past = !P.join && (size_t)t.outs * c.experts * c.d_out * m * (c.y_bf16 ? 2 : 4) >= (size_t)128 << 20;
     switch (c.elt) {
         case MM_BF16: e = mm_launch_bf16(c.form, t, P, st); break;
         case MM_E8: e = mm_launch_e8(c.form, t, P, st); break;

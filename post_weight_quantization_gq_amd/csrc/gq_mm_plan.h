@@ -34,6 +34,7 @@ struct MmTile {
     void* hs;
     int64_t hq_row, hs_row;       // bytes of a packed row, its scales
     int act;
+    int past;                     // MM_GATE's h in bfloat16, MM_TN's outputs: stored past the caches' order
     float* part;                  // sums [split][n][m] (MM_GATE: [split][2][n][m], MM_TN:
                                   // [split][outs][experts][d_out][m]), or null
 };

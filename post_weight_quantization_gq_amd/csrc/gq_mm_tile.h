@@ -54,6 +54,14 @@ __device__ __forceinline__ void mm_dma_first(__amdgpu_buffer_rsrc_t r, void* dst
                      : "=&s"(all) : "s"(at), "s"((uint64_t(1) << LANES) - 1), "v"(voff), "s"(r) : "m0", "memory");
 }
 
+// Past the caches' order.  (The empty statements keep the compiler from making one ordinary store of this one and that of
+// the other branch, before or behind both.)
+__device__ __forceinline__ void mm_store_past(u32x4_any v, u32x4_any* to) {
+    asm volatile("" ::: "memory");
+    __builtin_nontemporal_store(v, to);
+    asm volatile("" ::: "memory");
+}
+
 template <int ELT, int FORM, int BM, int BN, int WM, int NW, int R>
 struct MmGeo {
     static constexpr int ES = ELT == MM_BF16 ? 2 : 1, KE = 128 / ES;    // bytes of a value, values of a stage
@@ -575,9 +583,8 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                 }
             });
             const int row0 = wm * TM + 16 * q, left = rows - row0;
-            // products out, whole lines at a time, and h past the caches' order, which leaves them the operands (4 rounds of
-            // 25 stages in bfloat16: 184 us for h alone, 178 so; with both products 227 and 214.  The products too: 209, but
-            // the backward pass that reads them next is slower by as much)
+            // products out, whole lines at a time (past the caches' order 4 rounds of 25 stages in bfloat16 take 209 us and 214
+            // so, but the backward pass that reads them next is slower by as much)
             if (z0) {
                 constexpr int FOURS = HC / 4;
 #pragma unroll 1
@@ -656,9 +663,11 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                 if (!p.y_bf16) {
                     values((float*)p.y[0], h);
                 } else if (some >= 8) {
-                    __builtin_nontemporal_store((u32x4_any)u32x4{pack_bf16x2(h[0][0], h[0][1]), pack_bf16x2(h[0][2], h[0][3]),
-                                                                 pack_bf16x2(h[1][0], h[1][1]), pack_bf16x2(h[1][2], h[1][3])},
-                                                (u32x4_any*)((uint16_t*)p.y[0] + to));
+                    const u32x4_any v = u32x4{pack_bf16x2(h[0][0], h[0][1]), pack_bf16x2(h[0][2], h[0][3]),
+                                              pack_bf16x2(h[1][0], h[1][1]), pack_bf16x2(h[1][2], h[1][3])};
+                    u32x4_any* const at16 = (u32x4_any*)((uint16_t*)p.y[0] + to);
+                    if (p.past) mm_store_past(v, at16);
+                    else *at16 = v;
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -725,9 +734,7 @@ __global__ __launch_bounds__(64 * NW) void k_mm_tile(MmTile p) {
                     if (row >= left || some <= 0) continue;
                     uint8_t* const to = out + (int64_t)(row0 + row) * p.m * wide + at16;
                     if (!decltype(ends)::value || some >= 16) {
-                        // (weights' gradients past the caches' order: forward and back of 4096 tokens, 4096 -> 11008 1957
-                        // us, 1945 so; the other forms' outputs, which are read next, gain nothing)
-                        if constexpr (FORM == MM_TN) __builtin_nontemporal_store((u32x4_any)v, (u32x4_any*)to);
+                        if (FORM == MM_TN && p.past) mm_store_past(v, (u32x4_any*)to);
                         else *(u32x4_any*)to = v;
                     } else {
                         for (int b = 0; b < some; b += wide) {

@@ -1566,7 +1566,7 @@ def ffn_gate_backward(dh, x, G, U, zg, zu, act: str = "silu", offsets=None, whic
     """(dx, dG, dU), the gradients of ffn_gate's x, G and U from that of h (float32 or bfloat16) and
     the products that ffn_gate saved: ffn_gate_dz, ffn_gate_dx and ffn_gate_dw in one call.  which: the
     ones wanted (None for the others).  New outputs are bfloat16; given ones can be float32, dG and dU of one
-    type.  Rows of no expert: zeros in a new dx, a given one's values in it."""
+    type (of dz in bfloat16 all the same).  Rows of no expert: zeros in a new dx, a given one's values in it."""
     if _fw._current_level >= 0:
         _no_tangents(dh=dh, x=x, G=G, U=U, zg=zg, zu=zu)
     lib = _lib or library()

@@ -1239,7 +1239,7 @@ gq_status ffn_gate_dz(const void* dh, gq_dtype dh_dt, const float* zg, const flo
                       gq_activation act, void* dzg, void* dzu, void* stream) {
     if (!dtype_ok(dh_dt)) return fail(GQ_EDTYPE, "unsupported dtype %d", (int)dh_dt);
     if (count < 0) return fail(GQ_ESHAPE, "count=%lld", (long long)count);
-    // (pieces of 8 are counted in 32 bits; 14 bytes a value, so more do not fit a card)
+    // (the header's limit; of 2^35 values the pieces of 8 would pass 32 bits)
     if (count > (int64_t)1 << 34) return fail(GQ_ENOTIMPL, "count=%lld above 2^34", (long long)count);
     if ((int)act < gq::ACT_SILU || (int)act > gq::ACT_GELU_TANH) return fail(GQ_EINVAL, "unknown activation %d", (int)act);
     if (count == 0) return GQ_OK;

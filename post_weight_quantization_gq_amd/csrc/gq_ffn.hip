@@ -4,7 +4,9 @@
 //
 // zg and zu are the forward pass's float32 products: rounded to bfloat16 they would add its half step to
 // every gradient a second time, and their bytes are a twentieth of a training step's time.  dzg and dzu are
-// rounded once, to the bfloat16 that the products after them multiply (and that the Fisher takes).
+// rounded once, to the bfloat16 that the products after them multiply (and that the Fisher takes), also for float32
+// gradients: 0.00166 of a gradient's norm, as much as rounding the gradient itself takes, 0.00235 together.  A
+// second bfloat16 for what the first leaves would double the products after it, 1.1 of a training step's 1.9 ms.
 // One pass, bound by HBM: 14 bytes a value with a bfloat16 dh (4096 x 11008: 125 us, 5.0 TB/s).
 #include "gq_mm.h"
 

@@ -74,14 +74,15 @@ def test_zero_sums_under_the_largest_scales(device, n, streamed, op, out):
     assert bool(((y.double() - v).abs() <= limit + 1e-30)[:, keep].all())
 
 
+@pytest.mark.parametrize("out", [BF, F32])
 @pytest.mark.parametrize("op", ["gemm", "dx"])
 @pytest.mark.parametrize("n,streamed", ROWS)
 @pytest.mark.parametrize("left,right", [(-75, -75), (-126, -24), (-24, -126), (100, 26), (127, -127), (-127, 127)])
-def test_sums_within_the_range_under_scales_past_it(device, n, streamed, left, right, op):
-    """float32 sums: scales whose product is no float32 number, or at the end of the bytes' range, of sums whose
+def test_sums_within_the_range_under_scales_past_it(device, n, streamed, left, right, op, out):
+    """Scales whose product is no float32 number, or at the end of the bytes' range, of sums whose
     product with them is one."""
     d = 128
-    assert plan(op, n, d, F32)["streamed"] == (streamed and op != "dx")
+    assert plan(op, n, d, out)["streamed"] == (streamed and op != "dx")
     # for small products of scales the largest codes, 128 448^2 2^-150 = 1.5 2^-126; for large ones one small code
     if left + right < -100:
         x, w = torch.full((n, d), 448.0, device=device), torch.full((d, d), 448.0, device=device)
@@ -90,7 +91,7 @@ def test_sums_within_the_range_under_scales_past_it(device, n, streamed, left, r
         x[:, 0], w[0], w[:, 0] = 2.0 ** -6, 1.0, 1.0
     XS = torch.full((n, 4), 127 + left, dtype=U8, device=device)
     S = torch.full((1, 1), 127 + right, dtype=U8, device=device)
-    y = call(op, x.to(FP8), XS, w.to(FP8), S, d, F32)
+    y = call(op, x.to(FP8), XS, w.to(FP8), S, d, out)
     want = (x.double() @ (w.double() if op == "dx" else w.double().T)) * 2.0 ** (left + right)
     assert bool((want.abs() >= 2.0 ** -126)[want != 0].all()) and bool(torch.isfinite(want.float()).all())
     assert torch.equal(y.double(), want)

@@ -680,6 +680,17 @@ def _mx_tensor(t, name, index, dtypes=_MX_DTYPES):
     raise GQError(GQ_EINVAL, f"{name} is on {t.device}, the call's first tensor is not")
 
 
+def _mx_given(t, shape, name, index, dtypes=_MX_DTYPES):
+    """An output of the caller's: as _mx_shape and _mx_tensor have it, and known to autograd as changed in place, so that a
+    backward pass that has saved its old values says so."""
+    _mx_shape(t, shape, name)
+    _mx_tensor(t, name, index, dtypes)
+    if t.requires_grad and torch.is_grad_enabled():
+        raise GQError(GQ_EINVAL, f"{name} requires a gradient, which the values written into it would not have: give "
+                                 "another output, or call under torch.no_grad()")
+    torch._C._increment_version((t,))
+
+
 def _no_tangents(**tensors):
     """Inside a forward-mode level: the calls give no tangents, and would drop those of their tensors."""
     for name, t in tensors.items():
@@ -712,8 +723,7 @@ def mxfp4_quantize(x, Q=None, S=None, stream=None):
     index = x.get_device()
     for t, width, name in ((Q, rb, "Q"), (S, rs, "S")):
         if t is not None:
-            _mx_shape(t, (*lead, width), name)
-            _mx_tensor(t, name, index, _U8)
+            _mx_given(t, (*lead, width), name, index, _U8)
     _mx_tensor(x, "x", index)
     where, st = _place(x, stream)
     with where:
@@ -739,8 +749,7 @@ def mxfp4_dequantize(Q, S, d: int, dtype=torch.bfloat16, y=None, stream=None) ->
     _mx_shape(Q, (*lead, rb), "Q")
     _mx_shape(S, (*lead, rs), "S")
     if y is not None:
-        _mx_shape(y, (*lead, d), "y")
-        _mx_tensor(y, "y", index, (dtype,))
+        _mx_given(y, (*lead, d), "y", index, (dtype,))
     _mx_tensor(Q, "Q", index, _U8)
     _mx_tensor(S, "S", index, _U8)
     where, st = _place(Q, stream)
@@ -803,8 +812,7 @@ def _mx_product(fn, size, x, first, size_args, n, width, Q, S, last, experts, of
     if y is not None:
         if out_dtype is not None and y.dtype != out_dtype:
             raise GQError(GQ_EDTYPE, f"y is {y.dtype}, out_dtype {out_dtype}")
-        _mx_shape(y, (n, width), "y")
-        _mx_tensor(y, "y", index)
+        _mx_given(y, (n, width), "y", index)
     elif out_dtype not in _MX_DTYPES:
         raise GQError(GQ_EDTYPE, f"unsupported dtype {out_dtype}")
     wp, wn = None, 0
@@ -995,12 +1003,10 @@ def _pack(fn, x, codes, scale_shape, sizes, Q, S, scales, stream):
         dt = S.dtype
         if scales is not None and dt != scales:
             raise GQError(GQ_EDTYPE, f"S is {S.dtype}, scales {scales}")
-        _mx_shape(S, scale_shape, "S")
-        _mx_tensor(S, "S", index, _SCALES)
+        _mx_given(S, scale_shape, "S", index, _SCALES)
     st_dt = _scale_type(dt)
     if Q is not None:
-        _mx_shape(Q, codes, "Q")
-        _mx_tensor(Q, "Q", index, _FP8)
+        _mx_given(Q, codes, "Q", index, _FP8)
     _mx_tensor(x, "x", index)
     where, st = _place(x, stream)
     with where:
@@ -1046,8 +1052,7 @@ def _unpack(fn, Q, S, sizes, shape, dtype, y, stream):
         raise GQError(GQ_EDTYPE, f"unsupported dtype {dtype}")
     index = Q.get_device()
     if y is not None:
-        _mx_shape(y, shape, "y")
-        _mx_tensor(y, "y", index, (dtype,))
+        _mx_given(y, shape, "y", index, (dtype,))
     _mx_tensor(Q, "Q", index, _FP8)
     _scales(S, "S", index)
     where, st = _place(Q, stream)
@@ -1138,8 +1143,7 @@ def _mm_output(y, out_dtype, shape, index):
         return
     if out_dtype is not None and y.dtype != out_dtype:
         raise GQError(GQ_EDTYPE, f"y is {y.dtype}, out_dtype {out_dtype}")
-    _mx_shape(y, shape, "y")
-    _mx_tensor(y, "y", index)
+    _mx_given(y, shape, "y", index)
 
 
 def _mm_scratch(x, ws, size, size_args):
@@ -1293,8 +1297,7 @@ def fp8_ffn_gate(XQ, XS, GQ, GS, UQ, US, d_in: int, act: str = "silu", offsets=N
     hb, hs = _fp8_width(d_ff)
     for t, shape, name, kinds in ((HQ, (n, hb), "HQ", _FP8), (HS, (n, hs), "HS", (XS.dtype,))):
         if t is not None:
-            _mx_shape(t, shape, name)
-            _mx_tensor(t, name, index, kinds)
+            _mx_given(t, shape, name, index, kinds)
     if ws is not None and ws is not False:
         _mx_tensor(ws, "ws", index, _U8)
     where, st = _place(XQ, stream)
@@ -1446,8 +1449,7 @@ def ffn_gate_dz(dh, zg, zu, act: str = "silu", dzg=None, dzu=None, stream=None):
         _mx_tensor(t, name, index, _F32)
     for t, name in ((dzg, "dzg"), (dzu, "dzu")):
         if t is not None:
-            _mx_shape(t, dh.shape, name)
-            _mx_tensor(t, name, index, _BF16)
+            _mx_given(t, dh.shape, name, index, _BF16)
     _mx_tensor(dh, "dh", index)
     where, st = _place(dh, stream)
     with where:
@@ -1518,8 +1520,7 @@ def ffn_gate_dw(dzg, dzu, x, experts=None, offsets=None, which=(True, True), dG=
             if dt is not None and out[i].dtype != dt:
                 raise GQError(GQ_EDTYPE, f"{name} is {out[i].dtype}, not {dt}")
             dt = out[i].dtype
-            _mx_shape(out[i], shape, name)
-            _mx_tensor(out[i], name, index)
+            _mx_given(out[i], shape, name, index)
     dt = torch.bfloat16 if dt is None else dt
     if dt not in _MX_DTYPES:
         raise GQError(GQ_EDTYPE, f"unsupported dtype {dt}")
@@ -1588,8 +1589,7 @@ def ffn_gate_backward(dh, x, G, U, zg, zu, act: str = "silu", offsets=None, whic
         if out[i] is not None:
             if not which[i]:
                 raise GQError(GQ_EINVAL, f"{name} is given, but not asked for")
-            _mx_shape(out[i], shapes[i], name)
-            _mx_tensor(out[i], name, index)
+            _mx_given(out[i], shapes[i], name, index)
     if not any(which):
         return None, None, None
     dw = torch.bfloat16 if dG is None and dU is None else (dG if dG is not None else dU).dtype

@@ -206,3 +206,65 @@ def test_saved_tensors_that_hooks_change(device, experts):
             assert len(place) == count
             with pytest.raises(B.GQError):
                 torch.autograd.grad(h, (x, G, U), dh)
+
+
+# ---- outputs of the caller's ------------------------------------------------------------
+
+def _writing_calls(device):
+    """(name, call that writes into the given tensors, those tensors)."""
+    n, d, f = 5, 200, 136
+    x, w = torch.randn(n, d, device=device).to(BF), torch.randn(f, d, device=device).to(BF)
+    dh = torch.randn(n, f, device=device).to(BF)
+    new = lambda *shape, dtype=BF: torch.zeros(shape, device=device, dtype=dtype)
+    X, W = gq.fp8_quantize(x, scales=F32), gq.fp8_quantize_weight(w, scales=F32)
+    g8, M, XM = gq.fp8_quantize(dh, scales=F32), gq.mxfp4_quantize(w), gq.mxfp4_quantize(x)
+    h, zg, zu = gq.ffn_gate(x, w, w, save=True)
+    codes = lambda *shape: new(*shape, dtype=U8).view(FP8)
+    yield "fp8_quantize", lambda q, s: gq.fp8_quantize(x, Q=q, S=s), [codes(n, 256), new(n, 4, dtype=F32)]
+    yield "fp8_quantize_weight", lambda q, s: gq.fp8_quantize_weight(w, Q=q, S=s), [codes(f, 256), new(2, 2, dtype=F32)]
+    yield "fp8_dequantize", lambda y: gq.fp8_dequantize(*X, d, y=y), [new(n, d)]
+    yield "fp8_dequantize_weight", lambda y: gq.fp8_dequantize_weight(*W, d, y=y), [new(f, d)]
+    yield "fp8_gemm", lambda y: gq.fp8_gemm(*X, *W, d, y=y), [new(n, f)]
+    yield "fp8_gemm_dx", lambda y: gq.fp8_gemm_dx(*g8, *W, d, y=y), [new(n, d)]
+    yield "fp8_ffn_gate", lambda y: gq.fp8_ffn_gate(*X, *W, *W, d, y=y), [new(n, f)]
+    yield ("fp8_ffn_gate packed", lambda q, s: gq.fp8_ffn_gate(*X, *W, *W, d, packed=True, HQ=q, HS=s),
+           [codes(n, 256), new(n, 4, dtype=F32)])
+    yield "ffn_gate", lambda y: gq.ffn_gate(x, w, w, y=y), [new(n, f)]
+    yield "ffn_gate_dz", lambda a, b: gq.ffn_gate_dz(dh, zg, zu, dzg=a, dzu=b), [new(n, f), new(n, f)]
+    yield "ffn_gate_dx", lambda y: gq.ffn_gate_dx(dh, dh, w, w, y=y), [new(n, d)]
+    yield "ffn_gate_dw", lambda a, b: gq.ffn_gate_dw(dh, dh, x, dG=a, dU=b), [new(f, d), new(f, d)]
+    yield ("ffn_gate_backward", lambda a, b, c: gq.ffn_gate_backward(dh, x, w, w, zg, zu, dx=a, dG=b, dU=c),
+           [new(n, d), new(f, d), new(f, d)])
+    yield "mxfp4_quantize", lambda q, s: gq.mxfp4_quantize(w, Q=q, S=s), [new(f, 128, dtype=U8), new(f, 8, dtype=U8)]
+    yield "mxfp4_dequantize", lambda y: gq.mxfp4_dequantize(*M, d, y=y), [new(f, d)]
+    yield "mxfp4_gemm", lambda y: gq.mxfp4_gemm(x, *M, y=y), [new(n, f)]
+    yield "mxfp4_gemm_mx", lambda y: gq.mxfp4_gemm_mx(*XM, *M, d, y=y), [new(n, f)]
+    yield "mxfp4_gemm_dx", lambda y: gq.mxfp4_gemm_dx(dh, *M, d, y=y), [new(n, d)]
+
+
+@pytest.mark.gpu
+def test_given_outputs_are_changed_in_place(device):
+    """A backward pass that has saved an output's old values refuses; an output that requires a gradient is refused while
+    gradients are recorded."""
+    for name, fn, outs in _writing_calls(device):
+        for i, out in enumerate(outs):
+            print(name, i, flush=True)
+            if out.dtype in (BF, F32):
+                leaf = torch.ones_like(out, requires_grad=True)
+                product = (out * leaf).sum()
+                fn(*outs)
+                with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                    product.backward()
+                some = [o.clone().requires_grad_(i == k) if k == i else o for k, o in enumerate(outs)]
+                with pytest.raises(B.GQError, match="requires a gradient"):
+                    fn(*some)
+                with torch.no_grad():
+                    fn(*some)
+                assert torch.equal(some[i], out)
+            else:
+                before = out._version
+                fn(*outs)
+                assert out._version > before
+    with torch.inference_mode():
+        for name, fn, outs in _writing_calls(device):
+            fn(*outs)

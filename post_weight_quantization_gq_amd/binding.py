@@ -1370,12 +1370,15 @@ def _ffn_gradients(ctx, dh):
     dh = dh.contiguous()
     index = x.get_device()
     _mx_tensor(dh, "dh", index)
-    _mx_shape(x, (n, d_in), "x")
-    _mx_tensor(x, "x", index, _BF16)
-    if _ffn_weights(G, U, offsets, index) != (experts, d_ff, d_in):
-        raise GQError(GQ_ESHAPE, f"G was [..][{d_ff}][{d_in}], saved as {tuple(G.shape)}")
-    _mx_shape(z, (2, n, d_ff), "the saved products")
-    _mx_tensor(z, "the saved products", index, _F32)
+    w = (d_ff, d_in) if offsets is None else (experts, d_ff, d_in)
+    if not (x.shape == (n, d_in) and z.shape == (2, n, d_ff) and G.shape == w and U.shape == w and
+            x.dtype == G.dtype == U.dtype == torch.bfloat16 and z.dtype == torch.float32 and
+            G.get_device() == U.get_device() == z.get_device() == index and
+            x.is_contiguous() and G.is_contiguous() and U.is_contiguous() and z.is_contiguous()):
+        for t, shape, name, kinds in ((x, (n, d_in), "x", _BF16), (G, w, "G", _BF16), (U, w, "U", _BF16),
+                                      (z, (2, n, d_ff), "the saved products", _F32)):
+            _mx_shape(t, shape, name)
+            _mx_tensor(t, name, index, kinds)
     _mm_offsets(offsets, experts, index)
     zg = z.data_ptr()
     return (*_ffn_backward(dh, x, G, U, zg, zg + 4 * n * d_ff, offsets, ctx.sizes, ctx.needs_input_grad,

@@ -268,3 +268,29 @@ def test_given_outputs_are_changed_in_place(device):
     with torch.inference_mode():
         for name, fn, outs in _writing_calls(device):
             fn(*outs)
+
+
+# ---- streams ----------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts", [None, 3])
+def test_a_gate_on_a_stream_of_its_own(device, experts):
+    """The forward pass on a given stream, the gradient asked for on another: the backward pass follows the forward one's
+    stream, and its results the asker's."""
+    n, d_in, d_ff = 600, 512, 1000
+    lead = (experts,) if experts else ()
+    offsets = torch.tensor([0, 200, 200, 550], device=device) if experts else None
+    G, U = ((torch.randn(*lead, d_ff, d_in, device=device) * 0.04).to(BF).requires_grad_() for _ in range(2))
+    xs = [torch.randn(n, d_in, device=device).to(BF).requires_grad_() for _ in range(4)]
+    dhs = [torch.randn(n, d_ff, device=device).to(BF) for _ in range(4)]
+    want = [torch.autograd.grad(gq.ffn_gate(x, G, U, offsets=offsets), (x, G, U), dh) for x, dh in zip(xs, dhs)]
+    here, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    side.wait_stream(here)
+    for turn in range(8):
+        x, dh = xs[turn % 4], dhs[turn % 4]
+        h = gq.ffn_gate(x, G, U, offsets=offsets, stream=side)
+        here.wait_stream(side)
+        got = torch.autograd.grad(h, (x, G, U), dh * 1)
+        del h
+        torch.empty(3 * n * d_ff, device=device).fill_(float("nan"))         # over whatever has been freed here
+        assert all(torch.equal(a, b) for a, b in zip(got, want[turn % 4])), turn
